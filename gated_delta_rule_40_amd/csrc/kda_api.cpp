@@ -7,12 +7,12 @@
 
 #include <atomic>
 #include <cstdint>
-#include <cstdlib>
-#include <cstring>
 #include <mutex>
-#include <vector>
 
 #include "kda.h"
+#include "kda_host.hpp"
+
+using namespace kda_host;
 
 extern "C" hipError_t kda_launch_prefill(int bf16, int chunk, int dv_block, const void *q,
                                          const void *k, const void *v, const float *g,
@@ -71,8 +71,6 @@ namespace {
 
 constexpr int32_t kHeadDim = 128;
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 kda_status check_common(const void *q, const void *k, const void *v, const float *g,
                         const float *beta, const void *out, int32_t dk, int32_t dv,
                         kda_dtype dtype)
@@ -85,35 +83,6 @@ kda_status check_common(const void *q, const void *k, const void *v, const float
         !aligned(beta, 4))
         return KDA_ERR_INVALID_ARG;
     if (dk != kHeadDim || dv != kHeadDim) return KDA_ERR_UNSUPPORTED;
-    return KDA_OK;
-}
-
-// KDA_VALIDATE=1 in the environment (read once): the entry points that take
-// cu_seqlens copy it to the host, synchronising `stream`, and check it before
-// launching anything.  Off by default, since it costs a synchronisation.
-bool validate_enabled()
-{
-    static std::atomic<int> state{-1};
-    int v = state.load(std::memory_order_relaxed);
-    if (v < 0) {
-        const char *e = std::getenv("KDA_VALIDATE");
-        v = (e && std::strcmp(e, "1") == 0) ? 1 : 0;
-        state.store(v, std::memory_order_relaxed);
-    }
-    return v == 1;
-}
-
-// cu[0] = 0, non-decreasing, cu[N] <= T.  Returns KDA_ERR_INVALID_ARG for
-// contents that break this, KDA_ERR_LAUNCH if the copy itself fails.
-kda_status validate_cu(const int32_t *cu, int32_t N, int32_t T, hipStream_t stream)
-{
-    std::vector<int32_t> h((size_t)N + 1);
-    if (hipMemcpyAsync(h.data(), cu, sizeof(int32_t) * h.size(), hipMemcpyDeviceToHost, stream) != hipSuccess ||
-        hipStreamSynchronize(stream) != hipSuccess)
-        return KDA_ERR_LAUNCH;
-    if (h[0] != 0 || h[N] > T) return KDA_ERR_INVALID_ARG;
-    for (int32_t n = 0; n < N; ++n)
-        if (h[n + 1] < h[n]) return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
 
@@ -237,8 +206,6 @@ struct CpLayout {
     // output workgroup per (piece, head); units are then the segments
     int32_t pieces, piece_len;
 };
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Summary units: when there are at least as many (segment, head) pairs as
 // compute units (T / seg_len * H >= 256) and segments are long (at least

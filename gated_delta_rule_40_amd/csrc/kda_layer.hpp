@@ -1,0 +1,40 @@
+// kda_layer.hpp -- launchers of the layer operators' kernels, as the host API
+// calls them (kda_scan.hip, kda_conv.hip, kda_norm.hip).  Arguments have been
+// checked; every launcher returns the HIP status of its launches.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+constexpr int32_t kMaxNormChannels = 16384;
+
+size_t kda_scan_ws_bytes(int32_t T, int32_t D);
+hipError_t kda_launch_scan(bool bf16, const void *x, const float *g, const float *init, const int32_t *cu, int32_t N,
+                           int32_t T, int32_t D, void *out, float *fin, float *checkpoints, void *ws, hipStream_t s);
+hipError_t kda_launch_scan_step(bool bf16, const void *x, const float *g, float *state, int64_t n, void *out,
+                                hipStream_t s);
+size_t kda_scan_bwd_ws_bytes(int32_t T, int32_t D, bool has_checkpoints);
+hipError_t kda_launch_scan_backward(bool bf16, const void *x, const float *g, const float *init, const int32_t *cu,
+                                    int32_t N, int32_t T, int32_t D, const void *dout, const float *dfinal,
+                                    const float *checkpoints, void *dx, float *dg, float *dinit, void *ws,
+                                    hipStream_t s);
+
+hipError_t kda_launch_conv(bool bf16, const void *x, const float *w, const float *bias, const void *init,
+                           const int32_t *cu, int32_t N, int32_t T, int32_t D, int32_t width, bool silu, void *out,
+                           void *fin, hipStream_t s);
+hipError_t kda_launch_conv_step(bool bf16, const void *x, const float *w, const float *bias, void *state, int32_t N,
+                                int32_t D, int32_t width, bool silu, void *out, hipStream_t s);
+size_t kda_conv_bwd_ws_bytes(int32_t T, int32_t D, int32_t width, bool bf16);
+hipError_t kda_launch_conv_backward(bool bf16, const void *x, const float *w, const float *bias, const void *init,
+                                    const int32_t *cu, int32_t N, int32_t T, int32_t D, int32_t width, bool silu,
+                                    const void *dout, const void *dfinal, void *dx, float *dw, float *dbias,
+                                    void *dinit, void *ws, hipStream_t s);
+
+hipError_t kda_launch_rmsnorm(bool bf16, const void *x, const void *residual, const float *w, int32_t rows, int32_t D,
+                              float eps, void *sum, void *out, uint8_t *mx, uint8_t *scales, hipStream_t s);
+size_t kda_rmsnorm_bwd_ws_bytes(int32_t rows, int32_t D);
+hipError_t kda_launch_rmsnorm_backward(bool bf16, const void *x, const float *w, const void *dout, const void *dres,
+                                       int32_t rows, int32_t D, float eps, void *dx, float *dw, void *ws,
+                                       hipStream_t s);

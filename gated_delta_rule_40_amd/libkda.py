@@ -14,6 +14,17 @@ fallback: if the library is missing the calls raise.
     kda_decode_step(q, k, v, g, beta, state_inout, out)
     kda_decode_tokens(q, k, v, g, beta, cu_seqlens, state_in, state_out=None, out=None, num_tokens=None)
     kda_backward(q, k, v, g, beta, initial_state, cu_seqlens, dout, dfinal=None, ...) -> gradients
+
+The operators around the recurrence in a layer:
+
+    kda_scan_prefill(x, g, initial_state, cu_seqlens, out, final_state, checkpoints=None, workspace=None)
+    kda_scan_decode_step(x, g, state_inout, out)
+    kda_scan_backward(x, g, initial_state, cu_seqlens, dout, dfinal=None, checkpoints=None, ...) -> gradients
+    kda_conv_prefill(x, weight, bias, initial_state, cu_seqlens, out, final_state, silu=True)
+    kda_conv_decode_step(x, weight, bias, state_inout, out, silu=True)
+    kda_conv_backward(x, weight, bias, initial_state, cu_seqlens, dout, dfinal=None, silu=True, ...) -> gradients
+    kda_rmsnorm(x, weight, out=None, residual=None, residual_out=None, out_mx=None, scales=None, eps=1e-6)
+    kda_rmsnorm_backward(x, weight, dout, dresidual=None, eps=1e-6, ...) -> gradients
 """
 from __future__ import annotations
 
@@ -29,10 +40,14 @@ LIB_PATH = os.path.join(_HERE, "lib", "libkda.so")
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_LAUNCH, KDA_ERR_SCRATCH = 0, 1, 2, 3, 4
 KDA_STATIC_SCRATCH_BYTES = 256 * 1024 * 1024      # include/kda.h
 KDA_F32, KDA_BF16 = 0, 1
+KDA_SCAN_TILE, KDA_MX_BLOCK = 128, 32              # include/kda.h
 
 EXPORTS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_snapshots", "kda_prefill_cp",
            "kda_prefill_cp_workspace_size", "kda_prefill_cp_noalloc", "kda_decode_step", "kda_decode_tokens", "kda_backward",
-           "kda_backward_workspace_size", "kda_status_string", "kda_version")
+           "kda_backward_workspace_size", "kda_scan_prefill", "kda_scan_workspace_size", "kda_scan_decode_step",
+           "kda_scan_backward", "kda_scan_backward_workspace_size", "kda_conv_prefill", "kda_conv_decode_step",
+           "kda_conv_backward", "kda_conv_backward_workspace_size", "kda_rmsnorm", "kda_rmsnorm_backward",
+           "kda_rmsnorm_backward_workspace_size", "kda_status_string", "kda_version")
 
 _lib = None
 
@@ -79,6 +94,25 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kda_backward.restype = ctypes.c_int
     lib.kda_backward_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.c_int]
     lib.kda_backward_workspace_size.restype = ctypes.c_size_t
+    size = ctypes.c_size_t
+    for name, restype, args in (
+            ("kda_scan_prefill", ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, ctypes.c_int, vp, vp, vp, vp, size, vp]),
+            ("kda_scan_workspace_size", size, [i32, i32, i32, ctypes.c_int]),
+            ("kda_scan_decode_step", ctypes.c_int, [vp, vp, vp, i32, i32, ctypes.c_int, vp, vp]),
+            ("kda_scan_backward", ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, ctypes.c_int, vp, vp, vp, vp, vp, vp,
+                                                 vp, size, vp]),
+            ("kda_scan_backward_workspace_size", size, [i32, i32, i32, ctypes.c_int, i32]),
+            ("kda_conv_prefill", ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, vp, vp]),
+            ("kda_conv_decode_step", ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, i32, ctypes.c_int, vp, vp]),
+            ("kda_conv_backward", ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, vp, vp,
+                                                 vp, vp, vp, vp, size, vp]),
+            ("kda_conv_backward_workspace_size", size, [i32, i32, i32, i32, ctypes.c_int]),
+            ("kda_rmsnorm", ctypes.c_int, [vp, vp, vp, i32, i32, ctypes.c_float, ctypes.c_int, vp, vp, vp, vp, vp]),
+            ("kda_rmsnorm_backward", ctypes.c_int, [vp, vp, vp, vp, i32, i32, ctypes.c_float, ctypes.c_int, vp, vp, vp,
+                                                    size, vp]),
+            ("kda_rmsnorm_backward_workspace_size", size, [i32, i32, ctypes.c_int])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = restype, args
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_version.argtypes = []
@@ -334,4 +368,296 @@ def kda_backward(q, k, v, g, beta, initial_state, cu_seqlens, dout, dfinal=None,
                             N, T, H, dk, dv, _dtype_code(q), _ptr(dout), _ptr(dfinal), _ptr(grads["dq"]),
                             _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads["dg"]), _ptr(grads["dbeta"]),
                             _ptr(grads.get("dinit")), _ptr(workspace), nbytes, _stream(stream)))
+    return grads
+
+
+# ---------------------------------------------------------------- layer operators
+# One call of these is a few microseconds of GPU time at decode sizes, so the
+# checks of a tensor are one expression each, the reasons are worked out only
+# when it fails, and pointers and the stream go to the library as plain ints.
+_MOST = 2 ** 31 - 1                                # int32 sizes in the C ABI
+_DTYPE_CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+
+
+def _bad(name, t, ref, dtype, shape) -> None:
+    _require(torch.is_tensor(t) and t.is_cuda and t.device == ref.device,
+             "%s must be a tensor on %s" % (name, ref.device))
+    _require(t.dtype == dtype, "%s must be %s, got %s" % (name, dtype, t.dtype))
+    _require(tuple(t.shape) == tuple(shape), "%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _addr(name, t, ref, dtype, shape, optional=False) -> Optional[int]:
+    """The address of a contiguous tensor of this type and shape on ref's device, after checking that it is one."""
+    if t is None and optional:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == ref.device and t.dtype == dtype and
+            t.shape == shape and t.is_contiguous()):
+        _bad(name, t, ref, dtype, shape)
+    return t.data_ptr()
+
+
+def _rows(name, x):
+    """A contiguous device tensor of rows in a supported type: its address, type code, rows, row shape and row length."""
+    _require(isinstance(x, torch.Tensor) and x.is_cuda, "%s must be a device tensor" % name)
+    code = _DTYPE_CODE.get(x.dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, x.dtype))
+    _require(x.dim() >= 2 and x.is_contiguous(), "%s must be contiguous, [rows, ...channels]" % name)
+    shape = x.shape
+    rest = shape[1:]
+    D = rest[0] if len(rest) == 1 else rest.numel()
+    _require(shape[0] <= _MOST and D <= _MOST, "%s has too many rows or channels" % name)
+    return x.data_ptr(), code, shape[0], rest, D
+
+
+def _cu(cu_seqlens, ref):
+    _require(isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda and cu_seqlens.device == ref.device,
+             "cu_seqlens must be a tensor on %s" % ref.device)
+    _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] >= 1 and
+             cu_seqlens.is_contiguous(), "cu_seqlens must be contiguous int32 [N + 1]")
+    return cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1
+
+
+def _empty(shape, dtype, ref, stream) -> torch.Tensor:
+    """A new tensor on ref's device.  Given another stream than the current one it comes from that stream's pool: what
+    the current stream still does with memory freed there is not ordered before the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                           device=ref.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+
+
+def _workspace(workspace, need, ref, stream):
+    """The given workspace, or a new one of `need` bytes: (tensor, address, bytes)."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = _empty((need,), torch.uint8, ref, stream)
+    else:
+        _require(isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.device == ref.device and
+                 workspace.is_contiguous(), "workspace must be a contiguous tensor on %s" % ref.device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _call(fn, ref, stream, *args) -> None:
+    """fn(*args, stream) with ref's device current; stream None: that device's current stream."""
+    index = ref.device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(fn, ref, stream, *args)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    status = fn(*args, raw)
+    if status != KDA_OK:
+        _check(status)
+
+
+def kda_scan_workspace_size(num_seqs: int, total_tokens: int, channels: int, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace kda_scan_prefill needs."""
+    return int(load().kda_scan_workspace_size(num_seqs, total_tokens, channels, _code(dtype)))
+
+
+def _code(dtype) -> int:
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise TypeError("dtype must be torch.bfloat16 or torch.float32, got %s" % dtype)
+    return code
+
+
+def kda_scan_prefill(x, g, initial_state, cu_seqlens, out, final_state, checkpoints=None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t over packed
+    sequences.  x, out: [T, ...channels]; g: the same shape, fp32;
+    initial_state / final_state: [N, ...channels] fp32 or None; checkpoints:
+    [ceil(T / 128), ...channels] fp32 or None, the states kda_scan_backward
+    starts from; workspace: kda_scan_workspace_size(...) bytes, allocated if
+    None."""
+    px, code, T, rest, D = _rows("x", x)
+    pcu, N = _cu(cu_seqlens, x)
+    f32 = torch.float32
+    lib = _lib or load()
+    args = (px, _addr("g", g, x, f32, x.shape), _addr("initial_state", initial_state, x, f32, (N, *rest), True), pcu,
+            N, T, D, code, _addr("out", out, x, x.dtype, x.shape),
+            _addr("final_state", final_state, x, f32, (N, *rest), True),
+            _addr("checkpoints", checkpoints, x, f32, (-(-T // KDA_SCAN_TILE), *rest), True))
+    ws, pws, nbytes = _workspace(workspace, lib.kda_scan_workspace_size(N, T, D, code), x, stream)
+    _call(lib.kda_scan_prefill, x, stream, *args, pws, nbytes)
+
+
+def kda_scan_decode_step(x, g, state_inout, out, stream=None) -> None:
+    """One token per sequence, state updated in place.  x, out: [N, ...channels];
+    g, state_inout: the same shape, fp32."""
+    px, code, N, _, D = _rows("x", x)
+    f32 = torch.float32
+    _call((_lib or load()).kda_scan_decode_step, x, stream, px, _addr("g", g, x, f32, x.shape),
+          _addr("state_inout", state_inout, x, f32, x.shape), N, D, code, _addr("out", out, x, x.dtype, x.shape))
+
+
+def kda_scan_backward_workspace_size(num_seqs: int, total_tokens: int, channels: int, dtype=torch.bfloat16,
+                                     has_checkpoints: bool = False) -> int:
+    """Bytes of workspace kda_scan_backward needs."""
+    return int(load().kda_scan_backward_workspace_size(num_seqs, total_tokens, channels, _code(dtype),
+                                                       int(has_checkpoints)))
+
+
+def _grads(given, ref, want, stream) -> dict:
+    """The gradients' tensors: those given, or new ones.  want: name -> (dtype, shape), or None (left out)."""
+    if given is None:
+        return {name: None if w is None else _empty(w[1], w[0], ref, stream) for name, w in want.items()}
+    return given
+
+
+def kda_scan_backward(x, g, initial_state, cu_seqlens, dout, dfinal=None, checkpoints=None, grads=None,
+                      want_dinit: bool = True, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of kda_scan_prefill given dout [T, ...channels] (x's type) and
+    dfinal [N, ...channels] fp32 or None.  ``checkpoints`` are those
+    kda_scan_prefill wrote for the same inputs; without them the states are
+    computed again.  Returns a dict of dx (x's type), dg (fp32) and dinit (fp32;
+    None unless want_dinit); ``grads`` may supply the tensors."""
+    px, code, T, rest, D = _rows("x", x)
+    pcu, N = _cu(cu_seqlens, x)
+    f32 = torch.float32
+    state = (N, *rest)
+    lib = _lib or load()
+    grads = _grads(grads, x, {"dx": (x.dtype, x.shape), "dg": (f32, x.shape),
+                              "dinit": (f32, state) if want_dinit else None}, stream)
+    args = (px, _addr("g", g, x, f32, x.shape), _addr("initial_state", initial_state, x, f32, state, True), pcu, N, T,
+            D, code, _addr("dout", dout, x, x.dtype, x.shape), _addr("dfinal", dfinal, x, f32, state, True),
+            _addr("checkpoints", checkpoints, x, f32, (-(-T // KDA_SCAN_TILE), *rest), True),
+            _addr("grads['dx']", grads.get("dx"), x, x.dtype, x.shape),
+            _addr("grads['dg']", grads.get("dg"), x, f32, x.shape),
+            _addr("grads['dinit']", grads.get("dinit"), x, f32, state, True))
+    ws, pws, nbytes = _workspace(
+        workspace, lib.kda_scan_backward_workspace_size(N, T, D, code, int(checkpoints is not None)), x, stream)
+    _call(lib.kda_scan_backward, x, stream, *args, pws, nbytes)
+    return grads
+
+
+def _conv_width(weight, rest) -> int:
+    _require(isinstance(weight, torch.Tensor) and weight.dim() == len(rest) + 1, "weight must be [...channels, width]")
+    return weight.shape[-1]
+
+
+def kda_conv_prefill(x, weight, bias, initial_state, cu_seqlens, out, final_state, silu: bool = True,
+                     stream=None) -> None:
+    """Short causal convolution over packed sequences, with SiLU unless silu is
+    False.  x, out: [T, ...channels]; weight: [...channels, width] fp32, width 2
+    to 4; bias: [...channels] fp32 or None; initial_state / final_state:
+    [N, width - 1, ...channels] of x's type or None."""
+    px, code, T, rest, D = _rows("x", x)
+    pcu, N = _cu(cu_seqlens, x)
+    W = _conv_width(weight, rest)
+    f32, state = torch.float32, (N, W - 1, *rest)
+    _call((_lib or load()).kda_conv_prefill, x, stream, px, _addr("weight", weight, x, f32, (*rest, W)),
+          _addr("bias", bias, x, f32, rest, True), _addr("initial_state", initial_state, x, x.dtype, state, True), pcu,
+          N, T, D, W, int(silu), code, _addr("out", out, x, x.dtype, x.shape),
+          _addr("final_state", final_state, x, x.dtype, state, True))
+
+
+def kda_conv_decode_step(x, weight, bias, state_inout, out, silu: bool = True, stream=None) -> None:
+    """One token per sequence, state shifted in place.  x, out: [N, ...channels];
+    state_inout: [N, width - 1, ...channels] of x's type."""
+    px, code, N, rest, D = _rows("x", x)
+    W = _conv_width(weight, rest)
+    f32 = torch.float32
+    _call((_lib or load()).kda_conv_decode_step, x, stream, px, _addr("weight", weight, x, f32, (*rest, W)),
+          _addr("bias", bias, x, f32, rest, True),
+          _addr("state_inout", state_inout, x, x.dtype, (N, W - 1, *rest)), N, D, W, int(silu), code,
+          _addr("out", out, x, x.dtype, x.shape))
+
+
+def kda_conv_backward_workspace_size(num_seqs: int, total_tokens: int, channels: int, width: int,
+                                     dtype=torch.bfloat16) -> int:
+    """Bytes of workspace kda_conv_backward needs."""
+    return int(load().kda_conv_backward_workspace_size(num_seqs, total_tokens, channels, width, _code(dtype)))
+
+
+def kda_conv_backward(x, weight, bias, initial_state, cu_seqlens, dout, dfinal=None, silu: bool = True, grads=None,
+                      want_dinit: bool = True, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of kda_conv_prefill given dout [T, ...channels] and dfinal
+    [N, width - 1, ...channels] (x's type) or None.  Returns a dict of dx and
+    dinit (x's type; dinit None unless want_dinit), dweight and dbias (fp32;
+    dbias None without a bias); ``grads`` may supply the tensors."""
+    px, code, T, rest, D = _rows("x", x)
+    pcu, N = _cu(cu_seqlens, x)
+    W = _conv_width(weight, rest)
+    f32, state = torch.float32, (N, W - 1, *rest)
+    lib = _lib or load()
+    grads = _grads(grads, x, {"dx": (x.dtype, x.shape), "dweight": (f32, (*rest, W)),
+                              "dbias": None if bias is None else (f32, rest),
+                              "dinit": (x.dtype, state) if want_dinit else None}, stream)
+    args = (px, _addr("weight", weight, x, f32, (*rest, W)), _addr("bias", bias, x, f32, rest, True),
+            _addr("initial_state", initial_state, x, x.dtype, state, True), pcu, N, T, D, W, int(silu), code,
+            _addr("dout", dout, x, x.dtype, x.shape), _addr("dfinal", dfinal, x, x.dtype, state, True),
+            _addr("grads['dx']", grads.get("dx"), x, x.dtype, x.shape),
+            _addr("grads['dweight']", grads.get("dweight"), x, f32, (*rest, W)),
+            _addr("grads['dbias']", grads.get("dbias"), x, f32, rest, True),
+            _addr("grads['dinit']", grads.get("dinit"), x, x.dtype, state, True))
+    ws, pws, nbytes = _workspace(workspace, lib.kda_conv_backward_workspace_size(N, T, D, W, code), x, stream)
+    _call(lib.kda_conv_backward, x, stream, *args, pws, nbytes)
+    return grads
+
+
+def _norm_rows(name, x):
+    """As _rows, for tensors whose rows are their last dimension."""
+    _require(isinstance(x, torch.Tensor) and x.is_cuda, "%s must be a device tensor" % name)
+    code = _DTYPE_CODE.get(x.dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, x.dtype))
+    _require(x.dim() >= 1 and x.is_contiguous() and x.shape[-1] > 0, "%s must be contiguous, [..., channels]" % name)
+    D = x.shape[-1]
+    rows = x.numel() // D
+    _require(rows <= _MOST and D <= _MOST, "%s has too many rows or channels" % name)
+    return x.data_ptr(), code, rows, D
+
+
+def kda_rmsnorm(x, weight, out=None, residual=None, residual_out=None, out_mx=None, scales=None, eps: float = 1e-6,
+                stream=None) -> None:
+    """r = x + residual; y = r / sqrt(mean(r^2) + eps) * weight over the last
+    dimension.  x, residual, residual_out (r), out (y): [..., channels] of one
+    type; weight: [channels] fp32 or None.  out_mx: [..., channels] uint8 or
+    float8_e4m3fn and scales: [..., ceil(channels / 32)] uint8 or
+    float8_e8m0fnu, y in 8 bits with a power-of-two scale for every 32
+    channels."""
+    px, code, rows, D = _norm_rows("x", x)
+    shape, dt = x.shape, x.dtype
+    mx = sc = None
+    if out_mx is not None or scales is not None:
+        _require(out_mx is not None and scales is not None, "out_mx and scales go together")
+        mx = _addr("out_mx", out_mx, x, torch.uint8 if out_mx.dtype == torch.uint8 else torch.float8_e4m3fn, shape)
+        sc = _addr("scales", scales, x, torch.uint8 if scales.dtype == torch.uint8 else torch.float8_e8m0fnu,
+                   (*shape[:-1], -(-D // KDA_MX_BLOCK)))
+    _call((_lib or load()).kda_rmsnorm, x, stream, px, _addr("residual", residual, x, dt, shape, True),
+          _addr("weight", weight, x, torch.float32, (D,), True), rows, D, eps, code,
+          _addr("residual_out", residual_out, x, dt, shape, True), _addr("out", out, x, dt, shape, True), mx, sc)
+
+
+def kda_rmsnorm_backward_workspace_size(rows: int, channels: int, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace kda_rmsnorm_backward needs."""
+    return int(load().kda_rmsnorm_backward_workspace_size(rows, channels, _code(dtype)))
+
+
+def kda_rmsnorm_backward(x, weight, dout, dresidual=None, eps: float = 1e-6, grads=None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of kda_rmsnorm's y given the normed rows x (its residual_out,
+    where it added one) and dout; dresidual, a gradient of x from elsewhere, is
+    added.  Returns a dict of dx (x's type) and dweight (fp32; None without a
+    weight); ``grads`` may supply the tensors."""
+    px, code, rows, D = _norm_rows("x", x)
+    shape, dt, f32 = x.shape, x.dtype, torch.float32
+    lib = _lib or load()
+    grads = _grads(grads, x, {"dx": (dt, shape), "dweight": None if weight is None else (f32, (D,))}, stream)
+    pdw = _addr("grads['dweight']", grads.get("dweight"), x, f32, (D,), True)
+    args = (px, _addr("weight", weight, x, f32, (D,), True), _addr("dout", dout, x, dt, shape),
+            _addr("dresidual", dresidual, x, dt, shape, True), rows, D, eps, code,
+            _addr("grads['dx']", grads.get("dx"), x, dt, shape), pdw)
+    ws, pws, nbytes = _workspace(
+        workspace, lib.kda_rmsnorm_backward_workspace_size(rows, D, code) if pdw is not None else 0, x, stream)
+    _call(lib.kda_rmsnorm_backward, x, stream, *args, pws, nbytes)
     return grads

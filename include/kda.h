@@ -354,6 +354,207 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
                         float *dinit, void *workspace, size_t workspace_bytes,
                         kda_stream_t stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * The operators around the recurrence in a layer: a gated linear recurrence
+ * with a state of one value per channel, the short causal convolution, and the
+ * residual's addition with a root-mean-square norm.  Conventions as above
+ * (packed sequences, cu_seqlens on the device, caller-owned buffers, no
+ * allocation, asynchronous on `stream`), with these differences:
+ *   - `channels` is any positive count (a [T, H, d] tensor is [T, channels]
+ *     with channels = H * d).  Pointers need the alignment of their element
+ *     type only; rows of 16-byte multiples at 16-byte aligned pointers are
+ *     read and written in wider pieces.
+ *   - Token arrays may be NULL when there are no tokens (total_tokens = 0).
+ *   - Gradients of activations and of convolution states are in `dtype`, those
+ *     of gates, weights, biases and fp32 states in fp32.
+ *   - No result depends on the order in which workgroups run: every sum has a
+ *     fixed order, so calls on the same inputs give the same bits.
+ */
+
+/*
+ * kda_scan_prefill -- the gated linear recurrence over packed sequences, per
+ * sequence and channel c, for tokens t in order:
+ *
+ *     h_t = exp(g_t) h_{t-1} + x_t,      out_t = h_t
+ *
+ * the recurrence of kda_prefill with the state of a channel a single value:
+ * the same log-decay gate, no keys.
+ *
+ *   x             [total_tokens, channels]        dtype
+ *   g             [total_tokens, channels]        fp32, log-decay, any value
+ *                 (-infinity: the state is dropped)
+ *   initial_state [num_seqs, channels]            fp32, or NULL for zeros
+ *   cu_seqlens    [num_seqs + 1]                  int32, DEVICE (as kda_prefill)
+ *   out           [total_tokens, channels]        dtype; rows owned by a
+ *                 sequence are written, other rows are left untouched
+ *   final_state   [num_seqs, channels]            fp32, or NULL (not written);
+ *                 may equal initial_state
+ *   checkpoints   [ceil(total_tokens / KDA_SCAN_TILE), channels] fp32, or NULL:
+ *                 row j receives the state that enters token KDA_SCAN_TILE * j
+ *                 from the token before it in its sequence (unspecified where
+ *                 that token is the first of a sequence, or of none).
+ *                 kda_scan_backward takes them in place of a second forward
+ *                 pass.
+ *   workspace     device memory of at least kda_scan_workspace_size(...) bytes,
+ *                 8-byte aligned, contents ignored on entry; NULL when that is
+ *                 0.  Calls that share one must not overlap in time.
+ * An empty sequence has final_state = initial_state (zeros if NULL).
+ */
+#define KDA_SCAN_TILE 128
+
+size_t kda_scan_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t channels, kda_dtype dtype);
+
+kda_status kda_scan_prefill(const void *x, const float *g, const float *initial_state,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                            int32_t channels, kda_dtype dtype, void *out, float *final_state,
+                            float *checkpoints, void *workspace, size_t workspace_bytes,
+                            kda_stream_t stream);
+
+/*
+ * kda_scan_decode_step -- one new token per sequence, state updated in place:
+ *   x [num_seqs, channels] dtype, g [num_seqs, channels] fp32,
+ *   state_inout [num_seqs, channels] fp32, out [num_seqs, channels] dtype
+ */
+kda_status kda_scan_decode_step(const void *x, const float *g, float *state_inout, int32_t num_seqs,
+                                int32_t channels, kda_dtype dtype, void *out, kda_stream_t stream);
+
+/*
+ * kda_scan_backward -- gradients of kda_scan_prefill: with dh_t the gradient
+ * of a loss with respect to h_t,
+ *     dh_t = dout_t + exp(g_{t+1}) dh_{t+1}   (+ dfinal at a sequence's last token)
+ *     dx_t = dh_t,   dg_t = dh_t exp(g_t) h_{t-1},   dinit = exp(g_0) dh_0
+ *
+ *   x, g, initial_state, cu_seqlens, dtype: as kda_scan_prefill
+ *   dout          [total_tokens, channels]        dtype
+ *   dfinal        [num_seqs, channels]            fp32, or NULL (zero)
+ *   checkpoints   as kda_scan_prefill wrote them for the same inputs, or NULL:
+ *                 the states are then computed here, in the workspace
+ *   dx            [total_tokens, channels]        dtype, rows of sequences written
+ *   dg            [total_tokens, channels]        fp32, rows of sequences written
+ *   dinit         [num_seqs, channels]            fp32, or NULL (not written);
+ *                 of an empty sequence: dfinal (zeros if NULL)
+ *   workspace     at least kda_scan_backward_workspace_size(...) bytes, as above
+ */
+size_t kda_scan_backward_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t channels,
+                                        kda_dtype dtype, int32_t has_checkpoints);
+
+kda_status kda_scan_backward(const void *x, const float *g, const float *initial_state,
+                             const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                             int32_t channels, kda_dtype dtype, const void *dout, const float *dfinal,
+                             const float *checkpoints, void *dx, float *dg, float *dinit,
+                             void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_conv_prefill -- short causal convolution over the tokens of packed
+ * sequences, per channel, with an optional SiLU:
+ *
+ *     pre_t = bias + sum_{j < width} weight[j] x_{t - (width - 1) + j}
+ *     out_t = pre_t / (1 + exp(-pre_t)) if silu, else pre_t
+ *
+ * where x before a sequence's first token is its initial state.  This is the
+ * convolution whose state a prefix cache restores next to the recurrent one
+ * (page ailearn.mscapital.top/kimi-k3.html, section
+ * "目标模型太大，缓存和草稿都必须理解 KDA").
+ *
+ *   x             [total_tokens, channels]           dtype
+ *   weight        [channels, width]                  fp32; width 2, 3 or 4
+ *                 (others: KDA_ERR_UNSUPPORTED)
+ *   bias          [channels]                         fp32, or NULL for zeros
+ *   initial_state [num_seqs, width - 1, channels]    dtype, or NULL for zeros:
+ *                 the inputs before the first token, oldest first
+ *   out           [total_tokens, channels]           dtype; must not overlap x
+ *   final_state   [num_seqs, width - 1, channels]    dtype, or NULL: the last
+ *                 width - 1 inputs, those of the initial state among them where
+ *                 the sequence is shorter; may equal initial_state
+ */
+kda_status kda_conv_prefill(const void *x, const float *weight, const float *bias, const void *initial_state,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                            int32_t channels, int32_t width, int32_t silu, kda_dtype dtype, void *out,
+                            void *final_state, kda_stream_t stream);
+
+/*
+ * kda_conv_decode_step -- one new token per sequence, state shifted in place:
+ *   x [num_seqs, channels], state_inout [num_seqs, width - 1, channels],
+ *   out [num_seqs, channels], all dtype; weight and bias as kda_conv_prefill.
+ *   out may equal x.
+ */
+kda_status kda_conv_decode_step(const void *x, const float *weight, const float *bias, void *state_inout,
+                                int32_t num_seqs, int32_t channels, int32_t width, int32_t silu,
+                                kda_dtype dtype, void *out, kda_stream_t stream);
+
+/*
+ * kda_conv_backward -- gradients of kda_conv_prefill (pre_t is computed anew):
+ *   x, weight, bias, initial_state, cu_seqlens, width, silu, dtype: as there
+ *   dout          [total_tokens, channels]           dtype
+ *   dfinal        [num_seqs, width - 1, channels]    dtype, or NULL (zero)
+ *   dx            [total_tokens, channels]           dtype, rows of sequences
+ *                 written; must not overlap x or dout
+ *   dweight       [channels, width]                  fp32, written
+ *   dbias         [channels]                         fp32, or NULL (not written)
+ *   dinit         [num_seqs, width - 1, channels]    dtype, or NULL (not written)
+ *   workspace     at least kda_conv_backward_workspace_size(...) bytes, 4-byte
+ *                 aligned (the partial sums of dweight and dbias)
+ */
+size_t kda_conv_backward_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t channels,
+                                        int32_t width, kda_dtype dtype);
+
+kda_status kda_conv_backward(const void *x, const float *weight, const float *bias, const void *initial_state,
+                             const int32_t *cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                             int32_t channels, int32_t width, int32_t silu, kda_dtype dtype,
+                             const void *dout, const void *dfinal, void *dx, float *dweight, float *dbias,
+                             void *dinit, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_rmsnorm -- the residual's addition and root-mean-square norm of rows:
+ *
+ *     r = x + residual (x where residual is NULL)
+ *     y = r / sqrt(mean(r^2) + eps) * weight
+ *
+ *   x, residual   [rows, channels]                dtype; residual may be NULL
+ *   weight        [channels]                      fp32, or NULL for ones
+ *   eps           finite, >= 0
+ *   residual_out  [rows, channels]                dtype, or NULL: r, rounded.
+ *                 Given only with a residual; may equal x or residual.
+ *   out           [rows, channels]                dtype, or NULL: y; may equal
+ *                 x (and residual, when that is not residual_out)
+ *   out_mx        [rows, channels]                one byte each (OCP e4m3), or
+ *                 NULL: y in blocks of KDA_MX_BLOCK channels that share a
+ *                 scale, y = value * 2^(scale - 127)
+ *   scales        [rows, ceil(channels / KDA_MX_BLOCK)]  one byte each (OCP
+ *                 e8m0), given exactly when out_mx is: the smallest power of
+ *                 two with max|y| / scale <= 448, so that no value of a block
+ *                 saturates (at least 2^-127, the smallest there is; 1 for a
+ *                 block of zeros; 255, which is NaN, for a block that holds an
+ *                 infinity or a NaN).
+ * At least one of out and out_mx is given.  y is computed from the unrounded r
+ * and rounded once, into each output by itself.  channels at most 16,384
+ * (KDA_ERR_UNSUPPORTED above).
+ */
+#define KDA_MX_BLOCK 32
+
+kda_status kda_rmsnorm(const void *x, const void *residual, const float *weight, int32_t rows,
+                       int32_t channels, float eps, kda_dtype dtype, void *residual_out, void *out,
+                       uint8_t *out_mx, uint8_t *scales, kda_stream_t stream);
+
+/*
+ * kda_rmsnorm_backward -- gradients of y = x / sqrt(mean(x^2) + eps) * weight,
+ * with x the normed rows (kda_rmsnorm's residual_out where it added one):
+ *   dout          [rows, channels]                dtype, gradient of y
+ *   dresidual     [rows, channels]                dtype, or NULL: a gradient of x
+ *                 from elsewhere (the residual stream's), added to dx
+ *   dx            [rows, channels]                dtype; may equal x, dout or dresidual
+ *   dweight       [channels]                      fp32, or NULL (not written)
+ *   workspace     at least kda_rmsnorm_backward_workspace_size(...) bytes,
+ *                 4-byte aligned; NULL allowed when dweight is NULL
+ */
+size_t kda_rmsnorm_backward_workspace_size(int32_t rows, int32_t channels, kda_dtype dtype);
+
+kda_status kda_rmsnorm_backward(const void *x, const float *weight, const void *dout, const void *dresidual,
+                                int32_t rows, int32_t channels, float eps, kda_dtype dtype, void *dx,
+                                float *dweight, void *workspace, size_t workspace_bytes,
+                                kda_stream_t stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *kda_status_string(kda_status status);
 

@@ -1,0 +1,185 @@
+"""The layer operators in a row, as a KDA layer uses them: norm with the
+residual, convolution of the q, k and v channels, the recurrence, a norm for
+each head; and the gated linear recurrence in the recurrence's place, forward,
+backward and token by token."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as R
+from gated_delta_rule_40_amd import libkda as K
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    K.load()
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+LENS = [70, 0, 1, 200, 33]
+CU = [0] + list(np.cumsum(LENS))
+
+
+def block(D=96, W=4, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=gen)   # noqa: E731
+    T, N = sum(LENS), len(LENS)
+    return dict(x=rnd(T, D), res=rnd(T, D), nw=1 + 0.1 * rnd(D), cw=0.5 * rnd(D, W), cb=0.1 * rnd(D),
+                cinit=rnd(N, W - 1, D), g=-0.3 * torch.rand(T, D, generator=gen), hinit=rnd(N, D),
+                dout=rnd(T, D), dsum=rnd(T, D), cu=torch.tensor(CU, dtype=torch.int32))
+
+
+def forward(d, chk=None):
+    e = torch.empty_like
+    total, y, u, cfin, h, hfin = e(d["x"]), e(d["x"]), e(d["x"]), e(d["cinit"]), e(d["x"]), e(d["hinit"])
+    K.kda_rmsnorm(d["x"], d["nw"], y, residual=d["res"], residual_out=total)
+    K.kda_conv_prefill(y, d["cw"], d["cb"], d["cinit"], d["cu"], u, cfin)
+    K.kda_scan_prefill(u, d["g"], d["hinit"], d["cu"], h, hfin, checkpoints=chk)
+    return total, y, u, cfin, h, hfin
+
+
+def plain_block(d):
+    """The same in torch, fp64, with a graph for autograd."""
+    r = d["x"] + d["res"]
+    y = r / torch.sqrt((r * r).mean(1, keepdim=True) + 1e-6) * d["nw"]
+    outs, W = [], d["cw"].shape[1]
+    for n in range(len(LENS)):
+        rows = torch.cat((d["cinit"][n], y[CU[n]:CU[n + 1]]))
+        h = d["hinit"][n]
+        for p in range(LENS[n]):
+            pre = (rows[p:p + W] * d["cw"].t()).sum(0) + d["cb"]
+            h = torch.exp(d["g"][CU[n] + p]) * h + pre * torch.sigmoid(pre)
+            outs.append(h)
+    return r, torch.stack(outs)
+
+
+def test_forward_and_backward_through_the_block():
+    hd = block()
+    leaves = {k: hd[k].double().requires_grad_() for k in ("x", "res", "nw", "cw", "cb", "cinit", "g", "hinit")}
+    r, h = plain_block(leaves)
+    ((h * hd["dout"].double()).sum() + (r * hd["dsum"].double()).sum()).backward()
+    d = {k: v.cuda() for k, v in hd.items()}
+    chk = torch.empty(-(-sum(LENS) // 128), 96, device="cuda")
+    total, y, u, _, out, _ = forward(d, chk)
+    gs = K.kda_scan_backward(u, d["g"], d["hinit"], d["cu"], d["dout"], checkpoints=chk)
+    gc = K.kda_conv_backward(y, d["cw"], d["cb"], d["cinit"], d["cu"], gs["dx"])
+    gn = K.kda_rmsnorm_backward(total, d["nw"], gc["dx"], dresidual=d["dsum"])
+    got = dict(x=gn["dx"], res=gn["dx"], nw=gn["dweight"], cw=gc["dweight"], cb=gc["dbias"], cinit=gc["dinit"],
+               g=gs["dg"], hinit=gs["dinit"])
+    # fp32 throughout: three operators of at most a few hundred roundings of 2^-24 each, relative to the largest value
+    near = lambda a, b: float((a.double().cpu() - b).abs().max() / b.abs().max())   # noqa: E731
+    assert near(out, h.detach()) < 1000 * 2.0 ** -24
+    for k, v in got.items():
+        assert near(v, leaves[k].grad) < 3000 * 2.0 ** -24, k
+
+
+def test_gradient_against_differences():
+    # the kernels' own forward, stepped: a central difference of the loss along a direction against the gradient
+    d = {k: v.cuda() for k, v in block(seed=1).items()}
+
+    def loss(dd):
+        return float((forward(dd)[4].double() * d["dout"].double()).sum())
+
+    _, y, u, _, _, _ = forward(d)
+    gs = K.kda_scan_backward(u, d["g"], d["hinit"], d["cu"], d["dout"])
+    gc = K.kda_conv_backward(y, d["cw"], d["cb"], d["cinit"], d["cu"], gs["dx"])
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    for name, grad in (("g", gs["dg"]), ("hinit", gs["dinit"]), ("cw", gc["dweight"]), ("cb", gc["dbias"]),
+                       ("cinit", gc["dinit"])):
+        v = torch.randn(grad.shape, device="cuda", generator=gen) * (0.05 if name == "g" else 1.0)
+        eps = 2.0 ** -7
+        diff = (loss({**d, name: d[name] + eps * v}) - loss({**d, name: d[name] - eps * v})) / (2 * eps)
+        slope = float((grad.double() * v.double()).sum())
+        # third-order term: eps^2 / 6 of a third derivative; the sum's scale stands for it (measured in fp64: < 1e-3)
+        scale = float((grad.double().abs() * v.double().abs()).sum())
+        assert abs(diff - slope) < 2e-3 * scale, (name, diff, slope, scale)
+
+
+def test_tokens_one_by_one_equal_the_prompt():
+    d = {k: v.cuda() for k, v in block(seed=2).items()}
+    N, L, D = 3, 33, 96
+    x, res, g = (d[k][:N * L].view(N, L, D) for k in ("x", "res", "g"))
+    d2 = dict(d, x=d["x"][:N * L].contiguous(), res=d["res"][:N * L].contiguous(), g=d["g"][:N * L].contiguous(),
+              cinit=d["cinit"][:N].contiguous(), hinit=d["hinit"][:N].contiguous(),
+              cu=torch.arange(N + 1, dtype=torch.int32, device="cuda") * L)
+    _, _, _, cfin, h, hfin = forward(d2)
+    conv, state = d2["cinit"].clone(), d2["hinit"].clone()
+    y, total, u, o = (torch.empty(N, D, device="cuda") for _ in range(4))
+    for p in range(L):
+        K.kda_rmsnorm(x[:, p].contiguous(), d["nw"], y, residual=res[:, p].contiguous(), residual_out=total)
+        K.kda_conv_decode_step(y, d["cw"], d["cb"], conv, u)
+        K.kda_scan_decode_step(u, g[:, p].contiguous(), state, o)
+        assert float((o - h.view(N, L, D)[:, p]).abs().max()) < 1000 * 2.0 ** -24 * float(h.abs().max())
+    assert torch.allclose(conv, cfin, rtol=0, atol=100 * 2.0 ** -24 * float(cfin.abs().max()))
+    assert torch.allclose(state, hfin, rtol=0, atol=1000 * 2.0 ** -24 * float(hfin.abs().max()))
+
+
+def test_around_the_delta_rule():
+    # q, k and v through one convolution, the KDA recurrence, a norm for each head: shapes meet without copies
+    T, H, D, N = sum(LENS), 2, 128, len(LENS)
+    gen = torch.Generator().manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=gen)   # noqa: E731
+    qkv = [(rnd(T, H, D) * 0.3).bfloat16().cuda() for _ in range(3)]
+    w = (0.4 * rnd(H, D, 4)).cuda()
+    g, beta = (-0.3 * torch.rand(T, H, D, generator=gen)).cuda(), torch.rand(T, H, generator=gen).cuda()
+    cu = torch.tensor(CU, dtype=torch.int32, device="cuda")
+    conv = [torch.empty_like(t) for t in qkv]
+    for a, b in zip(qkv, conv):
+        K.kda_conv_prefill(a, w, None, None, cu, b, None)
+    out, fin = torch.empty_like(conv[2]), torch.empty(N, H, D, D, device="cuda")
+    K.kda_prefill(*conv, g, beta, None, cu, out, fin)
+    y = torch.empty_like(out)
+    mx = torch.empty(T, H, D, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = torch.empty(T, H, 4, dtype=torch.float8_e8m0fnu, device="cuda")
+    K.kda_rmsnorm(out, None, y, out_mx=mx, scales=sc)
+    f = R.conv(host(qkv[0]).reshape(T, H * D), host(w).reshape(H * D, 4), None, None, CU, True)
+    R.close(host(conv[0]).reshape(T, H * D), f["out"], f["e_out"], "bf16", "conv of q")
+    n = R.rmsnorm(host(out).reshape(T * H, D), None, None, 1e-6)
+    R.close(host(y).reshape(T * H, D), n["y"], n["e_y"], "bf16", "norm of a head")
+    back = mx.float() * sc.float().repeat_interleave(32, 2)
+    assert float((back - y.float()).abs().max()) <= (2.0 ** -4 + 2.0 ** -8) * float(y.float().abs().max())
+
+
+CHILD = r'''
+import sys, torch
+sys.path.insert(0, %(root)r)
+from gated_delta_rule_40_amd import libkda as K
+T, D = 70, 16
+x, g, w = torch.randn(T, D, device="cuda"), -torch.rand(T, D, device="cuda"), torch.randn(D, 4, device="cuda")
+o = torch.empty_like(x)
+calls = {"kda_scan_prefill": lambda cu: K.kda_scan_prefill(x, g, None, cu, o, None),
+         "kda_scan_backward": lambda cu: K.kda_scan_backward(x, g, None, cu, x),
+         "kda_conv_prefill": lambda cu: K.kda_conv_prefill(x, w, None, None, cu, o, None),
+         "kda_conv_backward": lambda cu: K.kda_conv_backward(x, w, None, None, cu, x)}
+for name, fn in calls.items():
+    fn(torch.tensor([0, 40, 70], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    for cu in ([0, 50, 40], [0, 40, T + 1], [1, 40, 70]):
+        try:
+            fn(torch.tensor(cu, dtype=torch.int32, device="cuda"))
+            print("%%s %%s: accepted" %% (name, cu))
+        except K.KdaError as e:
+            print("%%s %%s: %%d" %% (name, cu, e.status))
+'''
+
+
+def test_validate_rejects_bad_cu_seqlens():
+    # in a child: KDA_VALIDATE is read at the first call.  Rejected on the host: no kernel sees them.
+    res = subprocess.run([sys.executable, "-c", CHILD % {"root": ROOT}], env=dict(os.environ, KDA_VALIDATE="1"),
+                         capture_output=True, text=True, timeout=300)
+    print(res.stdout, res.stderr[-2000:], flush=True)
+    lines = [line for line in res.stdout.splitlines() if ": " in line]
+    assert res.returncode == 0 and len(lines) == 12 and all(line.endswith(": 1") for line in lines)

@@ -1,0 +1,138 @@
+"""Refusals of the layer operators that need no GPU: the C entry points return
+the documented status before any HIP call, and the binding raises for host
+tensors."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from gated_delta_rule_40_amd import libkda as K
+
+P = ctypes.c_void_p(0x10000)       # aligned, never dereferenced
+ODD = ctypes.c_void_p(0x10001)
+WS = ctypes.c_void_p(0x100000)
+B, F = K.KDA_BF16, K.KDA_F32
+INVALID, UNSUPPORTED = K.KDA_ERR_INVALID_ARG, K.KDA_ERR_UNSUPPORTED
+
+CALLS = {
+    "kda_scan_prefill": dict(x=P, g=P, init=None, cu=P, N=1, T=300, D=8, dt=B, out=P, fin=None, chk=None, ws=WS,
+                             wsb=1 << 40, stream=None),
+    "kda_scan_decode_step": dict(x=P, g=P, state=P, N=1, D=8, dt=B, out=P, stream=None),
+    "kda_scan_backward": dict(x=P, g=P, init=None, cu=P, N=1, T=300, D=8, dt=B, dout=P, dfin=None, chk=None, dx=P,
+                              dg=P, dinit=None, ws=WS, wsb=1 << 40, stream=None),
+    "kda_conv_prefill": dict(x=P, w=P, b=None, init=None, cu=P, N=1, T=300, D=8, W=4, silu=1, dt=B, out=P, fin=None,
+                             stream=None),
+    "kda_conv_decode_step": dict(x=P, w=P, b=None, state=P, N=1, D=8, W=4, silu=1, dt=B, out=P, stream=None),
+    "kda_conv_backward": dict(x=P, w=P, b=None, init=None, cu=P, N=1, T=300, D=8, W=4, silu=1, dt=B, dout=P,
+                              dfin=None, dx=P, dw=P, db=None, dinit=None, ws=WS, wsb=1 << 40, stream=None),
+    "kda_rmsnorm": dict(x=P, res=None, w=P, rows=4, D=64, eps=1e-6, dt=B, sum=None, out=P, mx=None, sc=None,
+                        stream=None),
+    "kda_rmsnorm_backward": dict(x=P, w=P, dout=P, dres=None, rows=4, D=64, eps=1e-6, dt=B, dx=P, dw=P, ws=WS,
+                                 wsb=1 << 40, stream=None),
+}
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(K.LIB_PATH):
+        from gated_delta_rule_40_amd import build
+        build.build()
+    return K.load()
+
+
+def call(lib, name, **kw):
+    a = dict(CALLS[name])
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return getattr(lib, name)(*a.values())
+
+
+BAD = [(name, {field: None}) for name, fields in (
+    ("kda_scan_prefill", "x g cu out"), ("kda_scan_decode_step", "x g state out"),
+    ("kda_scan_backward", "x g cu dout dx dg"), ("kda_conv_prefill", "x w cu out"),
+    ("kda_conv_decode_step", "x w state out"), ("kda_conv_backward", "x w cu dout dx dw"), ("kda_rmsnorm", "x out"),
+    ("kda_rmsnorm_backward", "x dout dx")) for field in fields.split()]
+BAD += [(name, {field: ODD}) for name, a in CALLS.items() for field, v in a.items()
+        if v is P or v is None and field in ("init", "fin", "dfin", "chk", "dinit", "b", "db", "res", "dres", "sum")
+        if not (name == "kda_rmsnorm" and field == "sum")]
+BAD += [(name, {"dt": 7}) for name in CALLS]
+BAD += [(name, {"D": d}) for name in CALLS for d in (0, -3)]
+BAD += [(name, {"N": -1}) for name, a in CALLS.items() if "N" in a]
+BAD += [(name, {"T": -1}) for name, a in CALLS.items() if "T" in a]
+BAD += [(name, {"rows": -1}) for name, a in CALLS.items() if "rows" in a]
+BAD += [(name, {"W": w}) for name, a in CALLS.items() if "W" in a for w in (0, -2)]
+BAD += [(name, {"eps": e}) for name, a in CALLS.items() if "eps" in a for e in (-1e-6, float("nan"), float("inf"))]
+BAD += [("kda_rmsnorm", {"sum": P}),                    # a sum without a residual
+        ("kda_rmsnorm", {"mx": P}), ("kda_rmsnorm", {"sc": P}), ("kda_rmsnorm", {"res": P, "sum": ODD})]
+
+
+@pytest.mark.parametrize("name,kw", BAD, ids=["%s-%s" % (n, "-".join("%s=%s" % (k, getattr(v, "value", v))
+                                                                     for k, v in kw.items())) for n, kw in BAD])
+def test_rejects(lib, name, kw):
+    assert call(lib, name, **kw) == INVALID
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("kda_conv_prefill", dict(W=5)), ("kda_conv_prefill", dict(W=1)), ("kda_conv_decode_step", dict(W=5)),
+    ("kda_conv_backward", dict(W=1)), ("kda_conv_backward", dict(W=8)), ("kda_rmsnorm", dict(D=16385)),
+    ("kda_rmsnorm_backward", dict(D=16385)),
+])
+def test_does_not_support(lib, name, kw):
+    assert call(lib, name, **kw) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("kda_scan_prefill", dict(N=0, T=0, x=None, g=None, out=None, ws=None, wsb=0)), ("kda_scan_prefill", dict(N=0)),
+    ("kda_scan_decode_step", dict(N=0, x=None, g=None, state=None, out=None)),
+    ("kda_scan_backward", dict(N=0, T=0, x=None, g=None, dout=None, dx=None, dg=None, ws=None, wsb=0)),
+    ("kda_conv_prefill", dict(N=0, T=0, x=None, out=None)), ("kda_conv_prefill", dict(N=0)),
+    ("kda_conv_decode_step", dict(N=0, x=None, state=None, out=None)),
+    ("kda_rmsnorm", dict(rows=0, x=None, out=None)),
+    ("kda_rmsnorm_backward", dict(rows=0, x=None, dout=None, dx=None, dw=None, ws=None, wsb=0)),
+])
+def test_nothing_to_do_is_a_no_op(lib, name, kw):
+    assert call(lib, name, **kw) == K.KDA_OK
+
+
+def _sizes(lib):
+    return {"kda_scan_backward": lib.kda_scan_backward_workspace_size(1, 300, 8, B, 0),
+            "kda_scan_prefill": lib.kda_scan_workspace_size(1, 300, 8, B),
+            "kda_conv_backward": lib.kda_conv_backward_workspace_size(1, 300, 8, 4, B),
+            "kda_rmsnorm_backward": lib.kda_rmsnorm_backward_workspace_size(4, 64, B)}
+
+
+@pytest.mark.parametrize("name", ["kda_scan_prefill", "kda_scan_backward", "kda_conv_backward", "kda_rmsnorm_backward"])
+def test_workspace_is_checked(lib, name):
+    need = _sizes(lib)[name]
+    if need == 0:
+        pytest.skip("needs no workspace at this size")
+    assert call(lib, name, ws=None) == INVALID
+    assert call(lib, name, ws=ODD) == INVALID
+    assert call(lib, name, wsb=need - 1) == INVALID
+
+
+def test_workspace_sizes_of_bad_sizes_are_zero(lib):
+    assert lib.kda_scan_workspace_size(-1, 300, 8, B) == lib.kda_scan_workspace_size(1, 300, 0, B) == 0
+    assert lib.kda_scan_backward_workspace_size(1, -1, 8, B, 0) == lib.kda_scan_backward_workspace_size(1, 300, 8, 9, 0) == 0
+    assert lib.kda_conv_backward_workspace_size(1, 300, 8, 5, B) == lib.kda_conv_backward_workspace_size(1, 300, -8, 4, B) == 0
+    assert lib.kda_rmsnorm_backward_workspace_size(-4, 64, B) == lib.kda_rmsnorm_backward_workspace_size(4, 20000, B) == 0
+
+
+def test_binding_rejects_host_tensors():
+    x, g, cu = torch.zeros(4, 8), torch.zeros(4, 8), torch.tensor([0, 4], dtype=torch.int32)
+    w = torch.zeros(8, 4)
+    for fn, args in ((K.kda_scan_prefill, (x, g, None, cu, x, None)), (K.kda_scan_decode_step, (x, g, g, x)),
+                     (K.kda_scan_backward, (x, g, None, cu, x)), (K.kda_conv_prefill, (x, w, None, None, cu, x, None)),
+                     (K.kda_conv_decode_step, (x, w, None, torch.zeros(4, 3, 8), x)),
+                     (K.kda_conv_backward, (x, w, None, None, cu, x)), (K.kda_rmsnorm, (x, None, x)),
+                     (K.kda_rmsnorm_backward, (x, None, x))):
+        with pytest.raises(ValueError, match="device tensor"):
+            fn(*args)
+
+
+def test_binding_workspace_sizes_reject_unknown_types():
+    for fn, args in ((K.kda_scan_workspace_size, (1, 16, 8)), (K.kda_scan_backward_workspace_size, (1, 16, 8)),
+                     (K.kda_conv_backward_workspace_size, (1, 16, 8, 4)), (K.kda_rmsnorm_backward_workspace_size, (4, 8))):
+        with pytest.raises(TypeError):
+            fn(*args, torch.float16)
