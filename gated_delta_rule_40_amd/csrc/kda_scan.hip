@@ -1,93 +1,619 @@
 // kda_scan.hip -- the gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t per
 // channel over packed sequences, its decode step and its gradients.
 //
-// One thread per (sequence, channel) walks its tokens.
+// With a_t = exp(g_t), a run of tokens maps the state that enters it to the
+// state that leaves it by h -> A h + B, A the product of its a_t and B its end
+// state from zero, and two runs in a row map by (A2 A1, A2 B1 + B2).  The packed
+// tokens are cut into tiles of 128, whatever the sequences; a sequence's start
+// drops what entered (A = RESET) and takes the initial state into B.  One
+// workgroup of eight waves reads a tile of 128 tokens x 64 V channels once, 16
+// tokens a wave, keeps it in registers, publishes its (A, B), obtains the state
+// that enters it from the tiles before it, and writes its outputs: every input
+// is read once and every output written once, which is all the traffic there
+// has to be (8 bytes an element with bf16 x), and HBM's rate is the bound.
+//
+// The state that enters a tile is joined from three levels of published runs:
+// the tiles of its group of 8 before it, the groups of its super-group of 8
+// before its own, and the state that enters the super-group, which is passed
+// from super-group to super-group (8,192 tokens a hop).  Which runs are joined,
+// and in which order, depends on the tile alone, not on what is ready first, so
+// that results are the same bits on every call.  A published run is one
+// 64-bit word a channel, written and polled with relaxed device-scope atomics:
+// the word is its own flag (all ones: not there yet), so no fence is needed
+// between data and flag.  Tiles of a channel block are handed out in order by a
+// counter, so a tile waits only for workgroups that are already running, and
+// these wait for earlier ones in turn: every wait ends.
+//
+// The gradients run the same scheme from the end to the start,
+//     dh_t = dout_t + e,  e <- a_t dh_t,
+// with the state entering each tile taken from the forward pass's checkpoints.
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
 #include "kda_seq.hpp"
 
 namespace kda {
 
-constexpr int TILE = 128;   // tokens between checkpoints
+constexpr int TILE = 128;             // tokens of a tile, and between checkpoints
+constexpr int WAVES = 8;              // waves of a workgroup
+constexpr int L = TILE / WAVES;       // tokens of a wave
+constexpr int NTH = WAVES * 64;
+constexpr int GROUP = 8;              // tiles of a group
+constexpr int SUPER = GROUP * GROUP;  // tiles of a super-group
+constexpr float RESET = -1.f;         // an A that drops what enters (products of exp() are never negative)
+constexpr uint64_t NOT_YET = ~(uint64_t)0;
 
-// out: h; chk: the state entering every TILE-th token; carried: exp(g_t) h_{t-1}
-template <typename T>
-__global__ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int64_t D, T *out, float *fin,
-                                float *chk, float *carried)
+// ---------------------------------------------------------------- published runs
+struct Chain {
+    uint32_t *ticket;                 // [column of channels], from ~0
+    uint64_t *tile, *group, *super;   // [index][D]
+    int32_t ntiles;
+    int64_t D;
+};
+
+struct Run {
+    float A, B;
+};
+
+// first, then second
+__device__ __forceinline__ Run join(const Run &first, const Run &second)
 {
-    const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (id >= sq.N * D) return;
-    const int32_t n = (int32_t)(id / D);
-    const int64_t c = id % D;
-    const int32_t t0 = sq.at(n), t1 = sq.at(n + 1);
-    float h = init ? init[id] : 0.f;
-    for (int32_t t = t0; t < t1; ++t) {
-        const int64_t i = t * D + c;
-        if (chk && t % TILE == 0) chk[(int64_t)(t / TILE) * D + c] = h;
-        const float p = expf(g[i]) * h;
-        if (carried) carried[i] = p;
-        h = p + to_f(x[i]);
-        if (out) out[i] = from_f<T>(h);
-    }
-    if (fin) fin[id] = h;
+    if (second.A == RESET) return second;
+    return {first.A == RESET ? RESET : first.A * second.A, second.A * first.B + second.B};
+}
+__device__ __forceinline__ float apply(const Run &r, float h) { return r.A == RESET ? r.B : r.A * h + r.B; }
+
+__device__ __forceinline__ uint64_t pack(const Run &r)
+{
+    const uint64_t w = (uint64_t)__float_as_uint(r.A) | ((uint64_t)__float_as_uint(r.B) << 32);
+    return w == NOT_YET ? 0x7fc000007fc00000ull : w;   // two NaNs stay two NaNs
+}
+__device__ __forceinline__ Run unpack(uint64_t w)
+{
+    return {__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t *p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish(uint64_t *p, const Run &r)
+{
+    __hip_atomic_store(p, pack(r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// the m < GROUP runs p[0], p[D], ... joined in order; all are asked for before any is waited for
+__device__ __forceinline__ Run gather(const uint64_t *p, int64_t D, int m)
+{
+    uint64_t w[GROUP - 1];
+#pragma unroll
+    for (int i = 0; i < GROUP - 1; ++i) w[i] = i < m ? peek(p + i * D) : 0;
+    Run r = {1.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < GROUP - 1; ++i) {
+        if (i < m) {
+            while (w[i] == NOT_YET) {
+                __builtin_amdgcn_s_sleep(1);
+                w[i] = peek(p + i * D);
+            }
+            r = i == 0 ? unpack(w[i]) : join(r, unpack(w[i]));
+        }
+    }
+    return r;
+}
+
+// The value that enters tile k (counted in the direction of the walk) for
+// every channel of the workgroup, in `enter`; publishes the tile's own run.
+// `runs` holds the waves' runs in the order of the walk.  `fresh`: nothing
+// enters (the tile begins at a boundary); `resets`: it has a boundary.  The
+// first 64 V threads join the tiles, the next the groups.  Ends with a barrier.
+template <int CB>
+__device__ __forceinline__ void pass_on(const Chain &ch, int k, int64_t c0, bool fresh, bool resets,
+                                        const Run (*runs)[CB], Run *groups, float *enter)
+{
+    const int tid = threadIdx.x, c = tid % CB, role = tid / CB;
+    const bool in = c0 + c < ch.D;
+    const int in_group = k % GROUP, group = k / GROUP, in_super = group % GROUP, super = k / SUPER;
+    const bool last_in_group = in_group == GROUP - 1, last_in_super = k % SUPER == SUPER - 1;
+    const int64_t ci = c0 + c;
+    Run own = {1.f, 0.f}, before = {1.f, 0.f};
+    if (role == 0 && in) {
+        own = runs[0][c];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) own = join(own, runs[w][c]);
+        if (!last_in_group) publish(ch.tile + k * ch.D + ci, own);
+        if (resets) {   // what leaves does not depend on what enters
+            if (last_in_group && !last_in_super) publish(ch.group + group * ch.D + ci, own);
+            if (last_in_super) publish(ch.super + (super + 1) * ch.D + ci, own);
+        }
+        if (!fresh) before = gather(ch.tile + (k - in_group) * ch.D + ci, ch.D, in_group);
+        if (!resets && last_in_group && !last_in_super)
+            publish(ch.group + group * ch.D + ci, in_group ? join(before, own) : own);
+    }
+    if (role == 1 && in && !fresh) {
+        Run r = gather(ch.group + (group - in_super) * ch.D + ci, ch.D, in_super);
+        if (super > 0) {
+            uint64_t w;
+            while ((w = peek(ch.super + super * ch.D + ci)) == NOT_YET) __builtin_amdgcn_s_sleep(1);
+            r = in_super ? Run{RESET, apply(r, unpack(w).B)} : Run{RESET, unpack(w).B};
+        }
+        groups[c] = r;
+    }
+    __syncthreads();
+    if (role == 0 && in && !fresh) {
+        const Run g = groups[c];
+        // nothing enters the first tile of all: its value stands for that of no sequence
+        const float h = (super > 0 || in_super > 0) ? (in_group ? apply(before, g.B) : g.B) : before.B;
+        enter[c] = h;
+        if (!resets && last_in_super) publish(ch.super + (super + 1) * ch.D + ci, {RESET, apply(own, h)});
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- tokens in registers
+template <typename T, int V> struct Vec;
+template <> struct Vec<float, 4> { typedef f32x4 raw; };
+template <> struct Vec<float, 2> { typedef f32x2 raw; };
+template <> struct Vec<float, 1> { typedef float raw; };
+template <> struct Vec<bf16_t, 4> { typedef bf16x4 raw; };
+template <> struct Vec<bf16_t, 2> { typedef bf16x2 raw; };
+template <> struct Vec<bf16_t, 1> { typedef bf16_t raw; };
+
+template <typename R> __device__ __forceinline__ float elem(const R &r, int j) { return to_f(r[j]); }
+template <> __device__ __forceinline__ float elem<float>(const float &r, int) { return r; }
+template <> __device__ __forceinline__ float elem<bf16_t>(const bf16_t &r, int) { return to_f(r); }
+template <typename R, typename T> __device__ __forceinline__ void put(R &r, int j, T v) { r[j] = v; }
+template <> __device__ __forceinline__ void put<float, float>(float &r, int, float v) { r = v; }
+template <> __device__ __forceinline__ void put<bf16_t, bf16_t>(bf16_t &r, int, bf16_t v) { r = v; }
+
+// exp(g) within about one unit in the last place: the product with log2(e) is
+// carried in two parts, since its rounding alone would be |g| units, and slow
+// gates let errors of one sign add up over a thousand tokens.
+__device__ __forceinline__ float gate(float g)
+{
+    const float L2E = 1.44269502f, L2E_LO = 1.92596299e-8f, LN2 = 0.693147182f;
+    const float t = g * L2E;
+    const float lo = __builtin_fmaf(g, L2E_LO, __builtin_fmaf(g, L2E, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    // (for an infinite g the parts are NaN, and e is right by itself)
+    return lo == lo ? __builtin_fmaf(e, lo * LN2, e) : e;
+}
+
+// Boundaries of sequences at a wave's tokens: bit i stands for token t0 + i,
+// i = 0 .. L.  `end` is the first token of no sequence.
+struct Edges {
+    uint32_t mask;
+    int32_t end;
+};
+
+__device__ __forceinline__ Edges edges(const Seqs &sq, int32_t t0, int32_t *first)
+{
+    Edges e = {0, sq.at(sq.N)};
+    int32_t n = sq.first_at_or_after(t0);
+    *first = n;
+    for (; n <= sq.N; ++n) {
+        const int32_t p = sq.at(n);
+        if (p > t0 + L || p < t0) break;
+        e.mask |= 1u << (p - t0);
+    }
+    return e;
+}
+
+// `copy(n)` for the empty sequences that lie at tokens [t0, t0 + L), or at any later place for the last wave of all
+template <typename F>
+__device__ __forceinline__ void empty_seqs(const Seqs &sq, int32_t t0, int32_t first, bool last, F copy)
+{
+    for (int32_t n = first; n < sq.N; ++n) {
+        const int32_t p = sq.at(n);
+        if (p >= t0 + L && !last) break;
+        if (sq.at(n + 1) <= p) copy(n);
+    }
+}
+
+// ---------------------------------------------------------------- forward
+template <typename T, int V>
+__global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(4)))   // two workgroups per CU
+void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int64_t D, int32_t cols, T *out,
+                     float *fin, float *chk, Chain ch)
+{
+    constexpr int CB = 64 * V;
+    typedef typename Vec<T, V>::raw XR;
+    typedef typename Vec<float, V>::raw GR;
+    __shared__ Run runs[WAVES][CB];
+    __shared__ Run groups[CB];
+    __shared__ float enter[CB];
+    __shared__ uint32_t s_tile;
+
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = blockIdx.x % cols;
+    int k = 0;
+    if (ch.ntiles > 1) {
+        if (threadIdx.x == 0) s_tile = atomicAdd(ch.ticket + col, 1u) + 1u;
+        __syncthreads();
+        k = __builtin_amdgcn_readfirstlane((int)s_tile);
+    }
+    const int64_t c0 = (int64_t)col * CB, c = c0 + lane * V;
+    const bool in = c < D;
+    const int32_t tile0 = k * TILE, t0 = tile0 + w * L;
+
+    XR xr[L];
+    float a[L][V];
+    GR gr[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if (in && t0 + i < sq.T) {
+            const int64_t at = (int64_t)(t0 + i) * D + c;
+            xr[i] = *reinterpret_cast<const XR *>(x + at);
+            gr[i] = *reinterpret_cast<const GR *>(g + at);
+        } else {
+            xr[i] = XR{};
+            gr[i] = GR{};
+        }
+    }
+    int32_t first;
+    const Edges e = edges(sq, t0, &first);
+    const uint32_t starts = e.mask & ((1u << L) - 1);
+    if (fin)
+        empty_seqs(sq, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {
+            if (in)
+                for (int j = 0; j < V; ++j) fin[n * D + c + j] = init ? init[n * D + c + j] : 0.f;
+        });
+    // what a token leaves: its output, and the final state of a sequence that ends with it
+    auto leave = [&](int i, const float (&h)[V]) {
+        if (!in || t0 + i >= e.end) return;
+        if (out) {
+            XR o;
+            for (int j = 0; j < V; ++j) put(o, j, from_f<T>(h[j]));
+            *reinterpret_cast<XR *>(out + (int64_t)(t0 + i) * D + c) = o;
+        }
+        if (fin && (e.mask >> (i + 1) & 1)) {
+            const int64_t n = sq.owner(t0 + i);
+            if (n >= 0)
+                for (int j = 0; j < V; ++j) fin[n * D + c + j] = h[j];
+        }
+    };
+
+    // the wave's run; after its first start the states are known, and leave at once
+    {
+        float A[V], B[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) A[j] = 1.f, B[j] = 0.f;
+        bool known = false;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (starts >> i & 1) {
+                known = true;
+                const int64_t n = init ? sq.owner(t0 + i) : -1;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    A[j] = RESET;
+                    B[j] = (n >= 0 && in) ? init[n * D + c + j] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                a[i][j] = gate(elem(gr[i], j));
+                if (!known) A[j] *= a[i][j];
+                B[j] = a[i][j] * B[j] + elem(xr[i], j);
+            }
+            if (known) leave(i, B);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) runs[w][lane * V + j] = {A[j], B[j]};
+    }
+    const bool fresh = __syncthreads_or(w == 0 && (starts & 1)) || k == 0;
+    const bool resets = __syncthreads_or(starts != 0);
+    if (ch.ntiles > 1) {
+        pass_on<CB>(ch, k, c0, fresh, resets, runs, groups, enter);
+        if (chk && w == 0 && in && !fresh)
+            for (int j = 0; j < V; ++j) chk[k * D + c + j] = enter[lane * V + j];
+    }
+    // the tokens before the wave's first start
+    if (starts & 1) return;
+    float h[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        h[j] = fresh ? 0.f : enter[lane * V + j];
+        for (int v = 0; v < w; ++v) h[j] = apply(runs[v][lane * V + j], h[j]);
+    }
+    if (e.mask == 0 && t0 + L <= e.end) {
+        if (!out) return;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            XR o;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                h[j] = a[i][j] * h[j] + elem(xr[i], j);
+                put(o, j, from_f<T>(h[j]));
+            }
+            if (in) *reinterpret_cast<XR *>(out + (int64_t)(t0 + i) * D + c) = o;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (starts & ((2u << i) - 1)) break;
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[j] = a[i][j] * h[j] + elem(xr[i], j);
+            leave(i, h);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradients
+template <typename T, int V>
+__global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(4)))   // two workgroups per CU
+void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq, int64_t D, int32_t cols,
+                         const T *dout, const float *dfin, const float *chk, T *dx, float *dg, float *dinit, Chain ch)
+{
+    constexpr int CB = 64 * V;
+    typedef typename Vec<T, V>::raw XR;
+    typedef typename Vec<float, V>::raw GR;
+    __shared__ Run fwd[WAVES][CB];      // forward runs of the waves, first to last
+    __shared__ Run back[WAVES][CB];     // backward runs of the waves, last to first
+    __shared__ Run groups[CB];
+    __shared__ float enter[CB];
+    __shared__ uint32_t s_tile;
+
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = blockIdx.x % cols;
+    int kb = 0;                         // the tile's number from the end
+    if (ch.ntiles > 1) {
+        if (threadIdx.x == 0) s_tile = atomicAdd(ch.ticket + col, 1u) + 1u;
+        __syncthreads();
+        kb = __builtin_amdgcn_readfirstlane((int)s_tile);
+    }
+    const int k = ch.ntiles - 1 - kb;
+    const int64_t c0 = (int64_t)col * CB, c = c0 + lane * V;
+    const bool in = c < D;
+    const int32_t tile0 = k * TILE, t0 = tile0 + w * L;
+
+    XR xr[L], dr[L];
+    GR gr[L];
+    float a[L][V];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if (in && t0 + i < sq.T) {
+            const int64_t at = (int64_t)(t0 + i) * D + c;
+            gr[i] = *reinterpret_cast<const GR *>(g + at);
+            xr[i] = *reinterpret_cast<const XR *>(x + at);
+            dr[i] = *reinterpret_cast<const XR *>(dout + at);
+        } else {
+            gr[i] = GR{};
+            xr[i] = XR{};
+            dr[i] = XR{};
+        }
+    }
+    float h[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) h[j] = (in && k > 0) ? chk[k * D + c + j] : 0.f;
+    int32_t first;
+    const Edges e = edges(sq, t0, &first);
+    const uint32_t starts = e.mask & ((1u << L) - 1);
+    if (dinit)
+        empty_seqs(sq, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {
+            if (in)
+                for (int j = 0; j < V; ++j) dinit[n * D + c + j] = dfin ? dfin[n * D + c + j] : 0.f;
+        });
+    {
+        float A[V], B[V], E[V], Ae[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) A[j] = 1.f, B[j] = 0.f, E[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (starts >> i & 1) {
+                const int64_t n = init ? sq.owner(t0 + i) : -1;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    A[j] = RESET;
+                    B[j] = (n >= 0 && in) ? init[n * D + c + j] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                a[i][j] = gate(elem(gr[i], j));
+                if (!(starts & ((2u << i) - 1))) A[j] *= a[i][j];
+                B[j] = a[i][j] * B[j] + elem(xr[i], j);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            fwd[w][lane * V + j] = {A[j], B[j]};
+            Ae[j] = 1.f;
+        }
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i) {
+            if (e.mask >> (i + 1) & 1) {   // the gradient of the final state enters here
+                const int64_t n = dfin ? sq.owner(t0 + i) : -1;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    Ae[j] = RESET;
+                    E[j] = (n >= 0 && in) ? dfin[n * D + c + j] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (!(e.mask >> (i + 1))) Ae[j] *= a[i][j];
+                E[j] = a[i][j] * (elem(dr[i], j) + E[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) back[WAVES - 1 - w][lane * V + j] = {Ae[j], E[j]};
+    }
+    const uint32_t ends = e.mask >> 1;
+    const bool fresh = __syncthreads_or(w == WAVES - 1 && (ends >> (L - 1) & 1)) || kb == 0;
+    const bool resets = __syncthreads_or(ends != 0);
+    if (ch.ntiles > 1) pass_on<CB>(ch, kb, c0, fresh, resets, back, groups, enter);
+
+    // the states again, forward: p_t = a_t h_{t-1}
+    float p[L][V], E[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        for (int v = 0; v < w; ++v) h[j] = apply(fwd[v][lane * V + j], h[j]);
+        E[j] = fresh ? 0.f : enter[lane * V + j];
+        for (int v = 0; v < WAVES - 1 - w; ++v) E[j] = apply(back[v][lane * V + j], E[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if (starts >> i & 1) {
+            const int64_t n = init ? sq.owner(t0 + i) : -1;
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[j] = (n >= 0 && in) ? init[n * D + c + j] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            p[i][j] = a[i][j] * h[j];
+            h[j] = p[i][j] + elem(xr[i], j);
+        }
+    }
+#pragma unroll
+    for (int i = L - 1; i >= 0; --i) {
+        if (ends >> i & 1) {
+            const int64_t n = dfin ? sq.owner(t0 + i) : -1;
+#pragma unroll
+            for (int j = 0; j < V; ++j) E[j] = (n >= 0 && in) ? dfin[n * D + c + j] : 0.f;
+        }
+        XR ox;
+        GR og;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float dh = elem(dr[i], j) + E[j];
+            put(ox, j, from_f<T>(dh));
+            put(og, j, dh * p[i][j]);
+            E[j] = a[i][j] * dh;
+        }
+        if (in && t0 + i < e.end) {
+            const int64_t at = (int64_t)(t0 + i) * D + c;
+            *reinterpret_cast<XR *>(dx + at) = ox;
+            *reinterpret_cast<GR *>(dg + at) = og;
+            if (dinit && (starts >> i & 1)) {
+                const int64_t n = sq.owner(t0 + i);
+                if (n >= 0)
+                    for (int j = 0; j < V; ++j) dinit[n * D + c + j] = E[j];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- decode
 template <typename T>
 __global__ void kda_scan_step_kernel(const T *x, const float *g, float *state, int64_t n, T *out)
 {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        const float h = expf(g[i]) * state[i] + to_f(x[i]);
+        const float h = gate(g[i]) * state[i] + to_f(x[i]);
         state[i] = h;
         out[i] = from_f<T>(h);
     }
 }
 
-template <typename T>
-__global__ void kda_scan_bwd_kernel(const float *g, Seqs sq, int64_t D, const T *dout, const float *dfinal,
-                                    const float *carried, T *dx, float *dg, float *dinit)
+// marks every published word and counter as not there yet (a kernel: a memset
+// node of a captured graph is not relied on)
+__global__ void kda_scan_fill_kernel(uint64_t *p, int64_t n)
 {
-    const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (id >= sq.N * D) return;
-    const int32_t n = (int32_t)(id / D);
-    const int64_t c = id % D;
-    const int32_t t0 = sq.at(n), t1 = sq.at(n + 1);
-    float e = dfinal ? dfinal[id] : 0.f;   // gradient of the state that leaves the token
-    for (int32_t t = t1 - 1; t >= t0; --t) {
-        const int64_t i = t * D + c;
-        const float dh = to_f(dout[i]) + e;
-        dx[i] = from_f<T>(dh);
-        dg[i] = dh * carried[i];
-        e = expf(g[i]) * dh;
-    }
-    if (dinit) dinit[id] = e;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+        p[i] = NOT_YET;
 }
 
-inline unsigned blocks_of(int64_t n, int per) { return (unsigned)((n + per - 1) / per); }
+// ---------------------------------------------------------------- host
+inline int32_t tiles_of(int32_t T) { return T > 0 ? (int32_t)(((int64_t)T + TILE - 1) / TILE) : 1; }
+
+// Words of a chain: counters of up to ceil(D / 64) columns, then the tiles',
+// groups' and super-groups' runs.  A single tile needs none.
+struct ChainLayout {
+    size_t tile, group, super, words;
+};
+inline ChainLayout chain_layout(int32_t T, int32_t D)
+{
+    const size_t nt = tiles_of(T), d = D;
+    ChainLayout l = {};
+    if (nt <= 1) return l;
+    l.tile = ((d + 63) / 64 + 1) / 2;
+    l.group = l.tile + nt * d;
+    l.super = l.group + (nt / GROUP + 1) * d;
+    l.words = l.super + (nt / SUPER + 1) * d;
+    return l;
+}
+inline Chain chain_at(uint64_t *p, int32_t T, int32_t D)
+{
+    const ChainLayout l = chain_layout(T, D);
+    return {reinterpret_cast<uint32_t *>(p), p + l.tile, p + l.group, p + l.super, tiles_of(T), (int64_t)D};
+}
+
+inline hipError_t fill_chain(uint64_t *p, size_t words, hipStream_t s)
+{
+    if (words == 0) return hipSuccess;
+    const size_t blocks = (words + 255) / 256;
+    hipLaunchKernelGGL(kda_scan_fill_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, p,
+                       (int64_t)words);
+    return hipGetLastError();
+}
+
+inline bool fits(const void *p, size_t bytes) { return !p || reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+template <typename T, int V>
+hipError_t run_scan(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D, void *out, float *fin,
+                    float *chk, const Chain &ch, hipStream_t s)
+{
+    const int32_t cols = (int32_t)(((int64_t)D + 64 * V - 1) / (64 * V));
+    hipLaunchKernelGGL((kda_scan_kernel<T, V>), dim3((unsigned)((int64_t)cols * ch.ntiles)), dim3(NTH), 0, s,
+                       (const T *)x, g, init, sq, (int64_t)D, cols, (T *)out, fin, chk, ch);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t scan(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D, void *out, float *fin,
+                float *chk, const Chain &ch, hipStream_t s)
+{
+    const size_t e = sizeof(T);
+    constexpr int V = 2;
+    if (D % V == 0 && fits(x, V * e) && fits(out, V * e) && fits(g, V * 4))
+        return run_scan<T, V>(x, g, init, sq, D, out, fin, chk, ch, s);
+    return run_scan<T, 1>(x, g, init, sq, D, out, fin, chk, ch, s);
+}
+
+template <typename T, int V>
+hipError_t run_scan_backward(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D,
+                             const void *dout, const float *dfin, const float *chk, void *dx, float *dg, float *dinit,
+                             const Chain &ch, hipStream_t s)
+{
+    const int32_t cols = (int32_t)(((int64_t)D + 64 * V - 1) / (64 * V));
+    hipLaunchKernelGGL((kda_scan_bwd_kernel<T, V>), dim3((unsigned)((int64_t)cols * ch.ntiles)), dim3(NTH), 0, s,
+                       (const T *)x, g, init, sq, (int64_t)D, cols, (const T *)dout, dfin, chk, (T *)dx, dg, dinit,
+                       ch);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t scan_backward(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D, const void *dout,
+                         const float *dfin, const float *chk, void *dx, float *dg, float *dinit, const Chain &ch,
+                         hipStream_t s)
+{
+    const size_t e = sizeof(T);
+    if (D % 2 == 0 && fits(x, 2 * e) && fits(dout, 2 * e) && fits(dx, 2 * e) && fits(g, 8) && fits(dg, 8))
+        return run_scan_backward<T, 2>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
+    return run_scan_backward<T, 1>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
+}
 
 }  // namespace kda
 
 using namespace kda;
 
-size_t kda_scan_ws_bytes(int32_t, int32_t) { return 0; }
+size_t kda_scan_ws_bytes(int32_t T, int32_t D) { return chain_layout(T, D).words * sizeof(uint64_t); }
 
 hipError_t kda_launch_scan(bool bf16, const void *x, const float *g, const float *init, const int32_t *cu, int32_t N,
-                           int32_t T, int32_t D, void *out, float *fin, float *chk, void *, hipStream_t s)
+                           int32_t T, int32_t D, void *out, float *fin, float *chk, void *ws, hipStream_t s)
 {
     const Seqs sq{cu, N, T};
-    const unsigned blocks = blocks_of((int64_t)N * D, 64);
-    if (bf16)
-        hipLaunchKernelGGL(kda_scan_kernel<bf16_t>, dim3(blocks), dim3(64), 0, s, (const bf16_t *)x, g, init, sq,
-                           (int64_t)D, (bf16_t *)out, fin, chk, (float *)nullptr);
-    else
-        hipLaunchKernelGGL(kda_scan_kernel<float>, dim3(blocks), dim3(64), 0, s, (const float *)x, g, init, sq,
-                           (int64_t)D, (float *)out, fin, chk, (float *)nullptr);
-    return hipGetLastError();
+    const Chain ch = chain_at((uint64_t *)ws, T, D);
+    if (hipError_t e = fill_chain((uint64_t *)ws, chain_layout(T, D).words, s)) return e;
+    return bf16 ? scan<bf16_t>(x, g, init, sq, D, out, fin, chk, ch, s)
+                : scan<float>(x, g, init, sq, D, out, fin, chk, ch, s);
 }
 
 hipError_t kda_launch_scan_step(bool bf16, const void *x, const float *g, float *state, int64_t n, void *out,
                                 hipStream_t s)
 {
-    const unsigned blocks = blocks_of(n, 256) < 65536 ? blocks_of(n, 256) : 65536;
+    const int64_t want = (n + 255) / 256;
+    const unsigned blocks = (unsigned)(want < 65536 ? want : 65536);
     if (bf16)
         hipLaunchKernelGGL(kda_scan_step_kernel<bf16_t>, dim3(blocks), dim3(256), 0, s, (const bf16_t *)x, g, state, n,
                            (bf16_t *)out);
@@ -97,25 +623,33 @@ hipError_t kda_launch_scan_step(bool bf16, const void *x, const float *g, float 
     return hipGetLastError();
 }
 
-size_t kda_scan_bwd_ws_bytes(int32_t T, int32_t D, bool) { return (size_t)T * D * sizeof(float); }
+// Without checkpoints: a second chain and the checkpoints of a forward pass of our own.
+size_t kda_scan_bwd_ws_bytes(int32_t T, int32_t D, bool has_checkpoints)
+{
+    const size_t words = chain_layout(T, D).words;
+    if (words == 0 || has_checkpoints) return words * sizeof(uint64_t);
+    return 2 * words * sizeof(uint64_t) + (size_t)tiles_of(T) * D * sizeof(float);
+}
 
 hipError_t kda_launch_scan_backward(bool bf16, const void *x, const float *g, const float *init, const int32_t *cu,
                                     int32_t N, int32_t T, int32_t D, const void *dout, const float *dfinal,
-                                    const float *, void *dx, float *dg, float *dinit, void *ws, hipStream_t s)
+                                    const float *checkpoints, void *dx, float *dg, float *dinit, void *ws,
+                                    hipStream_t s)
 {
     const Seqs sq{cu, N, T};
-    const unsigned blocks = blocks_of((int64_t)N * D, 64);
-    float *carried = (float *)ws;
-    if (bf16) {
-        hipLaunchKernelGGL(kda_scan_kernel<bf16_t>, dim3(blocks), dim3(64), 0, s, (const bf16_t *)x, g, init, sq,
-                           (int64_t)D, (bf16_t *)nullptr, (float *)nullptr, (float *)nullptr, carried);
-        hipLaunchKernelGGL(kda_scan_bwd_kernel<bf16_t>, dim3(blocks), dim3(64), 0, s, g, sq, (int64_t)D,
-                           (const bf16_t *)dout, dfinal, carried, (bf16_t *)dx, dg, dinit);
-    } else {
-        hipLaunchKernelGGL(kda_scan_kernel<float>, dim3(blocks), dim3(64), 0, s, (const float *)x, g, init, sq,
-                           (int64_t)D, (float *)nullptr, (float *)nullptr, (float *)nullptr, carried);
-        hipLaunchKernelGGL(kda_scan_bwd_kernel<float>, dim3(blocks), dim3(64), 0, s, g, sq, (int64_t)D,
-                           (const float *)dout, dfinal, carried, (float *)dx, dg, dinit);
+    const size_t words = chain_layout(T, D).words;
+    uint64_t *w = (uint64_t *)ws;
+    const bool states = words > 0 && !checkpoints;
+    if (hipError_t e = fill_chain(w, states ? 2 * words : words, s)) return e;
+    if (states) {
+        float *chk = reinterpret_cast<float *>(w + 2 * words);
+        const Chain ch = chain_at(w + words, T, D);
+        if (hipError_t e = bf16 ? scan<bf16_t>(x, g, init, sq, D, nullptr, nullptr, chk, ch, s)
+                                : scan<float>(x, g, init, sq, D, nullptr, nullptr, chk, ch, s))
+            return e;
+        checkpoints = chk;
     }
-    return hipGetLastError();
+    const Chain ch = chain_at(w, T, D);
+    return bf16 ? scan_backward<bf16_t>(x, g, init, sq, D, dout, dfinal, checkpoints, dx, dg, dinit, ch, s)
+                : scan_backward<float>(x, g, init, sq, D, dout, dfinal, checkpoints, dx, dg, dinit, ch, s);
 }
