@@ -1,193 +1,491 @@
 // kda_conv.hip -- short causal convolution over the tokens of packed
 // sequences, per channel, with an optional SiLU; its decode step and gradients.
 //
-// One thread per (token, channel).
+//     pre_t = bias + sum_{j < W} w_j x_{t - (W - 1) + j},  out_t = silu(pre_t)
+//     dpre_t = dout_t silu'(pre_t),  dx_t = sum_k w_{W-1-k} dpre_{t + k}
+//     dw_j = sum_t dpre_t x_{t - (W - 1) + j},  dbias = sum_t dpre_t
+//
+// One wave walks a strip of tokens of 64 V channels (V consecutive channels a
+// lane, 16 bytes of them where alignment allows), the last W - 1 inputs and
+// the weights in registers: every input is read once (and W - 1 rows of it at a
+// strip's edge once more, mostly from cache) and every output written once, so
+// HBM's rate is the bound.  Rows are read a batch ahead of their use.
+//
+// A sequence's initial state is read by the wave whose strip holds the
+// sequence's first token and by no other: that wave also computes the first
+// W - 1 tokens where they lie beyond its strip, and writes the final state, so
+// that the state may be updated in place.
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
 #include "kda_seq.hpp"
 
+#include <type_traits>
+
 namespace kda {
 
-constexpr int MAXW = 4;
-
 struct ConvArgs {
-    const float *w, *bias;
-    int32_t D, width;
+    const float *w, *bias;   // [D][W], [D] or null
+    int64_t D;
     bool silu;
 };
 
-__device__ __forceinline__ float silu_f(float p) { return p / (1.f + expf(-p)); }
+// VW consecutive elements, moved as one access
+template <typename T, int V> struct Row {
+    typedef T raw __attribute__((ext_vector_type(V)));
+    __device__ static __forceinline__ float at(const raw &r, int j) { return to_f(r[j]); }
+    __device__ static __forceinline__ void set(raw &r, int j, float v) { r[j] = from_f<T>(v); }
+};
+template <typename T> struct Row<T, 1> {
+    typedef T raw;
+    __device__ static __forceinline__ float at(const raw &r, int) { return to_f(r); }
+    __device__ static __forceinline__ void set(raw &r, int, float v) { r = from_f<T>(v); }
+};
+template <typename T, int V> __device__ __forceinline__ typename Row<T, V>::raw load_row(const T *p)
+{
+    return *reinterpret_cast<const typename Row<T, V>::raw *>(p);
+}
+template <typename T, int V> __device__ __forceinline__ void store_row(T *p, const typename Row<T, V>::raw &r)
+{
+    *reinterpret_cast<typename Row<T, V>::raw *>(p) = r;
+}
+
+// 1 / (1 + exp(-p)): exp within |p| + 2 units in the last place, the quotient
+// one more.  Where exp overflows the quotient is 0, the limit.
+__device__ __forceinline__ float sigmoid_f(float p) { return __builtin_amdgcn_rcpf(1.f + __expf(-p)); }
+__device__ __forceinline__ float silu_f(float p) { return p * sigmoid_f(p); }
 __device__ __forceinline__ float dsilu_f(float p)
 {
-    const float sig = 1.f / (1.f + expf(-p));
-    return sig * (1.f + p * (1.f - sig));
+    const float s = sigmoid_f(p);
+    return s * (1.f + p * (1.f - s));
 }
 
-// input at place p (from -(width - 1)) of sequence n, which starts at token t0
-template <typename T>
-__device__ __forceinline__ float conv_input(const T *x, const T *init, const ConvArgs &a, int32_t n, int32_t t0,
-                                            int32_t p, int32_t c)
-{
-    if (p >= 0) return to_f(x[(int64_t)(t0 + p) * a.D + c]);
-    return init ? to_f(init[((int64_t)n * (a.width - 1) + a.width - 1 + p) * a.D + c]) : 0.f;
-}
-
-template <typename T>
-__device__ __forceinline__ float conv_pre(const T *x, const T *init, const ConvArgs &a, int32_t n, int32_t t0,
-                                          int32_t p, int32_t c)
-{
-    float s = a.bias ? a.bias[c] : 0.f;
-    for (int j = 0; j < a.width; ++j)
-        s += a.w[(int64_t)c * a.width + j] * conv_input(x, init, a, n, t0, p - (a.width - 1) + j, c);
-    return s;
-}
-
-template <typename T>
-__global__ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, T *out)
-{
-    const int64_t total = (int64_t)sq.T * a.D;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int32_t t = (int32_t)(i / a.D), c = (int32_t)(i % a.D), n = sq.owner(t);
-        if (n < 0) continue;
-        const int32_t t0 = sq.at(n);
-        const float p = conv_pre(x, init, a, n, t0, t - t0, c);
-        out[i] = from_f<T>(a.silu ? silu_f(p) : p);
-    }
-}
-
-// final_state, after the outputs: it may take initial_state's place
-template <typename T>
-__global__ void kda_conv_final_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, T *fin)
-{
-    const int64_t total = (int64_t)sq.N * a.D;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int32_t n = (int32_t)(i / a.D), c = (int32_t)(i % a.D), t0 = sq.at(n);
-        const int32_t len = max(sq.at(n + 1) - t0, 0);
-        float v[MAXW - 1];
-        for (int j = 0; j < a.width - 1; ++j) v[j] = conv_input(x, init, a, n, t0, len - (a.width - 1) + j, c);
-        for (int j = 0; j < a.width - 1; ++j) fin[((int64_t)n * (a.width - 1) + j) * a.D + c] = from_f<T>(v[j]);
-    }
-}
-
-template <typename T>
-__global__ void kda_conv_step_kernel(const T *x, T *state, ConvArgs a, int32_t N, T *out)
-{
-    const int64_t total = (int64_t)N * a.D;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int32_t n = (int32_t)(i / a.D), c = (int32_t)(i % a.D);
-        T *st = state + (int64_t)n * (a.width - 1) * a.D + c;
-        T v[MAXW];
-        for (int j = 0; j < a.width - 1; ++j) v[j] = st[(int64_t)j * a.D];
-        v[a.width - 1] = x[i];
-        float p = a.bias ? a.bias[c] : 0.f;
-        for (int j = 0; j < a.width; ++j) p += a.w[(int64_t)c * a.width + j] * to_f(v[j]);
-        for (int j = 0; j < a.width - 1; ++j) st[(int64_t)j * a.D] = v[j + 1];
-        out[i] = from_f<T>(a.silu ? silu_f(p) : p);
-    }
-}
-
-// gradient of pre at place p of sequence n
-template <typename T>
-__device__ __forceinline__ float conv_dpre(const T *x, const T *init, const ConvArgs &a, const T *dout, int32_t n,
-                                           int32_t t0, int32_t p, int32_t c)
-{
-    const float d = to_f(dout[(int64_t)(t0 + p) * a.D + c]);
-    return a.silu ? d * dsilu_f(conv_pre(x, init, a, n, t0, p, c)) : d;
-}
-
-// gradient of the input at place p (from -(width - 1)) of sequence n of length len
-template <typename T>
-__device__ __forceinline__ float conv_dinput(const T *x, const T *init, const ConvArgs &a, const T *dout,
-                                             const T *dfinal, int32_t n, int32_t t0, int32_t len, int32_t p, int32_t c)
-{
-    float s = 0.f;
-    for (int k = 0; k < a.width; ++k) {
-        const int32_t q = p + k;
-        if (q >= 0 && q < len)
-            s += a.w[(int64_t)c * a.width + a.width - 1 - k] * conv_dpre(x, init, a, dout, n, t0, q, c);
-    }
-    const int32_t j = p - (len - (a.width - 1));   // its place in the final state
-    if (dfinal && j >= 0) s += to_f(dfinal[((int64_t)n * (a.width - 1) + j) * a.D + c]);
-    return s;
-}
-
-template <typename T>
-__global__ void kda_conv_bwd_dx_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, const T *dout, const T *dfinal,
-                                       T *dx)
-{
-    const int64_t total = (int64_t)sq.T * a.D;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int32_t t = (int32_t)(i / a.D), c = (int32_t)(i % a.D), n = sq.owner(t);
-        if (n < 0) continue;
-        const int32_t t0 = sq.at(n), len = max(sq.at(n + 1) - t0, 0);
-        dx[i] = from_f<T>(conv_dinput(x, init, a, dout, dfinal, n, t0, len, t - t0, c));
-    }
-}
-
-template <typename T>
-__global__ void kda_conv_bwd_dinit_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, const T *dout,
-                                          const T *dfinal, T *dinit)
-{
-    const int64_t total = (int64_t)sq.N * (a.width - 1) * a.D;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int32_t c = (int32_t)(i % a.D), j = (int32_t)(i / a.D % (a.width - 1));
-        const int32_t n = (int32_t)(i / a.D / (a.width - 1)), t0 = sq.at(n), len = max(sq.at(n + 1) - t0, 0);
-        dinit[i] = from_f<T>(conv_dinput(x, init, a, dout, dfinal, n, t0, len, j - (a.width - 1), c));
-    }
-}
-
-template <typename T>
-__global__ void kda_conv_bwd_dw_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, const T *dout, float *dw,
-                                       float *dbias)
-{
-    const int32_t c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= a.D) return;
-    float s[MAXW] = {}, b = 0.f;
-    for (int32_t n = 0; n < sq.N; ++n) {
-        const int32_t t0 = sq.at(n), len = max(sq.at(n + 1) - t0, 0);
-        for (int32_t p = 0; p < len; ++p) {
-            const float d = conv_dpre(x, init, a, dout, n, t0, p, c);
-            b += d;
-            for (int j = 0; j < a.width; ++j) s[j] += d * conv_input(x, init, a, n, t0, p - (a.width - 1) + j, c);
+template <int W, int V> struct Weights {
+    float w[W][V], b[V];
+    __device__ __forceinline__ void load(const ConvArgs &a, int64_t c) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            b[v] = a.bias ? a.bias[c + v] : 0.f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][v] = a.w[(c + v) * W + j];
         }
     }
-    for (int j = 0; j < a.width; ++j) dw[(int64_t)c * a.width + j] = s[j];
-    if (dbias) dbias[c] = b;
+};
+
+// The row that lies k tokens before token t of a sequence whose first token is
+// s: an input, or a row of its initial state (null: zeros).
+template <typename T, int W, int V>
+__device__ __forceinline__ typename Row<T, V>::raw row_before(const T *x, const T *init, const ConvArgs &a, int64_t c,
+                                                              int32_t n, int32_t s, int32_t t, int k)
+{
+    const int32_t p = t - s - k;
+    if (p >= 0) return load_row<T, V>(x + (int64_t)(t - k) * a.D + c);
+    if (init) return load_row<T, V>(init + ((int64_t)n * (W - 1) + W - 1 + p) * a.D + c);
+    return typename Row<T, V>::raw{};
 }
 
-inline unsigned conv_blocks(int64_t n, int per)
+// ---------------------------------------------------------------- forward
+template <typename T, int W, int V>
+__global__ __launch_bounds__(256) void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip,
+                                                       int32_t nstrips, T *out, T *fin)
 {
-    const int64_t b = (n + per - 1) / per;
-    return (unsigned)(b < (1 << 20) ? b : (1 << 20));
+    typedef typename Row<T, V>::raw R;
+    constexpr int BATCH = 8;
+    const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t k = blockIdx.x * 4 + wave;
+    const int64_t c = ((int64_t)blockIdx.y * 64 + (threadIdx.x & 63)) * V;
+    if (k >= nstrips || c >= a.D) return;
+    const int32_t t0 = k * strip, t1 = (int32_t)min((int64_t)t0 + strip, (int64_t)sq.T);
+    const int32_t tend = sq.at(sq.N);
+    Weights<W, V> wt;
+    wt.load(a, c);
+
+    // the final states of the sequences that begin here, after the walk has read the initial ones
+    auto finals = [&]() {
+        for (int32_t n = sq.first_at_or_after(t0); n < sq.N; ++n) {
+            const int32_t s = sq.at(n), e = max(sq.at(n + 1), s);
+            if (s >= t1 && k < nstrips - 1) break;
+            R r[W - 1];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) r[j] = row_before<T, W, V>(x, init, a, c, n, s, e, W - 1 - j);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) store_row<T, V>(fin + ((int64_t)n * (W - 1) + j) * a.D + c, r[j]);
+        }
+    };
+
+    if (t0 < tend) {
+        int32_t n = sq.owner(t0);
+        if (n < 0) return;                     // (cu_seqlens against its rules)
+        int32_t s = sq.at(n), next = max(sq.at(n + 1), t0 + 1), t = t0;
+        // tokens that belong to the wave of their sequence's start
+        if (s < t0 && t0 - s < W - 1) t = min(s + W - 1, next);
+        const int32_t stop = min(t1, tend);
+        R win[W - 1];
+        auto enter = [&]() {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) win[j] = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
+        };
+        auto advance = [&]() {                 // to the sequence that owns token t, its start
+            while (n < sq.N - 1 && next <= t) next = sq.at(++n + 1);
+            s = t;
+        };
+        auto token = [&](const R &r) {
+            R o;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float p = wt.b[v];
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) p += wt.w[j][v] * Row<T, V>::at(win[j], v);
+                p += wt.w[W - 1][v] * Row<T, V>::at(r, v);
+                Row<T, V>::set(o, v, a.silu ? silu_f(p) : p);
+            }
+            store_row<T, V>(out + (int64_t)t * a.D + c, o);
+#pragma unroll
+            for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
+            win[W - 2] = r;
+        };
+        if (t < stop) {
+            if (t == next) advance();
+            enter();
+        }
+        while (t < stop) {
+            const int32_t m = min(stop - t, BATCH);
+            R rows[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) rows[i] = load_row<T, V>(x + (int64_t)min(t + i, stop - 1) * a.D + c);
+            if (m == BATCH && next >= t + BATCH) {
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    token(rows[i]);
+                    ++t;
+                }
+                if (t < stop && t == next) {
+                    advance();
+                    enter();
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    if (i < m) {
+                        token(rows[i]);
+                        ++t;
+                        if (t < stop && t == next) {
+                            advance();
+                            enter();
+                        }
+                    }
+                }
+            }
+        }
+        // the first W - 1 tokens of the last sequence that begins here, beyond the strip
+        if (s >= t0 && t > s && t >= t1) {
+            const int32_t most = min(min(s + W - 1, next), tend);
+            while (t < most) {
+                token(load_row<T, V>(x + (int64_t)t * a.D + c));
+                ++t;
+            }
+        }
+    }
+    if (fin) finals();
 }
 
-template <typename T>
-hipError_t launch_conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, void *out, void *fin,
-                       hipStream_t s)
+// ---------------------------------------------------------------- decode
+template <typename T, int W, int V>
+__global__ __launch_bounds__(256) void kda_conv_step_kernel(const T *x, T *state, ConvArgs a, int32_t N, int32_t per,
+                                                            T *out)
 {
-    if (sq.T > 0)
-        hipLaunchKernelGGL(kda_conv_kernel<T>, dim3(conv_blocks((int64_t)sq.T * a.D, 256)), dim3(256), 0, s,
-                           (const T *)x, (const T *)init, a, sq, (T *)out);
-    if (fin)
-        hipLaunchKernelGGL(kda_conv_final_kernel<T>, dim3(conv_blocks((int64_t)sq.N * a.D, 256)), dim3(256), 0, s,
-                           (const T *)x, (const T *)init, a, sq, (T *)fin);
+    typedef typename Row<T, V>::raw R;
+    const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V;
+    if (c >= a.D) return;
+    Weights<W, V> wt;
+    wt.load(a, c);
+    const int32_t n1 = min(N, (int32_t)(blockIdx.y + 1) * per);
+    for (int32_t n = blockIdx.y * per; n < n1; ++n) {
+        T *st = state + (int64_t)n * (W - 1) * a.D + c;
+        R r[W], o;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) r[j] = load_row<T, V>(st + j * a.D);
+        r[W - 1] = load_row<T, V>(x + n * a.D + c);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float p = wt.b[v];
+#pragma unroll
+            for (int j = 0; j < W; ++j) p += wt.w[j][v] * Row<T, V>::at(r[j], v);
+            Row<T, V>::set(o, v, a.silu ? silu_f(p) : p);
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) store_row<T, V>(st + j * a.D, r[j + 1]);
+        store_row<T, V>(out + n * a.D + c, o);
+    }
+}
+
+// ---------------------------------------------------------------- gradients
+// The walk keeps the W - 1 newest places' dx unfinished in `acc` (the place of
+// token t takes from dpre_t .. dpre_{t + W - 1}); at a sequence's start they
+// stand for its initial state's rows, at its end the final state's gradient
+// joins them.  A strip's wave finishes the places of its tokens, and of the
+// initial states of the sequences that begin in it, by walking W - 1 tokens
+// beyond the strip; only its own tokens count for dw and dbias.
+template <typename T, int W, int V>
+__global__ __launch_bounds__(256) void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq,
+                                                           int32_t strip, int32_t nstrips, const T *dout,
+                                                           const T *dfin, T *dx, T *dinit, float *partial)
+{
+    typedef typename Row<T, V>::raw R;
+    constexpr int BATCH = 4;
+    __shared__ float sums[4][W + 1][64 * V];
+    const int32_t lane = threadIdx.x & 63;
+    const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t k = blockIdx.x * 4 + wave;
+    const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * V;
+    const bool live = k < nstrips && c < a.D;
+    float dw[W][V] = {}, db[V] = {};
+    if (live) {
+        const int32_t t0 = (int32_t)min((int64_t)k * strip, (int64_t)sq.T);
+        const int32_t t1 = (int32_t)min((int64_t)t0 + strip, (int64_t)sq.T), tend = sq.at(sq.N);
+        auto put_dinit = [&](int32_t n, int j, const float (&v)[V]) {
+            R r;
+#pragma unroll
+            for (int i = 0; i < V; ++i) Row<T, V>::set(r, i, v[i]);
+            store_row<T, V>(dinit + ((int64_t)n * (W - 1) + j) * a.D + c, r);
+        };
+        auto get_dfin = [&](int32_t n, int j) {
+            return dfin ? load_row<T, V>(dfin + ((int64_t)n * (W - 1) + j) * a.D + c) : R{};
+        };
+        if (dinit)   // empty sequences
+            for (int32_t n = sq.first_at_or_after(t0); n < sq.N; ++n) {
+                const int32_t s = sq.at(n);
+                if (s >= t1 && k < nstrips - 1) break;
+                if (sq.at(n + 1) <= s)
+                    for (int j = 0; j < W - 1; ++j)
+                        store_row<T, V>(dinit + ((int64_t)n * (W - 1) + j) * a.D + c, get_dfin(n, j));
+            }
+        int32_t n = t0 < min(tend, t1) ? sq.owner(t0) : -1;
+        if (n >= 0) {
+            Weights<W, V> wt;
+            wt.load(a, c);
+            int32_t s = sq.at(n), next = max(sq.at(n + 1), t0 + 1), t = t0;
+            R win[W - 1];
+            float acc[W - 1][V] = {};
+            auto enter = [&]() {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) win[j] = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
+            };
+            // place p of the sequence (p < 0: of its initial state) is finished
+            auto finish = [&](int32_t p, const float (&v)[V]) {
+                if (p >= 0) {
+                    if (s + p < t0 || s + p >= t1) return;
+                    R r;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) Row<T, V>::set(r, i, v[i]);
+                    store_row<T, V>(dx + (int64_t)(s + p) * a.D + c, r);
+                } else if (dinit && s >= t0 && s < t1) {
+                    put_dinit(n, p + W - 1, v);
+                }
+            };
+            enter();
+            const int32_t stop = (int32_t)min((int64_t)t1 + W - 1, (int64_t)tend);
+            auto token = [&](const R &r, const R &d) {
+                float done[V];
+                const bool mine = t < t1;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float p = wt.b[v], in[W];
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) in[j] = Row<T, V>::at(win[j], v);
+                    in[W - 1] = Row<T, V>::at(r, v);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) p += wt.w[j][v] * in[j];
+                    float g = Row<T, V>::at(d, v);
+                    if (a.silu) g *= dsilu_f(p);
+                    if (mine) {
+                        db[v] += g;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][v] += g * in[j];
+                    }
+                    done[v] = acc[0][v] + g * wt.w[0][v];
+#pragma unroll
+                    for (int j = 0; j + 1 < W - 1; ++j) acc[j][v] = acc[j + 1][v] + g * wt.w[j + 1][v];
+                    acc[W - 2][v] = g * wt.w[W - 1][v];
+                }
+                finish(t - s - (W - 1), done);
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
+                win[W - 2] = r;
+                ++t;
+            };
+            // the sequence ends before token t: its unfinished places, then the next sequence
+            auto leave = [&]() {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) {
+                    const R f = get_dfin(n, j);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[j][v] += Row<T, V>::at(f, v);
+                    finish(t - s - (W - 1) + j, acc[j]);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
+                }
+                while (n < sq.N - 1 && next <= t) next = sq.at(++n + 1);
+                s = t;
+            };
+            while (t < stop) {
+                const int32_t m = min(stop - t, BATCH);
+                R xr[BATCH], dr[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int64_t at = (int64_t)min(t + i, stop - 1) * a.D + c;
+                    xr[i] = load_row<T, V>(x + at);
+                    dr[i] = load_row<T, V>(dout + at);
+                }
+                bool over = false;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    if (i < m && !over) {
+                        token(xr[i], dr[i]);
+                        if (t == next) {
+                            leave();
+                            over = t >= t1 || t >= stop;   // nothing of ours is unfinished
+                            if (!over) enter();
+                        }
+                    }
+                }
+                if (over) break;
+            }
+        }
+    }
+    // the four waves' sums, in order, as the workgroup's part
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        sums[wave][W][lane * V + v] = db[v];
+#pragma unroll
+        for (int j = 0; j < W; ++j) sums[wave][j][lane * V + v] = dw[j][v];
+    }
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.y * 64 * V;
+    for (int i = threadIdx.x; i < (W + 1) * 64 * V; i += 256) {
+        const int j = i / (64 * V), cc = i % (64 * V);
+        const float total = ((sums[0][j][cc] + sums[1][j][cc]) + sums[2][j][cc]) + sums[3][j][cc];
+        if (first + cc < a.D) partial[((int64_t)blockIdx.x * (W + 1) + j) * a.D + first + cc] = total;
+    }
+}
+
+// dw[c][j] and dbias[c] from the workgroups' parts [n][W + 1][D]: 32 columns
+// and 32 strided walks a workgroup, the walks' sums added in order
+template <int W>
+__global__ __launch_bounds__(1024) void kda_conv_sums_kernel(const float *src, int32_t n, int64_t D, float *dw,
+                                                             float *dbias)
+{
+    __shared__ float part[32][33];
+    const int cx = threadIdx.x & 31, walk = threadIdx.x >> 5;
+    const int64_t cols = (W + 1) * D, i = (int64_t)blockIdx.x * 32 + cx;
+    float s = 0.f;
+    if (i < cols)
+        for (int32_t r = walk; r < n; r += 32) s += src[r * cols + i];
+    part[walk][cx] = s;
+    __syncthreads();
+    if (walk == 0 && i < cols) {
+        for (int v = 1; v < 32; ++v) s += part[v][cx];
+        const int64_t j = i / D, c = i % D;
+        if (j < W) dw[c * W + j] = s;
+        else if (dbias) dbias[c] = s;
+    }
+}
+
+// ---------------------------------------------------------------- host
+inline bool wide(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+inline int64_t up(int64_t n, int64_t per) { return (n + per - 1) / per; }
+
+constexpr int32_t BWD_PARTS = 512;    // workgroups along the tokens, at most
+constexpr int32_t BWD_STRIP = 16;     // tokens of a wave, at least
+
+inline int32_t bwd_strip(int32_t T)
+{
+    const int64_t len = up(up(T, (int64_t)BWD_PARTS * 4), 4) * 4;
+    return (int32_t)(len < BWD_STRIP ? BWD_STRIP : len);
+}
+inline int32_t bwd_parts(int32_t T) { return (int32_t)(T > 0 ? up(up(T, bwd_strip(T)), 4) : 1); }
+
+template <typename T, int W, int V>
+hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, void *out, void *fin,
+                    hipStream_t s)
+{
+    const int64_t cols = up(a.D, 64 * V);
+    // strips of 64 tokens where these give every SIMD its waves, shorter ones otherwise
+    const int32_t strip = up(sq.T, 64) * cols >= 4096 ? 64 : 16;
+    const int32_t nstrips = (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1);
+    hipLaunchKernelGGL((kda_conv_kernel<T, W, V>), dim3((unsigned)up(nstrips, 4), (unsigned)cols), dim3(256), 0, s,
+                       (const T *)x, (const T *)init, a, sq, strip, nstrips, (T *)out, (T *)fin);
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_conv_backward(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, const void *dout,
-                                const void *dfinal, void *dx, float *dw, float *dbias, void *dinit, hipStream_t s)
+template <typename T, int W, int V>
+hipError_t run_conv_step(const void *x, const ConvArgs &a, void *state, int32_t N, void *out, hipStream_t s)
 {
-    if (sq.T > 0 && sq.N > 0)
-        hipLaunchKernelGGL(kda_conv_bwd_dx_kernel<T>, dim3(conv_blocks((int64_t)sq.T * a.D, 256)), dim3(256), 0, s,
-                           (const T *)x, (const T *)init, a, sq, (const T *)dout, (const T *)dfinal, (T *)dx);
-    if (dinit && sq.N > 0)
-        hipLaunchKernelGGL(kda_conv_bwd_dinit_kernel<T>, dim3(conv_blocks((int64_t)sq.N * (a.width - 1) * a.D, 256)),
-                           dim3(256), 0, s, (const T *)x, (const T *)init, a, sq, (const T *)dout, (const T *)dfinal,
-                           (T *)dinit);
-    hipLaunchKernelGGL(kda_conv_bwd_dw_kernel<T>, dim3((unsigned)((a.D + 63) / 64)), dim3(64), 0, s, (const T *)x,
-                       (const T *)init, a, sq, (const T *)dout, dw, dbias);
+    const int64_t cols = up(a.D, 256 * V);
+    const int32_t per = N * cols >= 4096 ? 4 : 1;   // sequences a thread takes with one reading of the weights
+    hipLaunchKernelGGL((kda_conv_step_kernel<T, W, V>), dim3((unsigned)cols, (unsigned)up(N, per)), dim3(256), 0, s,
+                       (const T *)x, (T *)state, a, N, per, (T *)out);
     return hipGetLastError();
+}
+
+template <typename T, int W, int V>
+hipError_t run_conv_backward(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, const void *dout,
+                             const void *dfin, void *dx, float *dw, float *dbias, void *dinit, void *ws,
+                             hipStream_t s)
+{
+    const int32_t strip = bwd_strip(sq.T), parts = sq.N > 0 ? bwd_parts(sq.T) : 0;
+    if (parts > 0)
+        hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V>), dim3((unsigned)parts, (unsigned)up(a.D, 64 * V)), dim3(256),
+                           0, s, (const T *)x, (const T *)init, a, sq, strip,
+                           (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1), (const T *)dout, (const T *)dfin, (T *)dx,
+                           (T *)dinit, (float *)ws);
+    hipLaunchKernelGGL(kda_conv_sums_kernel<W>, dim3((unsigned)up((W + 1) * a.D, 32)), dim3(1024), 0, s,
+                       (const float *)ws, parts, a.D, dw, dbias);
+    return hipGetLastError();
+}
+
+// calls f with the width and the piece as compile-time numbers
+template <int V, typename F> hipError_t with_width(int32_t width, F f)
+{
+    switch (width) {
+    case 2: return f(std::integral_constant<int, 2>(), std::integral_constant<int, V>());
+    case 3: return f(std::integral_constant<int, 3>(), std::integral_constant<int, V>());
+    default: return f(std::integral_constant<int, 4>(), std::integral_constant<int, V>());
+    }
+}
+
+template <typename T>
+hipError_t conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, int32_t width, void *out, void *fin,
+                hipStream_t s)
+{
+    constexpr int V = 16 / sizeof(T);
+    auto f = [&](auto w, auto v) { return run_conv<T, w(), v()>(x, a, init, sq, out, fin, s); };
+    return a.D % V == 0 && wide(x, 16) && wide(init, 16) && wide(out, 16) && wide(fin, 16) ? with_width<V>(width, f)
+                                                                                           : with_width<1>(width, f);
+}
+
+template <typename T>
+hipError_t conv_step(const void *x, const ConvArgs &a, void *state, int32_t N, int32_t width, void *out, hipStream_t s)
+{
+    constexpr int V = 16 / sizeof(T);
+    auto f = [&](auto w, auto v) { return run_conv_step<T, w(), v()>(x, a, state, N, out, s); };
+    return a.D % V == 0 && wide(x, 16) && wide(state, 16) && wide(out, 16) ? with_width<V>(width, f)
+                                                                           : with_width<1>(width, f);
+}
+
+template <typename T>
+hipError_t conv_backward(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, int32_t width,
+                         const void *dout, const void *dfin, void *dx, float *dw, float *dbias, void *dinit, void *ws,
+                         hipStream_t s)
+{
+    constexpr int V = 4;   // (eight channels' sums and unfinished places would not fit the registers)
+    constexpr size_t B = V * sizeof(T);
+    auto f = [&](auto w, auto v) {
+        return run_conv_backward<T, w(), v()>(x, a, init, sq, dout, dfin, dx, dw, dbias, dinit, ws, s);
+    };
+    return a.D % V == 0 && wide(x, B) && wide(init, B) && wide(dout, B) && wide(dfin, B) && wide(dx, B) &&
+                   wide(dinit, B)
+               ? with_width<V>(width, f)
+               : with_width<1>(width, f);
 }
 
 }  // namespace kda
@@ -198,34 +496,30 @@ hipError_t kda_launch_conv(bool bf16, const void *x, const float *w, const float
                            const int32_t *cu, int32_t N, int32_t T, int32_t D, int32_t width, bool silu, void *out,
                            void *fin, hipStream_t s)
 {
-    const ConvArgs a{w, bias, D, width, silu};
+    const ConvArgs a{w, bias, D, silu};
     const Seqs sq{cu, N, T};
-    return bf16 ? launch_conv<bf16_t>(x, a, init, sq, out, fin, s) : launch_conv<float>(x, a, init, sq, out, fin, s);
+    return bf16 ? conv<bf16_t>(x, a, init, sq, width, out, fin, s) : conv<float>(x, a, init, sq, width, out, fin, s);
 }
 
 hipError_t kda_launch_conv_step(bool bf16, const void *x, const float *w, const float *bias, void *state, int32_t N,
                                 int32_t D, int32_t width, bool silu, void *out, hipStream_t s)
 {
-    const ConvArgs a{w, bias, D, width, silu};
-    const unsigned blocks = conv_blocks((int64_t)N * D, 256);
-    if (bf16)
-        hipLaunchKernelGGL(kda_conv_step_kernel<bf16_t>, dim3(blocks), dim3(256), 0, s, (const bf16_t *)x,
-                           (bf16_t *)state, a, N, (bf16_t *)out);
-    else
-        hipLaunchKernelGGL(kda_conv_step_kernel<float>, dim3(blocks), dim3(256), 0, s, (const float *)x,
-                           (float *)state, a, N, (float *)out);
-    return hipGetLastError();
+    const ConvArgs a{w, bias, D, silu};
+    return bf16 ? conv_step<bf16_t>(x, a, state, N, width, out, s) : conv_step<float>(x, a, state, N, width, out, s);
 }
 
-size_t kda_conv_bwd_ws_bytes(int32_t, int32_t, int32_t, bool) { return 0; }
+size_t kda_conv_bwd_ws_bytes(int32_t T, int32_t D, int32_t width, bool)
+{
+    return (size_t)bwd_parts(T) * (width + 1) * D * sizeof(float);
+}
 
 hipError_t kda_launch_conv_backward(bool bf16, const void *x, const float *w, const float *bias, const void *init,
                                     const int32_t *cu, int32_t N, int32_t T, int32_t D, int32_t width, bool silu,
                                     const void *dout, const void *dfinal, void *dx, float *dw, float *dbias,
-                                    void *dinit, void *, hipStream_t s)
+                                    void *dinit, void *ws, hipStream_t s)
 {
-    const ConvArgs a{w, bias, D, width, silu};
+    const ConvArgs a{w, bias, D, silu};
     const Seqs sq{cu, N, T};
-    return bf16 ? launch_conv_backward<bf16_t>(x, a, init, sq, dout, dfinal, dx, dw, dbias, dinit, s)
-                : launch_conv_backward<float>(x, a, init, sq, dout, dfinal, dx, dw, dbias, dinit, s);
+    return bf16 ? conv_backward<bf16_t>(x, a, init, sq, width, dout, dfinal, dx, dw, dbias, dinit, ws, s)
+                : conv_backward<float>(x, a, init, sq, width, dout, dfinal, dx, dw, dbias, dinit, ws, s);
 }
