@@ -26,10 +26,12 @@ kda_status from_hip(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_LA
 
 hipStream_t hip_stream(kda_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
 
-// What the packed calls share: sizes, type, cu_seqlens.
+// What the packed calls share: sizes, type, cu_seqlens.  The kernels look a
+// tile beyond a token in int32.
 bool packed_ok(const int32_t *cu, int32_t N, int32_t T, int32_t D, kda_dtype dtype)
 {
-    return dtype_ok(dtype) && N >= 0 && T >= 0 && D > 0 && cu && aligned(cu, 4);
+    return dtype_ok(dtype) && N >= 0 && N < INT32_MAX && T >= 0 && T <= INT32_MAX - 65536 && D > 0 && cu &&
+           aligned(cu, 4);
 }
 
 bool workspace_ok(const void *ws, size_t bytes, size_t need, size_t align)

@@ -12,17 +12,16 @@
 // is read once and every output written once, which is all the traffic there
 // has to be (8 bytes an element with bf16 x), and HBM's rate is the bound.
 //
-// The state that enters a tile is joined from three levels of published runs:
-// the tiles of its group of 8 before it, the groups of its super-group of 8
-// before its own, and the state that enters the super-group, which is passed
-// from super-group to super-group (8,192 tokens a hop).  Which runs are joined,
-// and in which order, depends on the tile alone, not on what is ready first, so
-// that results are the same bits on every call.  A published run is one
-// 64-bit word a channel, written and polled with relaxed device-scope atomics:
-// the word is its own flag (all ones: not there yet), so no fence is needed
-// between data and flag.  Tiles of a channel block are handed out in order by a
-// counter, so a tile waits only for workgroups that are already running, and
-// these wait for earlier ones in turn: every wait ends.
+// The state that enters a tile is joined from the runs of the tiles before it
+// in its block of 16 or 32 tiles, all read side by side, and the state that
+// enters the block, which is passed from block to block.  Which runs are
+// joined, and in which order, depends on the tile alone, not on what is ready
+// first, so that results are the same bits on every call.  A published run is
+// one 64-bit word a channel, written and polled with relaxed device-scope
+// atomics: the word is its own flag (all ones: not there yet), so no fence is
+// needed between data and flag.  Tiles of a channel block are handed out in
+// order by a counter, so a tile waits only for workgroups that are already
+// running, and these wait for earlier ones in turn: every wait ends.
 //
 // The gradients run the same scheme from the end to the start,
 //     dh_t = dout_t + e,  e <- a_t dh_t,
@@ -37,15 +36,14 @@ constexpr int TILE = 128;             // tokens of a tile, and between checkpoin
 constexpr int WAVES = 8;              // waves of a workgroup
 constexpr int L = TILE / WAVES;       // tokens of a wave
 constexpr int NTH = WAVES * 64;
-constexpr int GROUP = 8;              // tiles of a group
-constexpr int SUPER = GROUP * GROUP;  // tiles of a super-group
+constexpr int GATHER = 8;             // published runs a thread joins
 constexpr float RESET = -1.f;         // an A that drops what enters (products of exp() are never negative)
 constexpr uint64_t NOT_YET = ~(uint64_t)0;
 
 // ---------------------------------------------------------------- published runs
 struct Chain {
     uint32_t *ticket;                 // [column of channels], from ~0
-    uint64_t *tile, *group, *super;   // [index][D]
+    uint64_t *tile, *block;           // [index][D]: tiles' runs, states that enter blocks
     int32_t ntiles;
     int64_t D;
 };
@@ -80,70 +78,70 @@ __device__ __forceinline__ void publish(uint64_t *p, const Run &r)
     __hip_atomic_store(p, pack(r), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// the m < GROUP runs p[0], p[D], ... joined in order; all are asked for before any is waited for
+// the m <= GATHER runs p[0], p[D], ... joined in order; all are asked for before any is waited for
 __device__ __forceinline__ Run gather(const uint64_t *p, int64_t D, int m)
 {
-    uint64_t w[GROUP - 1];
+    uint64_t w[GATHER];
 #pragma unroll
-    for (int i = 0; i < GROUP - 1; ++i) w[i] = i < m ? peek(p + i * D) : 0;
+    for (int i = 0; i < GATHER; ++i) w[i] = i < m ? peek(p + i * D) : 0;
     Run r = {1.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < GROUP - 1; ++i) {
+    for (int i = 0; i < GATHER; ++i) {
         if (i < m) {
-            while (w[i] == NOT_YET) {
-                __builtin_amdgcn_s_sleep(1);
-                w[i] = peek(p + i * D);
-            }
+            while (w[i] == NOT_YET) w[i] = peek(p + i * D);
             r = i == 0 ? unpack(w[i]) : join(r, unpack(w[i]));
         }
     }
     return r;
 }
 
+// Roles of a workgroup's threads in passing a state on: CB threads each, one a
+// channel.  Each role joins GATHER of the tiles of the block before this one.
+template <int CB> struct Roles {
+    static constexpr int N = NTH / CB < 4 ? NTH / CB : 4;
+    static constexpr int BLOCK = N * GATHER;   // tiles of a block
+};
+
 // The value that enters tile k (counted in the direction of the walk) for
 // every channel of the workgroup, in `enter`; publishes the tile's own run.
 // `runs` holds the waves' runs in the order of the walk.  `fresh`: nothing
-// enters (the tile begins at a boundary); `resets`: it has a boundary.  The
-// first 64 V threads join the tiles, the next the groups.  Ends with a barrier.
+// enters (the tile begins at a boundary); `resets`: it has a boundary.  Begins
+// after a barrier and ends with one.
 template <int CB>
 __device__ __forceinline__ void pass_on(const Chain &ch, int k, int64_t c0, bool fresh, bool resets,
-                                        const Run (*runs)[CB], Run *groups, float *enter)
+                                        const Run (*runs)[CB], Run (*parts)[CB], float *enter)
 {
-    const int tid = threadIdx.x, c = tid % CB, role = tid / CB;
+    constexpr int N = Roles<CB>::N, BLOCK = Roles<CB>::BLOCK;
+    const int c = threadIdx.x % CB, role = threadIdx.x / CB;
     const bool in = c0 + c < ch.D;
-    const int in_group = k % GROUP, group = k / GROUP, in_super = group % GROUP, super = k / SUPER;
-    const bool last_in_group = in_group == GROUP - 1, last_in_super = k % SUPER == SUPER - 1;
+    const int place = k % BLOCK, block = k / BLOCK;   // the tile's place in its block
+    const bool last = place == BLOCK - 1;
     const int64_t ci = c0 + c;
-    Run own = {1.f, 0.f}, before = {1.f, 0.f};
+    Run own = {1.f, 0.f};
+    uint64_t before = 0;
     if (role == 0 && in) {
         own = runs[0][c];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) own = join(own, runs[w][c]);
-        if (!last_in_group) publish(ch.tile + k * ch.D + ci, own);
-        if (resets) {   // what leaves does not depend on what enters
-            if (last_in_group && !last_in_super) publish(ch.group + group * ch.D + ci, own);
-            if (last_in_super) publish(ch.super + (super + 1) * ch.D + ci, own);
-        }
-        if (!fresh) before = gather(ch.tile + (k - in_group) * ch.D + ci, ch.D, in_group);
-        if (!resets && last_in_group && !last_in_super)
-            publish(ch.group + group * ch.D + ci, in_group ? join(before, own) : own);
+        if (!last) publish(ch.tile + k * ch.D + ci, own);
+        else if (resets) publish(ch.block + (block + 1) * ch.D + ci, {RESET, own.B});   // whatever enters
     }
-    if (role == 1 && in && !fresh) {
-        Run r = gather(ch.group + (group - in_super) * ch.D + ci, ch.D, in_super);
-        if (super > 0) {
-            uint64_t w;
-            while ((w = peek(ch.super + super * ch.D + ci)) == NOT_YET) __builtin_amdgcn_s_sleep(1);
-            r = in_super ? Run{RESET, apply(r, unpack(w).B)} : Run{RESET, unpack(w).B};
+    if (!fresh) {
+        if (role == 0 && in && block > 0) before = peek(ch.block + block * ch.D + ci);
+        const int m = min(place - role * GATHER, GATHER);
+        if (role < N && in && m > 0)
+            parts[role][c] = gather(ch.tile + (int64_t)(k - place + role * GATHER) * ch.D + ci, ch.D, m);
+        __syncthreads();
+        if (role == 0 && in) {
+            // nothing enters the first block: its first run drops what would
+            while (before == NOT_YET) before = peek(ch.block + block * ch.D + ci);
+            float h = unpack(before).B;
+#pragma unroll
+            for (int r = 0; r < N; ++r)
+                if (place > r * GATHER) h = apply(parts[r][c], h);
+            enter[c] = h;
+            if (!resets && last) publish(ch.block + (block + 1) * ch.D + ci, {RESET, apply(own, h)});
         }
-        groups[c] = r;
-    }
-    __syncthreads();
-    if (role == 0 && in && !fresh) {
-        const Run g = groups[c];
-        // nothing enters the first tile of all: its value stands for that of no sequence
-        const float h = (super > 0 || in_super > 0) ? (in_group ? apply(before, g.B) : g.B) : before.B;
-        enter[c] = h;
-        if (!resets && last_in_super) publish(ch.super + (super + 1) * ch.D + ci, {RESET, apply(own, h)});
     }
     __syncthreads();
 }
@@ -177,6 +175,28 @@ __device__ __forceinline__ float gate(float g)
     return lo == lo ? __builtin_fmaf(e, lo * LN2, e) : e;
 }
 
+// A wave's rows: scalar addresses, and a lane's place in a row of its own.
+// Rows past the last token stand for the last one, lanes past the last channel
+// for the last channels.  Without tokens nothing may be read.
+struct Rows {
+    int64_t first, D;
+    int32_t last;
+    uint32_t lane;
+    __device__ __forceinline__ Rows(const Seqs &sq, int32_t t0, int64_t D_, int64_t c0, int l, int V) : D(D_) {
+        const int32_t t = min(t0, sq.T - 1);
+        first = t * D + c0;
+        last = sq.T - 1 - t;
+        lane = (uint32_t)min((int64_t)l, D - V - c0);
+    }
+    template <typename R, typename T> __device__ __forceinline__ R at(const T *p, int i) const {
+        return __builtin_nontemporal_load(reinterpret_cast<const R *>(p + first + min(i, last) * D + lane));
+    }
+};
+
+// The compiler keeps a value that it could unpack again: this makes it forget
+// how `r` was unpacked, so that only the packed form stays in registers.
+template <typename R> __device__ __forceinline__ void repack(R &r) { asm volatile("" : "+v"(r)); }
+
 // Boundaries of sequences at a wave's tokens: bit i stands for token t0 + i,
 // i = 0 .. L.  `end` is the first token of no sequence.
 struct Edges {
@@ -184,12 +204,12 @@ struct Edges {
     int32_t end;
 };
 
-__device__ __forceinline__ Edges edges(const Seqs &sq, int32_t t0, int32_t *first)
+__device__ __forceinline__ Edges edges(const SeqWindow &sq, int32_t t0, int32_t end, int32_t *first)
 {
-    Edges e = {0, sq.at(sq.N)};
+    Edges e = {0, end};
     int32_t n = sq.first_at_or_after(t0);
     *first = n;
-    for (; n <= sq.N; ++n) {
+    for (; n <= sq.sq.N; ++n) {
         const int32_t p = sq.at(n);
         if (p > t0 + L || p < t0) break;
         e.mask |= 1u << (p - t0);
@@ -197,11 +217,20 @@ __device__ __forceinline__ Edges edges(const Seqs &sq, int32_t t0, int32_t *firs
     return e;
 }
 
+// whether a sequence's boundary lies at a token of [t, t + len), and whether at t
+__device__ __forceinline__ void boundary_in(const SeqWindow &sq, int32_t t, int len, bool *any, bool *at_first)
+{
+    const int32_t n = sq.first_at_or_after(t);
+    const int64_t p = n <= sq.sq.N ? sq.at(n) : INT64_MAX;
+    *any = p < (int64_t)t + len;
+    *at_first = p == t;
+}
+
 // `copy(n)` for the empty sequences that lie at tokens [t0, t0 + L), or at any later place for the last wave of all
 template <typename F>
-__device__ __forceinline__ void empty_seqs(const Seqs &sq, int32_t t0, int32_t first, bool last, F copy)
+__device__ __forceinline__ void empty_seqs(const SeqWindow &sq, int32_t t0, int32_t first, bool last, F copy)
 {
-    for (int32_t n = first; n < sq.N; ++n) {
+    for (int32_t n = first; n < sq.sq.N; ++n) {
         const int32_t p = sq.at(n);
         if (p >= t0 + L && !last) break;
         if (sq.at(n + 1) <= p) copy(n);
@@ -218,13 +247,22 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
     typedef typename Vec<T, V>::raw XR;
     typedef typename Vec<float, V>::raw GR;
     __shared__ Run runs[WAVES][CB];
-    __shared__ Run groups[CB];
+    __shared__ Run parts[Roles<CB>::N][CB];
     __shared__ float enter[CB];
     __shared__ uint32_t s_tile;
 
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = blockIdx.x % cols;
+    if (sq.T == 0) {
+        if (fin && w == 0)
+            for (int32_t n = 0; n < sq.N; ++n)
+                for (int64_t c = (int64_t)col * CB + lane; c < min(D, (int64_t)(col + 1) * CB); c += 64)
+                    fin[n * D + c] = init ? init[n * D + c] : 0.f;
+        return;
+    }
+    const int32_t tend = sq.at(sq.N);
+    SeqWindow win(sq);
     int k = 0;
     if (ch.ntiles > 1) {
         if (threadIdx.x == 0) s_tile = atomicAdd(ch.ticket + col, 1u) + 1u;
@@ -233,46 +271,46 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
     }
     const int64_t c0 = (int64_t)col * CB, c = c0 + lane * V;
     const bool in = c < D;
-    const int32_t tile0 = k * TILE, t0 = tile0 + w * L;
-
     XR xr[L];
-    float a[L][V];
     GR gr[L];
+    const int32_t t0 = k * TILE + w * L;
+    {
+        const Rows rows(sq, t0, D, c0, lane * V, V);
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-        if (in && t0 + i < sq.T) {
-            const int64_t at = (int64_t)(t0 + i) * D + c;
-            xr[i] = *reinterpret_cast<const XR *>(x + at);
-            gr[i] = *reinterpret_cast<const GR *>(g + at);
-        } else {
-            xr[i] = XR{};
-            gr[i] = GR{};
+        for (int i = 0; i < L; ++i) {
+            xr[i] = rows.at<XR>(x, i);
+            gr[i] = rows.at<GR>(g, i);
         }
     }
     int32_t first;
-    const Edges e = edges(sq, t0, &first);
+    win.locate(k * TILE);
+    const Edges e = edges(win, t0, tend, &first);
     const uint32_t starts = e.mask & ((1u << L) - 1);
+    bool fresh, resets;
+    boundary_in(win, k * TILE, TILE, &resets, &fresh);
+    fresh = fresh || k == 0;
     if (fin)
-        empty_seqs(sq, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {
+        empty_seqs(win, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {
             if (in)
                 for (int j = 0; j < V; ++j) fin[n * D + c + j] = init ? init[n * D + c + j] : 0.f;
         });
     // what a token leaves: its output, and the final state of a sequence that ends with it
     auto leave = [&](int i, const float (&h)[V]) {
-        if (!in || t0 + i >= e.end) return;
-        if (out) {
+        if (t0 + i >= e.end) return;
+        if (out && in) {
             XR o;
             for (int j = 0; j < V; ++j) put(o, j, from_f<T>(h[j]));
             *reinterpret_cast<XR *>(out + (int64_t)(t0 + i) * D + c) = o;
         }
         if (fin && (e.mask >> (i + 1) & 1)) {
-            const int64_t n = sq.owner(t0 + i);
-            if (n >= 0)
+            const int64_t n = win.owner(t0 + i);
+            if (n >= 0 && in)
                 for (int j = 0; j < V; ++j) fin[n * D + c + j] = h[j];
         }
     };
 
     // the wave's run; after its first start the states are known, and leave at once
+    float a[L][V];
     {
         float A[V], B[V];
 #pragma unroll
@@ -282,7 +320,7 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
         for (int i = 0; i < L; ++i) {
             if (starts >> i & 1) {
                 known = true;
-                const int64_t n = init ? sq.owner(t0 + i) : -1;
+                const int64_t n = init ? win.owner(t0 + i) : -1;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     A[j] = RESET;
@@ -299,11 +337,12 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) runs[w][lane * V + j] = {A[j], B[j]};
+#pragma unroll
+        for (int i = 0; i < L; ++i) repack(xr[i]);
     }
-    const bool fresh = __syncthreads_or(w == 0 && (starts & 1)) || k == 0;
-    const bool resets = __syncthreads_or(starts != 0);
+    __syncthreads();
     if (ch.ntiles > 1) {
-        pass_on<CB>(ch, k, c0, fresh, resets, runs, groups, enter);
+        pass_on<CB>(ch, k, c0, fresh, resets, runs, parts, enter);
         if (chk && w == 0 && in && !fresh)
             for (int j = 0; j < V; ++j) chk[k * D + c + j] = enter[lane * V + j];
     }
@@ -325,7 +364,7 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
                 h[j] = a[i][j] * h[j] + elem(xr[i], j);
                 put(o, j, from_f<T>(h[j]));
             }
-            if (in) *reinterpret_cast<XR *>(out + (int64_t)(t0 + i) * D + c) = o;
+            if (in) __builtin_nontemporal_store(o, reinterpret_cast<XR *>(out + (int64_t)(t0 + i) * D + c));
         }
     } else {
 #pragma unroll
@@ -349,48 +388,57 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
     typedef typename Vec<float, V>::raw GR;
     __shared__ Run fwd[WAVES][CB];      // forward runs of the waves, first to last
     __shared__ Run back[WAVES][CB];     // backward runs of the waves, last to first
-    __shared__ Run groups[CB];
+    __shared__ Run parts[Roles<CB>::N][CB];
     __shared__ float enter[CB];
     __shared__ uint32_t s_tile;
 
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = blockIdx.x % cols;
+    if (sq.T == 0) {
+        if (dinit && w == 0)
+            for (int32_t n = 0; n < sq.N; ++n)
+                for (int64_t c = (int64_t)col * CB + lane; c < min(D, (int64_t)(col + 1) * CB); c += 64)
+                    dinit[n * D + c] = dfin ? dfin[n * D + c] : 0.f;
+        return;
+    }
+    const int32_t tend = sq.at(sq.N);
+    SeqWindow win(sq);
     int kb = 0;                         // the tile's number from the end
     if (ch.ntiles > 1) {
         if (threadIdx.x == 0) s_tile = atomicAdd(ch.ticket + col, 1u) + 1u;
         __syncthreads();
         kb = __builtin_amdgcn_readfirstlane((int)s_tile);
     }
-    const int k = ch.ntiles - 1 - kb;
     const int64_t c0 = (int64_t)col * CB, c = c0 + lane * V;
     const bool in = c < D;
-    const int32_t tile0 = k * TILE, t0 = tile0 + w * L;
-
     XR xr[L], dr[L];
     GR gr[L];
-    float a[L][V];
+    const int k = ch.ntiles - 1 - kb;
+    const int32_t t0 = k * TILE + w * L;
+    {
+        const Rows rows(sq, t0, D, c0, lane * V, V);
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-        if (in && t0 + i < sq.T) {
-            const int64_t at = (int64_t)(t0 + i) * D + c;
-            gr[i] = *reinterpret_cast<const GR *>(g + at);
-            xr[i] = *reinterpret_cast<const XR *>(x + at);
-            dr[i] = *reinterpret_cast<const XR *>(dout + at);
-        } else {
-            gr[i] = GR{};
-            xr[i] = XR{};
-            dr[i] = XR{};
+        for (int i = 0; i < L; ++i) {
+            gr[i] = rows.at<GR>(g, i);
+            xr[i] = rows.at<XR>(x, i);
+            dr[i] = rows.at<XR>(dout, i);
         }
     }
+    float a[L][V];
     float h[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) h[j] = (in && k > 0) ? chk[k * D + c + j] : 0.f;
     int32_t first;
-    const Edges e = edges(sq, t0, &first);
+    win.locate(k * TILE);
+    const Edges e = edges(win, t0, tend, &first);
     const uint32_t starts = e.mask & ((1u << L) - 1);
+    bool fresh, resets, unused;         // boundaries behind a token of the tile
+    boundary_in(win, k * TILE + 1, TILE, &resets, &unused);
+    boundary_in(win, (k + 1) * TILE, 1, &fresh, &unused);
+    fresh = fresh || kb == 0;
     if (dinit)
-        empty_seqs(sq, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {
+        empty_seqs(win, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {
             if (in)
                 for (int j = 0; j < V; ++j) dinit[n * D + c + j] = dfin ? dfin[n * D + c + j] : 0.f;
         });
@@ -401,7 +449,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             if (starts >> i & 1) {
-                const int64_t n = init ? sq.owner(t0 + i) : -1;
+                const int64_t n = init ? win.owner(t0 + i) : -1;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     A[j] = RESET;
@@ -423,7 +471,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) {
             if (e.mask >> (i + 1) & 1) {   // the gradient of the final state enters here
-                const int64_t n = dfin ? sq.owner(t0 + i) : -1;
+                const int64_t n = dfin ? win.owner(t0 + i) : -1;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     Ae[j] = RESET;
@@ -440,9 +488,8 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
         for (int j = 0; j < V; ++j) back[WAVES - 1 - w][lane * V + j] = {Ae[j], E[j]};
     }
     const uint32_t ends = e.mask >> 1;
-    const bool fresh = __syncthreads_or(w == WAVES - 1 && (ends >> (L - 1) & 1)) || kb == 0;
-    const bool resets = __syncthreads_or(ends != 0);
-    if (ch.ntiles > 1) pass_on<CB>(ch, kb, c0, fresh, resets, back, groups, enter);
+    __syncthreads();
+    if (ch.ntiles > 1) pass_on<CB>(ch, kb, c0, fresh, resets, back, parts, enter);
 
     // the states again, forward: p_t = a_t h_{t-1}
     float p[L][V], E[V];
@@ -455,7 +502,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
 #pragma unroll
     for (int i = 0; i < L; ++i) {
         if (starts >> i & 1) {
-            const int64_t n = init ? sq.owner(t0 + i) : -1;
+            const int64_t n = init ? win.owner(t0 + i) : -1;
 #pragma unroll
             for (int j = 0; j < V; ++j) h[j] = (n >= 0 && in) ? init[n * D + c + j] : 0.f;
         }
@@ -468,7 +515,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
 #pragma unroll
     for (int i = L - 1; i >= 0; --i) {
         if (ends >> i & 1) {
-            const int64_t n = dfin ? sq.owner(t0 + i) : -1;
+            const int64_t n = dfin ? win.owner(t0 + i) : -1;
 #pragma unroll
             for (int j = 0; j < V; ++j) E[j] = (n >= 0 && in) ? dfin[n * D + c + j] : 0.f;
         }
@@ -483,13 +530,13 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
         }
         if (in && t0 + i < e.end) {
             const int64_t at = (int64_t)(t0 + i) * D + c;
-            *reinterpret_cast<XR *>(dx + at) = ox;
-            *reinterpret_cast<GR *>(dg + at) = og;
-            if (dinit && (starts >> i & 1)) {
-                const int64_t n = sq.owner(t0 + i);
-                if (n >= 0)
-                    for (int j = 0; j < V; ++j) dinit[n * D + c + j] = E[j];
-            }
+            __builtin_nontemporal_store(ox, reinterpret_cast<XR *>(dx + at));
+            __builtin_nontemporal_store(og, reinterpret_cast<GR *>(dg + at));
+        }
+        if (dinit && t0 + i < e.end && (starts >> i & 1)) {
+            const int64_t n = win.owner(t0 + i);
+            if (n >= 0 && in)
+                for (int j = 0; j < V; ++j) dinit[n * D + c + j] = E[j];
         }
     }
 }
@@ -516,10 +563,11 @@ __global__ void kda_scan_fill_kernel(uint64_t *p, int64_t n)
 // ---------------------------------------------------------------- host
 inline int32_t tiles_of(int32_t T) { return T > 0 ? (int32_t)(((int64_t)T + TILE - 1) / TILE) : 1; }
 
-// Words of a chain: counters of up to ceil(D / 64) columns, then the tiles',
-// groups' and super-groups' runs.  A single tile needs none.
+// Words of a chain: counters of up to ceil(D / 64) columns, then the tiles'
+// runs and the states that enter blocks (of 16 tiles at least).  A single tile
+// needs none.
 struct ChainLayout {
-    size_t tile, group, super, words;
+    size_t tile, block, words;
 };
 inline ChainLayout chain_layout(int32_t T, int32_t D)
 {
@@ -527,15 +575,14 @@ inline ChainLayout chain_layout(int32_t T, int32_t D)
     ChainLayout l = {};
     if (nt <= 1) return l;
     l.tile = ((d + 63) / 64 + 1) / 2;
-    l.group = l.tile + nt * d;
-    l.super = l.group + (nt / GROUP + 1) * d;
-    l.words = l.super + (nt / SUPER + 1) * d;
+    l.block = l.tile + nt * d;
+    l.words = l.block + (nt / Roles<256>::BLOCK + 1) * d;
     return l;
 }
 inline Chain chain_at(uint64_t *p, int32_t T, int32_t D)
 {
     const ChainLayout l = chain_layout(T, D);
-    return {reinterpret_cast<uint32_t *>(p), p + l.tile, p + l.group, p + l.super, tiles_of(T), (int64_t)D};
+    return {reinterpret_cast<uint32_t *>(p), p + l.tile, p + l.block, tiles_of(T), (int64_t)D};
 }
 
 inline hipError_t fill_chain(uint64_t *p, size_t words, hipStream_t s)
@@ -564,9 +611,12 @@ hipError_t scan(const void *x, const float *g, const float *init, const Seqs &sq
                 float *chk, const Chain &ch, hipStream_t s)
 {
     const size_t e = sizeof(T);
-    constexpr int V = 2;
-    if (D % V == 0 && fits(x, V * e) && fits(out, V * e) && fits(g, V * 4))
-        return run_scan<T, V>(x, g, init, sq, D, out, fin, chk, ch, s);
+    // Wide rows for bf16 where they leave two workgroups for every CU; fp32
+    // tokens of four channels a lane would not fit the registers.
+    auto aligned = [&](int V) { return D % V == 0 && fits(x, V * e) && fits(out, V * e) && fits(g, V * 4); };
+    if (sizeof(T) == 2 && aligned(4) && (int64_t)ch.ntiles * ((D + 255) / 256) >= 512)
+        return run_scan<T, sizeof(T) == 2 ? 4 : 2>(x, g, init, sq, D, out, fin, chk, ch, s);
+    if (aligned(2)) return run_scan<T, 2>(x, g, init, sq, D, out, fin, chk, ch, s);
     return run_scan<T, 1>(x, g, init, sq, D, out, fin, chk, ch, s);
 }
 

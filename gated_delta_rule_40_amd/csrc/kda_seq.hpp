@@ -29,4 +29,50 @@ struct Seqs {
     }
 };
 
+// The same lookups for a wave around one place, from entries held a lane each:
+// one read where there are at most 64 entries (it does not depend on the
+// place), a few for more, against a chain of dependent reads for a binary search.
+// All arguments are uniform over the wave, and all 64 lanes have to be active.
+struct SeqWindow {
+    Seqs sq;
+    int32_t base, stride, entry;   // lane l holds entry base + l * stride
+
+    __device__ __forceinline__ explicit SeqWindow(const Seqs &s) : sq(s), base(0), stride((s.N + 64) / 64) { read(); }
+    // lanes past the last entry hold a value above every token
+    __device__ __forceinline__ void read() {
+        const int64_t n = base + (int64_t)(threadIdx.x & 63) * stride;
+        entry = n <= sq.N ? sq.at((int32_t)n) : INT32_MAX;
+    }
+    __device__ __forceinline__ int below(int32_t t) const { return __popcll(__ballot(entry < t)); }
+    // brings in the 64 entries from the first one >= t on
+    __device__ __forceinline__ void locate(int32_t t) {
+        if (sq.N < 64) return;     // they are here already
+        while (stride > 1) {
+            const int n = below(t);
+            if (n > 0) base += (n - 1) * stride + 1;   // behind the last sample below t
+            stride = n > 0 ? (stride + 62) / 64 : 1;   // the stride - 1 entries up to the next sample
+            if (stride < 1) stride = 1;
+            read();
+        }
+        const int n = below(t);
+        if (n > 0) {
+            base += n;
+            read();
+        }
+    }
+    __device__ __forceinline__ int32_t at(int32_t n) const {
+        const int32_t i = n - base;
+        return (i >= 0 && i < 64 && stride == 1) ? __builtin_amdgcn_readlane(entry, i) : sq.at(n);
+    }
+    // as Seqs', for t >= the place located
+    __device__ __forceinline__ int32_t first_at_or_after(int32_t t) const {
+        const int n = below(t);
+        return n < 64 ? min(base + n, sq.N + 1) : sq.first_at_or_after(t);
+    }
+    __device__ __forceinline__ int32_t owner(int32_t t) const {
+        const int32_t n = first_at_or_after(t + 1) - 1;
+        return (n >= 0 && n < sq.N) ? n : -1;
+    }
+};
+
 }  // namespace kda

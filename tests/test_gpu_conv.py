@@ -88,6 +88,24 @@ def test_backward(lens, D, W, dtype, silu, init, bias):
         R.close(host(grads["dinit"]), g["dinit"], g["e_dinit"], dtype, "dinit")
 
 
+@pytest.mark.parametrize("N,most", [(63, 9), (64, 9), (65, 90), (700, 8), (4100, 3)])
+def test_many_sequences(N, most):
+    # more entries of cu_seqlens than a wave holds at once, empty sequences among them
+    lens = np.random.default_rng(N).integers(0, most, N).tolist() + [0] * 70 + [3]
+    h, d = make(lens, 8, 4, "fp32", tail=1, seed=6)
+    T = sum(lens)
+    out, fin = torch.full_like(d["x"], 77.0), torch.full_like(d["init"], 77.0)
+    K.kda_conv_prefill(d["x"], d["w"], d["b"], d["init"], d["cu"], out, fin)
+    g = K.kda_conv_backward(d["x"], d["w"], d["b"], d["init"], d["cu"], d["dout"], d["dfinal"])
+    r = R.conv_backward(h["x"][:T], h["w"], h["b"], h["init"], h["cu"], True, h["dout"][:T], h["dfinal"])
+    R.close(host(out)[:T], r["fwd"]["out"], r["fwd"]["e_out"], "fp32", "out")
+    assert np.array_equal(host(fin), r["fwd"]["final"]) and float(out[T:].min()) == 77.0
+    R.close(host(g["dx"])[:T], r["dx"], r["e_dx"], "fp32", "dx")
+    R.close(host(g["dweight"]), r["dweight"], r["e_dweight"], "fp32", "dweight")
+    R.close(host(g["dbias"]), r["dbias"], r["e_dbias"], "fp32", "dbias")
+    R.close(host(g["dinit"]), r["dinit"], r["e_dinit"], "fp32", "dinit")
+
+
 @pytest.mark.parametrize("N,D", [(1, 1), (3, 5), (8, 512), (65, 999)])
 @pytest.mark.parametrize("W", [2, 3, 4])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])

@@ -101,6 +101,24 @@ def test_backward(lens, D, dtype, init, checkpoints):
         R.close(host(grads["dinit"]), b["dinit"], b["e_dinit"], "fp32", "dinit")
 
 
+@pytest.mark.parametrize("N,most", [(63, 9), (64, 9), (65, 400), (700, 20), (4100, 3), (9000, 2)])
+def test_many_sequences(N, most):
+    # more entries of cu_seqlens than a wave holds at once, empty sequences among them
+    lens = np.random.default_rng(N).integers(0, most, N).tolist() + [0] * 70 + [3]
+    h, d = make(lens, 6, "fp32", tail=1, seed=11)
+    T = sum(lens)
+    out, fin = torch.full_like(d["x"], 77.0), torch.full_like(d["init"], 77.0)
+    K.kda_scan_prefill(d["x"], d["g"], d["init"], d["cu"], out, fin)
+    b = R.scan_backward(h["x"], h["g"], h["init"], h["cu"], h["dout"], h["dfinal"])
+    R.close(host(out)[:T], b["fwd"]["h"][:T], b["fwd"]["e_h"][:T], "fp32", "out")
+    R.close(host(fin), b["fwd"]["final"], b["fwd"]["e_final"], "fp32", "final")
+    g = K.kda_scan_backward(d["x"], d["g"], d["init"], d["cu"], d["dout"], d["dfinal"])
+    R.close(host(g["dx"])[:T], b["dx"][:T], b["e_dx"][:T], "fp32", "dx")
+    R.close(host(g["dg"])[:T], b["dg"][:T], b["e_dg"][:T], "fp32", "dg")
+    R.close(host(g["dinit"]), b["dinit"], b["e_dinit"], "fp32", "dinit")
+    assert float(out[T:].min()) == 77.0
+
+
 @pytest.mark.parametrize("N,D", [(1, 1), (1, 64), (3, 5), (8, 2048), (513, 999)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_decode(N, D, dtype):
