@@ -29,24 +29,30 @@ struct ConvArgs {
     bool silu;
 };
 
-// VW consecutive elements, moved as one access
+// V consecutive channels of a row, as held and as they lie in memory
 template <typename T, int V> struct Row {
     typedef T raw __attribute__((ext_vector_type(V)));
+    typedef raw mem __attribute__((aligned(sizeof(T))));
     __device__ static __forceinline__ float at(const raw &r, int j) { return to_f(r[j]); }
     __device__ static __forceinline__ void set(raw &r, int j, float v) { r[j] = from_f<T>(v); }
 };
 template <typename T> struct Row<T, 1> {
-    typedef T raw;
+    typedef T raw, mem;
     __device__ static __forceinline__ float at(const raw &r, int) { return to_f(r); }
     __device__ static __forceinline__ void set(raw &r, int, float v) { r = from_f<T>(v); }
 };
 template <typename T, int V> __device__ __forceinline__ typename Row<T, V>::raw load_row(const T *p)
 {
-    return *reinterpret_cast<const typename Row<T, V>::raw *>(p);
+    return *reinterpret_cast<const typename Row<T, V>::mem *>(p);
 }
 template <typename T, int V> __device__ __forceinline__ void store_row(T *p, const typename Row<T, V>::raw &r)
 {
-    *reinterpret_cast<typename Row<T, V>::raw *>(p) = r;
+    *reinterpret_cast<typename Row<T, V>::mem *>(p) = r;
+}
+// outputs are not read here again: past the caches
+template <typename T, int V> __device__ __forceinline__ void write_once(T *p, const typename Row<T, V>::raw &r)
+{
+    __builtin_nontemporal_store(r, reinterpret_cast<typename Row<T, V>::mem *>(p));
 }
 
 // 1 / (1 + exp(-p)): exp within |p| + 2 units in the last place, the quotient
@@ -85,47 +91,38 @@ __device__ __forceinline__ typename Row<T, V>::raw row_before(const T *x, const 
 
 // ---------------------------------------------------------------- forward
 template <typename T, int W, int V>
-__global__ __launch_bounds__(256) void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip,
-                                                       int32_t nstrips, T *out, T *fin)
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4)))
+void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip, int32_t nstrips, int32_t cols,
+                     T *out, T *fin)
 {
     typedef typename Row<T, V>::raw R;
-    constexpr int BATCH = 8;
+    constexpr int BATCH = 4;
     const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int32_t k = blockIdx.x * 4 + wave;
-    const int64_t c = ((int64_t)blockIdx.y * 64 + (threadIdx.x & 63)) * V;
-    if (k >= nstrips || c >= a.D) return;
+    const int32_t k = (int32_t)(blockIdx.x / cols) * 4 + wave;
+    const int64_t c0 = (int64_t)(blockIdx.x % cols) * 64 * V;
+    const int64_t c = min(c0 + (int64_t)(threadIdx.x & 63) * V, a.D - V);
+    if (k >= nstrips) return;
+    SeqWindow win(sq);
     const int32_t t0 = k * strip, t1 = (int32_t)min((int64_t)t0 + strip, (int64_t)sq.T);
     const int32_t tend = sq.at(sq.N);
     Weights<W, V> wt;
     wt.load(a, c);
-
-    // the final states of the sequences that begin here, after the walk has read the initial ones
-    auto finals = [&]() {
-        for (int32_t n = sq.first_at_or_after(t0); n < sq.N; ++n) {
-            const int32_t s = sq.at(n), e = max(sq.at(n + 1), s);
-            if (s >= t1 && k < nstrips - 1) break;
-            R r[W - 1];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) r[j] = row_before<T, W, V>(x, init, a, c, n, s, e, W - 1 - j);
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) store_row<T, V>(fin + ((int64_t)n * (W - 1) + j) * a.D + c, r[j]);
-        }
-    };
+    win.locate(t0);
 
     if (t0 < tend) {
-        int32_t n = sq.owner(t0);
+        int32_t n = win.owner(t0);
         if (n < 0) return;                     // (cu_seqlens against its rules)
-        int32_t s = sq.at(n), next = max(sq.at(n + 1), t0 + 1), t = t0;
+        int32_t s = win.at(n), next = max(win.at(n + 1), t0 + 1), t = t0;
         // tokens that belong to the wave of their sequence's start
         if (s < t0 && t0 - s < W - 1) t = min(s + W - 1, next);
         const int32_t stop = min(t1, tend);
-        R win[W - 1];
+        R before[W - 1];
         auto enter = [&]() {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) win[j] = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
+            for (int j = 0; j < W - 1; ++j) before[j] = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
         };
-        auto advance = [&]() {                 // to the sequence that owns token t, its start
-            while (n < sq.N - 1 && next <= t) next = sq.at(++n + 1);
+        auto advance = [&]() {                 // to the sequence that begins at token t
+            while (n < sq.N - 1 && next <= t) next = win.at(++n + 1);
             s = t;
         };
         auto token = [&](const R &r) {
@@ -134,86 +131,105 @@ __global__ __launch_bounds__(256) void kda_conv_kernel(const T *x, const T *init
             for (int v = 0; v < V; ++v) {
                 float p = wt.b[v];
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) p += wt.w[j][v] * Row<T, V>::at(win[j], v);
+                for (int j = 0; j < W - 1; ++j) p += wt.w[j][v] * Row<T, V>::at(before[j], v);
                 p += wt.w[W - 1][v] * Row<T, V>::at(r, v);
                 Row<T, V>::set(o, v, a.silu ? silu_f(p) : p);
             }
-            store_row<T, V>(out + (int64_t)t * a.D + c, o);
+            write_once<T, V>(out + (int64_t)t * a.D + c, o);
 #pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
-            win[W - 2] = r;
+            for (int j = 0; j + 1 < W - 1; ++j) before[j] = before[j + 1];
+            before[W - 2] = r;
+            ++t;
+        };
+        auto read = [&](R (&rows)[BATCH], int32_t from) {
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) rows[i] = load_row<T, V>(x + (int64_t)min(from + i, stop - 1) * a.D + c);
         };
         if (t < stop) {
             if (t == next) advance();
+            R rows[BATCH], ahead[BATCH];
+            read(rows, t);
             enter();
-        }
-        while (t < stop) {
-            const int32_t m = min(stop - t, BATCH);
-            R rows[BATCH];
+            while (t < stop) {
+                read(ahead, t + BATCH);
+                if (stop - t >= BATCH && next >= t + BATCH) {
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) rows[i] = load_row<T, V>(x + (int64_t)min(t + i, stop - 1) * a.D + c);
-            if (m == BATCH && next >= t + BATCH) {
+                    for (int i = 0; i < BATCH; ++i) token(rows[i]);
+                    if (t == next && t < stop) {
+                        advance();
+                        enter();
+                    }
+                } else {
+                    const int32_t m = min(stop - t, BATCH);
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    token(rows[i]);
-                    ++t;
-                }
-                if (t < stop && t == next) {
-                    advance();
-                    enter();
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    if (i < m) {
-                        token(rows[i]);
-                        ++t;
-                        if (t < stop && t == next) {
-                            advance();
-                            enter();
+                    for (int i = 0; i < BATCH; ++i) {
+                        if (i < m) {
+                            token(rows[i]);
+                            if (t == next && t < stop) {
+                                advance();
+                                enter();
+                            }
                         }
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) rows[i] = ahead[i];
             }
         }
         // the first W - 1 tokens of the last sequence that begins here, beyond the strip
         if (s >= t0 && t > s && t >= t1) {
             const int32_t most = min(min(s + W - 1, next), tend);
-            while (t < most) {
-                token(load_row<T, V>(x + (int64_t)t * a.D + c));
-                ++t;
-            }
+            while (t < most) token(load_row<T, V>(x + (int64_t)t * a.D + c));
         }
     }
-    if (fin) finals();
+    // the final states of the sequences that begin here, after the walk has read the initial ones
+    if (fin)
+        for (int32_t n = win.first_at_or_after(t0); n < sq.N; ++n) {
+            const int32_t s = win.at(n), e = max(win.at(n + 1), s);
+            if (s >= t1 && k < nstrips - 1) break;
+            R r[W - 1];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) r[j] = row_before<T, W, V>(x, init, a, c, n, s, e, W - 1 - j);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) store_row<T, V>(fin + ((int64_t)n * (W - 1) + j) * a.D + c, r[j]);
+        }
 }
 
 // ---------------------------------------------------------------- decode
-template <typename T, int W, int V>
-__global__ __launch_bounds__(256) void kda_conv_step_kernel(const T *x, T *state, ConvArgs a, int32_t N, int32_t per,
+// A thread takes PER sequences of its channels with one reading of the weights,
+// all their rows read before any is used.
+template <typename T, int W, int V, int PER>
+__global__ __launch_bounds__(256) void kda_conv_step_kernel(const T *x, T *state, ConvArgs a, int32_t N, int32_t cols,
                                                             T *out)
 {
     typedef typename Row<T, V>::raw R;
-    const int64_t c = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V;
+    const int64_t c = ((int64_t)(blockIdx.x % cols) * blockDim.x + threadIdx.x) * V;
     if (c >= a.D) return;
+    const int64_t n0 = (int64_t)(blockIdx.x / cols) * PER;
+    R r[PER][W];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int64_t n = min(n0 + i, (int64_t)N - 1);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) r[i][j] = load_row<T, V>(state + (n * (W - 1) + j) * a.D + c);
+        r[i][W - 1] = load_row<T, V>(x + n * a.D + c);
+    }
     Weights<W, V> wt;
     wt.load(a, c);
-    const int32_t n1 = min(N, (int32_t)(blockIdx.y + 1) * per);
-    for (int32_t n = blockIdx.y * per; n < n1; ++n) {
-        T *st = state + (int64_t)n * (W - 1) * a.D + c;
-        R r[W], o;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) r[j] = load_row<T, V>(st + j * a.D);
-        r[W - 1] = load_row<T, V>(x + n * a.D + c);
+    for (int i = 0; i < PER; ++i) {
+        const int64_t n = n0 + i;
+        if (n >= N) break;
+        R o;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float p = wt.b[v];
 #pragma unroll
-            for (int j = 0; j < W; ++j) p += wt.w[j][v] * Row<T, V>::at(r[j], v);
+            for (int j = 0; j < W; ++j) p += wt.w[j][v] * Row<T, V>::at(r[i][j], v);
             Row<T, V>::set(o, v, a.silu ? silu_f(p) : p);
         }
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) store_row<T, V>(st + j * a.D, r[j + 1]);
+        for (int j = 0; j < W - 1; ++j) store_row<T, V>(state + (n * (W - 1) + j) * a.D + c, r[i][j + 1]);
         store_row<T, V>(out + n * a.D + c, o);
     }
 }
@@ -226,22 +242,23 @@ __global__ __launch_bounds__(256) void kda_conv_step_kernel(const T *x, T *state
 // initial states of the sequences that begin in it, by walking W - 1 tokens
 // beyond the strip; only its own tokens count for dw and dbias.
 template <typename T, int W, int V>
-__global__ __launch_bounds__(256) void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq,
-                                                           int32_t strip, int32_t nstrips, const T *dout,
-                                                           const T *dfin, T *dx, T *dinit, float *partial)
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4)))
+void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip, int32_t nstrips, int32_t cols,
+                         const T *dout, const T *dfin, T *dx, T *dinit, float *partial)
 {
     typedef typename Row<T, V>::raw R;
     constexpr int BATCH = 4;
     __shared__ float sums[4][W + 1][64 * V];
     const int32_t lane = threadIdx.x & 63;
     const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int32_t k = blockIdx.x * 4 + wave;
-    const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * V;
-    const bool live = k < nstrips && c < a.D;
+    const int32_t part = blockIdx.x / cols, k = part * 4 + wave;
+    const int64_t c0 = (int64_t)(blockIdx.x % cols) * 64 * V, c = min(c0 + lane * V, a.D - V);
     float dw[W][V] = {}, db[V] = {};
-    if (live) {
+    if (k < nstrips) {
+        SeqWindow win(sq);
         const int32_t t0 = (int32_t)min((int64_t)k * strip, (int64_t)sq.T);
         const int32_t t1 = (int32_t)min((int64_t)t0 + strip, (int64_t)sq.T), tend = sq.at(sq.N);
+        win.locate(t0);
         auto put_dinit = [&](int32_t n, int j, const float (&v)[V]) {
             R r;
 #pragma unroll
@@ -252,23 +269,23 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(const T *x, const T *
             return dfin ? load_row<T, V>(dfin + ((int64_t)n * (W - 1) + j) * a.D + c) : R{};
         };
         if (dinit)   // empty sequences
-            for (int32_t n = sq.first_at_or_after(t0); n < sq.N; ++n) {
-                const int32_t s = sq.at(n);
+            for (int32_t n = win.first_at_or_after(t0); n < sq.N; ++n) {
+                const int32_t s = win.at(n);
                 if (s >= t1 && k < nstrips - 1) break;
-                if (sq.at(n + 1) <= s)
+                if (win.at(n + 1) <= s)
                     for (int j = 0; j < W - 1; ++j)
                         store_row<T, V>(dinit + ((int64_t)n * (W - 1) + j) * a.D + c, get_dfin(n, j));
             }
-        int32_t n = t0 < min(tend, t1) ? sq.owner(t0) : -1;
+        int32_t n = t0 < min(tend, t1) ? win.owner(t0) : -1;
         if (n >= 0) {
             Weights<W, V> wt;
             wt.load(a, c);
-            int32_t s = sq.at(n), next = max(sq.at(n + 1), t0 + 1), t = t0;
-            R win[W - 1];
+            int32_t s = win.at(n), next = max(win.at(n + 1), t0 + 1), t = t0;
+            R before[W - 1];
             float acc[W - 1][V] = {};
             auto enter = [&]() {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) win[j] = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
+                for (int j = 0; j < W - 1; ++j) before[j] = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
             };
             // place p of the sequence (p < 0: of its initial state) is finished
             auto finish = [&](int32_t p, const float (&v)[V]) {
@@ -277,12 +294,11 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(const T *x, const T *
                     R r;
 #pragma unroll
                     for (int i = 0; i < V; ++i) Row<T, V>::set(r, i, v[i]);
-                    store_row<T, V>(dx + (int64_t)(s + p) * a.D + c, r);
+                    write_once<T, V>(dx + (int64_t)(s + p) * a.D + c, r);
                 } else if (dinit && s >= t0 && s < t1) {
                     put_dinit(n, p + W - 1, v);
                 }
             };
-            enter();
             const int32_t stop = (int32_t)min((int64_t)t1 + W - 1, (int64_t)tend);
             auto token = [&](const R &r, const R &d) {
                 float done[V];
@@ -291,7 +307,7 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(const T *x, const T *
                 for (int v = 0; v < V; ++v) {
                     float p = wt.b[v], in[W];
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) in[j] = Row<T, V>::at(win[j], v);
+                    for (int j = 0; j < W - 1; ++j) in[j] = Row<T, V>::at(before[j], v);
                     in[W - 1] = Row<T, V>::at(r, v);
 #pragma unroll
                     for (int j = 0; j < W; ++j) p += wt.w[j][v] * in[j];
@@ -309,8 +325,8 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(const T *x, const T *
                 }
                 finish(t - s - (W - 1), done);
 #pragma unroll
-                for (int j = 0; j + 1 < W - 1; ++j) win[j] = win[j + 1];
-                win[W - 2] = r;
+                for (int j = 0; j + 1 < W - 1; ++j) before[j] = before[j + 1];
+                before[W - 2] = r;
                 ++t;
             };
             // the sequence ends before token t: its unfinished places, then the next sequence
@@ -324,19 +340,24 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(const T *x, const T *
 #pragma unroll
                     for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
                 }
-                while (n < sq.N - 1 && next <= t) next = sq.at(++n + 1);
+                while (n < sq.N - 1 && next <= t) next = win.at(++n + 1);
                 s = t;
             };
-            while (t < stop) {
-                const int32_t m = min(stop - t, BATCH);
-                R xr[BATCH], dr[BATCH];
+            R xr[BATCH], dr[BATCH], xa[BATCH], da[BATCH];
+            auto read = [&](R (&xs)[BATCH], R (&ds)[BATCH], int32_t from) {
 #pragma unroll
                 for (int i = 0; i < BATCH; ++i) {
-                    const int64_t at = (int64_t)min(t + i, stop - 1) * a.D + c;
-                    xr[i] = load_row<T, V>(x + at);
-                    dr[i] = load_row<T, V>(dout + at);
+                    const int64_t at = (int64_t)min(from + i, stop - 1) * a.D + c;
+                    xs[i] = load_row<T, V>(x + at);
+                    ds[i] = load_row<T, V>(dout + at);
                 }
-                bool over = false;
+            };
+            read(xr, dr, t);
+            enter();
+            bool over = false;
+            while (t < stop && !over) {
+                read(xa, da, t + BATCH);
+                const int32_t m = min(stop - t, BATCH);
 #pragma unroll
                 for (int i = 0; i < BATCH; ++i) {
                     if (i < m && !over) {
@@ -348,23 +369,25 @@ __global__ __launch_bounds__(256) void kda_conv_bwd_kernel(const T *x, const T *
                         }
                     }
                 }
-                if (over) break;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) xr[i] = xa[i], dr[i] = da[i];
             }
         }
     }
     // the four waves' sums, in order, as the workgroup's part
+    // (a lane whose channels overlap its neighbour's writes the same values there)
+    const int place = (int)(c - c0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        sums[wave][W][lane * V + v] = db[v];
+        sums[wave][W][place + v] = db[v];
 #pragma unroll
-        for (int j = 0; j < W; ++j) sums[wave][j][lane * V + v] = dw[j][v];
+        for (int j = 0; j < W; ++j) sums[wave][j][place + v] = dw[j][v];
     }
     __syncthreads();
-    const int64_t first = (int64_t)blockIdx.y * 64 * V;
     for (int i = threadIdx.x; i < (W + 1) * 64 * V; i += 256) {
         const int j = i / (64 * V), cc = i % (64 * V);
         const float total = ((sums[0][j][cc] + sums[1][j][cc]) + sums[2][j][cc]) + sums[3][j][cc];
-        if (first + cc < a.D) partial[((int64_t)blockIdx.x * (W + 1) + j) * a.D + first + cc] = total;
+        if (c0 + cc < a.D) partial[((int64_t)part * (W + 1) + j) * a.D + c0 + cc] = total;
     }
 }
 
@@ -391,7 +414,6 @@ __global__ __launch_bounds__(1024) void kda_conv_sums_kernel(const float *src, i
 }
 
 // ---------------------------------------------------------------- host
-inline bool wide(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 inline int64_t up(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
 constexpr int32_t BWD_PARTS = 512;    // workgroups along the tokens, at most
@@ -412,8 +434,8 @@ hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Se
     // strips of 64 tokens where these give every SIMD its waves, shorter ones otherwise
     const int32_t strip = up(sq.T, 64) * cols >= 4096 ? 64 : 16;
     const int32_t nstrips = (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1);
-    hipLaunchKernelGGL((kda_conv_kernel<T, W, V>), dim3((unsigned)up(nstrips, 4), (unsigned)cols), dim3(256), 0, s,
-                       (const T *)x, (const T *)init, a, sq, strip, nstrips, (T *)out, (T *)fin);
+    hipLaunchKernelGGL((kda_conv_kernel<T, W, V>), dim3((unsigned)(up(nstrips, 4) * cols)), dim3(256), 0, s,
+                       (const T *)x, (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (T *)out, (T *)fin);
     return hipGetLastError();
 }
 
@@ -421,9 +443,12 @@ template <typename T, int W, int V>
 hipError_t run_conv_step(const void *x, const ConvArgs &a, void *state, int32_t N, void *out, hipStream_t s)
 {
     const int64_t cols = up(a.D, 256 * V);
-    const int32_t per = N * cols >= 4096 ? 4 : 1;   // sequences a thread takes with one reading of the weights
-    hipLaunchKernelGGL((kda_conv_step_kernel<T, W, V>), dim3((unsigned)cols, (unsigned)up(N, per)), dim3(256), 0, s,
-                       (const T *)x, (T *)state, a, N, per, (T *)out);
+    if (N * cols >= 2048)
+        hipLaunchKernelGGL((kda_conv_step_kernel<T, W, V, 4>), dim3((unsigned)(cols * up(N, 4))), dim3(256), 0, s,
+                           (const T *)x, (T *)state, a, N, (int32_t)cols, (T *)out);
+    else
+        hipLaunchKernelGGL((kda_conv_step_kernel<T, W, V, 1>), dim3((unsigned)(cols * N)), dim3(256), 0, s,
+                           (const T *)x, (T *)state, a, N, (int32_t)cols, (T *)out);
     return hipGetLastError();
 }
 
@@ -433,11 +458,11 @@ hipError_t run_conv_backward(const void *x, const ConvArgs &a, const void *init,
                              hipStream_t s)
 {
     const int32_t strip = bwd_strip(sq.T), parts = sq.N > 0 ? bwd_parts(sq.T) : 0;
+    const int64_t cols = up(a.D, 64 * V);
     if (parts > 0)
-        hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V>), dim3((unsigned)parts, (unsigned)up(a.D, 64 * V)), dim3(256),
-                           0, s, (const T *)x, (const T *)init, a, sq, strip,
-                           (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1), (const T *)dout, (const T *)dfin, (T *)dx,
-                           (T *)dinit, (float *)ws);
+        hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V>), dim3((unsigned)(parts * cols)), dim3(256), 0, s,
+                           (const T *)x, (const T *)init, a, sq, strip, (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1),
+                           (int32_t)cols, (const T *)dout, (const T *)dfin, (T *)dx, (T *)dinit, (float *)ws);
     hipLaunchKernelGGL(kda_conv_sums_kernel<W>, dim3((unsigned)up((W + 1) * a.D, 32)), dim3(1024), 0, s,
                        (const float *)ws, parts, a.D, dw, dbias);
     return hipGetLastError();
@@ -453,14 +478,17 @@ template <int V, typename F> hipError_t with_width(int32_t width, F f)
     }
 }
 
+// whether V channels a lane leave no lane that overlaps one of another wave
+// (two waves must not share a state)
+inline bool whole(int64_t D, int V) { return D % (64 * V) == 0 || D % (64 * V) >= V; }
+
 template <typename T>
 hipError_t conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, int32_t width, void *out, void *fin,
                 hipStream_t s)
 {
     constexpr int V = 16 / sizeof(T);
     auto f = [&](auto w, auto v) { return run_conv<T, w(), v()>(x, a, init, sq, out, fin, s); };
-    return a.D % V == 0 && wide(x, 16) && wide(init, 16) && wide(out, 16) && wide(fin, 16) ? with_width<V>(width, f)
-                                                                                           : with_width<1>(width, f);
+    return whole(a.D, V) ? with_width<V>(width, f) : with_width<1>(width, f);
 }
 
 template <typename T>
@@ -468,8 +496,7 @@ hipError_t conv_step(const void *x, const ConvArgs &a, void *state, int32_t N, i
 {
     constexpr int V = 16 / sizeof(T);
     auto f = [&](auto w, auto v) { return run_conv_step<T, w(), v()>(x, a, state, N, out, s); };
-    return a.D % V == 0 && wide(x, 16) && wide(state, 16) && wide(out, 16) ? with_width<V>(width, f)
-                                                                           : with_width<1>(width, f);
+    return a.D % V == 0 ? with_width<V>(width, f) : with_width<1>(width, f);
 }
 
 template <typename T>
@@ -478,14 +505,10 @@ hipError_t conv_backward(const void *x, const ConvArgs &a, const void *init, con
                          hipStream_t s)
 {
     constexpr int V = 4;   // (eight channels' sums and unfinished places would not fit the registers)
-    constexpr size_t B = V * sizeof(T);
     auto f = [&](auto w, auto v) {
         return run_conv_backward<T, w(), v()>(x, a, init, sq, dout, dfin, dx, dw, dbias, dinit, ws, s);
     };
-    return a.D % V == 0 && wide(x, B) && wide(init, B) && wide(dout, B) && wide(dfin, B) && wide(dx, B) &&
-                   wide(dinit, B)
-               ? with_width<V>(width, f)
-               : with_width<1>(width, f);
+    return whole(a.D, V) ? with_width<V>(width, f) : with_width<1>(width, f);
 }
 
 }  // namespace kda

@@ -107,16 +107,16 @@ template <int CB> struct Roles {
 // `runs` holds the waves' runs in the order of the walk.  `fresh`: nothing
 // enters (the tile begins at a boundary); `resets`: it has a boundary.  Begins
 // after a barrier and ends with one.
-template <int CB>
+template <int CB, int V>
 __device__ __forceinline__ void pass_on(const Chain &ch, int k, int64_t c0, bool fresh, bool resets,
                                         const Run (*runs)[CB], Run (*parts)[CB], float *enter)
 {
     constexpr int N = Roles<CB>::N, BLOCK = Roles<CB>::BLOCK;
     const int c = threadIdx.x % CB, role = threadIdx.x / CB;
-    const bool in = c0 + c < ch.D;
+    const bool in = c0 + c / V * V < ch.D;
     const int place = k % BLOCK, block = k / BLOCK;   // the tile's place in its block
     const bool last = place == BLOCK - 1;
-    const int64_t ci = c0 + c;
+    const int64_t ci = min(c0 + c / V * V, ch.D - V) + c % V;
     Run own = {1.f, 0.f};
     uint64_t before = 0;
     if (role == 0 && in) {
@@ -147,13 +147,24 @@ __device__ __forceinline__ void pass_on(const Chain &ch, int k, int64_t c0, bool
 }
 
 // ---------------------------------------------------------------- tokens in registers
-template <typename T, int V> struct Vec;
-template <> struct Vec<float, 4> { typedef f32x4 raw; };
-template <> struct Vec<float, 2> { typedef f32x2 raw; };
-template <> struct Vec<float, 1> { typedef float raw; };
-template <> struct Vec<bf16_t, 4> { typedef bf16x4 raw; };
-template <> struct Vec<bf16_t, 2> { typedef bf16x2 raw; };
-template <> struct Vec<bf16_t, 1> { typedef bf16_t raw; };
+// V consecutive channels of a row.  In memory they need the alignment of one:
+// rows of a channel count that V does not divide begin anywhere, and the last
+// lane's channels overlap its neighbour's (both compute the same).
+template <typename T, int V> struct Vec {
+    typedef T raw __attribute__((ext_vector_type(V)));
+    typedef raw mem __attribute__((aligned(sizeof(T))));
+};
+template <typename T> struct Vec<T, 1> {
+    typedef T raw, mem;
+};
+template <typename T, int V> __device__ __forceinline__ typename Vec<T, V>::raw read_once(const T *p)
+{
+    return __builtin_nontemporal_load(reinterpret_cast<const typename Vec<T, V>::mem *>(p));
+}
+template <typename T, int V> __device__ __forceinline__ void write_once(T *p, const typename Vec<T, V>::raw &v)
+{
+    __builtin_nontemporal_store(v, reinterpret_cast<typename Vec<T, V>::mem *>(p));
+}
 
 template <typename R> __device__ __forceinline__ float elem(const R &r, int j) { return to_f(r[j]); }
 template <> __device__ __forceinline__ float elem<float>(const float &r, int) { return r; }
@@ -176,20 +187,19 @@ __device__ __forceinline__ float gate(float g)
 }
 
 // A wave's rows: scalar addresses, and a lane's place in a row of its own.
-// Rows past the last token stand for the last one, lanes past the last channel
-// for the last channels.  Without tokens nothing may be read.
-struct Rows {
+// Rows past the last token stand for the last one.
+template <int V> struct Rows {
     int64_t first, D;
     int32_t last;
-    uint32_t lane;
-    __device__ __forceinline__ Rows(const Seqs &sq, int32_t t0, int64_t D_, int64_t c0, int l, int V) : D(D_) {
+    int32_t lane;
+    __device__ __forceinline__ Rows(const Seqs &sq, int32_t t0, int64_t D_, int64_t c0, int32_t lane_) : D(D_) {
         const int32_t t = min(t0, sq.T - 1);
         first = t * D + c0;
         last = sq.T - 1 - t;
-        lane = (uint32_t)min((int64_t)l, D - V - c0);
+        lane = lane_;
     }
-    template <typename R, typename T> __device__ __forceinline__ R at(const T *p, int i) const {
-        return __builtin_nontemporal_load(reinterpret_cast<const R *>(p + first + min(i, last) * D + lane));
+    template <typename T> __device__ __forceinline__ typename Vec<T, V>::raw at(const T *p, int i) const {
+        return read_once<T, V>(p + first + min(i, last) * D + lane);
     }
 };
 
@@ -198,21 +208,27 @@ struct Rows {
 template <typename R> __device__ __forceinline__ void repack(R &r) { asm volatile("" : "+v"(r)); }
 
 // Boundaries of sequences at a wave's tokens: bit i stands for token t0 + i,
-// i = 0 .. L.  `end` is the first token of no sequence.
+// i = 0 .. L; lane i holds the number of the sequence that owns the token
+// (outside [0, N): none).  `end` is the first token of no sequence.
 struct Edges {
     uint32_t mask;
-    int32_t end;
+    int32_t end, own;
+    __device__ __forceinline__ int32_t owner(int i, int32_t N) const {
+        const int32_t n = __builtin_amdgcn_readlane(own, i);
+        return n < N ? n : -1;
+    }
 };
 
 __device__ __forceinline__ Edges edges(const SeqWindow &sq, int32_t t0, int32_t end, int32_t *first)
 {
-    Edges e = {0, end};
     int32_t n = sq.first_at_or_after(t0);
     *first = n;
+    Edges e = {0, end, n - 1};
     for (; n <= sq.sq.N; ++n) {
         const int32_t p = sq.at(n);
         if (p > t0 + L || p < t0) break;
         e.mask |= 1u << (p - t0);
+        e.own += (int32_t)(threadIdx.x & 63) >= p - t0;
     }
     return e;
 }
@@ -269,17 +285,17 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
         __syncthreads();
         k = __builtin_amdgcn_readfirstlane((int)s_tile);
     }
-    const int64_t c0 = (int64_t)col * CB, c = c0 + lane * V;
-    const bool in = c < D;
+    const int64_t c0 = (int64_t)col * CB, c = min(c0 + lane * V, D - V);
+    const bool in = c0 + lane * V < D;
     XR xr[L];
     GR gr[L];
     const int32_t t0 = k * TILE + w * L;
     {
-        const Rows rows(sq, t0, D, c0, lane * V, V);
+        const Rows<V> rows(sq, t0, D, c0, (int32_t)(c - c0));
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            xr[i] = rows.at<XR>(x, i);
-            gr[i] = rows.at<GR>(g, i);
+            xr[i] = rows.at(x, i);
+            gr[i] = rows.at(g, i);
         }
     }
     int32_t first;
@@ -300,10 +316,10 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
         if (out && in) {
             XR o;
             for (int j = 0; j < V; ++j) put(o, j, from_f<T>(h[j]));
-            *reinterpret_cast<XR *>(out + (int64_t)(t0 + i) * D + c) = o;
+            write_once<T, V>(out + (int64_t)(t0 + i) * D + c, o);
         }
         if (fin && (e.mask >> (i + 1) & 1)) {
-            const int64_t n = win.owner(t0 + i);
+            const int64_t n = e.owner(i, sq.N);
             if (n >= 0 && in)
                 for (int j = 0; j < V; ++j) fin[n * D + c + j] = h[j];
         }
@@ -320,7 +336,7 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
         for (int i = 0; i < L; ++i) {
             if (starts >> i & 1) {
                 known = true;
-                const int64_t n = init ? win.owner(t0 + i) : -1;
+                const int64_t n = init ? e.owner(i, sq.N) : -1;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     A[j] = RESET;
@@ -342,7 +358,7 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
     }
     __syncthreads();
     if (ch.ntiles > 1) {
-        pass_on<CB>(ch, k, c0, fresh, resets, runs, parts, enter);
+        pass_on<CB, V>(ch, k, c0, fresh, resets, runs, parts, enter);
         if (chk && w == 0 && in && !fresh)
             for (int j = 0; j < V; ++j) chk[k * D + c + j] = enter[lane * V + j];
     }
@@ -364,7 +380,7 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
                 h[j] = a[i][j] * h[j] + elem(xr[i], j);
                 put(o, j, from_f<T>(h[j]));
             }
-            if (in) __builtin_nontemporal_store(o, reinterpret_cast<XR *>(out + (int64_t)(t0 + i) * D + c));
+            if (in) write_once<T, V>(out + (int64_t)(t0 + i) * D + c, o);
         }
     } else {
 #pragma unroll
@@ -410,19 +426,19 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
         __syncthreads();
         kb = __builtin_amdgcn_readfirstlane((int)s_tile);
     }
-    const int64_t c0 = (int64_t)col * CB, c = c0 + lane * V;
-    const bool in = c < D;
+    const int64_t c0 = (int64_t)col * CB, c = min(c0 + lane * V, D - V);
+    const bool in = c0 + lane * V < D;
     XR xr[L], dr[L];
     GR gr[L];
     const int k = ch.ntiles - 1 - kb;
     const int32_t t0 = k * TILE + w * L;
     {
-        const Rows rows(sq, t0, D, c0, lane * V, V);
+        const Rows<V> rows(sq, t0, D, c0, (int32_t)(c - c0));
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            gr[i] = rows.at<GR>(g, i);
-            xr[i] = rows.at<XR>(x, i);
-            dr[i] = rows.at<XR>(dout, i);
+            gr[i] = rows.at(g, i);
+            xr[i] = rows.at(x, i);
+            dr[i] = rows.at(dout, i);
         }
     }
     float a[L][V];
@@ -449,7 +465,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             if (starts >> i & 1) {
-                const int64_t n = init ? win.owner(t0 + i) : -1;
+                const int64_t n = init ? e.owner(i, sq.N) : -1;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     A[j] = RESET;
@@ -471,7 +487,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) {
             if (e.mask >> (i + 1) & 1) {   // the gradient of the final state enters here
-                const int64_t n = dfin ? win.owner(t0 + i) : -1;
+                const int64_t n = dfin ? e.owner(i, sq.N) : -1;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     Ae[j] = RESET;
@@ -489,7 +505,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
     }
     const uint32_t ends = e.mask >> 1;
     __syncthreads();
-    if (ch.ntiles > 1) pass_on<CB>(ch, kb, c0, fresh, resets, back, parts, enter);
+    if (ch.ntiles > 1) pass_on<CB, V>(ch, kb, c0, fresh, resets, back, parts, enter);
 
     // the states again, forward: p_t = a_t h_{t-1}
     float p[L][V], E[V];
@@ -502,7 +518,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
 #pragma unroll
     for (int i = 0; i < L; ++i) {
         if (starts >> i & 1) {
-            const int64_t n = init ? win.owner(t0 + i) : -1;
+            const int64_t n = init ? e.owner(i, sq.N) : -1;
 #pragma unroll
             for (int j = 0; j < V; ++j) h[j] = (n >= 0 && in) ? init[n * D + c + j] : 0.f;
         }
@@ -515,7 +531,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
 #pragma unroll
     for (int i = L - 1; i >= 0; --i) {
         if (ends >> i & 1) {
-            const int64_t n = dfin ? win.owner(t0 + i) : -1;
+            const int64_t n = dfin ? e.owner(i, sq.N) : -1;
 #pragma unroll
             for (int j = 0; j < V; ++j) E[j] = (n >= 0 && in) ? dfin[n * D + c + j] : 0.f;
         }
@@ -530,11 +546,11 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
         }
         if (in && t0 + i < e.end) {
             const int64_t at = (int64_t)(t0 + i) * D + c;
-            __builtin_nontemporal_store(ox, reinterpret_cast<XR *>(dx + at));
-            __builtin_nontemporal_store(og, reinterpret_cast<GR *>(dg + at));
+            write_once<T, V>(dx + at, ox);
+            write_once<float, V>(dg + at, og);
         }
         if (dinit && t0 + i < e.end && (starts >> i & 1)) {
-            const int64_t n = win.owner(t0 + i);
+            const int64_t n = e.owner(i, sq.N);
             if (n >= 0 && in)
                 for (int j = 0; j < V; ++j) dinit[n * D + c + j] = E[j];
         }
@@ -594,8 +610,6 @@ inline hipError_t fill_chain(uint64_t *p, size_t words, hipStream_t s)
     return hipGetLastError();
 }
 
-inline bool fits(const void *p, size_t bytes) { return !p || reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-
 template <typename T, int V>
 hipError_t run_scan(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D, void *out, float *fin,
                     float *chk, const Chain &ch, hipStream_t s)
@@ -610,13 +624,14 @@ template <typename T>
 hipError_t scan(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D, void *out, float *fin,
                 float *chk, const Chain &ch, hipStream_t s)
 {
-    const size_t e = sizeof(T);
-    // Wide rows for bf16 where they leave two workgroups for every CU; fp32
-    // tokens of four channels a lane would not fit the registers.
-    auto aligned = [&](int V) { return D % V == 0 && fits(x, V * e) && fits(out, V * e) && fits(g, V * 4); };
-    if (sizeof(T) == 2 && aligned(4) && (int64_t)ch.ntiles * ((D + 255) / 256) >= 512)
+    // V channels a lane where a last lane that overlaps its neighbour has one in
+    // the same workgroup (two workgroups must not share a state).
+    auto whole = [&](int V) { return D % (64 * V) == 0 || D % (64 * V) >= V; };
+    // Four channels a lane for bf16 where that leaves two workgroups for every
+    // CU; fp32 tokens of four would not fit the registers.
+    if (sizeof(T) == 2 && whole(4) && (int64_t)ch.ntiles * ((D + 255) / 256) >= 512)
         return run_scan<T, sizeof(T) == 2 ? 4 : 2>(x, g, init, sq, D, out, fin, chk, ch, s);
-    if (aligned(2)) return run_scan<T, 2>(x, g, init, sq, D, out, fin, chk, ch, s);
+    if (whole(2)) return run_scan<T, 2>(x, g, init, sq, D, out, fin, chk, ch, s);
     return run_scan<T, 1>(x, g, init, sq, D, out, fin, chk, ch, s);
 }
 
@@ -637,9 +652,7 @@ hipError_t scan_backward(const void *x, const float *g, const float *init, const
                          const float *dfin, const float *chk, void *dx, float *dg, float *dinit, const Chain &ch,
                          hipStream_t s)
 {
-    const size_t e = sizeof(T);
-    if (D % 2 == 0 && fits(x, 2 * e) && fits(dout, 2 * e) && fits(dx, 2 * e) && fits(g, 8) && fits(dg, 8))
-        return run_scan_backward<T, 2>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
+    if (D % 128 != 1) return run_scan_backward<T, 2>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
     return run_scan_backward<T, 1>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
 }
 

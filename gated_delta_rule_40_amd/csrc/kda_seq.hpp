@@ -44,19 +44,18 @@ struct SeqWindow {
         entry = n <= sq.N ? sq.at((int32_t)n) : INT32_MAX;
     }
     __device__ __forceinline__ int below(int32_t t) const { return __popcll(__ballot(entry < t)); }
-    // brings in the 64 entries from the first one >= t on
+    // brings in the last entry < t and the 63 after it
     __device__ __forceinline__ void locate(int32_t t) {
-        if (sq.N < 64) return;     // they are here already
+        if (sq.N < 64) return;     // all are here already
         while (stride > 1) {
             const int n = below(t);
-            if (n > 0) base += (n - 1) * stride + 1;   // behind the last sample below t
-            stride = n > 0 ? (stride + 62) / 64 : 1;   // the stride - 1 entries up to the next sample
-            if (stride < 1) stride = 1;
+            if (n > 0) base += (n - 1) * stride;       // the last sample below t
+            stride = n > 0 ? (stride + 63) / 64 : 1;   // up to the next sample
             read();
         }
         const int n = below(t);
-        if (n > 0) {
-            base += n;
+        if (n > 1) {
+            base += n - 1;
             read();
         }
     }

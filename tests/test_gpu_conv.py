@@ -38,7 +38,7 @@ def host(t):
 
 
 LENS = [[1], [2, 1, 3], [0, 0], [4, 0, 0, 1, 2, 0, 3], [31, 33, 64, 65, 1], [128, 128], [257, 0, 500], [3] * 50 + [700]]
-SHAPES = [(1, 2), (3, 4), (64, 3), (130, 4), (512, 4), (520, 2), (1000, 3)]
+SHAPES = [(1, 2), (3, 4), (64, 3), (130, 4), (512, 4), (520, 2), (1000, 3), (257, 4), (515, 3), (1023, 2)]
 CASES = [(lens, *SHAPES[(i * 3 + j) % len(SHAPES)]) for i, lens in enumerate(LENS) for j in range(3)]
 
 

@@ -47,6 +47,9 @@ CASES = [
     ([1], 1), ([1], 64), ([1, 1, 1], 130), ([127], 8), ([128], 64), ([129], 256), ([5, 0, 3, 0, 0, 120], 33),
     ([0, 0], 16), ([300], 1), ([127, 1, 0, 130, 128], 96), ([0, 1, 3, 0, 255, 257, 64, 0], 520), ([1000, 24, 2049], 260),
     ([64] * 20 + [0] * 3 + [7] * 9, 1000), ([2 ** i for i in range(11)], 65), ([3000, 5000], 12),
+    # channel counts at a workgroup's edge, and enough tiles for the widest rows
+    ([300, 33], 129), ([200, 90, 0, 1], 257), ([64, 200], 259), ([129, 128], 383), ([5000, 11, 1000], 2562),
+    ([6000, 90], 2561),
 ]
 
 
