@@ -373,10 +373,12 @@ def kda_backward(q, k, v, g, beta, initial_state, cu_seqlens, dout, dfinal=None,
 
 # ---------------------------------------------------------------- layer operators
 # One call of these is a few microseconds of GPU time at decode sizes, so the
-# checks of a tensor are one expression each, the reasons are worked out only
-# when it fails, and pointers and the stream go to the library as plain ints.
+# checks of a tensor are one expression each (a host tensor's device number is
+# -1), the reasons are worked out only when it fails, and pointers and the
+# stream go to the library as plain ints.
 _MOST = 2 ** 31 - 1                                # int32 sizes in the C ABI
 _DTYPE_CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+_F32 = torch.float32
 
 
 def _bad(name, t, ref, dtype, shape) -> None:
@@ -387,28 +389,35 @@ def _bad(name, t, ref, dtype, shape) -> None:
     raise ValueError("%s must be contiguous" % name)
 
 
-def _addr(name, t, ref, dtype, shape, optional=False) -> Optional[int]:
+def _addr(name, t, ref, dtype, shape) -> int:
     """The address of a contiguous tensor of this type and shape on ref's device, after checking that it is one."""
-    if t is None and optional:
-        return None
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == ref.device and t.dtype == dtype and
+    if not (isinstance(t, torch.Tensor) and t.get_device() == ref.get_device() and t.dtype is dtype and
             t.shape == shape and t.is_contiguous()):
         _bad(name, t, ref, dtype, shape)
     return t.data_ptr()
 
 
+def _addr_if(name, t, ref, dtype, shape) -> Optional[int]:
+    """As _addr, for an argument that may be None."""
+    return None if t is None else _addr(name, t, ref, dtype, shape)
+
+
 def _rows(name, x):
-    """A contiguous device tensor of rows in a supported type: its address, type code, rows, row shape and row length."""
+    """A contiguous device tensor of rows in a supported type: its address, type code, shape, rows and row length."""
     _require(isinstance(x, torch.Tensor) and x.is_cuda, "%s must be a device tensor" % name)
     code = _DTYPE_CODE.get(x.dtype)
     if code is None:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, x.dtype))
-    _require(x.dim() >= 2 and x.is_contiguous(), "%s must be contiguous, [rows, ...channels]" % name)
     shape = x.shape
-    rest = shape[1:]
-    D = rest[0] if len(rest) == 1 else rest.numel()
-    _require(shape[0] <= _MOST and D <= _MOST, "%s has too many rows or channels" % name)
-    return x.data_ptr(), code, shape[0], rest, D
+    if len(shape) == 2:
+        rows, D = shape
+    else:
+        _require(len(shape) > 2, "%s must be [rows, ...channels]" % name)
+        rows, D = shape[0], shape[1:].numel()
+    if rows > _MOST or D > _MOST or not x.is_contiguous():
+        _require(x.is_contiguous(), "%s must be contiguous" % name)
+        raise ValueError("%s has too many rows or channels" % name)
+    return x.data_ptr(), code, shape, rows, D
 
 
 def _cu(cu_seqlens, ref):
@@ -445,8 +454,8 @@ def _workspace(workspace, need, ref, stream):
 
 def _call(fn, ref, stream, *args) -> None:
     """fn(*args, stream) with ref's device current; stream None: that device's current stream."""
-    index = ref.device.index
-    if index != torch.cuda.current_device():
+    index = ref.get_device()
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _call(fn, ref, stream, *args)
     if stream is None:
@@ -478,14 +487,13 @@ def kda_scan_prefill(x, g, initial_state, cu_seqlens, out, final_state, checkpoi
     [ceil(T / 128), ...channels] fp32 or None, the states kda_scan_backward
     starts from; workspace: kda_scan_workspace_size(...) bytes, allocated if
     None."""
-    px, code, T, rest, D = _rows("x", x)
+    px, code, shape, T, D = _rows("x", x)
     pcu, N = _cu(cu_seqlens, x)
-    f32 = torch.float32
+    state = (N, *shape[1:])
     lib = _lib or load()
-    args = (px, _addr("g", g, x, f32, x.shape), _addr("initial_state", initial_state, x, f32, (N, *rest), True), pcu,
-            N, T, D, code, _addr("out", out, x, x.dtype, x.shape),
-            _addr("final_state", final_state, x, f32, (N, *rest), True),
-            _addr("checkpoints", checkpoints, x, f32, (-(-T // KDA_SCAN_TILE), *rest), True))
+    args = (px, _addr("g", g, x, _F32, shape), _addr_if("initial_state", initial_state, x, _F32, state), pcu, N, T, D,
+            code, _addr("out", out, x, x.dtype, shape), _addr_if("final_state", final_state, x, _F32, state),
+            _addr_if("checkpoints", checkpoints, x, _F32, (-(-T // KDA_SCAN_TILE), *shape[1:])))
     ws, pws, nbytes = _workspace(workspace, lib.kda_scan_workspace_size(N, T, D, code), x, stream)
     _call(lib.kda_scan_prefill, x, stream, *args, pws, nbytes)
 
@@ -493,10 +501,9 @@ def kda_scan_prefill(x, g, initial_state, cu_seqlens, out, final_state, checkpoi
 def kda_scan_decode_step(x, g, state_inout, out, stream=None) -> None:
     """One token per sequence, state updated in place.  x, out: [N, ...channels];
     g, state_inout: the same shape, fp32."""
-    px, code, N, _, D = _rows("x", x)
-    f32 = torch.float32
-    _call((_lib or load()).kda_scan_decode_step, x, stream, px, _addr("g", g, x, f32, x.shape),
-          _addr("state_inout", state_inout, x, f32, x.shape), N, D, code, _addr("out", out, x, x.dtype, x.shape))
+    px, code, shape, N, D = _rows("x", x)
+    _call((_lib or load()).kda_scan_decode_step, x, stream, px, _addr("g", g, x, _F32, shape),
+          _addr("state_inout", state_inout, x, _F32, shape), N, D, code, _addr("out", out, x, x.dtype, shape))
 
 
 def kda_scan_backward_workspace_size(num_seqs: int, total_tokens: int, channels: int, dtype=torch.bfloat16,
@@ -520,28 +527,28 @@ def kda_scan_backward(x, g, initial_state, cu_seqlens, dout, dfinal=None, checkp
     kda_scan_prefill wrote for the same inputs; without them the states are
     computed again.  Returns a dict of dx (x's type), dg (fp32) and dinit (fp32;
     None unless want_dinit); ``grads`` may supply the tensors."""
-    px, code, T, rest, D = _rows("x", x)
+    px, code, shape, T, D = _rows("x", x)
     pcu, N = _cu(cu_seqlens, x)
-    f32 = torch.float32
-    state = (N, *rest)
+    dt, state = x.dtype, (N, *shape[1:])
     lib = _lib or load()
-    grads = _grads(grads, x, {"dx": (x.dtype, x.shape), "dg": (f32, x.shape),
-                              "dinit": (f32, state) if want_dinit else None}, stream)
-    args = (px, _addr("g", g, x, f32, x.shape), _addr("initial_state", initial_state, x, f32, state, True), pcu, N, T,
-            D, code, _addr("dout", dout, x, x.dtype, x.shape), _addr("dfinal", dfinal, x, f32, state, True),
-            _addr("checkpoints", checkpoints, x, f32, (-(-T // KDA_SCAN_TILE), *rest), True),
-            _addr("grads['dx']", grads.get("dx"), x, x.dtype, x.shape),
-            _addr("grads['dg']", grads.get("dg"), x, f32, x.shape),
-            _addr("grads['dinit']", grads.get("dinit"), x, f32, state, True))
+    grads = _grads(grads, x, {"dx": (dt, shape), "dg": (_F32, shape), "dinit": (_F32, state) if want_dinit else None},
+                   stream)
+    args = (px, _addr("g", g, x, _F32, shape), _addr_if("initial_state", initial_state, x, _F32, state), pcu, N, T, D,
+            code, _addr("dout", dout, x, dt, shape), _addr_if("dfinal", dfinal, x, _F32, state),
+            _addr_if("checkpoints", checkpoints, x, _F32, (-(-T // KDA_SCAN_TILE), *shape[1:])),
+            _addr("grads['dx']", grads.get("dx"), x, dt, shape), _addr("grads['dg']", grads.get("dg"), x, _F32, shape),
+            _addr_if("grads['dinit']", grads.get("dinit"), x, _F32, state))
     ws, pws, nbytes = _workspace(
         workspace, lib.kda_scan_backward_workspace_size(N, T, D, code, int(checkpoints is not None)), x, stream)
     _call(lib.kda_scan_backward, x, stream, *args, pws, nbytes)
     return grads
 
 
-def _conv_width(weight, rest) -> int:
-    _require(isinstance(weight, torch.Tensor) and weight.dim() == len(rest) + 1, "weight must be [...channels, width]")
-    return weight.shape[-1]
+def _conv_weight(weight, x, shape):
+    """The weight's address and width: [...channels, width] fp32 for rows of this shape."""
+    _require(isinstance(weight, torch.Tensor) and weight.dim() == len(shape), "weight must be [...channels, width]")
+    W = weight.shape[-1]
+    return _addr("weight", weight, x, _F32, (*shape[1:], W)), W
 
 
 def kda_conv_prefill(x, weight, bias, initial_state, cu_seqlens, out, final_state, silu: bool = True,
@@ -550,26 +557,23 @@ def kda_conv_prefill(x, weight, bias, initial_state, cu_seqlens, out, final_stat
     False.  x, out: [T, ...channels]; weight: [...channels, width] fp32, width 2
     to 4; bias: [...channels] fp32 or None; initial_state / final_state:
     [N, width - 1, ...channels] of x's type or None."""
-    px, code, T, rest, D = _rows("x", x)
+    px, code, shape, T, D = _rows("x", x)
     pcu, N = _cu(cu_seqlens, x)
-    W = _conv_width(weight, rest)
-    f32, state = torch.float32, (N, W - 1, *rest)
-    _call((_lib or load()).kda_conv_prefill, x, stream, px, _addr("weight", weight, x, f32, (*rest, W)),
-          _addr("bias", bias, x, f32, rest, True), _addr("initial_state", initial_state, x, x.dtype, state, True), pcu,
-          N, T, D, W, int(silu), code, _addr("out", out, x, x.dtype, x.shape),
-          _addr("final_state", final_state, x, x.dtype, state, True))
+    pw, W = _conv_weight(weight, x, shape)
+    dt, state = x.dtype, (N, W - 1, *shape[1:])
+    _call((_lib or load()).kda_conv_prefill, x, stream, px, pw, _addr_if("bias", bias, x, _F32, shape[1:]),
+          _addr_if("initial_state", initial_state, x, dt, state), pcu, N, T, D, W, int(silu), code,
+          _addr("out", out, x, dt, shape), _addr_if("final_state", final_state, x, dt, state))
 
 
 def kda_conv_decode_step(x, weight, bias, state_inout, out, silu: bool = True, stream=None) -> None:
     """One token per sequence, state shifted in place.  x, out: [N, ...channels];
     state_inout: [N, width - 1, ...channels] of x's type."""
-    px, code, N, rest, D = _rows("x", x)
-    W = _conv_width(weight, rest)
-    f32 = torch.float32
-    _call((_lib or load()).kda_conv_decode_step, x, stream, px, _addr("weight", weight, x, f32, (*rest, W)),
-          _addr("bias", bias, x, f32, rest, True),
-          _addr("state_inout", state_inout, x, x.dtype, (N, W - 1, *rest)), N, D, W, int(silu), code,
-          _addr("out", out, x, x.dtype, x.shape))
+    px, code, shape, N, D = _rows("x", x)
+    pw, W = _conv_weight(weight, x, shape)
+    _call((_lib or load()).kda_conv_decode_step, x, stream, px, pw, _addr_if("bias", bias, x, _F32, shape[1:]),
+          _addr("state_inout", state_inout, x, x.dtype, (N, W - 1, *shape[1:])), N, D, W, int(silu), code,
+          _addr("out", out, x, x.dtype, shape))
 
 
 def kda_conv_backward_workspace_size(num_seqs: int, total_tokens: int, channels: int, width: int,
@@ -584,21 +588,20 @@ def kda_conv_backward(x, weight, bias, initial_state, cu_seqlens, dout, dfinal=N
     [N, width - 1, ...channels] (x's type) or None.  Returns a dict of dx and
     dinit (x's type; dinit None unless want_dinit), dweight and dbias (fp32;
     dbias None without a bias); ``grads`` may supply the tensors."""
-    px, code, T, rest, D = _rows("x", x)
+    px, code, shape, T, D = _rows("x", x)
     pcu, N = _cu(cu_seqlens, x)
-    W = _conv_width(weight, rest)
-    f32, state = torch.float32, (N, W - 1, *rest)
+    pw, W = _conv_weight(weight, x, shape)
+    dt, row, state = x.dtype, shape[1:], (N, W - 1, *shape[1:])
     lib = _lib or load()
-    grads = _grads(grads, x, {"dx": (x.dtype, x.shape), "dweight": (f32, (*rest, W)),
-                              "dbias": None if bias is None else (f32, rest),
-                              "dinit": (x.dtype, state) if want_dinit else None}, stream)
-    args = (px, _addr("weight", weight, x, f32, (*rest, W)), _addr("bias", bias, x, f32, rest, True),
-            _addr("initial_state", initial_state, x, x.dtype, state, True), pcu, N, T, D, W, int(silu), code,
-            _addr("dout", dout, x, x.dtype, x.shape), _addr("dfinal", dfinal, x, x.dtype, state, True),
-            _addr("grads['dx']", grads.get("dx"), x, x.dtype, x.shape),
-            _addr("grads['dweight']", grads.get("dweight"), x, f32, (*rest, W)),
-            _addr("grads['dbias']", grads.get("dbias"), x, f32, rest, True),
-            _addr("grads['dinit']", grads.get("dinit"), x, x.dtype, state, True))
+    grads = _grads(grads, x, {"dx": (dt, shape), "dweight": (_F32, (*row, W)),
+                              "dbias": None if bias is None else (_F32, row),
+                              "dinit": (dt, state) if want_dinit else None}, stream)
+    args = (px, pw, _addr_if("bias", bias, x, _F32, row), _addr_if("initial_state", initial_state, x, dt, state), pcu,
+            N, T, D, W, int(silu), code, _addr("dout", dout, x, dt, shape), _addr_if("dfinal", dfinal, x, dt, state),
+            _addr("grads['dx']", grads.get("dx"), x, dt, shape),
+            _addr("grads['dweight']", grads.get("dweight"), x, _F32, (*row, W)),
+            _addr_if("grads['dbias']", grads.get("dbias"), x, _F32, row),
+            _addr_if("grads['dinit']", grads.get("dinit"), x, dt, state))
     ws, pws, nbytes = _workspace(workspace, lib.kda_conv_backward_workspace_size(N, T, D, W, code), x, stream)
     _call(lib.kda_conv_backward, x, stream, *args, pws, nbytes)
     return grads
@@ -610,11 +613,12 @@ def _norm_rows(name, x):
     code = _DTYPE_CODE.get(x.dtype)
     if code is None:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, x.dtype))
-    _require(x.dim() >= 1 and x.is_contiguous() and x.shape[-1] > 0, "%s must be contiguous, [..., channels]" % name)
-    D = x.shape[-1]
-    rows = x.numel() // D
+    shape = x.shape
+    D = shape[-1] if shape else 0
+    _require(D > 0 and x.is_contiguous(), "%s must be contiguous, [..., channels]" % name)
+    rows = shape[0] if len(shape) == 2 else x.numel() // D
     _require(rows <= _MOST and D <= _MOST, "%s has too many rows or channels" % name)
-    return x.data_ptr(), code, rows, D
+    return x.data_ptr(), code, shape, rows, D
 
 
 def kda_rmsnorm(x, weight, out=None, residual=None, residual_out=None, out_mx=None, scales=None, eps: float = 1e-6,
@@ -625,17 +629,18 @@ def kda_rmsnorm(x, weight, out=None, residual=None, residual_out=None, out_mx=No
     float8_e4m3fn and scales: [..., ceil(channels / 32)] uint8 or
     float8_e8m0fnu, y in 8 bits with a power-of-two scale for every 32
     channels."""
-    px, code, rows, D = _norm_rows("x", x)
-    shape, dt = x.shape, x.dtype
+    px, code, shape, rows, D = _norm_rows("x", x)
+    dt = x.dtype
     mx = sc = None
     if out_mx is not None or scales is not None:
-        _require(out_mx is not None and scales is not None, "out_mx and scales go together")
-        mx = _addr("out_mx", out_mx, x, torch.uint8 if out_mx.dtype == torch.uint8 else torch.float8_e4m3fn, shape)
-        sc = _addr("scales", scales, x, torch.uint8 if scales.dtype == torch.uint8 else torch.float8_e8m0fnu,
+        _require(isinstance(out_mx, torch.Tensor) and isinstance(scales, torch.Tensor),
+                 "out_mx and scales go together")
+        mx = _addr("out_mx", out_mx, x, torch.uint8 if out_mx.dtype is torch.uint8 else torch.float8_e4m3fn, shape)
+        sc = _addr("scales", scales, x, torch.uint8 if scales.dtype is torch.uint8 else torch.float8_e8m0fnu,
                    (*shape[:-1], -(-D // KDA_MX_BLOCK)))
-    _call((_lib or load()).kda_rmsnorm, x, stream, px, _addr("residual", residual, x, dt, shape, True),
-          _addr("weight", weight, x, torch.float32, (D,), True), rows, D, eps, code,
-          _addr("residual_out", residual_out, x, dt, shape, True), _addr("out", out, x, dt, shape, True), mx, sc)
+    _call((_lib or load()).kda_rmsnorm, x, stream, px, _addr_if("residual", residual, x, dt, shape),
+          _addr_if("weight", weight, x, _F32, (D,)), rows, D, eps, code,
+          _addr_if("residual_out", residual_out, x, dt, shape), _addr_if("out", out, x, dt, shape), mx, sc)
 
 
 def kda_rmsnorm_backward_workspace_size(rows: int, channels: int, dtype=torch.bfloat16) -> int:
@@ -649,13 +654,13 @@ def kda_rmsnorm_backward(x, weight, dout, dresidual=None, eps: float = 1e-6, gra
     where it added one) and dout; dresidual, a gradient of x from elsewhere, is
     added.  Returns a dict of dx (x's type) and dweight (fp32; None without a
     weight); ``grads`` may supply the tensors."""
-    px, code, rows, D = _norm_rows("x", x)
-    shape, dt, f32 = x.shape, x.dtype, torch.float32
+    px, code, shape, rows, D = _norm_rows("x", x)
+    dt = x.dtype
     lib = _lib or load()
-    grads = _grads(grads, x, {"dx": (dt, shape), "dweight": None if weight is None else (f32, (D,))}, stream)
-    pdw = _addr("grads['dweight']", grads.get("dweight"), x, f32, (D,), True)
-    args = (px, _addr("weight", weight, x, f32, (D,), True), _addr("dout", dout, x, dt, shape),
-            _addr("dresidual", dresidual, x, dt, shape, True), rows, D, eps, code,
+    grads = _grads(grads, x, {"dx": (dt, shape), "dweight": None if weight is None else (_F32, (D,))}, stream)
+    pdw = _addr_if("grads['dweight']", grads.get("dweight"), x, _F32, (D,))
+    args = (px, _addr_if("weight", weight, x, _F32, (D,)), _addr("dout", dout, x, dt, shape),
+            _addr_if("dresidual", dresidual, x, dt, shape), rows, D, eps, code,
             _addr("grads['dx']", grads.get("dx"), x, dt, shape), pdw)
     ws, pws, nbytes = _workspace(
         workspace, lib.kda_rmsnorm_backward_workspace_size(rows, D, code) if pdw is not None else 0, x, stream)
