@@ -15,6 +15,7 @@
 // sequence's first token and by no other: that wave also computes the first
 // W - 1 tokens where they lie beyond its strip, and writes the final state, so
 // that the state may be updated in place.
+#include "kda_colsum.hpp"
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
 #include "kda_seq.hpp"
@@ -90,8 +91,8 @@ __device__ __forceinline__ typename Row<T, V>::raw row_before(const T *x, const 
 }
 
 // ---------------------------------------------------------------- forward
-template <typename T, int W, int V>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4)))
+template <typename T, int W, int V, bool SILU>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip, int32_t nstrips, int32_t cols,
                      T *out, T *fin)
 {
@@ -116,10 +117,14 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
         // tokens that belong to the wave of their sequence's start
         if (s < t0 && t0 - s < W - 1) t = min(s + W - 1, next);
         const int32_t stop = min(t1, tend);
-        R before[W - 1];
+        float before[W - 1][V];                // the last W - 1 inputs, unpacked once
         auto enter = [&]() {
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) before[j] = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
+            for (int j = 0; j < W - 1; ++j) {
+                const R r = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
+#pragma unroll
+                for (int v = 0; v < V; ++v) before[j][v] = Row<T, V>::at(r, v);
+            }
         };
         auto advance = [&]() {                 // to the sequence that begins at token t
             while (n < sq.N - 1 && next <= t) next = win.at(++n + 1);
@@ -129,16 +134,16 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
             R o;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float p = wt.b[v];
+                const float in = Row<T, V>::at(r, v);
+                float p = wt.b[v] + wt.w[W - 1][v] * in;
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) p += wt.w[j][v] * Row<T, V>::at(before[j], v);
-                p += wt.w[W - 1][v] * Row<T, V>::at(r, v);
-                Row<T, V>::set(o, v, a.silu ? silu_f(p) : p);
+                for (int j = 0; j < W - 1; ++j) p += wt.w[j][v] * before[j][v];
+                Row<T, V>::set(o, v, SILU ? silu_f(p) : p);
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) before[j][v] = before[j + 1][v];
+                before[W - 2][v] = in;
             }
             write_once<T, V>(out + (int64_t)t * a.D + c, o);
-#pragma unroll
-            for (int j = 0; j + 1 < W - 1; ++j) before[j] = before[j + 1];
-            before[W - 2] = r;
             ++t;
         };
         auto read = [&](R (&rows)[BATCH], int32_t from) {
@@ -241,8 +246,8 @@ __global__ __launch_bounds__(256) void kda_conv_step_kernel(const T *x, T *state
 // joins them.  A strip's wave finishes the places of its tokens, and of the
 // initial states of the sequences that begin in it, by walking W - 1 tokens
 // beyond the strip; only its own tokens count for dw and dbias.
-template <typename T, int W, int V>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4)))
+template <typename T, int W, int V, bool SILU>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip, int32_t nstrips, int32_t cols,
                          const T *dout, const T *dfin, T *dx, T *dinit, float *partial)
 {
@@ -281,11 +286,15 @@ void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t
             Weights<W, V> wt;
             wt.load(a, c);
             int32_t s = win.at(n), next = max(win.at(n + 1), t0 + 1), t = t0;
-            R before[W - 1];
+            float before[W - 1][V];   // the last W - 1 inputs, unpacked once
             float acc[W - 1][V] = {};
             auto enter = [&]() {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) before[j] = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
+                for (int j = 0; j < W - 1; ++j) {
+                    const R r = row_before<T, W, V>(x, init, a, c, n, s, t, W - 1 - j);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) before[j][v] = Row<T, V>::at(r, v);
+                }
             };
             // place p of the sequence (p < 0: of its initial state) is finished
             auto finish = [&](int32_t p, const float (&v)[V]) {
@@ -301,32 +310,42 @@ void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t
             };
             const int32_t stop = (int32_t)min((int64_t)t1 + W - 1, (int64_t)tend);
             auto token = [&](const R &r, const R &d) {
-                float done[V];
-                const bool mine = t < t1;
+                float done[V], in[W][V], g[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    float p = wt.b[v], in[W];
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) in[j] = Row<T, V>::at(before[j], v);
-                    in[W - 1] = Row<T, V>::at(r, v);
+                    for (int j = 0; j < W - 1; ++j) in[j][v] = before[j][v];
+                    in[W - 1][v] = Row<T, V>::at(r, v);
+                    g[v] = Row<T, V>::at(d, v);
+                    if (SILU) {
+                        float p = wt.b[v];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) p += wt.w[j][v] * in[j];
-                    float g = Row<T, V>::at(d, v);
-                    if (a.silu) g *= dsilu_f(p);
-                    if (mine) {
-                        db[v] += g;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][v] += g * in[j];
+                        for (int j = 0; j < W; ++j) p += wt.w[j][v] * in[j][v];
+                        g[v] *= dsilu_f(p);
                     }
-                    done[v] = acc[0][v] + g * wt.w[0][v];
+                }
+                if (t < t1) {   // one branch for all channels
 #pragma unroll
-                    for (int j = 0; j + 1 < W - 1; ++j) acc[j][v] = acc[j + 1][v] + g * wt.w[j + 1][v];
-                    acc[W - 2][v] = g * wt.w[W - 1][v];
+                    for (int v = 0; v < V; ++v) {
+                        db[v] += g[v];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][v] += g[v] * in[j][v];
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    done[v] = acc[0][v] + g[v] * wt.w[0][v];
+#pragma unroll
+                    for (int j = 0; j + 1 < W - 1; ++j) acc[j][v] = acc[j + 1][v] + g[v] * wt.w[j + 1][v];
+                    acc[W - 2][v] = g[v] * wt.w[W - 1][v];
                 }
                 finish(t - s - (W - 1), done);
 #pragma unroll
-                for (int j = 0; j + 1 < W - 1; ++j) before[j] = before[j + 1];
-                before[W - 2] = r;
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int j = 0; j + 1 < W - 1; ++j) before[j][v] = before[j + 1][v];
+                    before[W - 2][v] = in[W - 1][v];
+                }
                 ++t;
             };
             // the sequence ends before token t: its unfinished places, then the next sequence
@@ -391,40 +410,39 @@ void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t
     }
 }
 
-// dw[c][j] and dbias[c] from the workgroups' parts [n][W + 1][D]: 32 columns
-// and 32 strided walks a workgroup, the walks' sums added in order
+// dw[c][j] and dbias[c] from the workgroups' parts [n][W + 1][D]
 template <int W>
-__global__ __launch_bounds__(1024) void kda_conv_sums_kernel(const float *src, int32_t n, int64_t D, float *dw,
-                                                             float *dbias)
+__global__ __launch_bounds__(COLSUM_THREADS) void kda_conv_sums_kernel(const float *src, int32_t n, int64_t D,
+                                                                       float *dw, float *dbias)
 {
-    __shared__ float part[32][33];
-    const int cx = threadIdx.x & 31, walk = threadIdx.x >> 5;
-    const int64_t cols = (W + 1) * D, i = (int64_t)blockIdx.x * 32 + cx;
-    float s = 0.f;
-    if (i < cols)
-        for (int32_t r = walk; r < n; r += 32) s += src[r * cols + i];
-    part[walk][cx] = s;
-    __syncthreads();
-    if (walk == 0 && i < cols) {
-        for (int v = 1; v < 32; ++v) s += part[v][cx];
-        const int64_t j = i / D, c = i % D;
-        if (j < W) dw[c * W + j] = s;
-        else if (dbias) dbias[c] = s;
-    }
+    const int64_t i = (int64_t)blockIdx.x * COLSUM_COLS + threadIdx.x % COLSUM_COLS;
+    const float s = column_sum(src, n, (W + 1) * D, i);
+    if (threadIdx.x >= COLSUM_COLS || i >= (W + 1) * D) return;
+    const int64_t j = i / D, c = i % D;
+    if (j < W) dw[c * W + j] = s;
+    else if (dbias) dbias[c] = s;
 }
 
 // ---------------------------------------------------------------- host
 inline int64_t up(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
-constexpr int32_t BWD_PARTS = 512;    // workgroups along the tokens, at most
-constexpr int32_t BWD_STRIP = 16;     // tokens of a wave, at least
+// whether V channels a lane leave no lane that overlaps one of another wave
+// (two waves must not share a state)
+inline bool whole(int64_t D, int V) { return D % (64 * V) == 0 || D % (64 * V) >= V; }
 
-inline int32_t bwd_strip(int32_t T)
+// The backward's strips: as long as three workgroups for every CU allow (what
+// its registers let be resident at once; longer strips also read fewer rows
+// twice and leave fewer partial sums), and 16 tokens at least.
+constexpr int32_t BWD_GROUPS = 768;
+constexpr int BWD_V = 4;   // channels a lane (the sums and unfinished places of eight would not fit the registers)
+
+inline int64_t bwd_cols(int64_t D) { return up(D, whole(D, BWD_V) ? 64 * BWD_V : 64); }
+inline int32_t bwd_strip(int32_t T, int64_t D)
 {
-    const int64_t len = up(up(T, (int64_t)BWD_PARTS * 4), 4) * 4;
-    return (int32_t)(len < BWD_STRIP ? BWD_STRIP : len);
+    const int64_t parts = up(BWD_GROUPS, bwd_cols(D)), len = up(T, parts * 4);
+    return (int32_t)(len < 16 ? 16 : len);
 }
-inline int32_t bwd_parts(int32_t T) { return (int32_t)(T > 0 ? up(up(T, bwd_strip(T)), 4) : 1); }
+inline int32_t bwd_parts(int32_t T, int64_t D) { return (int32_t)(T > 0 ? up(up(T, bwd_strip(T, D)), 4) : 1); }
 
 template <typename T, int W, int V>
 hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, void *out, void *fin,
@@ -434,8 +452,13 @@ hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Se
     // strips of 64 tokens where these give every SIMD its waves, shorter ones otherwise
     const int32_t strip = up(sq.T, 64) * cols >= 4096 ? 64 : 16;
     const int32_t nstrips = (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1);
-    hipLaunchKernelGGL((kda_conv_kernel<T, W, V>), dim3((unsigned)(up(nstrips, 4) * cols)), dim3(256), 0, s,
-                       (const T *)x, (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (T *)out, (T *)fin);
+    const dim3 grid((unsigned)(up(nstrips, 4) * cols));
+    if (a.silu)
+        hipLaunchKernelGGL((kda_conv_kernel<T, W, V, true>), grid, dim3(256), 0, s, (const T *)x, (const T *)init, a, sq,
+                           strip, nstrips, (int32_t)cols, (T *)out, (T *)fin);
+    else
+        hipLaunchKernelGGL((kda_conv_kernel<T, W, V, false>), grid, dim3(256), 0, s, (const T *)x, (const T *)init, a,
+                           sq, strip, nstrips, (int32_t)cols, (T *)out, (T *)fin);
     return hipGetLastError();
 }
 
@@ -457,13 +480,22 @@ hipError_t run_conv_backward(const void *x, const ConvArgs &a, const void *init,
                              const void *dfin, void *dx, float *dw, float *dbias, void *dinit, void *ws,
                              hipStream_t s)
 {
-    const int32_t strip = bwd_strip(sq.T), parts = sq.N > 0 ? bwd_parts(sq.T) : 0;
-    const int64_t cols = up(a.D, 64 * V);
-    if (parts > 0)
-        hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V>), dim3((unsigned)(parts * cols)), dim3(256), 0, s,
-                           (const T *)x, (const T *)init, a, sq, strip, (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1),
-                           (int32_t)cols, (const T *)dout, (const T *)dfin, (T *)dx, (T *)dinit, (float *)ws);
-    hipLaunchKernelGGL(kda_conv_sums_kernel<W>, dim3((unsigned)up((W + 1) * a.D, 32)), dim3(1024), 0, s,
+    const int32_t strip = bwd_strip(sq.T, a.D), parts = sq.N > 0 ? bwd_parts(sq.T, a.D) : 0;
+    const int64_t cols = bwd_cols(a.D);
+    if (parts > 0) {
+        const dim3 grid((unsigned)(parts * cols));
+        const int32_t nstrips = (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1);
+        if (a.silu)
+            hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V, true>), grid, dim3(256), 0, s, (const T *)x,
+                               (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (const T *)dout, (const T *)dfin,
+                               (T *)dx, (T *)dinit, (float *)ws);
+        else
+            hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V, false>), grid, dim3(256), 0, s, (const T *)x,
+                               (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (const T *)dout, (const T *)dfin,
+                               (T *)dx, (T *)dinit, (float *)ws);
+    }
+    hipLaunchKernelGGL(kda_conv_sums_kernel<W>, dim3((unsigned)up((W + 1) * a.D, COLSUM_COLS)),
+                       dim3(COLSUM_THREADS), 0, s,
                        (const float *)ws, parts, a.D, dw, dbias);
     return hipGetLastError();
 }
@@ -477,10 +509,6 @@ template <int V, typename F> hipError_t with_width(int32_t width, F f)
     default: return f(std::integral_constant<int, 4>(), std::integral_constant<int, V>());
     }
 }
-
-// whether V channels a lane leave no lane that overlaps one of another wave
-// (two waves must not share a state)
-inline bool whole(int64_t D, int V) { return D % (64 * V) == 0 || D % (64 * V) >= V; }
 
 template <typename T>
 hipError_t conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, int32_t width, void *out, void *fin,
@@ -504,11 +532,10 @@ hipError_t conv_backward(const void *x, const ConvArgs &a, const void *init, con
                          const void *dout, const void *dfin, void *dx, float *dw, float *dbias, void *dinit, void *ws,
                          hipStream_t s)
 {
-    constexpr int V = 4;   // (eight channels' sums and unfinished places would not fit the registers)
     auto f = [&](auto w, auto v) {
         return run_conv_backward<T, w(), v()>(x, a, init, sq, dout, dfin, dx, dw, dbias, dinit, ws, s);
     };
-    return whole(a.D, V) ? with_width<V>(width, f) : with_width<1>(width, f);
+    return whole(a.D, BWD_V) ? with_width<BWD_V>(width, f) : with_width<1>(width, f);
 }
 
 }  // namespace kda
@@ -533,7 +560,7 @@ hipError_t kda_launch_conv_step(bool bf16, const void *x, const float *w, const 
 
 size_t kda_conv_bwd_ws_bytes(int32_t T, int32_t D, int32_t width, bool)
 {
-    return (size_t)bwd_parts(T) * (width + 1) * D * sizeof(float);
+    return (size_t)bwd_parts(T, D) * (width + 1) * D * sizeof(float);
 }
 
 hipError_t kda_launch_conv_backward(bool bf16, const void *x, const float *w, const float *bias, const void *init,

@@ -10,6 +10,7 @@
 // A row of up to 256 pieces of 16 bytes takes one wave or a part of one (no
 // barrier), a longer one a workgroup.  Where a row's channels or pointers are
 // no multiples of 16 bytes, single elements stand for the pieces.
+#include "kda_colsum.hpp"
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
 
@@ -238,22 +239,13 @@ __global__ void kda_rmsnorm_bwd_kernel(const T *x, const float *w, const T *dout
             for (int j = 0; j < VW; ++j) partial[(int64_t)blockIdx.x * D + (int64_t)(i0 + k * tpr) * VW + j] = dw[k][j];
 }
 
-// dst[c] = the sum of src[i][c] over n rows: 32 columns and 32 strided walks a
-// workgroup, the walks' sums added in order
-__global__ __launch_bounds__(1024) void kda_column_sums_kernel(const float *src, int32_t n, int64_t D, float *dst)
+// dst[c] = the sum of src[i][c] over n rows
+__global__ __launch_bounds__(COLSUM_THREADS) void kda_column_sums_kernel(const float *src, int32_t n, int64_t D,
+                                                                         float *dst)
 {
-    __shared__ float part[32][33];
-    const int cx = threadIdx.x & 31, walk = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + cx;
-    float s = 0.f;
-    if (c < D)
-        for (int32_t i = walk; i < n; i += 32) s += src[i * D + c];
-    part[walk][cx] = s;
-    __syncthreads();
-    if (walk == 0 && c < D) {
-        for (int i = 1; i < 32; ++i) s += part[i][cx];
-        dst[c] = s;
-    }
+    const int64_t c = (int64_t)blockIdx.x * COLSUM_COLS + threadIdx.x % COLSUM_COLS;
+    const float s = column_sum(src, n, D, c);
+    if (threadIdx.x < COLSUM_COLS && c < D) dst[c] = s;
 }
 
 // ---------------------------------------------------------------- host
@@ -331,7 +323,8 @@ hipError_t rmsnorm_backward_as(const void *x, const float *w, const void *dout, 
                                dw ? (float *)ws : nullptr);
     }
     if (dw)
-        hipLaunchKernelGGL(kda_column_sums_kernel, dim3((unsigned)((D + 31) / 32)), dim3(1024), 0, s,
+        hipLaunchKernelGGL(kda_column_sums_kernel, dim3((unsigned)((D + COLSUM_COLS - 1) / COLSUM_COLS)),
+                           dim3(COLSUM_THREADS), 0, s,
                            (const float *)ws, (int32_t)blocks, (int64_t)D, dw);
     return hipGetLastError();
 }
