@@ -20,19 +20,25 @@ constexpr int MXB = 32;              // channels that share a scale
 constexpr int MAX_PARTIALS = 1024;   // partial sums of a weight's gradient
 
 // ---------------------------------------------------------------- pieces
-// VW consecutive elements, moved as one access: as read, and as fp32
-template <typename T, int VW> struct Piece {
+// VW consecutive elements, moved as one access: as read, and as fp32.  ONCE:
+// past the caches, for rows too many to be found there again (16,384 x 7,168
+// with the 8-bit output 152 -> 135 us); a few rows stay in them for the reader.
+template <typename T, int VW, bool ONCE> struct Piece {
     typedef T raw __attribute__((ext_vector_type(VW)));
-    __device__ static __forceinline__ raw load(const T *p) { return *reinterpret_cast<const raw *>(p); }
+    __device__ static __forceinline__ raw load(const T *p) {
+        const raw *q = reinterpret_cast<const raw *>(p);
+        return ONCE ? __builtin_nontemporal_load(q) : *q;
+    }
     __device__ static __forceinline__ void store(T *p, const float (&v)[VW]) {
         raw r;
 #pragma unroll
         for (int j = 0; j < VW; ++j) r[j] = from_f<T>(v[j]);
-        *reinterpret_cast<raw *>(p) = r;
+        if (ONCE) __builtin_nontemporal_store(r, reinterpret_cast<raw *>(p));
+        else *reinterpret_cast<raw *>(p) = r;
     }
     __device__ static __forceinline__ float at(const raw &r, int j) { return to_f(r[j]); }
 };
-template <typename T> struct Piece<T, 1> {
+template <typename T, bool ONCE> struct Piece<T, 1, ONCE> {
     typedef T raw;
     __device__ static __forceinline__ raw load(const T *p) { return *p; }
     __device__ static __forceinline__ void store(T *p, const float (&v)[1]) { *p = from_f<T>(v[0]); }
@@ -88,11 +94,11 @@ __device__ __forceinline__ int mx_scale(uint32_t amax_bits)
 
 // ---------------------------------------------------------------- forward
 // Pieces of a row: thread i of its tpr has pieces i, i + tpr, ... (C of them).
-template <typename T, int VW, int C, bool RES, bool MX>
+template <typename T, int VW, int C, bool ONCE, bool RES, bool MX>
 __global__ void kda_rmsnorm_kernel(const T *x, const T *res, const float *w, int32_t rows, int32_t D, int32_t tpr,
                                    float eps, T *sum, T *out, uint8_t *mx, uint8_t *scales)
 {
-    typedef Piece<T, VW> P;
+    typedef Piece<T, VW, ONCE> P;
     __shared__ float red[16][1];
     const int i0 = threadIdx.x & (tpr - 1);
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
@@ -165,11 +171,11 @@ __global__ void kda_rmsnorm_kernel(const T *x, const T *res, const float *w, int
 // its part of the weight's gradient in registers; the parts of its rows side by
 // side are added through LDS, and those of all workgroups by the next kernel,
 // all in a fixed order.
-template <typename T, int VW, int C, bool RES>
+template <typename T, int VW, int C, bool ONCE, bool RES>
 __global__ void kda_rmsnorm_bwd_kernel(const T *x, const float *w, const T *dout, const T *dres, int32_t rows,
                                        int32_t D, int32_t tpr, float eps, T *dx, float *partial)
 {
-    typedef Piece<T, VW> P;
+    typedef Piece<T, VW, ONCE> P;
     extern __shared__ float fold[];
     __shared__ float red[16][2];
     const int i0 = threadIdx.x & (tpr - 1), slot = threadIdx.x / tpr, slots = blockDim.x / tpr;
@@ -263,27 +269,27 @@ inline RowShape row_shape(int32_t pieces, int C, int lanes)
     return {tpr, tpr < 256 ? 256 : tpr};
 }
 
-template <typename T, int VW, int C, bool RES, bool MX>
+template <typename T, int VW, int C, bool ONCE, bool RES, bool MX>
 hipError_t run_rmsnorm(const void *x, const void *res, const float *w, int32_t rows, int32_t D, float eps, void *sum,
                        void *out, uint8_t *mx, uint8_t *scales, hipStream_t s)
 {
     const RowShape sh = row_shape(D / VW, C, MXB / VW);
     const int64_t per = sh.threads / sh.tpr;
-    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, RES, MX>), dim3((unsigned)((rows + per - 1) / per)),
+    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, RES, MX>), dim3((unsigned)((rows + per - 1) / per)),
                        dim3(sh.threads), 0, s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, eps, (T *)sum,
                        (T *)out, mx, scales);
     return hipGetLastError();
 }
 
-template <typename T, int VW, int C>
+template <typename T, int VW, int C, bool ONCE>
 hipError_t rmsnorm_as(const void *x, const void *res, const float *w, int32_t rows, int32_t D, float eps, void *sum,
                       void *out, uint8_t *mx, uint8_t *scales, hipStream_t s)
 {
     if (res)
-        return mx ? run_rmsnorm<T, VW, C, true, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s)
-                  : run_rmsnorm<T, VW, C, true, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
-    return mx ? run_rmsnorm<T, VW, C, false, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s)
-              : run_rmsnorm<T, VW, C, false, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+        return mx ? run_rmsnorm<T, VW, C, ONCE, true, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s)
+                  : run_rmsnorm<T, VW, C, ONCE, true, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+    return mx ? run_rmsnorm<T, VW, C, ONCE, false, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s)
+              : run_rmsnorm<T, VW, C, ONCE, false, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
 }
 
 template <typename T>
@@ -294,17 +300,18 @@ hipError_t rmsnorm(const void *x, const void *res, const float *w, int32_t rows,
     if (D % VW == 0 && on(x, 16) && on(res, 16) && on(w, 16) && on(sum, 16) && on(out, 16) && on(mx, VW)) {
         const int32_t pieces = D / VW;
         // few rows: one piece a thread, so that a row's latency is short
-        if (pieces <= 64 || (rows <= 512 && pieces <= 1024))
-            return rmsnorm_as<T, VW, 1>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
-        return rmsnorm_as<T, VW, 4>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+        if (rows <= 512 && pieces <= 1024)
+            return rmsnorm_as<T, VW, 1, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+        if (pieces <= 64) return rmsnorm_as<T, VW, 1, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+        return rmsnorm_as<T, VW, 4, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
     }
-    if (D <= 4096) return rmsnorm_as<T, 1, 4>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
-    return rmsnorm_as<T, 1, 16>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+    if (D <= 4096) return rmsnorm_as<T, 1, 4, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+    return rmsnorm_as<T, 1, 16, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
 }
 
 inline int32_t partials(int32_t rows) { return rows < MAX_PARTIALS ? rows : MAX_PARTIALS; }
 
-template <typename T, int VW, int C>
+template <typename T, int VW, int C, bool ONCE>
 hipError_t rmsnorm_backward_as(const void *x, const float *w, const void *dout, const void *dres, int32_t rows,
                                int32_t D, float eps, void *dx, float *dw, void *ws, hipStream_t s)
 {
@@ -314,11 +321,11 @@ hipError_t rmsnorm_backward_as(const void *x, const float *w, const void *dout, 
     const size_t lds = per > 1 ? sizeof(float) * sh.threads * C * VW : 0;
     if (blocks > 0) {
         if (dres)
-            hipLaunchKernelGGL((kda_rmsnorm_bwd_kernel<T, VW, C, true>), dim3(blocks), dim3(sh.threads), lds, s,
+            hipLaunchKernelGGL((kda_rmsnorm_bwd_kernel<T, VW, C, ONCE, true>), dim3(blocks), dim3(sh.threads), lds, s,
                                (const T *)x, w, (const T *)dout, (const T *)dres, rows, D, sh.tpr, eps, (T *)dx,
                                dw ? (float *)ws : nullptr);
         else
-            hipLaunchKernelGGL((kda_rmsnorm_bwd_kernel<T, VW, C, false>), dim3(blocks), dim3(sh.threads), lds, s,
+            hipLaunchKernelGGL((kda_rmsnorm_bwd_kernel<T, VW, C, ONCE, false>), dim3(blocks), dim3(sh.threads), lds, s,
                                (const T *)x, w, (const T *)dout, (const T *)dres, rows, D, sh.tpr, eps, (T *)dx,
                                dw ? (float *)ws : nullptr);
     }
@@ -336,13 +343,14 @@ hipError_t rmsnorm_backward(const void *x, const float *w, const void *dout, con
     constexpr int VW = 16 / sizeof(T);
     if (D % VW == 0 && on(x, 16) && on(dout, 16) && on(dres, 16) && on(w, 16) && on(dx, 16)) {
         const int32_t pieces = D / VW;
-        if (pieces <= 64 || (rows <= 512 && pieces <= 1024))
-            return rmsnorm_backward_as<T, VW, 1>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
+        if (rows <= 512 && pieces <= 1024)
+            return rmsnorm_backward_as<T, VW, 1, false>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
+        if (pieces <= 64) return rmsnorm_backward_as<T, VW, 1, true>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
         // two pieces of eight or four of four: more would not fit the registers
-        return rmsnorm_backward_as<T, VW, 16 / VW>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
+        return rmsnorm_backward_as<T, VW, 16 / VW, true>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
     }
-    if (D <= 4096) return rmsnorm_backward_as<T, 1, 4>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
-    return rmsnorm_backward_as<T, 1, 16>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
+    if (D <= 4096) return rmsnorm_backward_as<T, 1, 4, false>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
+    return rmsnorm_backward_as<T, 1, 16, false>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
 }
 
 }  // namespace kda
