@@ -94,14 +94,15 @@ __device__ __forceinline__ typename Row<T, V>::raw row_before(const T *x, const 
 template <typename T, int W, int V, bool SILU>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip, int32_t nstrips, int32_t cols,
-                     T *out, T *fin)
+                     int32_t width, T *out, T *fin)
 {
     typedef typename Row<T, V>::raw R;
     constexpr int BATCH = 4;
     const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t k = (int32_t)(blockIdx.x / cols) * 4 + wave;
-    const int64_t c0 = (int64_t)(blockIdx.x % cols) * 64 * V;
-    const int64_t c = min(c0 + (int64_t)(threadIdx.x & 63) * V, a.D - V);
+    // A lane past its column or the last channel repeats the column's last lane.
+    const int64_t c0 = (int64_t)(blockIdx.x % cols) * width;
+    const int64_t c = min(c0 + (int64_t)min((int32_t)(threadIdx.x & 63) * V, width - V), a.D - V);
     if (k >= nstrips) return;
     SeqWindow win(sq);
     const int32_t t0 = k * strip, t1 = (int32_t)min((int64_t)t0 + strip, (int64_t)sq.T);
@@ -394,10 +395,12 @@ void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t
         }
     }
     // the four waves' sums, in order, as the workgroup's part
-    // (a lane whose channels overlap its neighbour's writes the same values there)
+    // (a lane whose channels overlap its neighbour's writes the same values
+    // there; those of the workgroup before are that one's)
     const int place = (int)(c - c0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+        if (place + v < 0) continue;
         sums[wave][W][place + v] = db[v];
 #pragma unroll
         for (int j = 0; j < W; ++j) sums[wave][j][place + v] = dw[j][v];
@@ -426,17 +429,15 @@ __global__ __launch_bounds__(COLSUM_THREADS) void kda_conv_sums_kernel(const flo
 // ---------------------------------------------------------------- host
 inline int64_t up(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
-// whether V channels a lane leave no lane that overlaps one of another wave
-// (two waves must not share a state)
-inline bool whole(int64_t D, int V) { return D % (64 * V) == 0 || D % (64 * V) >= V; }
-
 // The backward's strips: as long as three workgroups for every CU allow (what
 // its registers let be resident at once; longer strips also read fewer rows
 // twice and leave fewer partial sums), and 16 tokens at least.
 constexpr int32_t BWD_GROUPS = 768;
 constexpr int BWD_V = 4;   // channels a lane (the sums and unfinished places of eight would not fit the registers)
 
-inline int64_t bwd_cols(int64_t D) { return up(D, whole(D, BWD_V) ? 64 * BWD_V : 64); }
+// Rows too short for BWD_V channels a lane (most lanes would be idle) take one.
+inline bool bwd_wide(int64_t D) { return D >= 128; }
+inline int64_t bwd_cols(int64_t D) { return up(D, bwd_wide(D) ? 64 * BWD_V : 64); }
 inline int32_t bwd_strip(int32_t T, int64_t D)
 {
     const int64_t parts = up(BWD_GROUPS, bwd_cols(D)), len = up(T, parts * 4);
@@ -448,17 +449,18 @@ template <typename T, int W, int V>
 hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, void *out, void *fin,
                     hipStream_t s)
 {
-    const int64_t cols = up(a.D, 64 * V);
+    const int32_t cw = kda_column_width((int32_t)a.D, V);
+    const int64_t cols = up(a.D, cw);
     // strips of 64 tokens where these give every SIMD its waves, shorter ones otherwise
     const int32_t strip = up(sq.T, 64) * cols >= 4096 ? 64 : 16;
     const int32_t nstrips = (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1);
     const dim3 grid((unsigned)(up(nstrips, 4) * cols));
     if (a.silu)
         hipLaunchKernelGGL((kda_conv_kernel<T, W, V, true>), grid, dim3(256), 0, s, (const T *)x, (const T *)init, a, sq,
-                           strip, nstrips, (int32_t)cols, (T *)out, (T *)fin);
+                           strip, nstrips, (int32_t)cols, cw, (T *)out, (T *)fin);
     else
         hipLaunchKernelGGL((kda_conv_kernel<T, W, V, false>), grid, dim3(256), 0, s, (const T *)x, (const T *)init, a,
-                           sq, strip, nstrips, (int32_t)cols, (T *)out, (T *)fin);
+                           sq, strip, nstrips, (int32_t)cols, cw, (T *)out, (T *)fin);
     return hipGetLastError();
 }
 
@@ -510,13 +512,16 @@ template <int V, typename F> hipError_t with_width(int32_t width, F f)
     }
 }
 
+// 16 bytes a lane, or fewer where that would leave most lanes idle.
 template <typename T>
 hipError_t conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, int32_t width, void *out, void *fin,
                 hipStream_t s)
 {
     constexpr int V = 16 / sizeof(T);
     auto f = [&](auto w, auto v) { return run_conv<T, w(), v()>(x, a, init, sq, out, fin, s); };
-    return whole(a.D, V) ? with_width<V>(width, f) : with_width<1>(width, f);
+    if (a.D > 32 * V) return with_width<V>(width, f);
+    if (sizeof(T) == 2 && a.D > 64) return with_width<sizeof(T) == 2 ? 2 : 1>(width, f);
+    return with_width<1>(width, f);
 }
 
 template <typename T>
@@ -535,7 +540,7 @@ hipError_t conv_backward(const void *x, const ConvArgs &a, const void *init, con
     auto f = [&](auto w, auto v) {
         return run_conv_backward<T, w(), v()>(x, a, init, sq, dout, dfin, dx, dw, dbias, dinit, ws, s);
     };
-    return whole(a.D, BWD_V) ? with_width<BWD_V>(width, f) : with_width<1>(width, f);
+    return bwd_wide(a.D) ? with_width<BWD_V>(width, f) : with_width<1>(width, f);
 }
 
 }  // namespace kda

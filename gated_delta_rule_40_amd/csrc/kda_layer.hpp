@@ -10,6 +10,17 @@
 
 constexpr int32_t kMaxNormChannels = 16384;
 
+// Channels of a column of work: 64 lanes of V, or a little less where the last
+// column would otherwise be narrower than a lane (D >= V).  A lane that reaches
+// past the last channel is moved back over its neighbour's; that neighbour is
+// then in the same column, so that no two columns touch one channel's state.
+inline int32_t kda_column_width(int32_t D, int V)
+{
+    int32_t w = 64 * V;
+    while (w > V && (D - 1) % w + 1 < V) w -= V;
+    return w;
+}
+
 size_t kda_scan_ws_bytes(int32_t T, int32_t D);
 hipError_t kda_launch_scan(bool bf16, const void *x, const float *g, const float *init, const int32_t *cu, int32_t N,
                            int32_t T, int32_t D, void *out, float *fin, float *checkpoints, void *ws, hipStream_t s);

@@ -8,11 +8,13 @@
 // A row is held in the registers of its threads from its read to its writes,
 // so every element is read once and written once, and HBM's rate is the bound.
 // A row of up to 256 pieces of 16 bytes takes one wave or a part of one (no
-// barrier), a longer one a workgroup.  Where a row's channels or pointers are
-// no multiples of 16 bytes, single elements stand for the pieces.
+// barrier), a longer one a workgroup.  Pieces need the alignment of an element
+// only; the last one of a row may be a part of one (TAIL).
 #include "kda_colsum.hpp"
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
+
+#include <type_traits>
 
 namespace kda {
 
@@ -25,38 +27,84 @@ constexpr int MAX_PARTIALS = 1024;   // partial sums of a weight's gradient
 // with the 8-bit output 152 -> 135 us); a few rows stay in them for the reader.
 template <typename T, int VW, bool ONCE> struct Piece {
     typedef T raw __attribute__((ext_vector_type(VW)));
+    typedef raw mem __attribute__((aligned(sizeof(T))));
     __device__ static __forceinline__ raw load(const T *p) {
-        const raw *q = reinterpret_cast<const raw *>(p);
+        const mem *q = reinterpret_cast<const mem *>(p);
         return ONCE ? __builtin_nontemporal_load(q) : *q;
     }
     __device__ static __forceinline__ void store(T *p, const float (&v)[VW]) {
         raw r;
 #pragma unroll
         for (int j = 0; j < VW; ++j) r[j] = from_f<T>(v[j]);
-        if (ONCE) __builtin_nontemporal_store(r, reinterpret_cast<raw *>(p));
-        else *reinterpret_cast<raw *>(p) = r;
+        if (ONCE) __builtin_nontemporal_store(r, reinterpret_cast<mem *>(p));
+        else *reinterpret_cast<mem *>(p) = r;
+    }
+    // the first n elements; the others read as zeros
+    __device__ static __forceinline__ raw load(const T *p, int n) {
+        raw r = {};
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+            if (j < n) r[j] = p[j];
+        return r;
+    }
+    __device__ static __forceinline__ void store(T *p, const float (&v)[VW], int n) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+            if (j < n) p[j] = from_f<T>(v[j]);
     }
     __device__ static __forceinline__ float at(const raw &r, int j) { return to_f(r[j]); }
 };
-template <typename T, bool ONCE> struct Piece<T, 1, ONCE> {
-    typedef T raw;
-    __device__ static __forceinline__ raw load(const T *p) { return *p; }
-    __device__ static __forceinline__ void store(T *p, const float (&v)[1]) { *p = from_f<T>(v[0]); }
-    __device__ static __forceinline__ float at(const raw &r, int) { return to_f(r); }
-};
-template <int VW> __device__ __forceinline__ void load_weight(const float *w, int64_t c, float (&v)[VW])
-{
-    if (VW % 4 == 0) {
-#pragma unroll
-        for (int j = 0; j < VW; j += 4) {
-            const f32x4 q = *reinterpret_cast<const f32x4 *>(w + c + j);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[j + i] = q[i];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < VW; ++j) v[j] = w[c + j];
+
+// The pieces of a row of D elements, as thread i0 of its tpr has them: piece k
+// is the row's number i0 + k * tpr, with `count` elements (0: beyond the row).
+template <int VW, bool TAIL> struct Pieces {
+    int32_t D, i0, tpr;
+    __device__ __forceinline__ int32_t index(int k) const { return i0 + k * tpr; }
+    __device__ __forceinline__ int32_t count(int k) const {
+        const int32_t left = D - index(k) * VW;
+        return TAIL ? max(min(left, VW), 0) : (left > 0 ? VW : 0);
     }
+    template <typename P, typename T> __device__ __forceinline__ typename P::raw load(const T *row, int k) const {
+        if (TAIL && count(k) < VW) return P::load(row + (int64_t)index(k) * VW, count(k));
+        // beyond the row: the last whole piece, for nothing
+        return P::load(row + min(index(k) * VW, D - VW));
+    }
+    template <typename P, typename T>
+    __device__ __forceinline__ void store(T *row, int k, const float (&v)[VW]) const {
+        const int n = count(k);
+        if (n == VW) P::store(row + index(k) * VW, v);
+        else if (TAIL && n > 0) P::store(row + (int64_t)index(k) * VW, v, n);
+    }
+    __device__ __forceinline__ void weight(const float *w, int k, float (&v)[VW]) const {
+        const int n = count(k);
+        const float *p = w + (int64_t)index(k) * VW;
+        if (n == VW) {
+            typedef f32x4 mem __attribute__((aligned(4)));
+#pragma unroll
+            for (int j = 0; j < VW; j += 4) {
+                const f32x4 q = *reinterpret_cast<const mem *>(p + j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[j + i] = q[i];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < VW; ++j) v[j] = j < n ? p[j] : 0.f;
+        }
+    }
+};
+
+// 4 or 8 bytes at any alignment (through the caches, which make whole lines of
+// them: past them 16,384 x 7,168 takes 141 us instead of 134)
+__device__ __forceinline__ void store_words(uint8_t *p, const uint32_t (&q)[1])
+{
+    typedef uint32_t mem __attribute__((aligned(1)));
+    *reinterpret_cast<mem *>(p) = q[0];
+}
+__device__ __forceinline__ void store_words(uint8_t *p, const uint32_t (&q)[2])
+{
+    typedef uint32_t pair __attribute__((ext_vector_type(2)));
+    typedef pair mem __attribute__((aligned(1)));
+    *reinterpret_cast<mem *>(p) = pair{q[0], q[1]};
 }
 
 // Sums over a row's tpr threads (a power of two; a part of a wave, or whole
@@ -93,73 +141,70 @@ __device__ __forceinline__ int mx_scale(uint32_t amax_bits)
 }
 
 // ---------------------------------------------------------------- forward
-// Pieces of a row: thread i of its tpr has pieces i, i + tpr, ... (C of them).
-template <typename T, int VW, int C, bool ONCE, bool RES, bool MX>
+// C pieces a thread
+template <typename T, int VW, int C, bool ONCE, bool TAIL, bool RES, bool MX>
 __global__ void kda_rmsnorm_kernel(const T *x, const T *res, const float *w, int32_t rows, int32_t D, int32_t tpr,
                                    float eps, T *sum, T *out, uint8_t *mx, uint8_t *scales)
 {
     typedef Piece<T, VW, ONCE> P;
     __shared__ float red[16][1];
-    const int i0 = threadIdx.x & (tpr - 1);
+    const Pieces<VW, TAIL> pc{D, (int32_t)(threadIdx.x & (tpr - 1)), tpr};
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     const bool live = row < rows;
     const int64_t base = (live ? row : 0) * D;
-    const int32_t pieces = D / VW;
 
     typename P::raw xr[C], rr[C];
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-        const int32_t i = min(i0 + k * tpr, pieces - 1);
-        xr[k] = P::load(x + base + (int64_t)i * VW);
-        if (RES) rr[k] = P::load(res + base + (int64_t)i * VW);
+        xr[k] = pc.template load<P>(x + base, k);
+        if (RES) rr[k] = pc.template load<P>(res + base, k);
     }
     float r[C][VW], ss[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-        const bool have = i0 + k * tpr < pieces;
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
             r[k][j] = P::at(xr[k], j) + (RES ? P::at(rr[k], j) : 0.f);
-            if (have) ss[0] += r[k][j] * r[k][j];
+            if (pc.count(k) > 0) ss[0] += r[k][j] * r[k][j];
         }
-        if (RES && sum && have && live) P::store(sum + base + (int64_t)(i0 + k * tpr) * VW, r[k]);
+        if (RES && sum && live) pc.template store<P>(sum + base, k, r[k]);
     }
     row_sums<1>(ss, tpr, red);
     const float rstd = 1.f / sqrtf(ss[0] / D + eps);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-        const int32_t i = i0 + k * tpr;
-        const bool have = i < pieces;
+        const int32_t i = pc.index(k), n = pc.count(k);
         float g[VW];
-        if (w) load_weight<VW>(w, (int64_t)min(i, pieces - 1) * VW, g);
+        if (w) pc.weight(w, k, g);
 #pragma unroll
         for (int j = 0; j < VW; ++j) r[k][j] = r[k][j] * rstd * (w ? g[j] : 1.f);
-        if (out && have && live) P::store(out + base + (int64_t)i * VW, r[k]);
+        if (out && live) pc.template store<P>(out + base, k, r[k]);
         if (MX) {   // a block's MXB / VW pieces lie in consecutive lanes
             uint32_t top = 0;   // of the magnitudes' bits, so that a NaN is the largest
 #pragma unroll
-            for (int j = 0; j < VW; ++j) top = max(top, __float_as_uint(r[k][j]) & 0x7fffffffu);
-            if (!have) top = 0;
+            for (int j = 0; j < VW; ++j)
+                if (j < n) top = max(top, __float_as_uint(r[k][j]) & 0x7fffffffu);
 #pragma unroll
             for (int off = MXB / VW / 2; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
             const int sc = mx_scale(top);
-            if (have && live) {
+            if (n > 0 && live) {
                 if (i % (MXB / VW) == 0) scales[row * ((D + MXB - 1) / MXB) + i / (MXB / VW)] = (uint8_t)sc;
-                float q[VW];
+                uint32_t q[VW / 4];
 #pragma unroll
-                for (int j = 0; j < VW; ++j) q[j] = ldexpf(r[k][j], 127 - sc);
+                for (int j = 0; j < VW; j += 4) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = ldexpf(r[k][j + e], 127 - sc);
+                    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+                    q[j / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+                }
                 uint8_t *p = mx + base + (int64_t)i * VW;
-                if (VW == 1) {
-                    *p = (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[0], 0, false) & 0xff);
+                if (n == VW) {
+                    store_words(p, q);
                 } else {
-                    uint32_t word[VW >= 4 ? VW / 4 : 1];
 #pragma unroll
-                    for (int j = 0; j + 3 < VW; j += 4) {
-                        int v = __builtin_amdgcn_cvt_pk_fp8_f32(q[j], q[j + 1], 0, false);
-                        word[j / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[j + 2], q[j + 3], v, true);
-                    }
-                    if (VW == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(word[0], word[VW >= 8 ? 1 : 0]);
-                    else *reinterpret_cast<uint32_t *>(p) = word[0];
+                    for (int j = 0; j < VW; ++j)
+                        if (j < n) p[j] = (uint8_t)(q[j / 4] >> (8 * (j % 4)));
                 }
             }
         }
@@ -171,7 +216,7 @@ __global__ void kda_rmsnorm_kernel(const T *x, const T *res, const float *w, int
 // its part of the weight's gradient in registers; the parts of its rows side by
 // side are added through LDS, and those of all workgroups by the next kernel,
 // all in a fixed order.
-template <typename T, int VW, int C, bool ONCE, bool RES>
+template <typename T, int VW, int C, bool ONCE, bool TAIL, bool RES>
 __global__ void kda_rmsnorm_bwd_kernel(const T *x, const float *w, const T *dout, const T *dres, int32_t rows,
                                        int32_t D, int32_t tpr, float eps, T *dx, float *partial)
 {
@@ -179,13 +224,13 @@ __global__ void kda_rmsnorm_bwd_kernel(const T *x, const float *w, const T *dout
     extern __shared__ float fold[];
     __shared__ float red[16][2];
     const int i0 = threadIdx.x & (tpr - 1), slot = threadIdx.x / tpr, slots = blockDim.x / tpr;
-    const int32_t pieces = D / VW;
+    const Pieces<VW, TAIL> pc{D, i0, tpr};
     float dw[C][VW] = {}, g[C][VW];
 #pragma unroll
     for (int k = 0; k < C; ++k) {
 #pragma unroll
         for (int j = 0; j < VW; ++j) g[k][j] = 1.f;
-        if (w) load_weight<VW>(w, (int64_t)min(i0 + k * tpr, pieces - 1) * VW, g[k]);
+        if (w) pc.weight(w, k, g[k]);
     }
     for (int64_t row0 = (int64_t)blockIdx.x * slots; row0 < rows; row0 += (int64_t)gridDim.x * slots) {
         const int64_t row = row0 + slot;
@@ -194,15 +239,14 @@ __global__ void kda_rmsnorm_bwd_kernel(const T *x, const float *w, const T *dout
         typename P::raw xr[C], dr[C], rr[C];
 #pragma unroll
         for (int k = 0; k < C; ++k) {
-            const int64_t at = base + (int64_t)min(i0 + k * tpr, pieces - 1) * VW;
-            xr[k] = P::load(x + at);
-            dr[k] = P::load(dout + at);
-            if (RES) rr[k] = P::load(dres + at);
+            xr[k] = pc.template load<P>(x + base, k);
+            dr[k] = pc.template load<P>(dout + base, k);
+            if (RES) rr[k] = pc.template load<P>(dres + base, k);
         }
         float s[2] = {0.f, 0.f};   // r^2 and w dy r
 #pragma unroll
         for (int k = 0; k < C; ++k)
-            if (i0 + k * tpr < pieces)
+            if (pc.count(k) > 0)
 #pragma unroll
                 for (int j = 0; j < VW; ++j) {
                     const float r = P::at(xr[k], j);
@@ -220,7 +264,7 @@ __global__ void kda_rmsnorm_bwd_kernel(const T *x, const float *w, const T *dout
                 d[j] = rstd * (dy * g[k][j] - m * r) + (RES ? P::at(rr[k], j) : 0.f);
                 if (live) dw[k][j] += dy * (r * rstd);
             }
-            if (live && i0 + k * tpr < pieces) P::store(dx + base + (int64_t)(i0 + k * tpr) * VW, d);
+            if (live) pc.template store<P>(dx + base, k, d);
         }
     }
     if (!partial) return;
@@ -240,9 +284,9 @@ __global__ void kda_rmsnorm_bwd_kernel(const T *x, const float *w, const T *dout
     }
 #pragma unroll
     for (int k = 0; k < C; ++k)
-        if (i0 + k * tpr < pieces)
 #pragma unroll
-            for (int j = 0; j < VW; ++j) partial[(int64_t)blockIdx.x * D + (int64_t)(i0 + k * tpr) * VW + j] = dw[k][j];
+        for (int j = 0; j < VW; ++j)
+            if (j < pc.count(k)) partial[(int64_t)blockIdx.x * D + (int64_t)pc.index(k) * VW + j] = dw[k][j];
 }
 
 // dst[c] = the sum of src[i][c] over n rows
@@ -255,8 +299,6 @@ __global__ __launch_bounds__(COLSUM_THREADS) void kda_column_sums_kernel(const f
 }
 
 // ---------------------------------------------------------------- host
-inline bool on(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
-
 // Threads of a row and of a workgroup, for rows of `pieces`, at most C pieces a
 // thread, and blocks of `lanes` lanes that have to lie in one row's threads.
 struct RowShape {
@@ -269,70 +311,79 @@ inline RowShape row_shape(int32_t pieces, int C, int lanes)
     return {tpr, tpr < 256 ? 256 : tpr};
 }
 
-template <typename T, int VW, int C, bool ONCE, bool RES, bool MX>
+template <typename T, int C, bool ONCE, bool TAIL, bool RES, bool MX>
 hipError_t run_rmsnorm(const void *x, const void *res, const float *w, int32_t rows, int32_t D, float eps, void *sum,
                        void *out, uint8_t *mx, uint8_t *scales, hipStream_t s)
 {
-    const RowShape sh = row_shape(D / VW, C, MXB / VW);
+    constexpr int VW = 16 / sizeof(T);
+    const RowShape sh = row_shape((D + VW - 1) / VW, C, MXB / VW);
     const int64_t per = sh.threads / sh.tpr;
-    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, RES, MX>), dim3((unsigned)((rows + per - 1) / per)),
+    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)((rows + per - 1) / per)),
                        dim3(sh.threads), 0, s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, eps, (T *)sum,
                        (T *)out, mx, scales);
     return hipGetLastError();
 }
 
-template <typename T, int VW, int C, bool ONCE>
+template <typename T, int C, bool ONCE, bool TAIL>
 hipError_t rmsnorm_as(const void *x, const void *res, const float *w, int32_t rows, int32_t D, float eps, void *sum,
                       void *out, uint8_t *mx, uint8_t *scales, hipStream_t s)
 {
     if (res)
-        return mx ? run_rmsnorm<T, VW, C, ONCE, true, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s)
-                  : run_rmsnorm<T, VW, C, ONCE, true, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
-    return mx ? run_rmsnorm<T, VW, C, ONCE, false, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s)
-              : run_rmsnorm<T, VW, C, ONCE, false, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+        return mx ? run_rmsnorm<T, C, ONCE, TAIL, true, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s)
+                  : run_rmsnorm<T, C, ONCE, TAIL, true, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+    return mx ? run_rmsnorm<T, C, ONCE, TAIL, false, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s)
+              : run_rmsnorm<T, C, ONCE, TAIL, false, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+}
+
+// calls f with the number of pieces a thread, whether rows go past the caches,
+// and whether they end in a part of a piece, as compile-time values.  Few rows:
+// one piece a thread, so that a row's latency is short.
+template <typename T, int MOST, typename F> hipError_t with_shape(int32_t rows, int32_t D, F f)
+{
+    constexpr int VW = 16 / sizeof(T);
+    const int32_t pieces = (D + VW - 1) / VW;
+    auto tail = [&](auto c, auto once) {
+        return D % VW ? f(c, once, std::true_type()) : f(c, once, std::false_type());
+    };
+    const std::integral_constant<int, 1> one;
+    if (rows <= 512 && pieces <= 1024) return tail(one, std::false_type());
+    if (pieces <= 64) return tail(one, std::true_type());
+    return tail(std::integral_constant<int, MOST>(), std::true_type());
 }
 
 template <typename T>
 hipError_t rmsnorm(const void *x, const void *res, const float *w, int32_t rows, int32_t D, float eps, void *sum,
                    void *out, uint8_t *mx, uint8_t *scales, hipStream_t s)
 {
-    constexpr int VW = 16 / sizeof(T);
-    if (D % VW == 0 && on(x, 16) && on(res, 16) && on(w, 16) && on(sum, 16) && on(out, 16) && on(mx, VW)) {
-        const int32_t pieces = D / VW;
-        // few rows: one piece a thread, so that a row's latency is short
-        if (rows <= 512 && pieces <= 1024)
-            return rmsnorm_as<T, VW, 1, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
-        if (pieces <= 64) return rmsnorm_as<T, VW, 1, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
-        return rmsnorm_as<T, VW, 4, true>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
-    }
-    if (D <= 4096) return rmsnorm_as<T, 1, 4, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
-    return rmsnorm_as<T, 1, 16, false>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+    return with_shape<T, 4>(rows, D, [&](auto c, auto once, auto tail) {
+        return rmsnorm_as<T, c(), once(), tail()>(x, res, w, rows, D, eps, sum, out, mx, scales, s);
+    });
 }
 
 inline int32_t partials(int32_t rows) { return rows < MAX_PARTIALS ? rows : MAX_PARTIALS; }
 
-template <typename T, int VW, int C, bool ONCE>
+template <typename T, int C, bool ONCE, bool TAIL>
 hipError_t rmsnorm_backward_as(const void *x, const float *w, const void *dout, const void *dres, int32_t rows,
                                int32_t D, float eps, void *dx, float *dw, void *ws, hipStream_t s)
 {
-    const RowShape sh = row_shape(D / VW, C, 1);
+    constexpr int VW = 16 / sizeof(T);
+    const RowShape sh = row_shape((D + VW - 1) / VW, C, 1);
     const int64_t per = sh.threads / sh.tpr, groups = (rows + per - 1) / per;
     const unsigned blocks = (unsigned)(groups < MAX_PARTIALS ? groups : MAX_PARTIALS);
     const size_t lds = per > 1 ? sizeof(float) * sh.threads * C * VW : 0;
     if (blocks > 0) {
         if (dres)
-            hipLaunchKernelGGL((kda_rmsnorm_bwd_kernel<T, VW, C, ONCE, true>), dim3(blocks), dim3(sh.threads), lds, s,
-                               (const T *)x, w, (const T *)dout, (const T *)dres, rows, D, sh.tpr, eps, (T *)dx,
-                               dw ? (float *)ws : nullptr);
+            hipLaunchKernelGGL((kda_rmsnorm_bwd_kernel<T, VW, C, ONCE, TAIL, true>), dim3(blocks), dim3(sh.threads),
+                               lds, s, (const T *)x, w, (const T *)dout, (const T *)dres, rows, D, sh.tpr, eps,
+                               (T *)dx, dw ? (float *)ws : nullptr);
         else
-            hipLaunchKernelGGL((kda_rmsnorm_bwd_kernel<T, VW, C, ONCE, false>), dim3(blocks), dim3(sh.threads), lds, s,
-                               (const T *)x, w, (const T *)dout, (const T *)dres, rows, D, sh.tpr, eps, (T *)dx,
-                               dw ? (float *)ws : nullptr);
+            hipLaunchKernelGGL((kda_rmsnorm_bwd_kernel<T, VW, C, ONCE, TAIL, false>), dim3(blocks), dim3(sh.threads),
+                               lds, s, (const T *)x, w, (const T *)dout, (const T *)dres, rows, D, sh.tpr, eps,
+                               (T *)dx, dw ? (float *)ws : nullptr);
     }
     if (dw)
         hipLaunchKernelGGL(kda_column_sums_kernel, dim3((unsigned)((D + COLSUM_COLS - 1) / COLSUM_COLS)),
-                           dim3(COLSUM_THREADS), 0, s,
-                           (const float *)ws, (int32_t)blocks, (int64_t)D, dw);
+                           dim3(COLSUM_THREADS), 0, s, (const float *)ws, (int32_t)blocks, (int64_t)D, dw);
     return hipGetLastError();
 }
 
@@ -340,17 +391,10 @@ template <typename T>
 hipError_t rmsnorm_backward(const void *x, const float *w, const void *dout, const void *dres, int32_t rows, int32_t D,
                             float eps, void *dx, float *dw, void *ws, hipStream_t s)
 {
-    constexpr int VW = 16 / sizeof(T);
-    if (D % VW == 0 && on(x, 16) && on(dout, 16) && on(dres, 16) && on(w, 16) && on(dx, 16)) {
-        const int32_t pieces = D / VW;
-        if (rows <= 512 && pieces <= 1024)
-            return rmsnorm_backward_as<T, VW, 1, false>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
-        if (pieces <= 64) return rmsnorm_backward_as<T, VW, 1, true>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
-        // two pieces of eight or four of four: more would not fit the registers
-        return rmsnorm_backward_as<T, VW, 16 / VW, true>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
-    }
-    if (D <= 4096) return rmsnorm_backward_as<T, 1, 4, false>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
-    return rmsnorm_backward_as<T, 1, 16, false>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
+    // two pieces of eight or four of four: more would not fit the registers
+    return with_shape<T, (int)sizeof(T)>(rows, D, [&](auto c, auto once, auto tail) {
+        return rmsnorm_backward_as<T, c(), once(), tail()>(x, w, dout, dres, rows, D, eps, dx, dw, ws, s);
+    });
 }
 
 }  // namespace kda

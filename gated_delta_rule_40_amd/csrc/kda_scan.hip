@@ -46,6 +46,7 @@ struct Chain {
     uint64_t *tile, *block;           // [index][D]: tiles' runs, states that enter blocks
     int32_t ntiles;
     int64_t D;
+    int32_t width;                    // channels of a column
 };
 
 struct Run {
@@ -98,7 +99,7 @@ __device__ __forceinline__ Run gather(const uint64_t *p, int64_t D, int m)
 // Roles of a workgroup's threads in passing a state on: CB threads each, one a
 // channel.  Each role joins GATHER of the tiles of the block before this one.
 template <int CB> struct Roles {
-    static constexpr int N = NTH / CB < 4 ? NTH / CB : 4;
+    static constexpr int N = NTH / CB;
     static constexpr int BLOCK = N * GATHER;   // tiles of a block
 };
 
@@ -113,7 +114,7 @@ __device__ __forceinline__ void pass_on(const Chain &ch, int k, int64_t c0, bool
 {
     constexpr int N = Roles<CB>::N, BLOCK = Roles<CB>::BLOCK;
     const int c = threadIdx.x % CB, role = threadIdx.x / CB;
-    const bool in = c0 + c / V * V < ch.D;
+    const bool in = c / V * V < ch.width && c0 + c / V * V < ch.D;
     const int place = k % BLOCK, block = k / BLOCK;   // the tile's place in its block
     const bool last = place == BLOCK - 1;
     const int64_t ci = min(c0 + c / V * V, ch.D - V) + c % V;
@@ -273,7 +274,7 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
     if (sq.T == 0) {
         if (fin && w == 0)
             for (int32_t n = 0; n < sq.N; ++n)
-                for (int64_t c = (int64_t)col * CB + lane; c < min(D, (int64_t)(col + 1) * CB); c += 64)
+                for (int64_t c = (int64_t)col * ch.width + lane; c < min(D, (int64_t)(col + 1) * ch.width); c += 64)
                     fin[n * D + c] = init ? init[n * D + c] : 0.f;
         return;
     }
@@ -285,8 +286,8 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
         __syncthreads();
         k = __builtin_amdgcn_readfirstlane((int)s_tile);
     }
-    const int64_t c0 = (int64_t)col * CB, c = min(c0 + lane * V, D - V);
-    const bool in = c0 + lane * V < D;
+    const int64_t c0 = (int64_t)col * ch.width, c = min(c0 + lane * V, D - V);
+    const bool in = lane * V < ch.width && c0 + lane * V < D;
     XR xr[L];
     GR gr[L];
     const int32_t t0 = k * TILE + w * L;
@@ -414,7 +415,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
     if (sq.T == 0) {
         if (dinit && w == 0)
             for (int32_t n = 0; n < sq.N; ++n)
-                for (int64_t c = (int64_t)col * CB + lane; c < min(D, (int64_t)(col + 1) * CB); c += 64)
+                for (int64_t c = (int64_t)col * ch.width + lane; c < min(D, (int64_t)(col + 1) * ch.width); c += 64)
                     dinit[n * D + c] = dfin ? dfin[n * D + c] : 0.f;
         return;
     }
@@ -426,8 +427,8 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
         __syncthreads();
         kb = __builtin_amdgcn_readfirstlane((int)s_tile);
     }
-    const int64_t c0 = (int64_t)col * CB, c = min(c0 + lane * V, D - V);
-    const bool in = c0 + lane * V < D;
+    const int64_t c0 = (int64_t)col * ch.width, c = min(c0 + lane * V, D - V);
+    const bool in = lane * V < ch.width && c0 + lane * V < D;
     XR xr[L], dr[L];
     GR gr[L];
     const int k = ch.ntiles - 1 - kb;
@@ -579,7 +580,7 @@ __global__ void kda_scan_fill_kernel(uint64_t *p, int64_t n)
 // ---------------------------------------------------------------- host
 inline int32_t tiles_of(int32_t T) { return T > 0 ? (int32_t)(((int64_t)T + TILE - 1) / TILE) : 1; }
 
-// Words of a chain: counters of up to ceil(D / 64) columns, then the tiles'
+// Words of a chain: counters of the columns (of 32 channels at least), then the tiles'
 // runs and the states that enter blocks (of 16 tiles at least).  A single tile
 // needs none.
 struct ChainLayout {
@@ -590,7 +591,7 @@ inline ChainLayout chain_layout(int32_t T, int32_t D)
     const size_t nt = tiles_of(T), d = D;
     ChainLayout l = {};
     if (nt <= 1) return l;
-    l.tile = ((d + 63) / 64 + 1) / 2;
+    l.tile = ((d + 31) / 32 + 1) / 2;
     l.block = l.tile + nt * d;
     l.words = l.block + (nt / Roles<256>::BLOCK + 1) * d;
     return l;
@@ -598,7 +599,7 @@ inline ChainLayout chain_layout(int32_t T, int32_t D)
 inline Chain chain_at(uint64_t *p, int32_t T, int32_t D)
 {
     const ChainLayout l = chain_layout(T, D);
-    return {reinterpret_cast<uint32_t *>(p), p + l.tile, p + l.block, tiles_of(T), (int64_t)D};
+    return {reinterpret_cast<uint32_t *>(p), p + l.tile, p + l.block, tiles_of(T), (int64_t)D, 0};
 }
 
 inline hipError_t fill_chain(uint64_t *p, size_t words, hipStream_t s)
@@ -612,9 +613,10 @@ inline hipError_t fill_chain(uint64_t *p, size_t words, hipStream_t s)
 
 template <typename T, int V>
 hipError_t run_scan(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D, void *out, float *fin,
-                    float *chk, const Chain &ch, hipStream_t s)
+                    float *chk, Chain ch, hipStream_t s)
 {
-    const int32_t cols = (int32_t)(((int64_t)D + 64 * V - 1) / (64 * V));
+    ch.width = kda_column_width(D, V);
+    const int32_t cols = (D - 1) / ch.width + 1;
     hipLaunchKernelGGL((kda_scan_kernel<T, V>), dim3((unsigned)((int64_t)cols * ch.ntiles)), dim3(NTH), 0, s,
                        (const T *)x, g, init, sq, (int64_t)D, cols, (T *)out, fin, chk, ch);
     return hipGetLastError();
@@ -624,23 +626,23 @@ template <typename T>
 hipError_t scan(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D, void *out, float *fin,
                 float *chk, const Chain &ch, hipStream_t s)
 {
-    // V channels a lane where a last lane that overlaps its neighbour has one in
-    // the same workgroup (two workgroups must not share a state).
-    auto whole = [&](int V) { return D % (64 * V) == 0 || D % (64 * V) >= V; };
     // Four channels a lane for bf16 where that leaves two workgroups for every
-    // CU; fp32 tokens of four would not fit the registers.
-    if (sizeof(T) == 2 && whole(4) && (int64_t)ch.ntiles * ((D + 255) / 256) >= 512)
+    // CU and few lanes idle (fp32 tokens of four would not fit the registers);
+    // one for rows of up to 64.
+    const int64_t wide = ((int64_t)D + 255) / 256;
+    if (sizeof(T) == 2 && ch.ntiles * wide >= 512 && 4 * (int64_t)D >= 3 * 256 * wide)
         return run_scan<T, sizeof(T) == 2 ? 4 : 2>(x, g, init, sq, D, out, fin, chk, ch, s);
-    if (whole(2)) return run_scan<T, 2>(x, g, init, sq, D, out, fin, chk, ch, s);
+    if (D > 64) return run_scan<T, 2>(x, g, init, sq, D, out, fin, chk, ch, s);
     return run_scan<T, 1>(x, g, init, sq, D, out, fin, chk, ch, s);
 }
 
 template <typename T, int V>
 hipError_t run_scan_backward(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D,
                              const void *dout, const float *dfin, const float *chk, void *dx, float *dg, float *dinit,
-                             const Chain &ch, hipStream_t s)
+                             Chain ch, hipStream_t s)
 {
-    const int32_t cols = (int32_t)(((int64_t)D + 64 * V - 1) / (64 * V));
+    ch.width = kda_column_width(D, V);
+    const int32_t cols = (D - 1) / ch.width + 1;
     hipLaunchKernelGGL((kda_scan_bwd_kernel<T, V>), dim3((unsigned)((int64_t)cols * ch.ntiles)), dim3(NTH), 0, s,
                        (const T *)x, g, init, sq, (int64_t)D, cols, (const T *)dout, dfin, chk, (T *)dx, dg, dinit,
                        ch);
@@ -652,7 +654,7 @@ hipError_t scan_backward(const void *x, const float *g, const float *init, const
                          const float *dfin, const float *chk, void *dx, float *dg, float *dinit, const Chain &ch,
                          hipStream_t s)
 {
-    if (D % 128 != 1) return run_scan_backward<T, 2>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
+    if (D > 64) return run_scan_backward<T, 2>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
     return run_scan_backward<T, 1>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
 }
 
