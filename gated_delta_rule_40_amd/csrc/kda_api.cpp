@@ -755,6 +755,6 @@ const char *kda_status_string(kda_status status)
     return "unknown kda_status";
 }
 
-int32_t kda_version(void) { return 100; }
+int32_t kda_version(void) { return 200; }
 
 }  // extern "C"

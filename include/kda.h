@@ -382,8 +382,10 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  * the same log-decay gate, no keys.
  *
  *   x             [total_tokens, channels]        dtype
- *   g             [total_tokens, channels]        fp32, log-decay, any value
- *                 (-infinity: the state is dropped)
+ *   g             [total_tokens, channels]        fp32, log-decay; -infinity
+ *                 drops the state.  Growth (g > 0) is taken as long as g sums
+ *                 to less than 88 over any 1,024 tokens of a channel: products
+ *                 of exp(g) over so many are formed.
  *   initial_state [num_seqs, channels]            fp32, or NULL for zeros
  *   cu_seqlens    [num_seqs + 1]                  int32, DEVICE (as kda_prefill)
  *   out           [total_tokens, channels]        dtype; rows owned by a
