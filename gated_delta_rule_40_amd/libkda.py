@@ -29,6 +29,7 @@ The operators around the recurrence in a layer:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -381,29 +382,31 @@ _DTYPE_CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 _F32 = torch.float32
 
 
-def _bad(name, t, ref, dtype, shape) -> None:
-    _require(torch.is_tensor(t) and t.is_cuda and t.device == ref.device,
-             "%s must be a tensor on %s" % (name, ref.device))
+def _bad(name, t, dev, dtype, shape) -> None:
+    _require(torch.is_tensor(t) and t.is_cuda and t.get_device() == dev, "%s must be a tensor on cuda:%d" % (name, dev))
     _require(t.dtype == dtype, "%s must be %s, got %s" % (name, dtype, t.dtype))
     _require(tuple(t.shape) == tuple(shape), "%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
     raise ValueError("%s must be contiguous" % name)
 
 
-def _addr(name, t, ref, dtype, shape) -> int:
-    """The address of a contiguous tensor of this type and shape on ref's device, after checking that it is one."""
-    if not (isinstance(t, torch.Tensor) and t.get_device() == ref.get_device() and t.dtype is dtype and
-            t.shape == shape and t.is_contiguous()):
-        _bad(name, t, ref, dtype, shape)
-    return t.data_ptr()
+def _addr(name, t, dev, dtype, shape) -> int:
+    """The address of a contiguous tensor of this type and shape on device `dev`, after checking that it is one."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:   # no tensor
+        pass
+    _bad(name, t, dev, dtype, shape)
 
 
-def _addr_if(name, t, ref, dtype, shape) -> Optional[int]:
+def _addr_if(name, t, dev, dtype, shape) -> Optional[int]:
     """As _addr, for an argument that may be None."""
-    return None if t is None else _addr(name, t, ref, dtype, shape)
+    return None if t is None else _addr(name, t, dev, dtype, shape)
 
 
 def _rows(name, x):
-    """A contiguous device tensor of rows in a supported type: its address, type code, shape, rows and row length."""
+    """A contiguous device tensor of rows in a supported type: its address, device, type code, shape, rows and row
+    length."""
     _require(isinstance(x, torch.Tensor) and x.is_cuda, "%s must be a device tensor" % name)
     code = _DTYPE_CODE.get(x.dtype)
     if code is None:
@@ -417,49 +420,57 @@ def _rows(name, x):
     if rows > _MOST or D > _MOST or not x.is_contiguous():
         _require(x.is_contiguous(), "%s must be contiguous" % name)
         raise ValueError("%s has too many rows or channels" % name)
-    return x.data_ptr(), code, shape, rows, D
+    return x.data_ptr(), x.get_device(), code, shape, rows, D
 
 
-def _cu(cu_seqlens, ref):
-    _require(isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda and cu_seqlens.device == ref.device,
-             "cu_seqlens must be a tensor on %s" % ref.device)
-    _require(cu_seqlens.dtype == torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] >= 1 and
-             cu_seqlens.is_contiguous(), "cu_seqlens must be contiguous int32 [N + 1]")
-    return cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1
+def _cu(cu_seqlens, dev):
+    """cu_seqlens' address and the number of sequences."""
+    _require(isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.get_device() == dev,
+             "cu_seqlens must be a tensor on the inputs' device")
+    n = cu_seqlens.numel()
+    _require(cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and n >= 1 and cu_seqlens.is_contiguous(),
+             "cu_seqlens must be contiguous int32 [N + 1]")
+    return cu_seqlens.data_ptr(), n - 1
 
 
-def _empty(shape, dtype, ref, stream) -> torch.Tensor:
-    """A new tensor on ref's device.  Given another stream than the current one it comes from that stream's pool: what
+def _empty(shape, dtype, dev, stream) -> torch.Tensor:
+    """A new tensor on device `dev`.  Given another stream than the current one it comes from that stream's pool: what
     the current stream still does with memory freed there is not ordered before the call."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=ref.device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
-                                           device=ref.device)
+                                           device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=ref.device)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _workspace(workspace, need, ref, stream):
-    """The given workspace, or a new one of `need` bytes: (tensor, address, bytes)."""
+@functools.lru_cache(maxsize=1024)
+def _need(query: str, *sizes) -> int:
+    """Bytes of workspace, as the library's function `query` says: it goes by the sizes alone."""
+    return getattr(load(), query)(*sizes)
+
+
+def _workspace(workspace, dev, stream, query, *sizes):
+    """The given workspace, or a new one of the size that `query` says: (tensor, address, bytes)."""
     if workspace is None:
+        need = _need(query, *sizes)
         if need == 0:
             return None, None, 0
-        workspace = _empty((need,), torch.uint8, ref, stream)
-    else:
-        _require(isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.device == ref.device and
-                 workspace.is_contiguous(), "workspace must be a contiguous tensor on %s" % ref.device)
+        workspace = _empty(need, torch.uint8, dev, stream)
+        return workspace, workspace.data_ptr(), need
+    _require(isinstance(workspace, torch.Tensor) and workspace.get_device() == dev and workspace.is_contiguous(),
+             "workspace must be a contiguous tensor on the inputs' device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _call(fn, ref, stream, *args) -> None:
-    """fn(*args, stream) with ref's device current; stream None: that device's current stream."""
-    index = ref.get_device()
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(index):
-            return _call(fn, ref, stream, *args)
+def _call(fn, dev, stream, *args) -> None:
+    """fn(*args, stream) with device `dev` current; stream None: that device's current stream."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, stream, *args)
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)
+        raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     status = fn(*args, raw)
@@ -487,23 +498,23 @@ def kda_scan_prefill(x, g, initial_state, cu_seqlens, out, final_state, checkpoi
     [ceil(T / 128), ...channels] fp32 or None, the states kda_scan_backward
     starts from; workspace: kda_scan_workspace_size(...) bytes, allocated if
     None."""
-    px, code, shape, T, D = _rows("x", x)
-    pcu, N = _cu(cu_seqlens, x)
+    px, dev, code, shape, T, D = _rows("x", x)
+    pcu, N = _cu(cu_seqlens, dev)
     state = (N, *shape[1:])
     lib = _lib or load()
-    args = (px, _addr("g", g, x, _F32, shape), _addr_if("initial_state", initial_state, x, _F32, state), pcu, N, T, D,
-            code, _addr("out", out, x, x.dtype, shape), _addr_if("final_state", final_state, x, _F32, state),
-            _addr_if("checkpoints", checkpoints, x, _F32, (-(-T // KDA_SCAN_TILE), *shape[1:])))
-    ws, pws, nbytes = _workspace(workspace, lib.kda_scan_workspace_size(N, T, D, code), x, stream)
-    _call(lib.kda_scan_prefill, x, stream, *args, pws, nbytes)
+    args = (px, _addr("g", g, dev, _F32, shape), _addr_if("initial_state", initial_state, dev, _F32, state), pcu, N, T, D,
+            code, _addr("out", out, dev, x.dtype, shape), _addr_if("final_state", final_state, dev, _F32, state),
+            _addr_if("checkpoints", checkpoints, dev, _F32, (-(-T // KDA_SCAN_TILE), *shape[1:])))
+    ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_scan_workspace_size", N, T, D, code)
+    _call(lib.kda_scan_prefill, dev, stream, *args, pws, nbytes)
 
 
 def kda_scan_decode_step(x, g, state_inout, out, stream=None) -> None:
     """One token per sequence, state updated in place.  x, out: [N, ...channels];
     g, state_inout: the same shape, fp32."""
-    px, code, shape, N, D = _rows("x", x)
-    _call((_lib or load()).kda_scan_decode_step, x, stream, px, _addr("g", g, x, _F32, shape),
-          _addr("state_inout", state_inout, x, _F32, shape), N, D, code, _addr("out", out, x, x.dtype, shape))
+    px, dev, code, shape, N, D = _rows("x", x)
+    _call((_lib or load()).kda_scan_decode_step, dev, stream, px, _addr("g", g, dev, _F32, shape),
+          _addr("state_inout", state_inout, dev, _F32, shape), N, D, code, _addr("out", out, dev, x.dtype, shape))
 
 
 def kda_scan_backward_workspace_size(num_seqs: int, total_tokens: int, channels: int, dtype=torch.bfloat16,
@@ -513,10 +524,10 @@ def kda_scan_backward_workspace_size(num_seqs: int, total_tokens: int, channels:
                                                        int(has_checkpoints)))
 
 
-def _grads(given, ref, want, stream) -> dict:
+def _grads(given, dev, want, stream) -> dict:
     """The gradients' tensors: those given, or new ones.  want: name -> (dtype, shape), or None (left out)."""
     if given is None:
-        return {name: None if w is None else _empty(w[1], w[0], ref, stream) for name, w in want.items()}
+        return {name: None if w is None else _empty(w[1], w[0], dev, stream) for name, w in want.items()}
     return given
 
 
@@ -527,28 +538,28 @@ def kda_scan_backward(x, g, initial_state, cu_seqlens, dout, dfinal=None, checkp
     kda_scan_prefill wrote for the same inputs; without them the states are
     computed again.  Returns a dict of dx (x's type), dg (fp32) and dinit (fp32;
     None unless want_dinit); ``grads`` may supply the tensors."""
-    px, code, shape, T, D = _rows("x", x)
-    pcu, N = _cu(cu_seqlens, x)
+    px, dev, code, shape, T, D = _rows("x", x)
+    pcu, N = _cu(cu_seqlens, dev)
     dt, state = x.dtype, (N, *shape[1:])
     lib = _lib or load()
-    grads = _grads(grads, x, {"dx": (dt, shape), "dg": (_F32, shape), "dinit": (_F32, state) if want_dinit else None},
+    grads = _grads(grads, dev, {"dx": (dt, shape), "dg": (_F32, shape), "dinit": (_F32, state) if want_dinit else None},
                    stream)
-    args = (px, _addr("g", g, x, _F32, shape), _addr_if("initial_state", initial_state, x, _F32, state), pcu, N, T, D,
-            code, _addr("dout", dout, x, dt, shape), _addr_if("dfinal", dfinal, x, _F32, state),
-            _addr_if("checkpoints", checkpoints, x, _F32, (-(-T // KDA_SCAN_TILE), *shape[1:])),
-            _addr("grads['dx']", grads.get("dx"), x, dt, shape), _addr("grads['dg']", grads.get("dg"), x, _F32, shape),
-            _addr_if("grads['dinit']", grads.get("dinit"), x, _F32, state))
-    ws, pws, nbytes = _workspace(
-        workspace, lib.kda_scan_backward_workspace_size(N, T, D, code, int(checkpoints is not None)), x, stream)
-    _call(lib.kda_scan_backward, x, stream, *args, pws, nbytes)
+    args = (px, _addr("g", g, dev, _F32, shape), _addr_if("initial_state", initial_state, dev, _F32, state), pcu, N, T, D,
+            code, _addr("dout", dout, dev, dt, shape), _addr_if("dfinal", dfinal, dev, _F32, state),
+            _addr_if("checkpoints", checkpoints, dev, _F32, (-(-T // KDA_SCAN_TILE), *shape[1:])),
+            _addr("grads['dx']", grads.get("dx"), dev, dt, shape), _addr("grads['dg']", grads.get("dg"), dev, _F32, shape),
+            _addr_if("grads['dinit']", grads.get("dinit"), dev, _F32, state))
+    ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_scan_backward_workspace_size", N, T, D, code,
+                                 int(checkpoints is not None))
+    _call(lib.kda_scan_backward, dev, stream, *args, pws, nbytes)
     return grads
 
 
-def _conv_weight(weight, x, shape):
+def _conv_weight(weight, dev, shape):
     """The weight's address and width: [...channels, width] fp32 for rows of this shape."""
     _require(isinstance(weight, torch.Tensor) and weight.dim() == len(shape), "weight must be [...channels, width]")
     W = weight.shape[-1]
-    return _addr("weight", weight, x, _F32, (*shape[1:], W)), W
+    return _addr("weight", weight, dev, _F32, (*shape[1:], W)), W
 
 
 def kda_conv_prefill(x, weight, bias, initial_state, cu_seqlens, out, final_state, silu: bool = True,
@@ -557,23 +568,23 @@ def kda_conv_prefill(x, weight, bias, initial_state, cu_seqlens, out, final_stat
     False.  x, out: [T, ...channels]; weight: [...channels, width] fp32, width 2
     to 4; bias: [...channels] fp32 or None; initial_state / final_state:
     [N, width - 1, ...channels] of x's type or None."""
-    px, code, shape, T, D = _rows("x", x)
-    pcu, N = _cu(cu_seqlens, x)
-    pw, W = _conv_weight(weight, x, shape)
+    px, dev, code, shape, T, D = _rows("x", x)
+    pcu, N = _cu(cu_seqlens, dev)
+    pw, W = _conv_weight(weight, dev, shape)
     dt, state = x.dtype, (N, W - 1, *shape[1:])
-    _call((_lib or load()).kda_conv_prefill, x, stream, px, pw, _addr_if("bias", bias, x, _F32, shape[1:]),
-          _addr_if("initial_state", initial_state, x, dt, state), pcu, N, T, D, W, int(silu), code,
-          _addr("out", out, x, dt, shape), _addr_if("final_state", final_state, x, dt, state))
+    _call((_lib or load()).kda_conv_prefill, dev, stream, px, pw, _addr_if("bias", bias, dev, _F32, shape[1:]),
+          _addr_if("initial_state", initial_state, dev, dt, state), pcu, N, T, D, W, int(silu), code,
+          _addr("out", out, dev, dt, shape), _addr_if("final_state", final_state, dev, dt, state))
 
 
 def kda_conv_decode_step(x, weight, bias, state_inout, out, silu: bool = True, stream=None) -> None:
     """One token per sequence, state shifted in place.  x, out: [N, ...channels];
     state_inout: [N, width - 1, ...channels] of x's type."""
-    px, code, shape, N, D = _rows("x", x)
-    pw, W = _conv_weight(weight, x, shape)
-    _call((_lib or load()).kda_conv_decode_step, x, stream, px, pw, _addr_if("bias", bias, x, _F32, shape[1:]),
-          _addr("state_inout", state_inout, x, x.dtype, (N, W - 1, *shape[1:])), N, D, W, int(silu), code,
-          _addr("out", out, x, x.dtype, shape))
+    px, dev, code, shape, N, D = _rows("x", x)
+    pw, W = _conv_weight(weight, dev, shape)
+    _call((_lib or load()).kda_conv_decode_step, dev, stream, px, pw, _addr_if("bias", bias, dev, _F32, shape[1:]),
+          _addr("state_inout", state_inout, dev, x.dtype, (N, W - 1, *shape[1:])), N, D, W, int(silu), code,
+          _addr("out", out, dev, x.dtype, shape))
 
 
 def kda_conv_backward_workspace_size(num_seqs: int, total_tokens: int, channels: int, width: int,
@@ -588,22 +599,22 @@ def kda_conv_backward(x, weight, bias, initial_state, cu_seqlens, dout, dfinal=N
     [N, width - 1, ...channels] (x's type) or None.  Returns a dict of dx and
     dinit (x's type; dinit None unless want_dinit), dweight and dbias (fp32;
     dbias None without a bias); ``grads`` may supply the tensors."""
-    px, code, shape, T, D = _rows("x", x)
-    pcu, N = _cu(cu_seqlens, x)
-    pw, W = _conv_weight(weight, x, shape)
+    px, dev, code, shape, T, D = _rows("x", x)
+    pcu, N = _cu(cu_seqlens, dev)
+    pw, W = _conv_weight(weight, dev, shape)
     dt, row, state = x.dtype, shape[1:], (N, W - 1, *shape[1:])
     lib = _lib or load()
-    grads = _grads(grads, x, {"dx": (dt, shape), "dweight": (_F32, (*row, W)),
+    grads = _grads(grads, dev, {"dx": (dt, shape), "dweight": (_F32, (*row, W)),
                               "dbias": None if bias is None else (_F32, row),
                               "dinit": (dt, state) if want_dinit else None}, stream)
-    args = (px, pw, _addr_if("bias", bias, x, _F32, row), _addr_if("initial_state", initial_state, x, dt, state), pcu,
-            N, T, D, W, int(silu), code, _addr("dout", dout, x, dt, shape), _addr_if("dfinal", dfinal, x, dt, state),
-            _addr("grads['dx']", grads.get("dx"), x, dt, shape),
-            _addr("grads['dweight']", grads.get("dweight"), x, _F32, (*row, W)),
-            _addr_if("grads['dbias']", grads.get("dbias"), x, _F32, row),
-            _addr_if("grads['dinit']", grads.get("dinit"), x, dt, state))
-    ws, pws, nbytes = _workspace(workspace, lib.kda_conv_backward_workspace_size(N, T, D, W, code), x, stream)
-    _call(lib.kda_conv_backward, x, stream, *args, pws, nbytes)
+    args = (px, pw, _addr_if("bias", bias, dev, _F32, row), _addr_if("initial_state", initial_state, dev, dt, state), pcu,
+            N, T, D, W, int(silu), code, _addr("dout", dout, dev, dt, shape), _addr_if("dfinal", dfinal, dev, dt, state),
+            _addr("grads['dx']", grads.get("dx"), dev, dt, shape),
+            _addr("grads['dweight']", grads.get("dweight"), dev, _F32, (*row, W)),
+            _addr_if("grads['dbias']", grads.get("dbias"), dev, _F32, row),
+            _addr_if("grads['dinit']", grads.get("dinit"), dev, dt, state))
+    ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_conv_backward_workspace_size", N, T, D, W, code)
+    _call(lib.kda_conv_backward, dev, stream, *args, pws, nbytes)
     return grads
 
 
@@ -618,7 +629,7 @@ def _norm_rows(name, x):
     _require(D > 0 and x.is_contiguous(), "%s must be contiguous, [..., channels]" % name)
     rows = shape[0] if len(shape) == 2 else x.numel() // D
     _require(rows <= _MOST and D <= _MOST, "%s has too many rows or channels" % name)
-    return x.data_ptr(), code, shape, rows, D
+    return x.data_ptr(), x.get_device(), code, shape, rows, D
 
 
 def kda_rmsnorm(x, weight, out=None, residual=None, residual_out=None, out_mx=None, scales=None, eps: float = 1e-6,
@@ -629,18 +640,18 @@ def kda_rmsnorm(x, weight, out=None, residual=None, residual_out=None, out_mx=No
     float8_e4m3fn and scales: [..., ceil(channels / 32)] uint8 or
     float8_e8m0fnu, y in 8 bits with a power-of-two scale for every 32
     channels."""
-    px, code, shape, rows, D = _norm_rows("x", x)
+    px, dev, code, shape, rows, D = _norm_rows("x", x)
     dt = x.dtype
     mx = sc = None
     if out_mx is not None or scales is not None:
         _require(isinstance(out_mx, torch.Tensor) and isinstance(scales, torch.Tensor),
                  "out_mx and scales go together")
-        mx = _addr("out_mx", out_mx, x, torch.uint8 if out_mx.dtype is torch.uint8 else torch.float8_e4m3fn, shape)
-        sc = _addr("scales", scales, x, torch.uint8 if scales.dtype is torch.uint8 else torch.float8_e8m0fnu,
+        mx = _addr("out_mx", out_mx, dev, torch.uint8 if out_mx.dtype is torch.uint8 else torch.float8_e4m3fn, shape)
+        sc = _addr("scales", scales, dev, torch.uint8 if scales.dtype is torch.uint8 else torch.float8_e8m0fnu,
                    (*shape[:-1], -(-D // KDA_MX_BLOCK)))
-    _call((_lib or load()).kda_rmsnorm, x, stream, px, _addr_if("residual", residual, x, dt, shape),
-          _addr_if("weight", weight, x, _F32, (D,)), rows, D, eps, code,
-          _addr_if("residual_out", residual_out, x, dt, shape), _addr_if("out", out, x, dt, shape), mx, sc)
+    _call((_lib or load()).kda_rmsnorm, dev, stream, px, _addr_if("residual", residual, dev, dt, shape),
+          _addr_if("weight", weight, dev, _F32, (D,)), rows, D, eps, code,
+          _addr_if("residual_out", residual_out, dev, dt, shape), _addr_if("out", out, dev, dt, shape), mx, sc)
 
 
 def kda_rmsnorm_backward_workspace_size(rows: int, channels: int, dtype=torch.bfloat16) -> int:
@@ -654,15 +665,17 @@ def kda_rmsnorm_backward(x, weight, dout, dresidual=None, eps: float = 1e-6, gra
     where it added one) and dout; dresidual, a gradient of x from elsewhere, is
     added.  Returns a dict of dx (x's type) and dweight (fp32; None without a
     weight); ``grads`` may supply the tensors."""
-    px, code, shape, rows, D = _norm_rows("x", x)
+    px, dev, code, shape, rows, D = _norm_rows("x", x)
     dt = x.dtype
     lib = _lib or load()
-    grads = _grads(grads, x, {"dx": (dt, shape), "dweight": None if weight is None else (_F32, (D,))}, stream)
-    pdw = _addr_if("grads['dweight']", grads.get("dweight"), x, _F32, (D,))
-    args = (px, _addr_if("weight", weight, x, _F32, (D,)), _addr("dout", dout, x, dt, shape),
-            _addr_if("dresidual", dresidual, x, dt, shape), rows, D, eps, code,
-            _addr("grads['dx']", grads.get("dx"), x, dt, shape), pdw)
-    ws, pws, nbytes = _workspace(
-        workspace, lib.kda_rmsnorm_backward_workspace_size(rows, D, code) if pdw is not None else 0, x, stream)
-    _call(lib.kda_rmsnorm_backward, x, stream, *args, pws, nbytes)
+    grads = _grads(grads, dev, {"dx": (dt, shape), "dweight": None if weight is None else (_F32, (D,))}, stream)
+    pdw = _addr_if("grads['dweight']", grads.get("dweight"), dev, _F32, (D,))
+    args = (px, _addr_if("weight", weight, dev, _F32, (D,)), _addr("dout", dout, dev, dt, shape),
+            _addr_if("dresidual", dresidual, dev, dt, shape), rows, D, eps, code,
+            _addr("grads['dx']", grads.get("dx"), dev, dt, shape), pdw)
+    ws = pws = None
+    nbytes = 0
+    if pdw is not None:
+        ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_rmsnorm_backward_workspace_size", rows, D, code)
+    _call(lib.kda_rmsnorm_backward, dev, stream, *args, pws, nbytes)
     return grads
