@@ -114,7 +114,8 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
     if (t0 < tend) {
         int32_t n = win.owner(t0);
         if (n < 0) return;                     // (cu_seqlens against its rules)
-        int32_t s = win.at(n), next = max(win.at(n + 1), t0 + 1), t = t0;
+        // (held to what a valid cu_seqlens gives: s <= t0 < next)
+        int32_t s = min(win.at(n), t0), next = max(win.at(n + 1), t0 + 1), t = t0;
         // tokens that belong to the wave of their sequence's start
         if (s < t0 && t0 - s < W - 1) t = min(s + W - 1, next);
         const int32_t stop = min(t1, tend);
@@ -286,7 +287,8 @@ void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t
         if (n >= 0) {
             Weights<W, V> wt;
             wt.load(a, c);
-            int32_t s = win.at(n), next = max(win.at(n + 1), t0 + 1), t = t0;
+            // (held to what a valid cu_seqlens gives: s <= t0 < next)
+            int32_t s = min(win.at(n), t0), next = max(win.at(n + 1), t0 + 1), t = t0;
             float before[W - 1][V];   // the last W - 1 inputs, unpacked once
             float acc[W - 1][V] = {};
             auto enter = [&]() {

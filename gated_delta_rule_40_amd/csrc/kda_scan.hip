@@ -115,8 +115,10 @@ template <int CB> struct Roles {
 // The value that enters tile k (counted in the direction of the walk) for
 // every channel of the workgroup, in `enter`; publishes the tile's own run.
 // `runs` holds the waves' runs in the order of the walk.  `fresh`: nothing
-// enters (the tile begins at a boundary); `resets`: it has a boundary.  Begins
-// after a barrier and ends with one.
+// enters (the tile begins at a boundary, or is the first); `resets`: it has a
+// boundary, which holds for every fresh tile but the first, so that every
+// block's last tile publishes on one of the two ways.  Begins after a barrier
+// and ends with one.
 template <int CB, int V>
 __device__ __forceinline__ void pass_on(const Chain &ch, int k, int64_t c0, bool fresh, bool resets,
                                         const Run (*runs)[CB], Run (*parts)[CB], float *enter)
@@ -462,6 +464,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
     bool fresh, resets, unused;         // boundaries behind a token of the tile
     boundary_in(win, k * TILE + 1, TILE, &resets, &unused);
     boundary_in(win, (k + 1) * TILE, 1, &fresh, &unused);
+    resets = resets || fresh;           // (so it is, unless cu_seqlens breaks its rules)
     fresh = fresh || kb == 0;
     if (dinit)
         empty_seqs(win, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {

@@ -183,3 +183,45 @@ def test_validate_rejects_bad_cu_seqlens():
     print(res.stdout, res.stderr[-2000:], flush=True)
     lines = [line for line in res.stdout.splitlines() if ": " in line]
     assert res.returncode == 0 and len(lines) == 12 and all(line.endswith(": 1") for line in lines)
+
+
+def test_offsets_beyond_32_bits():
+    # more than 2^31 elements before the last sequence's rows: they come out as in a call of their own
+    L, D = 300, 2056
+    T = (1 << 20) + L
+    assert (T - L) * D > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.empty(T, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    small = x[-L:].clone()
+    cu = torch.tensor([0, T - L, T], dtype=torch.int32, device="cuda")
+    own = torch.tensor([0, L], dtype=torch.int32, device="cuda")
+    out, ref = torch.empty_like(x), torch.empty_like(small)
+    g = torch.full((T, D), -0.05, device="cuda")
+    chk = torch.empty(-(-T // 128), D, device="cuda")
+    K.kda_scan_prefill(x, g, None, cu, out, None, checkpoints=chk)
+    K.kda_scan_prefill(small, g[-L:].contiguous(), None, own, ref, None)
+    # the tiles fall elsewhere in the sequence: fp32 rounding, then a rounding to bf16
+    near = lambda a, b, rel: float((a.float() - b.float()).abs().max()) <= rel * float(b.float().abs().max())   # noqa: E731
+    assert near(out[-L:], ref, 2.0 ** -8)
+    gb = K.kda_scan_backward(x, g, None, cu, x, checkpoints=chk, want_dinit=False)
+    gs = K.kda_scan_backward(small, g[-L:].contiguous(), None, own, small, want_dinit=False)
+    assert near(gb["dx"][-L:], gs["dx"], 2.0 ** -8) and near(gb["dg"][-L:], gs["dg"], 1000 * 2.0 ** -24)
+    del g, gb, chk
+    w, b = torch.randn(D, 4, device="cuda"), torch.randn(D, device="cuda")
+    K.kda_conv_prefill(x, w, b, None, cu, out, None)
+    K.kda_conv_prefill(small, w, b, None, own, ref, None)
+    assert torch.equal(out[-L:], ref)
+    gc = K.kda_conv_backward(x, w, b, None, cu, x, want_dinit=False)
+    assert torch.equal(gc["dx"][-L:], K.kda_conv_backward(small, w, b, None, own, small, want_dinit=False)["dx"])
+    del gc
+    mx = torch.empty(T, D, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(T, -(-D // 32), dtype=torch.uint8, device="cuda")
+    mx2, sc2 = torch.empty(L, D, dtype=torch.uint8, device="cuda"), torch.empty(L, -(-D // 32), dtype=torch.uint8, device="cuda")
+    K.kda_rmsnorm(x, b, out, residual=x, out_mx=mx, scales=sc)
+    K.kda_rmsnorm(small, b, ref, residual=small, out_mx=mx2, scales=sc2)
+    assert near(out[-L:], ref, 2.0 ** -8)
+    back = lambda m, s: m.view(torch.float8_e4m3fn).float() * torch.exp2(s.float() - 127).repeat_interleave(32, 1)[:, :D]   # noqa: E731
+    assert near(back(mx[-L:], sc[-L:]), back(mx2, sc2), 2.0 ** -3)
+    K.kda_rmsnorm_backward(x, b, x, grads=dict(dx=out, dweight=torch.empty(D, device="cuda")))
+    K.kda_rmsnorm_backward(small, b, small, grads=dict(dx=ref, dweight=torch.empty(D, device="cuda")))
+    assert near(out[-L:], ref, 2.0 ** -8)
