@@ -128,6 +128,19 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
                 for (int v = 0; v < V; ++v) before[j][v] = Row<T, V>::at(r, v);
             }
         };
+        // The sequence's last token is done: the window is its final state.  (Not
+        // where that takes the initial state's place: the wave of the sequence's
+        // start may still have to read it.)
+        auto leave = [&]() {
+            if (!fin || fin == init) return;
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                R r;
+#pragma unroll
+                for (int v = 0; v < V; ++v) Row<T, V>::set(r, v, before[j][v]);
+                store_row<T, V>(fin + ((int64_t)n * (W - 1) + j) * a.D + c, r);
+            }
+        };
         auto advance = [&]() {                 // to the sequence that begins at token t
             while (n < sq.N - 1 && next <= t) next = win.at(++n + 1);
             s = t;
@@ -162,9 +175,12 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
                 if (stop - t >= BATCH && next >= t + BATCH) {
 #pragma unroll
                     for (int i = 0; i < BATCH; ++i) token(rows[i]);
-                    if (t == next && t < stop) {
-                        advance();
-                        enter();
+                    if (t == next) {
+                        leave();
+                        if (t < stop) {
+                            advance();
+                            enter();
+                        }
                     }
                 } else {
                     const int32_t m = min(stop - t, BATCH);
@@ -172,9 +188,12 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
                     for (int i = 0; i < BATCH; ++i) {
                         if (i < m) {
                             token(rows[i]);
-                            if (t == next && t < stop) {
-                                advance();
-                                enter();
+                            if (t == next) {
+                                leave();
+                                if (t < stop) {
+                                    advance();
+                                    enter();
+                                }
                             }
                         }
                     }
@@ -186,14 +205,19 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
         // the first W - 1 tokens of the last sequence that begins here, beyond the strip
         if (s >= t0 && t > s && t >= t1) {
             const int32_t most = min(min(s + W - 1, next), tend);
-            while (t < most) token(load_row<T, V>(x + (int64_t)t * a.D + c));
+            while (t < most) {
+                token(load_row<T, V>(x + (int64_t)t * a.D + c));
+                if (t == next) leave();
+            }
         }
     }
-    // the final states of the sequences that begin here, after the walk has read the initial ones
+    // The final states of the empty sequences that begin here, or, where they take
+    // the initial states' place, of all: the walk has read those by now.
     if (fin)
         for (int32_t n = win.first_at_or_after(t0); n < sq.N; ++n) {
             const int32_t s = win.at(n), e = max(win.at(n + 1), s);
             if (s >= t1 && k < nstrips - 1) break;
+            if (e > s && fin != init) continue;
             R r[W - 1];
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) r[j] = row_before<T, W, V>(x, init, a, c, n, s, e, W - 1 - j);
