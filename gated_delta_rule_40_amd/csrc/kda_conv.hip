@@ -94,10 +94,11 @@ __device__ __forceinline__ typename Row<T, V>::raw row_before(const T *x, const 
 template <typename T, int W, int V, bool SILU>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip, int32_t nstrips, int32_t cols,
-                     int32_t width, T *out, T *fin)
+                     int32_t width, uint32_t work, T *out, T *fin)
 {
     typedef typename Row<T, V>::raw R;
     constexpr int BATCH = 4;
+    if (blockIdx.x >= work) return copy_empty(sq, blockIdx.x - work, (W - 1) * a.D, init, fin);
     const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int32_t k = (int32_t)(blockIdx.x / cols) * 4 + wave;
     // A lane past its column or the last channel repeats the column's last lane.
@@ -142,7 +143,7 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
             }
         };
         auto advance = [&]() {                 // to the sequence that begins at token t
-            while (n < sq.N - 1 && next <= t) next = win.at(++n + 1);
+            win.advance(t, n, next);
             s = t;
         };
         auto token = [&](const R &r) {
@@ -211,18 +212,19 @@ void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t str
             }
         }
     }
-    // The final states of the empty sequences that begin here, or, where they take
-    // the initial states' place, of all: the walk has read those by now.
-    if (fin)
-        for (int32_t n = win.first_at_or_after(t0); n < sq.N; ++n) {
-            const int32_t s = win.at(n), e = max(win.at(n + 1), s);
-            if (s >= t1 && k < nstrips - 1) break;
-            if (e > s && fin != init) continue;
+    // Final states in the initial states' place, of the sequences that begin here:
+    // the walk has read those by now.
+    if (fin && fin == init)
+        for (int32_t t = t0; t < min(t1, tend);) {
+            const int32_t s = win.sq.at(min(win.first_at_or_after(t), sq.N)), n = win.owner(s);
+            if (s < t || s >= min(t1, tend) || n < 0) break;
+            const int32_t e = max(win.at(n + 1), s + 1);
             R r[W - 1];
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) r[j] = row_before<T, W, V>(x, init, a, c, n, s, e, W - 1 - j);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) store_row<T, V>(fin + ((int64_t)n * (W - 1) + j) * a.D + c, r[j]);
+            t = e;
         }
 }
 
@@ -275,10 +277,11 @@ __global__ __launch_bounds__(256) void kda_conv_step_kernel(const T *x, T *state
 template <typename T, int W, int V, bool SILU>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
 void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip, int32_t nstrips, int32_t cols,
-                         const T *dout, const T *dfin, T *dx, T *dinit, float *partial)
+                         uint32_t work, const T *dout, const T *dfin, T *dx, T *dinit, float *partial)
 {
     typedef typename Row<T, V>::raw R;
     constexpr int BATCH = 4;
+    if (blockIdx.x >= work) return copy_empty(sq, blockIdx.x - work, (W - 1) * a.D, dfin, dinit);
     __shared__ float sums[4][W + 1][64 * V];
     const int32_t lane = threadIdx.x & 63;
     const int32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -299,14 +302,6 @@ void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t
         auto get_dfin = [&](int32_t n, int j) {
             return dfin ? load_row<T, V>(dfin + ((int64_t)n * (W - 1) + j) * a.D + c) : R{};
         };
-        if (dinit)   // empty sequences
-            for (int32_t n = win.first_at_or_after(t0); n < sq.N; ++n) {
-                const int32_t s = win.at(n);
-                if (s >= t1 && k < nstrips - 1) break;
-                if (win.at(n + 1) <= s)
-                    for (int j = 0; j < W - 1; ++j)
-                        store_row<T, V>(dinit + ((int64_t)n * (W - 1) + j) * a.D + c, get_dfin(n, j));
-            }
         int32_t n = t0 < min(tend, t1) ? win.owner(t0) : -1;
         if (n >= 0) {
             Weights<W, V> wt;
@@ -386,7 +381,7 @@ void kda_conv_bwd_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t
 #pragma unroll
                     for (int v = 0; v < V; ++v) acc[j][v] = 0.f;
                 }
-                while (n < sq.N - 1 && next <= t) next = win.at(++n + 1);
+                if (t < stop) win.advance(t, n, next);
                 s = t;
             };
             R xr[BATCH], dr[BATCH], xa[BATCH], da[BATCH];
@@ -479,14 +474,17 @@ hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Se
     const int64_t cols = up(a.D, cw);
     // strips of 64 tokens where these give every SIMD its waves, shorter ones otherwise
     const int32_t strip = up(sq.T, 64) * cols >= 4096 ? 64 : 16;
-    const int32_t nstrips = (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1);
-    const dim3 grid((unsigned)(up(nstrips, 4) * cols));
+    const int32_t nstrips = (int32_t)up(sq.T, strip);
+    const int64_t work = up(nstrips, 4) * cols, groups = work + empty_groups(sq.N, init, fin);
+    if (groups == 0) return hipSuccess;
     if (a.silu)
-        hipLaunchKernelGGL((kda_conv_kernel<T, W, V, true>), grid, dim3(256), 0, s, (const T *)x, (const T *)init, a, sq,
-                           strip, nstrips, (int32_t)cols, cw, (T *)out, (T *)fin);
+        hipLaunchKernelGGL((kda_conv_kernel<T, W, V, true>), dim3((unsigned)groups), dim3(256), 0, s, (const T *)x,
+                           (const T *)init, a, sq, strip, nstrips, (int32_t)cols, cw, (uint32_t)work, (T *)out,
+                           (T *)fin);
     else
-        hipLaunchKernelGGL((kda_conv_kernel<T, W, V, false>), grid, dim3(256), 0, s, (const T *)x, (const T *)init, a,
-                           sq, strip, nstrips, (int32_t)cols, cw, (T *)out, (T *)fin);
+        hipLaunchKernelGGL((kda_conv_kernel<T, W, V, false>), dim3((unsigned)groups), dim3(256), 0, s, (const T *)x,
+                           (const T *)init, a, sq, strip, nstrips, (int32_t)cols, cw, (uint32_t)work, (T *)out,
+                           (T *)fin);
     return hipGetLastError();
 }
 
@@ -509,19 +507,16 @@ hipError_t run_conv_backward(const void *x, const ConvArgs &a, const void *init,
                              hipStream_t s)
 {
     const int32_t strip = bwd_strip(sq.T, a.D), parts = sq.N > 0 ? bwd_parts(sq.T, a.D) : 0;
-    const int64_t cols = bwd_cols(a.D);
-    if (parts > 0) {
-        const dim3 grid((unsigned)(parts * cols));
-        const int32_t nstrips = (int32_t)(sq.T > 0 ? up(sq.T, strip) : 1);
-        if (a.silu)
-            hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V, true>), grid, dim3(256), 0, s, (const T *)x,
-                               (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (const T *)dout, (const T *)dfin,
-                               (T *)dx, (T *)dinit, (float *)ws);
-        else
-            hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V, false>), grid, dim3(256), 0, s, (const T *)x,
-                               (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (const T *)dout, (const T *)dfin,
-                               (T *)dx, (T *)dinit, (float *)ws);
-    }
+    const int64_t cols = bwd_cols(a.D), work = parts * cols, groups = work + empty_groups(sq.N, dfin, dinit);
+    const int32_t nstrips = (int32_t)up(sq.T, strip);
+    if (groups > 0 && a.silu)
+        hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V, true>), dim3((unsigned)groups), dim3(256), 0, s, (const T *)x,
+                           (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (uint32_t)work, (const T *)dout,
+                           (const T *)dfin, (T *)dx, (T *)dinit, (float *)ws);
+    else if (groups > 0)
+        hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V, false>), dim3((unsigned)groups), dim3(256), 0, s, (const T *)x,
+                           (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (uint32_t)work, (const T *)dout,
+                           (const T *)dfin, (T *)dx, (T *)dinit, (float *)ws);
     hipLaunchKernelGGL(kda_conv_sums_kernel<W>, dim3((unsigned)up((W + 1) * a.D, COLSUM_COLS)),
                        dim3(COLSUM_THREADS), 0, s,
                        (const float *)ws, parts, a.D, dw, dbias);

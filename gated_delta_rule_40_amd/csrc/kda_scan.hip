@@ -231,16 +231,20 @@ struct Edges {
     }
 };
 
-__device__ __forceinline__ Edges edges(const SeqWindow &sq, int32_t t0, int32_t end, int32_t *first)
+__device__ __forceinline__ Edges edges(const SeqWindow &sq, int32_t t0, int32_t end)
 {
+    const int32_t i = threadIdx.x & 63;
+    if (sq.below(t0 + L + 1) == 64) {   // more entries than are held: each lane looks for its own
+        const int32_t own = i <= L ? sq.sq.first_at_or_after(t0 + i + 1) - 1 : -1;
+        return {(uint32_t)__ballot(own >= 0 && sq.sq.at(own) == t0 + i), end, own};
+    }
     int32_t n = sq.first_at_or_after(t0);
-    *first = n;
     Edges e = {0, end, n - 1};
     for (; n <= sq.sq.N; ++n) {
         const int32_t p = sq.at(n);
         if (p > t0 + L || p < t0) break;
         e.mask |= 1u << (p - t0);
-        e.own += (int32_t)(threadIdx.x & 63) >= p - t0;
+        e.own += i >= p - t0;
     }
     return e;
 }
@@ -254,22 +258,11 @@ __device__ __forceinline__ void boundary_in(const SeqWindow &sq, int32_t t, int 
     *at_first = p == t;
 }
 
-// `copy(n)` for the empty sequences that lie at tokens [t0, t0 + L), or at any later place for the last wave of all
-template <typename F>
-__device__ __forceinline__ void empty_seqs(const SeqWindow &sq, int32_t t0, int32_t first, bool last, F copy)
-{
-    for (int32_t n = first; n < sq.sq.N; ++n) {
-        const int32_t p = sq.at(n);
-        if (p >= t0 + L && !last) break;
-        if (sq.at(n + 1) <= p) copy(n);
-    }
-}
-
 // ---------------------------------------------------------------- forward
 template <typename T, int V>
 __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(4)))   // two workgroups per CU
-void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int64_t D, int32_t cols, T *out,
-                     float *fin, float *chk, Chain ch)
+void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int64_t D, int32_t cols,
+                     uint32_t work, T *out, float *fin, float *chk, Chain ch)
 {
     constexpr int CB = 64 * V;
     typedef typename Vec<T, V>::raw XR;
@@ -282,13 +275,7 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = blockIdx.x % cols;
-    if (sq.T == 0) {
-        if (fin && w == 0)
-            for (int32_t n = 0; n < sq.N; ++n)
-                for (int64_t c = (int64_t)col * ch.width + lane; c < min(D, (int64_t)(col + 1) * ch.width); c += 64)
-                    fin[n * D + c] = init ? init[n * D + c] : 0.f;
-        return;
-    }
+    if (blockIdx.x >= work) return copy_empty(sq, blockIdx.x - work, D, init, fin);
     const int32_t tend = sq.at(sq.N);
     SeqWindow win(sq);
     int k = 0;
@@ -310,18 +297,12 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
             gr[i] = rows.at(g, i);
         }
     }
-    int32_t first;
     win.locate(k * TILE);
-    const Edges e = edges(win, t0, tend, &first);
+    const Edges e = edges(win, t0, tend);
     const uint32_t starts = e.mask & ((1u << L) - 1);
     bool fresh, resets;
     boundary_in(win, k * TILE, TILE, &resets, &fresh);
     fresh = fresh || k == 0;
-    if (fin)
-        empty_seqs(win, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {
-            if (in)
-                for (int j = 0; j < V; ++j) fin[n * D + c + j] = init ? init[n * D + c + j] : 0.f;
-        });
     // what a token leaves: its output, and the final state of a sequence that ends with it
     auto leave = [&](int i, const float (&h)[V]) {
         if (t0 + i >= e.end) return;
@@ -409,7 +390,7 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
 template <typename T, int V>
 __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(4)))   // two workgroups per CU
 void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq, int64_t D, int32_t cols,
-                         const T *dout, const float *dfin, const float *chk, T *dx, float *dg, float *dinit, Chain ch)
+                         uint32_t work, const T *dout, const float *dfin, const float *chk, T *dx, float *dg, float *dinit, Chain ch)
 {
     constexpr int CB = 64 * V;
     typedef typename Vec<T, V>::raw XR;
@@ -423,13 +404,7 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = blockIdx.x % cols;
-    if (sq.T == 0) {
-        if (dinit && w == 0)
-            for (int32_t n = 0; n < sq.N; ++n)
-                for (int64_t c = (int64_t)col * ch.width + lane; c < min(D, (int64_t)(col + 1) * ch.width); c += 64)
-                    dinit[n * D + c] = dfin ? dfin[n * D + c] : 0.f;
-        return;
-    }
+    if (blockIdx.x >= work) return copy_empty(sq, blockIdx.x - work, D, dfin, dinit);
     const int32_t tend = sq.at(sq.N);
     SeqWindow win(sq);
     int kb = 0;                         // the tile's number from the end
@@ -457,20 +432,14 @@ void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq,
     float h[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) h[j] = (in && k > 0) ? chk[k * D + c + j] : 0.f;
-    int32_t first;
     win.locate(k * TILE);
-    const Edges e = edges(win, t0, tend, &first);
+    const Edges e = edges(win, t0, tend);
     const uint32_t starts = e.mask & ((1u << L) - 1);
     bool fresh, resets, unused;         // boundaries behind a token of the tile
     boundary_in(win, k * TILE + 1, TILE, &resets, &unused);
     boundary_in(win, (k + 1) * TILE, 1, &fresh, &unused);
     resets = resets || fresh;           // (so it is, unless cu_seqlens breaks its rules)
     fresh = fresh || kb == 0;
-    if (dinit)
-        empty_seqs(win, t0, first, k == ch.ntiles - 1 && w == WAVES - 1, [&](int32_t n) {
-            if (in)
-                for (int j = 0; j < V; ++j) dinit[n * D + c + j] = dfin ? dfin[n * D + c + j] : 0.f;
-        });
     {
         float A[V], B[V], E[V], Ae[V];
 #pragma unroll
@@ -629,8 +598,10 @@ hipError_t run_scan(const void *x, const float *g, const float *init, const Seqs
 {
     ch.width = kda_column_width(D, V);
     const int32_t cols = (D - 1) / ch.width + 1;
-    hipLaunchKernelGGL((kda_scan_kernel<T, V>), dim3((unsigned)((int64_t)cols * ch.ntiles)), dim3(NTH), 0, s,
-                       (const T *)x, g, init, sq, (int64_t)D, cols, (T *)out, fin, chk, ch);
+    const int64_t work = sq.T > 0 ? (int64_t)cols * ch.ntiles : 0, groups = work + empty_groups(sq.N, init, fin);
+    if (groups > 0)
+        hipLaunchKernelGGL((kda_scan_kernel<T, V>), dim3((unsigned)groups), dim3(NTH), 0, s, (const T *)x, g, init, sq,
+                           (int64_t)D, cols, (uint32_t)work, (T *)out, fin, chk, ch);
     return hipGetLastError();
 }
 
@@ -657,9 +628,10 @@ hipError_t run_scan_backward(const void *x, const float *g, const float *init, c
 {
     ch.width = kda_column_width(D, V);
     const int32_t cols = (D - 1) / ch.width + 1;
-    hipLaunchKernelGGL((kda_scan_bwd_kernel<T, V>), dim3((unsigned)((int64_t)cols * ch.ntiles)), dim3(NTH), 0, s,
-                       (const T *)x, g, init, sq, (int64_t)D, cols, (const T *)dout, dfin, chk, (T *)dx, dg, dinit,
-                       ch);
+    const int64_t work = sq.T > 0 ? (int64_t)cols * ch.ntiles : 0, groups = work + empty_groups(sq.N, dfin, dinit);
+    if (groups > 0)
+        hipLaunchKernelGGL((kda_scan_bwd_kernel<T, V>), dim3((unsigned)groups), dim3(NTH), 0, s, (const T *)x, g, init,
+                           sq, (int64_t)D, cols, (uint32_t)work, (const T *)dout, dfin, chk, (T *)dx, dg, dinit, ch);
     return hipGetLastError();
 }
 

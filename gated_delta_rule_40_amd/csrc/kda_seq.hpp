@@ -72,6 +72,41 @@ struct SeqWindow {
         const int32_t n = first_at_or_after(t + 1) - 1;
         return (n >= 0 && n < sq.N) ? n : -1;
     }
+    // from sequence n, which ends before token t, to the one that begins there
+    __device__ __forceinline__ void advance(int32_t t, int32_t &n, int32_t &next) const {
+        if (n < sq.N - 1) next = at(++n + 1);
+        if (next > t) return;
+        const int32_t m = owner(t);   // past empty ones
+        n = m >= 0 ? m : sq.N - 1;
+        next = max(at(n + 1), t + 1);
+    }
 };
+
+// Rows of states that empty sequences keep: dst[n] = src[n] (null: zeros), both
+// [N][size]; a wave each, EMPTY_SEQS of them to a workgroup of its own.  They are
+// found by their number, not by their place: a batch with fixed slots has
+// hundreds of them at one token (511 of 512: 15 us, 320 when the wave at that
+// token copied them).  Neither array may reach into the other.
+constexpr int EMPTY_SEQS = 4;
+template <typename T>
+__device__ __forceinline__ void copy_empty(const Seqs &sq, uint32_t group, int64_t size, const T *__restrict__ src,
+                                           T *__restrict__ dst)
+{
+    const int64_t n = (int64_t)group * EMPTY_SEQS + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (threadIdx.x >= 64 * EMPTY_SEQS || n >= sq.N || sq.at((int32_t)n + 1) > sq.at((int32_t)n)) return;
+    dst += n * size;
+    if (src) {
+        src += n * size;
+#pragma unroll 8
+        for (int64_t e = threadIdx.x & 63; e < size; e += 64) dst[e] = src[e];
+    } else {
+        for (int64_t e = threadIdx.x & 63; e < size; e += 64) dst[e] = T(0.f);
+    }
+}
+// workgroups that takes (none where the rows are there already)
+inline int64_t empty_groups(int32_t N, const void *src, const void *dst)
+{
+    return dst && dst != src ? ((int64_t)N + EMPTY_SEQS - 1) / EMPTY_SEQS : 0;
+}
 
 }  // namespace kda

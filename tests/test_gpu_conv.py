@@ -106,6 +106,30 @@ def test_many_sequences(N, most):
     R.close(host(g["dinit"]), r["dinit"], r["e_dinit"], "fp32", "dinit")
 
 
+SLOTS = [[40] + [0] * 200, [0] * 130 + [300], [150] + [0] * 90 + [1, 2] + [0] * 70 + [200, 0, 0, 9], [0] * 300]
+
+
+@pytest.mark.parametrize("lens", SLOTS, ids=lambda v: "%dof%d" % (sum(map(bool, v)), len(v)))
+@pytest.mark.parametrize("init", [True, False])
+def test_slots_left_empty(lens, init):
+    # more sequences begin at one token than a wave holds entries
+    h, d = make(lens, 130, 4, "bf16", init, tail=2, seed=13)
+    T, N = sum(lens), len(lens)
+    out = torch.full_like(d["x"], 77.0)
+    fin = torch.full((N, 3, 130), 77.0, dtype=torch.bfloat16, device="cuda")
+    K.kda_conv_prefill(d["x"], d["w"], d["b"], d["init"], d["cu"], out, fin)
+    g = K.kda_conv_backward(d["x"], d["w"], d["b"], d["init"], d["cu"], d["dout"], d["dfinal"])
+    r = R.conv_backward(h["x"][:T], h["w"], h["b"], h["init"], h["cu"], True, h["dout"][:T], h["dfinal"])
+    R.close(host(out)[:T], r["fwd"]["out"], r["fwd"]["e_out"], "bf16", "out")
+    assert np.array_equal(host(fin), r["fwd"]["final"]) and float(out[T:].min()) == 77.0
+    R.close(host(g["dx"])[:T], r["dx"], r["e_dx"], "bf16", "dx")
+    R.close(host(g["dweight"]), r["dweight"], r["e_dweight"], "fp32", "dweight")
+    R.close(host(g["dinit"]), r["dinit"], r["e_dinit"], "bf16", "dinit")
+    if init:
+        K.kda_conv_prefill(d["x"], d["w"], d["b"], d["init"], d["cu"], out, d["init"])
+        assert torch.equal(d["init"], fin)
+
+
 @pytest.mark.parametrize("N,D", [(1, 1), (3, 5), (8, 512), (65, 999)])
 @pytest.mark.parametrize("W", [2, 3, 4])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])

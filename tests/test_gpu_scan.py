@@ -122,6 +122,29 @@ def test_many_sequences(N, most):
     assert float(out[T:].min()) == 77.0
 
 
+SLOTS = [[40] + [0] * 200, [0] * 130 + [300], [150] + [0] * 90 + [1, 2] + [0] * 70 + [200, 0, 0, 9], [0] * 300]
+
+
+@pytest.mark.parametrize("lens", SLOTS, ids=lambda v: "%dof%d" % (sum(map(bool, v)), len(v)))
+@pytest.mark.parametrize("init", [True, False])
+def test_slots_left_empty(lens, init):
+    # more sequences begin at one token than a wave holds entries
+    h, d = make(lens, 130, "bf16", init, tail=2, seed=13)
+    T, N = sum(lens), len(lens)
+    out, fin = torch.full_like(d["x"], 77.0), torch.full((N, 130), 77.0, device="cuda")
+    K.kda_scan_prefill(d["x"], d["g"], d["init"], d["cu"], out, fin)
+    b = R.scan_backward(h["x"], h["g"], h["init"], h["cu"], h["dout"], h["dfinal"])
+    R.close(host(out)[:T], b["fwd"]["h"][:T], b["fwd"]["e_h"][:T], "bf16", "out")
+    R.close(host(fin), b["fwd"]["final"], b["fwd"]["e_final"], "fp32", "final")
+    assert float(out[T:].min()) == 77.0
+    g = K.kda_scan_backward(d["x"], d["g"], d["init"], d["cu"], d["dout"], d["dfinal"])
+    R.close(host(g["dx"])[:T], b["dx"][:T], b["e_dx"][:T], "bf16", "dx")
+    R.close(host(g["dinit"]), b["dinit"], b["e_dinit"], "fp32", "dinit")
+    if init:
+        K.kda_scan_prefill(d["x"], d["g"], d["init"], d["cu"], out, d["init"])
+        assert torch.equal(d["init"], fin)
+
+
 @pytest.mark.parametrize("N,D", [(1, 1), (1, 64), (3, 5), (8, 2048), (513, 999)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_decode(N, D, dtype):
