@@ -477,6 +477,7 @@ hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Se
     const int32_t nstrips = (int32_t)up(sq.T, strip);
     const int64_t work = up(nstrips, 4) * cols, groups = work + empty_groups(sq.N, init, fin);
     if (groups == 0) return hipSuccess;
+    if (!kda_grid_ok(groups, 256)) return hipErrorInvalidConfiguration;
     if (a.silu)
         hipLaunchKernelGGL((kda_conv_kernel<T, W, V, true>), dim3((unsigned)groups), dim3(256), 0, s, (const T *)x,
                            (const T *)init, a, sq, strip, nstrips, (int32_t)cols, cw, (uint32_t)work, (T *)out,
@@ -492,6 +493,7 @@ template <typename T, int W, int V>
 hipError_t run_conv_step(const void *x, const ConvArgs &a, void *state, int32_t N, void *out, hipStream_t s)
 {
     const int64_t cols = up(a.D, 256 * V);
+    if (!kda_grid_ok(N * cols >= 2048 ? cols * up(N, 4) : cols * N, 256)) return hipErrorInvalidConfiguration;
     if (N * cols >= 2048)
         hipLaunchKernelGGL((kda_conv_step_kernel<T, W, V, 4>), dim3((unsigned)(cols * up(N, 4))), dim3(256), 0, s,
                            (const T *)x, (T *)state, a, N, (int32_t)cols, (T *)out);
@@ -509,6 +511,8 @@ hipError_t run_conv_backward(const void *x, const ConvArgs &a, const void *init,
     const int32_t strip = bwd_strip(sq.T, a.D), parts = sq.N > 0 ? bwd_parts(sq.T, a.D) : 0;
     const int64_t cols = bwd_cols(a.D), work = parts * cols, groups = work + empty_groups(sq.N, dfin, dinit);
     const int32_t nstrips = (int32_t)up(sq.T, strip);
+    if (!kda_grid_ok(groups, 256) || !kda_grid_ok(up((W + 1) * a.D, COLSUM_COLS), COLSUM_THREADS))
+        return hipErrorInvalidConfiguration;
     if (groups > 0 && a.silu)
         hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V, true>), dim3((unsigned)groups), dim3(256), 0, s, (const T *)x,
                            (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (uint32_t)work, (const T *)dout,

@@ -21,6 +21,10 @@ inline int32_t kda_column_width(int32_t D, int V)
     return w;
 }
 
+// A launch counts its threads in 32 bits.  Launchers whose grid has more return
+// hipErrorInvalidConfiguration before they launch anything.
+inline bool kda_grid_ok(int64_t blocks, int threads) { return blocks <= (int64_t)UINT32_MAX / threads; }
+
 size_t kda_scan_ws_bytes(int32_t T, int32_t D);
 hipError_t kda_launch_scan(bool bf16, const void *x, const float *g, const float *init, const int32_t *cu, int32_t N,
                            int32_t T, int32_t D, void *out, float *fin, float *checkpoints, void *ws, hipStream_t s);

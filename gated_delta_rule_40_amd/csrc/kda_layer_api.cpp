@@ -22,15 +22,27 @@ size_t elem_size(kda_dtype dtype) { return dtype == KDA_BF16 ? 2 : 4; }
 // A token array: present (unless it has no elements) and aligned to its type.
 bool array_ok(const void *p, int64_t elems, size_t size) { return (p || elems == 0) && aligned(p, size); }
 
-kda_status from_hip(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
+// Whether two arrays of n bytes share none.
+bool apart(const void *a, const void *b, size_t n)
+{
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return !a || !b || n == 0 || (p < q ? q - p : p - q) >= n;
+}
+bool same_or_apart(const void *a, const void *b, size_t n) { return a == b || apart(a, b, n); }
+
+// (hipErrorInvalidConfiguration: a grid of more threads than there can be)
+kda_status from_hip(hipError_t e)
+{
+    return e == hipSuccess ? KDA_OK : e == hipErrorInvalidConfiguration ? KDA_ERR_UNSUPPORTED : KDA_ERR_LAUNCH;
+}
 
 hipStream_t hip_stream(kda_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
 
 // What the packed calls share: sizes, type, cu_seqlens.  The kernels look a
-// tile beyond a token in int32.
+// tile beyond a token, and a wave beyond a sequence, in int32.
 bool packed_ok(const int32_t *cu, int32_t N, int32_t T, int32_t D, kda_dtype dtype)
 {
-    return dtype_ok(dtype) && N >= 0 && N < INT32_MAX && T >= 0 && T <= INT32_MAX - 65536 && D > 0 && cu &&
+    return dtype_ok(dtype) && N >= 0 && N <= INT32_MAX - 65536 && T >= 0 && T <= INT32_MAX - 65536 && D > 0 && cu &&
            aligned(cu, 4);
 }
 
@@ -69,6 +81,9 @@ kda_status kda_scan_prefill(const void *x, const float *g, const float *initial_
     if (!workspace_ok(workspace, workspace_bytes, kda_scan_ws_bytes(total_tokens, channels), 8))
         return KDA_ERR_INVALID_ARG;
     if (num_seqs == 0) return KDA_OK;
+    if (!same_or_apart(x, out, n * elem_size(dtype)) ||
+        !same_or_apart(initial_state, final_state, (size_t)num_seqs * channels * 4))
+        return KDA_ERR_INVALID_ARG;
     if (kda_status v = check_cu(cu_seqlens, num_seqs, total_tokens, stream)) return v;
     return from_hip(kda_launch_scan(dtype == KDA_BF16, x, g, initial_state, cu_seqlens, num_seqs, total_tokens,
                                     channels, out, final_state, checkpoints, workspace, hip_stream(stream)));
@@ -110,6 +125,10 @@ kda_status kda_scan_backward(const void *x, const float *g, const float *initial
                       kda_scan_bwd_ws_bytes(total_tokens, channels, checkpoints != nullptr), 8))
         return KDA_ERR_INVALID_ARG;
     if (num_seqs == 0) return KDA_OK;
+    const size_t state = (size_t)num_seqs * channels * 4;
+    if (!same_or_apart(x, dx, n * e) || !same_or_apart(dout, dx, n * e) || !same_or_apart(g, dg, n * 4) ||
+        !apart(initial_state, dinit, state) || !apart(dfinal, dinit, state))
+        return KDA_ERR_INVALID_ARG;
     if (kda_status v = check_cu(cu_seqlens, num_seqs, total_tokens, stream)) return v;
     return from_hip(kda_launch_scan_backward(dtype == KDA_BF16, x, g, initial_state, cu_seqlens, num_seqs,
                                              total_tokens, channels, dout, dfinal, checkpoints, dx, dg, dinit,
@@ -130,6 +149,9 @@ kda_status kda_conv_prefill(const void *x, const float *weight, const float *bia
         return KDA_ERR_INVALID_ARG;
     if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return KDA_OK;
+    if (!apart(x, out, n * e) ||
+        !same_or_apart(initial_state, final_state, (size_t)num_seqs * (width - 1) * channels * e))
+        return KDA_ERR_INVALID_ARG;
     if (kda_status v = check_cu(cu_seqlens, num_seqs, total_tokens, stream)) return v;
     return from_hip(kda_launch_conv(dtype == KDA_BF16, x, weight, bias, initial_state, cu_seqlens, num_seqs,
                                     total_tokens, channels, width, silu != 0, out, final_state,
@@ -175,6 +197,10 @@ kda_status kda_conv_backward(const void *x, const float *weight, const float *bi
     if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
     if (!workspace_ok(workspace, workspace_bytes,
                       kda_conv_bwd_ws_bytes(total_tokens, channels, width, dtype == KDA_BF16), 4))
+        return KDA_ERR_INVALID_ARG;
+    const size_t state = (size_t)num_seqs * (width - 1) * channels * e;
+    if (!apart(x, dx, n * e) || !apart(dout, dx, n * e) || !apart(initial_state, dinit, state) ||
+        !apart(dfinal, dinit, state))
         return KDA_ERR_INVALID_ARG;
     if (num_seqs > 0)
         if (kda_status v = check_cu(cu_seqlens, num_seqs, total_tokens, stream)) return v;

@@ -322,9 +322,9 @@ hipError_t run_rmsnorm(const void *x, const void *res, const float *w, int32_t r
 {
     constexpr int VW = 16 / sizeof(T);
     const RowShape sh = row_shape((D + VW - 1) / VW, C, MXB / VW);
-    const int64_t per = sh.threads / sh.tpr;
-    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)((rows + per - 1) / per)),
-                       dim3(sh.threads), 0, s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, eps, (T *)sum,
+    const int64_t per = sh.threads / sh.tpr, blocks = (rows + per - 1) / per;
+    if (!kda_grid_ok(blocks, sh.threads)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)blocks), dim3(sh.threads), 0, s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, eps, (T *)sum,
                        (T *)out, mx, scales);
     return hipGetLastError();
 }

@@ -428,7 +428,7 @@ def _cu(cu_seqlens, dev):
     _require(isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.get_device() == dev,
              "cu_seqlens must be a tensor on the inputs' device")
     n = cu_seqlens.numel()
-    _require(cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and n >= 1 and cu_seqlens.is_contiguous(),
+    _require(cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and 1 <= n <= _MOST and cu_seqlens.is_contiguous(),
              "cu_seqlens must be contiguous int32 [N + 1]")
     return cu_seqlens.data_ptr(), n - 1
 

@@ -370,6 +370,12 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  *     of gates, weights, biases and fp32 states in fp32.
  *   - No result depends on the order in which workgroups run: every sum has a
  *     fixed order, so calls on the same inputs give the same bits.
+ *   - An output shares no memory with another argument unless that is said
+ *     here; token arrays and states that overlap otherwise are refused
+ *     (KDA_ERR_INVALID_ARG).
+ *   - Sizes whose launch would have 2^32 threads or more are
+ *     KDA_ERR_UNSUPPORTED.  Only arrays of hundreds of GB, or of hundreds of
+ *     millions of rows of few channels, have them.
  */
 
 /*
@@ -389,7 +395,8 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  *   initial_state [num_seqs, channels]            fp32, or NULL for zeros
  *   cu_seqlens    [num_seqs + 1]                  int32, DEVICE (as kda_prefill)
  *   out           [total_tokens, channels]        dtype; rows owned by a
- *                 sequence are written, other rows are left untouched
+ *                 sequence are written, other rows are left untouched; may
+ *                 equal x
  *   final_state   [num_seqs, channels]            fp32, or NULL (not written);
  *                 may equal initial_state
  *   checkpoints   [ceil(total_tokens / KDA_SCAN_TILE), channels] fp32, or NULL:
@@ -416,7 +423,8 @@ kda_status kda_scan_prefill(const void *x, const float *g, const float *initial_
 /*
  * kda_scan_decode_step -- one new token per sequence, state updated in place:
  *   x [num_seqs, channels] dtype, g [num_seqs, channels] fp32,
- *   state_inout [num_seqs, channels] fp32, out [num_seqs, channels] dtype
+ *   state_inout [num_seqs, channels] fp32, out [num_seqs, channels] dtype,
+ *   which may equal x
  */
 kda_status kda_scan_decode_step(const void *x, const float *g, float *state_inout, int32_t num_seqs,
                                 int32_t channels, kda_dtype dtype, void *out, kda_stream_t stream);
@@ -432,8 +440,10 @@ kda_status kda_scan_decode_step(const void *x, const float *g, float *state_inou
  *   dfinal        [num_seqs, channels]            fp32, or NULL (zero)
  *   checkpoints   as kda_scan_prefill wrote them for the same inputs, or NULL:
  *                 the states are then computed here, in the workspace
- *   dx            [total_tokens, channels]        dtype, rows of sequences written
- *   dg            [total_tokens, channels]        fp32, rows of sequences written
+ *   dx            [total_tokens, channels]        dtype, rows of sequences
+ *                 written; may equal x or dout
+ *   dg            [total_tokens, channels]        fp32, rows of sequences
+ *                 written; may equal g
  *   dinit         [num_seqs, channels]            fp32, or NULL (not written);
  *                 of an empty sequence: dfinal (zeros if NULL)
  *   workspace     at least kda_scan_backward_workspace_size(...) bytes, as above
@@ -531,7 +541,9 @@ kda_status kda_conv_backward(const void *x, const float *weight, const float *bi
  *                 infinity or a NaN).
  * At least one of out and out_mx is given.  y is computed from the unrounded r
  * and rounded once, into each output by itself.  channels at most 16,384
- * (KDA_ERR_UNSUPPORTED above).
+ * (KDA_ERR_UNSUPPORTED above).  The sum of a row's r^2 is formed in fp32: it
+ * has to stay within that range (|r| up to 10^17 does), and a row whose mean(r^2)
+ * + eps is 0 has NaN in it.
  */
 #define KDA_MX_BLOCK 32
 

@@ -190,6 +190,21 @@ def test_silu_at_large_inputs():
     assert torch.allclose(g["dx"], torch.tensor([[0.0, 0.0, 0.0, 0.5, 1.0, 1.0, 1.0]], device="cuda"), atol=1e-30)
 
 
+def test_token_in_place_and_prompt_refused():
+    _, d = make([40, 3], 72, 4, "bf16", seed=15)
+    a, o, s1, s2 = d["x"][:2].clone(), torch.empty_like(d["x"][:2]), d["init"].clone(), d["init"].clone()
+    K.kda_conv_decode_step(d["x"][:2], d["w"], d["b"], s1, o)
+    K.kda_conv_decode_step(a, d["w"], d["b"], s2, a)
+    assert torch.equal(a, o) and torch.equal(s1, s2)
+    before = d["x"].clone()
+    with pytest.raises(RuntimeError):
+        K.kda_conv_prefill(d["x"], d["w"], d["b"], d["init"], d["cu"], d["x"], None)
+    with pytest.raises(RuntimeError):
+        K.kda_conv_backward(d["x"], d["w"], d["b"], None, d["cu"], d["dout"],
+                            grads=dict(dx=d["x"], dweight=torch.empty_like(d["w"])))
+    assert torch.equal(d["x"], before)
+
+
 def test_same_bits_streams_and_graph_replays():
     h, d = make([900, 1, 2000, 3], 264, 4, "bf16", seed=4)
     x, dout = d["x"].clone(), d["dout"].clone()

@@ -240,6 +240,29 @@ def test_same_bits_every_time_and_on_a_side_stream():
         assert all(torch.equal(g[k], g0[k]) for k in g0)
 
 
+@pytest.mark.parametrize("lens,D", [([5, 0, 300], 33), ([700, 129, 2000], 1024), ([100], 64)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_in_place(lens, D, dtype):
+    _, d = make(lens, D, dtype, seed=15)
+    x, g, init, cu, dout, dfinal = (d[k] for k in ("x", "g", "init", "cu", "dout", "dfinal"))
+    out, fin = torch.empty_like(x), torch.empty_like(init)
+    K.kda_scan_prefill(x, g, init, cu, out, fin)
+    a, s = x.clone(), init.clone()
+    K.kda_scan_prefill(a, g, s, cu, a, s)
+    assert torch.equal(a, out) and torch.equal(s, fin)
+    want = K.kda_scan_backward(x, g, init, cu, dout, dfinal)
+    for over in ("x", "dout"):
+        c = {"x": x.clone(), "dout": dout.clone(), "g": g.clone()}
+        got = dict(dx=c[over], dg=c["g"], dinit=torch.empty_like(init))
+        K.kda_scan_backward(c["x"], c["g"], init, cu, c["dout"], dfinal, grads=got)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+    n = len(lens)
+    o, s1, s2, a = torch.empty_like(x[:n]), init.clone(), init.clone(), x[:n].clone()
+    K.kda_scan_decode_step(x[:n], g[:n], s1, o)
+    K.kda_scan_decode_step(a, g[:n], s2, a)
+    assert torch.equal(a, o) and torch.equal(s1, s2)
+
+
 def test_two_calls_at_once():
     # two streams, each call with a workspace of its own
     h, d = make([20000, 13000], 256, "bf16", seed=7)

@@ -12,6 +12,7 @@ from gated_delta_rule_40_amd import libkda as K
 P = ctypes.c_void_p(0x10000)       # aligned, never dereferenced
 ODD = ctypes.c_void_p(0x10001)
 WS = ctypes.c_void_p(0x100000)
+Q, Q2 = ctypes.c_void_p(0x200000), ctypes.c_void_p(0x200010)
 B, F = K.KDA_BF16, K.KDA_F32
 INVALID, UNSUPPORTED = K.KDA_ERR_INVALID_ARG, K.KDA_ERR_UNSUPPORTED
 
@@ -21,11 +22,11 @@ CALLS = {
     "kda_scan_decode_step": dict(x=P, g=P, state=P, N=1, D=8, dt=B, out=P, stream=None),
     "kda_scan_backward": dict(x=P, g=P, init=None, cu=P, N=1, T=300, D=8, dt=B, dout=P, dfin=None, chk=None, dx=P,
                               dg=P, dinit=None, ws=WS, wsb=1 << 40, stream=None),
-    "kda_conv_prefill": dict(x=P, w=P, b=None, init=None, cu=P, N=1, T=300, D=8, W=4, silu=1, dt=B, out=P, fin=None,
+    "kda_conv_prefill": dict(x=P, w=P, b=None, init=None, cu=P, N=1, T=300, D=8, W=4, silu=1, dt=B, out=Q, fin=None,
                              stream=None),
     "kda_conv_decode_step": dict(x=P, w=P, b=None, state=P, N=1, D=8, W=4, silu=1, dt=B, out=P, stream=None),
     "kda_conv_backward": dict(x=P, w=P, b=None, init=None, cu=P, N=1, T=300, D=8, W=4, silu=1, dt=B, dout=P,
-                              dfin=None, dx=P, dw=P, db=None, dinit=None, ws=WS, wsb=1 << 40, stream=None),
+                              dfin=None, dx=Q, dw=P, db=None, dinit=None, ws=WS, wsb=1 << 40, stream=None),
     "kda_rmsnorm": dict(x=P, res=None, w=P, rows=4, D=64, eps=1e-6, dt=B, sum=None, out=P, mx=None, sc=None,
                         stream=None),
     "kda_rmsnorm_backward": dict(x=P, w=P, dout=P, dres=None, rows=4, D=64, eps=1e-6, dt=B, dx=P, dw=P, ws=WS,
@@ -54,7 +55,7 @@ BAD = [(name, {field: None}) for name, fields in (
     ("kda_conv_decode_step", "x w state out"), ("kda_conv_backward", "x w cu dout dx dw"), ("kda_rmsnorm", "x out"),
     ("kda_rmsnorm_backward", "x dout dx")) for field in fields.split()]
 BAD += [(name, {field: ODD}) for name, a in CALLS.items() for field, v in a.items()
-        if v is P or v is None and field in ("init", "fin", "dfin", "chk", "dinit", "b", "db", "res", "dres", "sum")
+        if v in (P, Q) or v is None and field in ("init", "fin", "dfin", "chk", "dinit", "b", "db", "res", "dres", "sum")
         if not (name == "kda_rmsnorm" and field == "sum")]
 BAD += [(name, {"dt": 7}) for name in CALLS]
 BAD += [(name, {"D": d}) for name in CALLS for d in (0, -3)]
@@ -63,6 +64,16 @@ BAD += [(name, {"T": -1}) for name, a in CALLS.items() if "T" in a]
 BAD += [(name, {"rows": -1}) for name, a in CALLS.items() if "rows" in a]
 BAD += [(name, {"W": w}) for name, a in CALLS.items() if "W" in a for w in (0, -2)]
 BAD += [(name, {"eps": e}) for name, a in CALLS.items() if "eps" in a for e in (-1e-6, float("nan"), float("inf"))]
+BAD += [(name, {"N": 2 ** 31 - 65536}) for name in ("kda_scan_prefill", "kda_scan_backward", "kda_conv_prefill",
+                                                    "kda_conv_backward")]
+# arrays that overlap: token arrays moved by 16 bytes or, where that is not allowed, in place; states likewise
+BAD += [("kda_scan_prefill", {"x": Q, "out": Q2}), ("kda_scan_prefill", {"init": Q, "fin": Q2}),
+        ("kda_scan_backward", {"x": Q, "dx": Q2}), ("kda_scan_backward", {"dout": Q2, "dx": Q}),
+        ("kda_scan_backward", {"g": Q2, "dg": Q}), ("kda_scan_backward", {"init": Q, "dinit": Q}),
+        ("kda_scan_backward", {"dfin": Q, "dinit": Q}), ("kda_conv_prefill", {"x": Q}),
+        ("kda_conv_prefill", {"x": Q2}), ("kda_conv_prefill", {"init": P, "fin": ctypes.c_void_p(0x10010)}),
+        ("kda_conv_backward", {"x": Q}), ("kda_conv_backward", {"dout": Q2}),
+        ("kda_conv_backward", {"init": P, "dinit": P}), ("kda_conv_backward", {"dfin": P, "dinit": P})]
 BAD += [("kda_rmsnorm", {"sum": P}),                    # a sum without a residual
         ("kda_rmsnorm", {"mx": P}), ("kda_rmsnorm", {"sc": P}), ("kda_rmsnorm", {"res": P, "sum": ODD})]
 
@@ -77,6 +88,12 @@ def test_rejects(lib, name, kw):
     ("kda_conv_prefill", dict(W=5)), ("kda_conv_prefill", dict(W=1)), ("kda_conv_decode_step", dict(W=5)),
     ("kda_conv_backward", dict(W=1)), ("kda_conv_backward", dict(W=8)), ("kda_rmsnorm", dict(D=16385)),
     ("kda_rmsnorm_backward", dict(D=16385)),
+    # launches of 2^32 threads and more
+    ("kda_scan_prefill", dict(T=2 ** 30 + 1, D=1, N=4)), ("kda_scan_backward", dict(T=2 ** 30 + 1, D=1, N=4)),
+    ("kda_scan_prefill", dict(N=2 ** 27)), ("kda_conv_decode_step", dict(N=2 ** 31 - 1, D=1)),
+    ("kda_conv_prefill", dict(N=2 ** 30, init=None, fin=ctypes.c_void_p(1 << 40))),
+    ("kda_conv_backward", dict(D=2 ** 28, T=1, x=ctypes.c_void_p(1 << 40), dout=ctypes.c_void_p(1 << 41))),
+    ("kda_rmsnorm", dict(rows=2 ** 31 - 1, D=1)),
 ])
 def test_does_not_support(lib, name, kw):
     assert call(lib, name, **kw) == UNSUPPORTED
