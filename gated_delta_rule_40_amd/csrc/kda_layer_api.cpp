@@ -98,6 +98,7 @@ kda_status kda_scan_decode_step(const void *x, const float *g, float *state_inou
         !array_ok(out, n, elem_size(dtype)))
         return KDA_ERR_INVALID_ARG;
     if (n == 0) return KDA_OK;
+    if (!same_or_apart(x, out, n * elem_size(dtype))) return KDA_ERR_INVALID_ARG;
     return from_hip(kda_launch_scan_step(dtype == KDA_BF16, x, g, state_inout, n, out, hip_stream(stream)));
 }
 
@@ -170,6 +171,7 @@ kda_status kda_conv_decode_step(const void *x, const float *weight, const float 
         return KDA_ERR_INVALID_ARG;
     if (width < 2 || width > 4) return KDA_ERR_UNSUPPORTED;
     if (n == 0) return KDA_OK;
+    if (!same_or_apart(x, out, n * e)) return KDA_ERR_INVALID_ARG;
     return from_hip(kda_launch_conv_step(dtype == KDA_BF16, x, weight, bias, state_inout, num_seqs, channels, width,
                                          silu != 0, out, hip_stream(stream)));
 }
@@ -225,6 +227,10 @@ kda_status kda_rmsnorm(const void *x, const void *residual, const float *weight,
         return KDA_ERR_INVALID_ARG;
     if (channels > kMaxNormChannels) return KDA_ERR_UNSUPPORTED;
     if (n == 0) return KDA_OK;
+    if (!same_or_apart(x, out, n * e) || !same_or_apart(x, residual_out, n * e) ||
+        !same_or_apart(residual, out, n * e) || !same_or_apart(residual, residual_out, n * e) ||
+        !apart(out, residual_out, n * e))
+        return KDA_ERR_INVALID_ARG;
     return from_hip(kda_launch_rmsnorm(dtype == KDA_BF16, x, residual, weight, rows, channels, eps, residual_out, out,
                                        out_mx, scales, hip_stream(stream)));
 }
@@ -250,6 +256,8 @@ kda_status kda_rmsnorm_backward(const void *x, const float *weight, const void *
     if (dweight && !workspace_ok(workspace, workspace_bytes, kda_rmsnorm_bwd_ws_bytes(rows, channels), 4))
         return KDA_ERR_INVALID_ARG;
     if (n == 0 && !dweight) return KDA_OK;
+    if (!same_or_apart(x, dx, n * e) || !same_or_apart(dout, dx, n * e) || !same_or_apart(dresidual, dx, n * e))
+        return KDA_ERR_INVALID_ARG;
     return from_hip(kda_launch_rmsnorm_backward(dtype == KDA_BF16, x, weight, dout, dresidual, rows, channels, eps,
                                                 dx, dweight, workspace, hip_stream(stream)));
 }

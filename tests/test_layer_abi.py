@@ -73,7 +73,12 @@ BAD += [("kda_scan_prefill", {"x": Q, "out": Q2}), ("kda_scan_prefill", {"init":
         ("kda_scan_backward", {"dfin": Q, "dinit": Q}), ("kda_conv_prefill", {"x": Q}),
         ("kda_conv_prefill", {"x": Q2}), ("kda_conv_prefill", {"init": P, "fin": ctypes.c_void_p(0x10010)}),
         ("kda_conv_backward", {"x": Q}), ("kda_conv_backward", {"dout": Q2}),
-        ("kda_conv_backward", {"init": P, "dinit": P}), ("kda_conv_backward", {"dfin": P, "dinit": P})]
+        ("kda_conv_backward", {"init": P, "dinit": P}), ("kda_conv_backward", {"dfin": P, "dinit": P}),
+        ("kda_scan_decode_step", {"N": 8, "x": Q, "out": Q2}), ("kda_conv_decode_step", {"N": 8, "x": Q2, "out": Q}),
+        ("kda_rmsnorm", {"x": Q, "out": Q2}), ("kda_rmsnorm", {"res": Q, "out": Q2}),
+        ("kda_rmsnorm", {"x": P, "res": Q, "sum": Q2}), ("kda_rmsnorm", {"res": Q, "sum": Q, "out": Q}),
+        ("kda_rmsnorm_backward", {"x": Q, "dx": Q2}), ("kda_rmsnorm_backward", {"dout": Q, "dx": Q2}),
+        ("kda_rmsnorm_backward", {"dres": Q2, "dx": Q})]
 BAD += [("kda_rmsnorm", {"sum": P}),                    # a sum without a residual
         ("kda_rmsnorm", {"mx": P}), ("kda_rmsnorm", {"sc": P}), ("kda_rmsnorm", {"res": P, "sum": ODD})]
 
