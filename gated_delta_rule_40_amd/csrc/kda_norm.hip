@@ -114,7 +114,7 @@ __device__ __forceinline__ void store_words(uint8_t *p, const uint32_t (&q)[2])
 
 // Sums over a row's tpr threads (a power of two; a part of a wave, or whole
 // waves).  `red` holds a value for every wave; called by the whole workgroup.
-template <int M> __device__ __forceinline__ void row_sums(float (&v)[M], int tpr, float (*red)[M])
+template <typename F, int M> __device__ __forceinline__ void row_sums(F (&v)[M], int tpr, F (*red)[M])
 {
     for (int off = min(tpr, 64) >> 1; off > 0; off >>= 1)
 #pragma unroll
@@ -128,7 +128,7 @@ template <int M> __device__ __forceinline__ void row_sums(float (&v)[M], int tpr
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-        float s = 0.f;
+        F s = 0;
         for (int i = 0; i < waves; ++i) s += red[first + i][m];
         v[m] = s;
     }
@@ -145,14 +145,37 @@ __device__ __forceinline__ int mx_scale(uint32_t amax_bits)
     return max(e - 9 + (m > 0.875f ? 1 : 0), -127) + 127;
 }
 
+// y = r w / sqrt(mean): in fp32, which is off by up to three steps, and where
+// that could matter to the 8-bit value in fp64, rounded to odd (towards zero,
+// the last bit set if that is not exact), so that the next rounding is as good
+// as the only one.
+struct Rstd {
+    float hi;
+    double exact;
+    __device__ __forceinline__ explicit Rstd(double mean) : hi(1.f / sqrtf((float)mean)), exact(hi) {
+        const double off = __builtin_fma(-mean * exact, exact, 1.0);   // 1 - mean hi^2: one step to the root
+        if (__builtin_fabs(off) < 1.0) exact = __builtin_fma(0.5 * exact, off, exact);   // (mean is not 0 or infinite)
+    }
+    __device__ __forceinline__ float times(float r, float w) const { return r * hi * w; }
+    __device__ __forceinline__ float odd(float r, float w) const {
+        const double y = (double)r * exact * w;
+        const float f = (float)y;
+        const double rest = y - f;
+        // (`exact` is within 2^-47: a smaller rest is none)
+        if (!(__builtin_fabs(rest) > 0x1p-44 * __builtin_fabs(y)) || __builtin_isinf(f)) return f;
+        const uint32_t bits = __float_as_uint(f), back = (rest < 0) != (f < 0.f);
+        return __uint_as_float((bits - back) | 1u);
+    }
+};
+
 // ---------------------------------------------------------------- forward
 // C pieces a thread
 template <typename T, int VW, int C, bool ONCE, bool TAIL, bool RES, bool MX>
 __global__ void kda_rmsnorm_kernel(const T *x, const T *res, const float *w, int32_t rows, int32_t D, int32_t tpr,
-                                   float eps, T *sum, T *out, uint8_t *mx, uint8_t *scales)
+                                   double per_channel, float eps, T *sum, T *out, uint8_t *mx, uint8_t *scales)
 {
     typedef Piece<T, VW, ONCE> P;
-    __shared__ float red[16][1];
+    __shared__ double red[16][1];
     const Pieces<VW, TAIL> pc{D, (int32_t)(threadIdx.x & (tpr - 1)), tpr};
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     const bool live = row < rows;
@@ -164,33 +187,50 @@ __global__ void kda_rmsnorm_kernel(const T *x, const T *res, const float *w, int
         xr[k] = pc.template load<P>(x + base, k);
         if (RES) rr[k] = pc.template load<P>(res + base, k);
     }
-    float r[C][VW], ss[1] = {0.f};
+    float r[C][VW];
+    double ss[1] = {0.};   // (fp32 over a piece)
 #pragma unroll
     for (int k = 0; k < C; ++k) {
+        float part = 0.f;
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
             r[k][j] = P::at(xr[k], j) + (RES ? P::at(rr[k], j) : 0.f);
-            if (pc.count(k) > 0) ss[0] += r[k][j] * r[k][j];
+            if (pc.count(k) > 0) part += r[k][j] * r[k][j];
         }
+        ss[0] += part;
         if (RES && sum && live) pc.template store<P>(sum + base, k, r[k]);
     }
-    row_sums<1>(ss, tpr, red);
-    const float rstd = 1.f / sqrtf(ss[0] / D + eps);
+    row_sums(ss, tpr, red);
+    const Rstd rstd(ss[0] * per_channel + eps);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
         const int32_t i = pc.index(k), n = pc.count(k);
-        float g[VW];
+        float g[VW], y[VW];
         if (w) pc.weight(w, k, g);
 #pragma unroll
-        for (int j = 0; j < VW; ++j) r[k][j] = r[k][j] * rstd * (w ? g[j] : 1.f);
-        if (out && live) pc.template store<P>(out + base, k, r[k]);
+        for (int j = 0; j < VW; ++j) y[j] = rstd.times(r[k][j], w ? g[j] : 1.f);
+        if (out && live) pc.template store<P>(out + base, k, y);
         if (MX) {   // a block's MXB / VW pieces lie in consecutive lanes
-            uint32_t top = 0;   // of the magnitudes' bits, so that a NaN is the largest
+            auto block_top = [&]() {   // the largest of the magnitudes' bits, so that a NaN is the largest
+                uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < VW; ++j)
-                if (j < n) top = max(top, __float_as_uint(r[k][j]) & 0x7fffffffu);
+                for (int j = 0; j < VW; ++j)
+                    if (j < n) top = max(top, __float_as_uint(y[j]) & 0x7fffffffu);
 #pragma unroll
-            for (int off = MXB / VW / 2; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+                for (int off = MXB / VW / 2; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off));
+                return top;
+            };
+            uint32_t top = block_top();
+            // within 4 steps of a tie of e4m3 (bit 19 is half a step of it) or of a
+            // scale's end (448, 1.75 2^8)?  One value in 10^5 is.
+            uint32_t near = (top & 0x7fffffu) - (0x600000u - 4);
+#pragma unroll
+            for (int j = 0; j < VW; ++j) near = min(near, (__float_as_uint(y[j]) & 0xfffffu) - (0x80000u - 4));
+            if (__any(near <= 8)) {
+#pragma unroll
+                for (int j = 0; j < VW; ++j) y[j] = rstd.odd(r[k][j], w ? g[j] : 1.f);
+                top = block_top();
+            }
             const int sc = mx_scale(top);
             if (n > 0 && live) {
                 if (i % (MXB / VW) == 0) scales[row * ((D + MXB - 1) / MXB) + i / (MXB / VW)] = (uint8_t)sc;
@@ -199,7 +239,7 @@ __global__ void kda_rmsnorm_kernel(const T *x, const T *res, const float *w, int
                 for (int j = 0; j < VW; j += 4) {
                     float v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = ldexpf(r[k][j + e], 127 - sc);
+                    for (int e = 0; e < 4; ++e) v[e] = ldexpf(y[j + e], 127 - sc);
                     const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
                     q[j / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
                 }
@@ -258,7 +298,7 @@ __global__ void kda_rmsnorm_bwd_kernel(const T *x, const float *w, const T *dout
                     s[0] += r * r;
                     s[1] += P::at(dr[k], j) * g[k][j] * r;
                 }
-        row_sums<2>(s, tpr, red);
+        row_sums(s, tpr, red);
         const float rstd = 1.f / sqrtf(s[0] / D + eps), m = s[1] / D * rstd * rstd;
 #pragma unroll
         for (int k = 0; k < C; ++k) {
@@ -324,7 +364,7 @@ hipError_t run_rmsnorm(const void *x, const void *res, const float *w, int32_t r
     const RowShape sh = row_shape((D + VW - 1) / VW, C, MXB / VW);
     const int64_t per = sh.threads / sh.tpr, blocks = (rows + per - 1) / per;
     if (!kda_grid_ok(blocks, sh.threads)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)blocks), dim3(sh.threads), 0, s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, eps, (T *)sum,
+    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)blocks), dim3(sh.threads), 0, s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, 1.0 / D, eps, (T *)sum,
                        (T *)out, mx, scales);
     return hipGetLastError();
 }

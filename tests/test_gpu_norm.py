@@ -141,6 +141,32 @@ def test_mx_scale_edges(D):
         assert bool((sc.view(torch.uint8)[0] == 127).all()) and bool((mx.view(torch.uint8)[0] == 0).all())
 
 
+@pytest.mark.parametrize("D", [128, 4096])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_mx_rounds_once(D, dtype):
+    """Rows of one magnitude c and eps = 0 have y = w or -w, exactly; the weights lie on ties of e4m3, on scales' ends,
+    and a step or two of fp32 beside them.  The squares of eight bits and their sums are exact in fp32, so the only
+    rounding there has to be is the last one."""
+    gen = np.random.default_rng(D)
+    c = np.array([1.0, 3.0, 129 / 128, 141 / 128, 182 / 256, 249.0, 193 * 2.0 ** -12, 255 * 2.0 ** 7])
+    x = torch.tensor(c[:, None] * gen.choice([-1.0, 1.0], (len(c), D))).to(DT[dtype])
+    assert np.array_equal(np.abs(host(x)), np.repeat(c[:, None], D, 1))
+    w = 2.0 ** gen.integers(-6, 7, D) * (1 + (2 * gen.integers(0, 8, D) + 1) / 16)
+    w[::32] = 448.0
+    w = w * np.repeat(2.0 ** gen.integers(-30, 30, D // 32), 32)
+    w = (w.astype(np.float32).view(np.int32) + gen.integers(-2, 3, D).astype(np.int32)).view(np.float32)
+    mx = torch.empty(len(c), D, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = torch.empty(len(c), D // 32, dtype=torch.uint8, device="cuda")
+    K.kda_rmsnorm(x.cuda(), torch.tensor(w).cuda(), out_mx=mx, scales=sc, eps=0.0)
+    y = np.sign(host(x)) * w.astype(np.float64)
+    m, e = np.frexp(np.abs(y).reshape(len(c), -1, 32).max(2))
+    e = e - 9 + (m > 0.875)
+    assert np.array_equal(sc.cpu().numpy(), e + 127)
+    v = y / np.repeat(2.0 ** e, 32, 1)
+    step = 2.0 ** (np.maximum(np.frexp(v)[1] - 1, -6) - 3)
+    assert np.array_equal(host(mx.float()), np.rint(v / step) * step)      # ties to even
+
+
 def test_mx_of_a_block_with_nan_or_infinity():
     x = torch.randn(4, 256, device="cuda")
     w = torch.ones(256, device="cuda")
