@@ -6,10 +6,15 @@
 //     dw_j = sum_t dpre_t x_{t - (W - 1) + j},  dbias = sum_t dpre_t
 //
 // One wave walks a strip of tokens of 64 V channels (V consecutive channels a
-// lane, 16 bytes of them where alignment allows), the last W - 1 inputs and
-// the weights in registers: every input is read once (and W - 1 rows of it at a
-// strip's edge once more, mostly from cache) and every output written once, so
-// HBM's rate is the bound.  Rows are read a batch ahead of their use.
+// lane), the last W - 1 inputs and the weights in registers: every input is read
+// once (and W - 1 rows of it at a strip's edge once more, mostly from cache) and
+// every output written once, so HBM's rate is the bound.  Rows are read a batch
+// ahead of their use.
+//
+// Measured on one MI355X (a large copy reaches 4.9-5.4 TB/s there), width 4 with
+// SiLU, bf16: 65,536 x 4,096 196 us (5.5 TB/s), its backward for 131,072 x 2,048
+// 326 us (4.9 TB/s; 32 vector instructions an element take two thirds of that),
+// 512 single tokens x 12,288 19.5 us (5.2 TB/s).
 //
 // A sequence's initial state is read by the wave whose strip holds the
 // sequence's first token and by no other: that wave also computes the first
@@ -92,7 +97,7 @@ __device__ __forceinline__ typename Row<T, V>::raw row_before(const T *x, const 
 
 // ---------------------------------------------------------------- forward
 template <typename T, int W, int V, bool SILU>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3)))
+__global__ __launch_bounds__(256)
 void kda_conv_kernel(const T *x, const T *init, ConvArgs a, Seqs sq, int32_t strip, int32_t nstrips, int32_t cols,
                      int32_t width, uint32_t work, T *out, T *fin)
 {
@@ -452,11 +457,13 @@ inline int64_t up(int64_t n, int64_t per) { return (n + per - 1) / per; }
 
 // The backward's strips: as long as three workgroups for every CU allow (what
 // its registers let be resident at once; longer strips also read fewer rows
-// twice and leave fewer partial sums), and 16 tokens at least.
+// twice and leave fewer partial sums: 131,072 x 2,048 with the forward 555 us,
+// 575 with 1,024 workgroups, 588 with 2,048), and 16 tokens at least.
 constexpr int32_t BWD_GROUPS = 768;
 constexpr int BWD_V = 4;   // channels a lane (the sums and unfinished places of eight would not fit the registers)
 
-// Rows too short for BWD_V channels a lane (most lanes would be idle) take one.
+// Rows too short for BWD_V channels a lane (most lanes would be idle) take one
+// (200,000 x 64 with the forward: 51 us, 74 with four; x 192: 128, 105).
 inline bool bwd_wide(int64_t D) { return D >= 128; }
 inline int64_t bwd_cols(int64_t D) { return up(D, bwd_wide(D) ? 64 * BWD_V : 64); }
 inline int32_t bwd_strip(int32_t T, int64_t D)
@@ -466,14 +473,18 @@ inline int32_t bwd_strip(int32_t T, int64_t D)
 }
 inline int32_t bwd_parts(int32_t T, int64_t D) { return (int32_t)(T > 0 ? up(up(T, bwd_strip(T, D)), 4) : 1); }
 
+// Short strips: the waves that begin and end spread reads and writes evenly
+// (65,536 x 4,096, V = 4: 8 tokens 222 us, 12 199, 16 196, 24 203, 64 207;
+// 8,192 x 2,048: 14.4, 14.2, 13.0, 13.9).
+constexpr int32_t STRIP = 16;
+
 template <typename T, int W, int V>
 hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, void *out, void *fin,
                     hipStream_t s)
 {
     const int32_t cw = kda_column_width((int32_t)a.D, V);
     const int64_t cols = up(a.D, cw);
-    // strips of 64 tokens where these give every SIMD its waves, shorter ones otherwise
-    const int32_t strip = up(sq.T, 64) * cols >= 4096 ? 64 : 16;
+    const int32_t strip = STRIP;
     const int32_t nstrips = (int32_t)up(sq.T, strip);
     const int64_t work = up(nstrips, 4) * cols, groups = work + empty_groups(sq.N, init, fin);
     if (groups == 0) return hipSuccess;
@@ -493,8 +504,11 @@ template <typename T, int W, int V>
 hipError_t run_conv_step(const void *x, const ConvArgs &a, void *state, int32_t N, void *out, hipStream_t s)
 {
     const int64_t cols = up(a.D, 256 * V);
-    if (!kda_grid_ok(N * cols >= 2048 ? cols * up(N, 4) : cols * N, 256)) return hipErrorInvalidConfiguration;
-    if (N * cols >= 2048)
+    // four sequences to a reading of the weights where there are many (512 x 4,096:
+    // 8.6 us, 13.3 with one; 64 x 12,288: 5.9, 7.2; 8 x 12,288: 5.1, 4.1)
+    const bool many = N * cols >= 384;
+    if (!kda_grid_ok(many ? cols * up(N, 4) : cols * N, 256)) return hipErrorInvalidConfiguration;
+    if (many)
         hipLaunchKernelGGL((kda_conv_step_kernel<T, W, V, 4>), dim3((unsigned)(cols * up(N, 4))), dim3(256), 0, s,
                            (const T *)x, (T *)state, a, N, (int32_t)cols, (T *)out);
     else
@@ -537,16 +551,17 @@ template <int V, typename F> hipError_t with_width(int32_t width, F f)
     }
 }
 
-// 16 bytes a lane, or fewer where that would leave most lanes idle.
+// Channels a lane: four (65,536 x 4,096 in bf16: 196 us, 203 with two, 206 with
+// eight; 16,384 x 4,096: 44, 47, 54), or fewer where many lanes would be idle
+// (200,000 x 320: 51 us, 45 with two; 200,000 x 64: 26, 16 with one).
 template <typename T>
 hipError_t conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, int32_t width, void *out, void *fin,
                 hipStream_t s)
 {
-    constexpr int V = 16 / sizeof(T);
     auto f = [&](auto w, auto v) { return run_conv<T, w(), v()>(x, a, init, sq, out, fin, s); };
-    if (a.D > 32 * V) return with_width<V>(width, f);
-    if (sizeof(T) == 2 && a.D > 64) return with_width<sizeof(T) == 2 ? 2 : 1>(width, f);
-    return with_width<1>(width, f);
+    if (a.D <= 64) return with_width<1>(width, f);
+    const bool idle = a.D > 256 && 4 * a.D <= 3 * 256 * up(a.D, 256);
+    return a.D <= 128 || idle ? with_width<2>(width, f) : with_width<4>(width, f);
 }
 
 template <typename T>

@@ -382,7 +382,9 @@ hipError_t rmsnorm_as(const void *x, const void *res, const float *w, int32_t ro
 
 // calls f with the number of pieces a thread, whether rows go past the caches,
 // and whether they end in a part of a piece, as compile-time values.  Few rows:
-// one piece a thread, so that a row's latency is short.
+// one piece a thread, so that a row's latency is short (64 x 4,096: 3.3 us, 4.5
+// with four; 512 x 7,168: 7.1, 6.9); and for short rows, so that a row has
+// threads enough (200,000 x 128: 35 us, 56 with four; 100,000 x 512: 68, 71).
 template <typename T, int MOST, typename F> hipError_t with_shape(int32_t rows, int32_t D, F f)
 {
     constexpr int VW = 16 / sizeof(T);

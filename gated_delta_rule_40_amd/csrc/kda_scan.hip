@@ -13,10 +13,10 @@
 // has to be (8 bytes an element with bf16 x), and HBM's rate is the bound.
 //
 // The state that enters a tile is joined from the runs of the tiles before it
-// in its block of 16, 32 or 64 tiles (for V = 4, 2, 1), all read side by side, and the state that
-// enters the block, which is passed from block to block.  Which runs are
-// joined, and in which order, depends on the tile alone, not on what is ready
-// first, so that results are the same bits on every call.  A published run is
+// in its block of 16, 32 or 64 tiles (for V = 4, 2, 1), all read side by side,
+// and the state that enters the block, which is passed from block to block.
+// Which runs are joined, and in which order, depends on the tile alone, not on
+// what is ready first, so that results are the same bits on every call.  A published run is
 // one 64-bit word a channel, written and polled with relaxed device-scope
 // atomics: the word is its own flag (all ones: not there yet), so no fence is
 // needed between data and flag.  Tiles of a channel block are handed out in
@@ -27,8 +27,8 @@
 //     dh_t = dout_t + e,  e <- a_t dh_t,
 // with the state entering each tile taken from the forward pass's checkpoints.
 //
-// Measured on one MI355X (a large copy reaches 5.0-5.4 TB/s there): 2^20 tokens
-// x 1,024 channels in bf16 1.59 ms (5.4 TB/s of the 8 bytes an element, counters
+// Measured on one MI355X (a large copy reaches 4.9-5.4 TB/s there): 2^20 tokens
+// x 1,024 channels in bf16 1.57 ms (5.5 TB/s of the 8 bytes an element, counters
 // show 3 % more read and 10 % more written, the published words), forward and
 // backward of 65,536 x 4,096 1.07 ms (5.5 TB/s of 22 bytes an element).  Short
 // batches are bound by the chain of waits: 4,096 x 1,024 takes 12 us in the
