@@ -11,10 +11,10 @@
 // barrier), a longer one a workgroup.  Pieces need the alignment of an element
 // only; the last one of a row may be a part of one (TAIL).
 //
-// Measured on one MI355X (a large copy reaches 5.0-5.4 TB/s there), bf16:
-// 16,384 x 7,168 with the residual and the 8-bit output 135-144 us (5.7-6.1 TB/s
-// of 7.03 bytes an element), 65,536 x 2,048 with the residual 176 us (6.1 TB/s
-// of 8 bytes), its gradients 196 us (5.5 TB/s of 8 bytes), 64 x 4,096 3.6 us.
+// Measured on one MI355X (a large copy reaches 4.9-5.4 TB/s there), bf16:
+// 16,384 x 7,168 with the residual and the 8-bit output 141-144 us (5.7-5.8 TB/s
+// of 7.03 bytes an element), 65,536 x 2,048 with the residual 176-179 us (6.0
+// TB/s of 8 bytes), its gradients 196 us (5.5 TB/s of 8 bytes), 64 x 4,096 3.6 us.
 #include "kda_colsum.hpp"
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
@@ -148,7 +148,9 @@ __device__ __forceinline__ int mx_scale(uint32_t amax_bits)
 // y = r w / sqrt(mean): in fp32, which is off by up to three steps, and where
 // that could matter to the 8-bit value in fp64, rounded to odd (towards zero,
 // the last bit set if that is not exact), so that the next rounding is as good
-// as the only one.
+// as the only one (16,384 x 7,168: 5-9 of 117 M values fall to a neighbour of the
+// exact one, 66-72 with fp32 alone, in the same time; exact products for every
+// value are 7 % slower).
 struct Rstd {
     float hi;
     double exact;
@@ -364,8 +366,9 @@ hipError_t run_rmsnorm(const void *x, const void *res, const float *w, int32_t r
     const RowShape sh = row_shape((D + VW - 1) / VW, C, MXB / VW);
     const int64_t per = sh.threads / sh.tpr, blocks = (rows + per - 1) / per;
     if (!kda_grid_ok(blocks, sh.threads)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)blocks), dim3(sh.threads), 0, s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, 1.0 / D, eps, (T *)sum,
-                       (T *)out, mx, scales);
+    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)blocks), dim3(sh.threads), 0,
+                       s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, 1.0 / D, eps, (T *)sum, (T *)out, mx,
+                       scales);
     return hipGetLastError();
 }
 

@@ -31,7 +31,7 @@
 // x 1,024 channels in bf16 1.57 ms (5.5 TB/s of the 8 bytes an element, counters
 // show 3 % more read and 10 % more written, the published words), forward and
 // backward of 65,536 x 4,096 1.07 ms (5.5 TB/s of 22 bytes an element).  Short
-// batches are bound by the chain of waits: 4,096 x 1,024 takes 12 us in the
+// batches are bound by the chain of waits: 4,096 x 1,024 takes 13 us in the
 // kernel, of which the counter's answer is 2, the reads 2, the gates and runs 2,
 // passing the state on 3 and the writes 2.
 #include "kda_device.hpp"
@@ -390,7 +390,8 @@ void kda_scan_kernel(const T *x, const float *g, const float *init, Seqs sq, int
 template <typename T, int V>
 __global__ __launch_bounds__(NTH) __attribute__((amdgpu_waves_per_eu(4)))   // two workgroups per CU
 void kda_scan_bwd_kernel(const T *x, const float *g, const float *init, Seqs sq, int64_t D, int32_t cols,
-                         uint32_t work, const T *dout, const float *dfin, const float *chk, T *dx, float *dg, float *dinit, Chain ch)
+                         uint32_t work, const T *dout, const float *dfin, const float *chk, T *dx, float *dg,
+                         float *dinit, Chain ch)
 {
     constexpr int CB = 64 * V;
     typedef typename Vec<T, V>::raw XR;
