@@ -612,6 +612,16 @@ hipError_t run_scan(const void *x, const float *g, const float *init, const Seqs
     return hipGetLastError();
 }
 
+// One channel a lane: for rows of up to 64 (300,000 x 64 in bf16: 68 us, 135 with
+// idle lanes of two), and where two would leave at most one workgroup for every
+// CU, so that there are twice as many (graph replays, bf16: 4,096 x 1,024 13.6 us,
+// 14.1 with two, with the gradients 30.8, 34.0; fp32: 14.5, 15.5 and 33.8, 40.8;
+// beyond, fp32 10,007 x 1,000: 41.5 us, 37.2 with two).
+inline bool one_channel(const Chain &ch)
+{
+    return ch.D <= 64 || ch.ntiles * ((ch.D + 127) / 128) <= 256;
+}
+
 template <typename T>
 hipError_t scan(const void *x, const float *g, const float *init, const Seqs &sq, int32_t D, void *out, float *fin,
                 float *chk, const Chain &ch, hipStream_t s)
@@ -619,13 +629,12 @@ hipError_t scan(const void *x, const float *g, const float *init, const Seqs &sq
     // Four channels a lane for bf16 where that leaves two workgroups for every
     // CU and few lanes idle (2^20 x 1,024: 1.70 ms, 1.94 with two; 4,096 x 1,024
     // with its 128 workgroups: 23.7 us, 19.4 with two; fp32 tokens of four would
-    // not fit the registers); one for rows of up to 64 (300,000 x 64: 68 us, 135
-    // with idle lanes).
+    // not fit the registers).
     const int64_t wide = ((int64_t)D + 255) / 256;
     if (sizeof(T) == 2 && ch.ntiles * wide >= 512 && 4 * (int64_t)D >= 3 * 256 * wide)
         return run_scan<T, sizeof(T) == 2 ? 4 : 2>(x, g, init, sq, D, out, fin, chk, ch, s);
-    if (D > 64) return run_scan<T, 2>(x, g, init, sq, D, out, fin, chk, ch, s);
-    return run_scan<T, 1>(x, g, init, sq, D, out, fin, chk, ch, s);
+    return one_channel(ch) ? run_scan<T, 1>(x, g, init, sq, D, out, fin, chk, ch, s)
+                           : run_scan<T, 2>(x, g, init, sq, D, out, fin, chk, ch, s);
 }
 
 template <typename T, int V>
@@ -647,8 +656,8 @@ hipError_t scan_backward(const void *x, const float *g, const float *init, const
                          const float *dfin, const float *chk, void *dx, float *dg, float *dinit, const Chain &ch,
                          hipStream_t s)
 {
-    if (D > 64) return run_scan_backward<T, 2>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
-    return run_scan_backward<T, 1>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
+    return one_channel(ch) ? run_scan_backward<T, 1>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s)
+                           : run_scan_backward<T, 2>(x, g, init, sq, D, dout, dfin, chk, dx, dg, dinit, ch, s);
 }
 
 }  // namespace kda

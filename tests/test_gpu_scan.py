@@ -49,7 +49,7 @@ CASES = [
     ([64] * 20 + [0] * 3 + [7] * 9, 1000), ([2 ** i for i in range(11)], 65), ([3000, 5000], 12),
     # channel counts at a workgroup's edge, and enough tiles for the widest rows
     ([300, 33], 129), ([200, 90, 0, 1], 257), ([64, 200], 259), ([129, 128], 383), ([5000, 11, 1000], 2562),
-    ([6000, 90], 2561),
+    ([6000, 90], 2561), ([9000, 0, 333, 7, 8001], 259), ([4100, 1, 8192], 385),
 ]
 
 
