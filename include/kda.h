@@ -539,14 +539,13 @@ kda_status kda_conv_backward(const void *x, const float *weight, const float *bi
  *                 saturates (at least 2^-127, the smallest there is; 1 for a
  *                 block of zeros; 255, which is NaN, for a block that holds an
  *                 infinity or a NaN).
- * At least one of out and out_mx is given.  y is computed from the unrounded r
+ * At least one of out and out_mx is given.  y is computed from r as fp32 holds it
  * and rounded into each output by itself: into `out` from fp32, into the 8-bit
- * values and scales as if once (fp64 decides where fp32 is too near a tie; only
- * the rounding of the fp32 squares, and values below 2^-6 of their scale, are
- * left).  channels at most 16,384
- * (KDA_ERR_UNSUPPORTED above).  The sum of a row's r^2 is formed in fp32: it
- * has to stay within that range (|r| up to 10^17 does), and a row whose mean(r^2)
- * + eps is 0 has NaN in it.
+ * values and scales as if once (r^2 is summed in fp64, and fp64 decides where
+ * fp32 is too near a tie; only values below 2^-6 of their scale may be rounded
+ * from fp32's y near a tie).  channels at most 16,384 (KDA_ERR_UNSUPPORTED above).
+ * mean(r^2) + eps has to lie in fp32's range (|r| up to 10^19 does); a row where
+ * it is 0 has NaN in it.
  */
 #define KDA_MX_BLOCK 32
 

@@ -266,3 +266,58 @@ def test_rejects_mismatched_tensors():
         with pytest.raises(K.KdaError) as e:
             K.kda_rmsnorm(d["x"], d["w"], **kw)
         assert e.value.status == K.KDA_ERR_INVALID_ARG
+
+
+def on_borders(x, eps, gen):
+    """A weight for the row x that puts y = x / sqrt(mean(x^2) + eps) * weight as near as fp32 weights come: in every
+    block 16 values below a scale's end (448 times a power of two) and 16 on either side of a tie of e4m3.  With it, y
+    in extended precision."""
+    D = len(x)
+    wide = x.astype(np.longdouble)
+    rms = np.sqrt((wide * wide).sum() / D + np.longdouble(np.float32(eps)))
+    ties = 2.0 ** gen.integers(0, 8, D) * (1 + (2 * gen.integers(0, 8, D) + 1) / 16)
+    end = np.arange(D) % 32 < 16
+    goal = np.where(end, 448.0, ties) * np.repeat(2.0 ** gen.integers(-6, 6, D // 32), 32)
+    w = (goal * rms / np.abs(wide)).astype(np.float32)
+    w = np.where(end & (np.abs(wide / rms * w) >= goal), np.nextafter(w, np.float32(0)), w)
+    return w, wide / rms * w
+
+
+@pytest.mark.parametrize("D", [128, 512, 4096, 7168])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [1.0, 300.0])
+def test_mx_scales_and_values_beside_their_borders(D, dtype, size):
+    """fp64 sums of exact squares are off by D 2^-53 at most, the root and the products by 2^-46: what lies further from
+    a border than that is rounded as y itself."""
+    gen = np.random.default_rng(int(D + size))
+    slack = D * 2.0 ** -53 + 2.0 ** -46
+    seen = 0
+    for _ in range(4):
+        x = torch.tensor(gen.standard_normal(D) * size).to(DT[dtype])
+        x[x == 0] = 1.0
+        w, y = on_borders(host(x), EPS, gen)
+        mx = torch.empty(1, D, dtype=torch.float8_e4m3fn, device="cuda")
+        sc = torch.empty(1, D // 32, dtype=torch.uint8, device="cuda")
+        K.kda_rmsnorm(x.view(1, D).cuda(), torch.tensor(w).cuda(), out_mx=mx, scales=sc, eps=EPS)
+        top = np.abs(y).reshape(-1, 32).max(1)
+        m, e = np.frexp(top)
+        e = e - 9 + (m > 0.875)
+        sure = np.abs(m / np.longdouble(0.875) - 1) > slack
+        assert np.array_equal(sc.cpu().numpy()[0][sure], (e + 127)[sure])
+        v = y / np.repeat(2.0 ** e, 32)
+        step = 2.0 ** (np.maximum(np.frexp(v)[1] - 1, -6) - 3)
+        frac = np.abs(v / step) % 1
+        sure = np.repeat(sure, 32) & (np.abs(frac - 0.5) * step > slack * np.abs(v))
+        assert np.array_equal(host(mx.float())[0][sure], (np.rint(v / step) * step).astype(np.float64)[sure])
+        seen += int(sure.sum())
+    assert seen > 0.99 * 4 * D
+
+
+def test_squares_beyond_fp32():
+    # the sum of the squares passes fp32's largest number, their mean does not
+    gen = torch.Generator().manual_seed(8)
+    x = (1e18 * torch.randn(3, 4096, generator=gen)).cuda()
+    out = torch.empty_like(x)
+    K.kda_rmsnorm(x, None, out, eps=EPS)
+    f = R.rmsnorm(host(x), None, None, EPS)
+    R.close(host(out), f["y"], f["e_y"], "fp32", "out")
