@@ -166,7 +166,8 @@ struct Rstd {
         const double rest = y - f;
         // (`exact` is within 2^-47: a smaller rest is none)
         if (!(__builtin_fabs(rest) > 0x1p-44 * __builtin_fabs(y)) || __builtin_isinf(f)) return f;
-        const uint32_t bits = __float_as_uint(f), back = (rest < 0) != (f < 0.f);
+        // (y's sign, not f's: f may be -0, from which a step back would be a NaN)
+        const uint32_t bits = __float_as_uint(f), back = (rest < 0) != (y < 0);
         return __uint_as_float((bits - back) | 1u);
     }
 };

@@ -321,3 +321,38 @@ def test_squares_beyond_fp32():
     K.kda_rmsnorm(x, None, out, eps=EPS)
     f = R.rmsnorm(host(x), None, None, EPS)
     R.close(host(out), f["y"], f["e_y"], "fp32", "out")
+
+
+@pytest.mark.parametrize("D", [128, 512, 4096])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("same_row", [True, False])
+def test_mx_of_values_below_fp32_beside_ties(D, dtype, same_row):
+    """y that vanishes in fp32, of either sign, in a wave that also holds a tie of e4m3: in the same row (whose rms is
+    exactly 1) or in the rows beside it."""
+    gen = np.random.default_rng(D)
+    x = gen.choice([-1.0, 1.0], (4, D))
+    x[:, ::D // 8] = 2.0                                           # 8 squares of 4 and 24 of nothing: rms 1
+    tiny = np.setdiff1d(np.arange(3, D, D // 32), np.arange(0, D, D // 8))[:24]
+    x[:, tiny] = 2.0 ** -126 * gen.choice([-1.0, 1.0], (4, len(tiny)))
+    x[:, tiny[0]] = -2.0 ** -126
+    tie = np.array([5, D // 2 + 6])
+    assert not set(tie) & (set(tiny) | set(range(0, D, D // 8)))
+    if not same_row:
+        x[[0, 2, 3]] *= 1.25                                       # a rms of 1.25 again gives ties: leave those rows none
+        x[np.ix_([0, 2, 3], tie)] = 0.75
+    w = np.full(D, 1.25)
+    w[tiny] = 2.0 ** gen.integers(-30, -20, len(tiny))             # y from 2^-156 to 2^-146
+    w[tiny[0]] = 2.0 ** -27                                        # -2^-153: nearer to zero than to fp32's smallest
+    w[tie] = 1.0625, 1.9375
+    xt = torch.tensor(x).to(DT[dtype])
+    assert np.array_equal(host(xt), x)
+    mx = torch.empty(4, D, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = torch.empty(4, D // 32, dtype=torch.uint8, device="cuda")
+    K.kda_rmsnorm(xt.cuda(), torch.tensor(w, dtype=torch.float32).cuda(), out_mx=mx, scales=sc, eps=0.0)
+    y = x / np.sqrt((x * x).sum(1, keepdims=True) / D) * w
+    m, e = np.frexp(np.abs(y).reshape(4, -1, 32).max(2))
+    e = e - 9 + (m > 0.875)
+    assert np.array_equal(sc.cpu().numpy(), e + 127)
+    v = y / np.repeat(2.0 ** e, 32, 1)
+    step = 2.0 ** (np.maximum(np.frexp(v)[1] - 1, -6) - 3)
+    assert np.array_equal(host(mx.float()), np.rint(v / step) * step)
