@@ -194,8 +194,9 @@ __device__ __forceinline__ float gate(float g)
     const float t = g * L2E;
     const float lo = __builtin_fmaf(g, L2E_LO, __builtin_fmaf(g, L2E, -t));
     const float e = __builtin_amdgcn_exp2f(t);
-    // (for an infinite g the parts are NaN, and e is right by itself)
-    return lo == lo ? __builtin_fmaf(e, lo * LN2, e) : e;
+    // (positive and finite: elsewhere e is right by itself, and the parts need not
+    // be numbers: t is infinite from g = -2.4e38 on, which a mask may hold)
+    return __builtin_amdgcn_classf(e, 0x180) ? __builtin_fmaf(e, lo * LN2, e) : e;
 }
 
 // A wave's rows: scalar addresses, and a lane's place in a row of its own.

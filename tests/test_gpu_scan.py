@@ -355,3 +355,30 @@ def test_rejects_mismatched_tensors():
         K.kda_scan_prefill(d["x"].half(), d["g"], d["init"], d["cu"], out, None)
     with pytest.raises(ValueError, match="tensor on"):
         K.kda_scan_decode_step(d["x"], d["g"], d["init"].cpu(), out)
+
+
+@pytest.mark.parametrize("lens,D", [([200, 150], 64), ([300, 33], 130), ([6000, 90], 2561)], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gates_of_the_lowest_values(lens, D, dtype):
+    # finite gates so low that g log2(e) is not: the decay is 0, as for -infinity
+    h, d = make(lens, D, dtype, seed=16)
+    T, g = sum(lens), d["g"].clone()
+    for i, v in enumerate((torch.finfo(torch.float32).min, -2.5e38, -2.3e38, -1e30, -151.0, -104.0)):
+        g[3 + 7 * i::50, i::4] = v
+    g[lens[0]:lens[0] + 9] = torch.finfo(torch.float32).min     # whole rows, a sequence's first among them
+    hg = host(g)
+    out, fin = torch.empty_like(d["x"]), torch.empty_like(d["init"])
+    K.kda_scan_prefill(d["x"], g, d["init"], d["cu"], out, fin)
+    b = R.scan_backward(h["x"], hg, h["init"], h["cu"], h["dout"], h["dfinal"])
+    R.close(host(out), b["fwd"]["h"], b["fwd"]["e_h"], dtype, "out")
+    R.close(host(fin), b["fwd"]["final"], b["fwd"]["e_final"], "fp32", "final")
+    grads = K.kda_scan_backward(d["x"], g, d["init"], d["cu"], d["dout"], d["dfinal"])
+    R.close(host(grads["dx"]), b["dx"], b["e_dx"], dtype, "dx")
+    R.close(host(grads["dg"]), b["dg"], b["e_dg"], "fp32", "dg")
+    R.close(host(grads["dinit"]), b["dinit"], b["e_dinit"], "fp32", "dinit")
+    n = min(T, 40)
+    state, o = torch.randn(n, D, device="cuda"), torch.empty_like(d["x"][:n])
+    f = R.scan(h["x"][:n], hg[:n], host(state), list(range(n + 1)))
+    K.kda_scan_decode_step(d["x"][:n], g[:n], state, o)
+    R.close(host(state), f["final"], f["e_final"], "fp32", "state")
+    R.close(host(o), f["h"], f["e_h"], dtype, "token")
