@@ -472,11 +472,18 @@ inline int32_t bwd_strip(int32_t T, int64_t D)
     return (int32_t)(len < 16 ? 16 : len);
 }
 inline int32_t bwd_parts(int32_t T, int64_t D) { return (int32_t)(T > 0 ? up(up(T, bwd_strip(T, D)), 4) : 1); }
+inline int32_t bwd_walks(int32_t N, int32_t T, int64_t D) { return N > 0 ? bwd_parts(T, D) : 0; }
 
 // Short strips: the waves that begin and end spread reads and writes evenly
 // (65,536 x 4,096, V = 4: 8 tokens 222 us, 12 199, 16 196, 24 203, 64 207;
 // 8,192 x 2,048: 14.4, 14.2, 13.0, 13.9).
 constexpr int32_t STRIP = 16;
+
+// workgroups of a prefill's walk, at V channels a lane
+inline int64_t conv_walks(int32_t T, int64_t D, int V)
+{
+    return up(up(T, STRIP), 4) * up(D, kda_column_width((int32_t)D, V));
+}
 
 template <typename T, int W, int V>
 hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, void *out, void *fin,
@@ -486,9 +493,8 @@ hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Se
     const int64_t cols = up(a.D, cw);
     const int32_t strip = STRIP;
     const int32_t nstrips = (int32_t)up(sq.T, strip);
-    const int64_t work = up(nstrips, 4) * cols, groups = work + empty_groups(sq.N, init, fin);
+    const int64_t work = conv_walks(sq.T, a.D, V), groups = work + empty_groups(sq.N, init, fin);
     if (groups == 0) return hipSuccess;
-    if (!kda_grid_ok(groups, 256)) return hipErrorInvalidConfiguration;
     if (a.silu)
         hipLaunchKernelGGL((kda_conv_kernel<T, W, V, true>), dim3((unsigned)groups), dim3(256), 0, s, (const T *)x,
                            (const T *)init, a, sq, strip, nstrips, (int32_t)cols, cw, (uint32_t)work, (T *)out,
@@ -500,15 +506,15 @@ hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Se
     return hipGetLastError();
 }
 
+// four sequences to a reading of the weights where there are many (512 x 4,096:
+// 8.6 us, 13.3 with one; 64 x 12,288: 5.9, 7.2; 8 x 12,288: 5.1, 4.1)
+inline bool step_many(int32_t N, int64_t cols) { return N * cols >= 384; }
+
 template <typename T, int W, int V>
 hipError_t run_conv_step(const void *x, const ConvArgs &a, void *state, int32_t N, void *out, hipStream_t s)
 {
     const int64_t cols = up(a.D, 256 * V);
-    // four sequences to a reading of the weights where there are many (512 x 4,096:
-    // 8.6 us, 13.3 with one; 64 x 12,288: 5.9, 7.2; 8 x 12,288: 5.1, 4.1)
-    const bool many = N * cols >= 384;
-    if (!kda_grid_ok(many ? cols * up(N, 4) : cols * N, 256)) return hipErrorInvalidConfiguration;
-    if (many)
+    if (step_many(N, cols))
         hipLaunchKernelGGL((kda_conv_step_kernel<T, W, V, 4>), dim3((unsigned)(cols * up(N, 4))), dim3(256), 0, s,
                            (const T *)x, (T *)state, a, N, (int32_t)cols, (T *)out);
     else
@@ -522,11 +528,9 @@ hipError_t run_conv_backward(const void *x, const ConvArgs &a, const void *init,
                              const void *dfin, void *dx, float *dw, float *dbias, void *dinit, void *ws,
                              hipStream_t s)
 {
-    const int32_t strip = bwd_strip(sq.T, a.D), parts = sq.N > 0 ? bwd_parts(sq.T, a.D) : 0;
+    const int32_t strip = bwd_strip(sq.T, a.D), parts = bwd_walks(sq.N, sq.T, a.D);
     const int64_t cols = bwd_cols(a.D), work = parts * cols, groups = work + empty_groups(sq.N, dfin, dinit);
     const int32_t nstrips = (int32_t)up(sq.T, strip);
-    if (!kda_grid_ok(groups, 256) || !kda_grid_ok(up((W + 1) * a.D, COLSUM_COLS), COLSUM_THREADS))
-        return hipErrorInvalidConfiguration;
     if (groups > 0 && a.silu)
         hipLaunchKernelGGL((kda_conv_bwd_kernel<T, W, V, true>), dim3((unsigned)groups), dim3(256), 0, s, (const T *)x,
                            (const T *)init, a, sq, strip, nstrips, (int32_t)cols, (uint32_t)work, (const T *)dout,
@@ -554,22 +558,30 @@ template <int V, typename F> hipError_t with_width(int32_t width, F f)
 // Channels a lane: four (65,536 x 4,096 in bf16: 196 us, 203 with two, 206 with
 // eight; 16,384 x 4,096: 44, 47, 54), or fewer where many lanes would be idle
 // (200,000 x 320: 51 us, 45 with two; 200,000 x 64: 26, 16 with one).
+inline int conv_lane(int64_t D)
+{
+    if (D <= 64) return 1;
+    const bool idle = D > 256 && 4 * D <= 3 * 256 * up(D, 256);
+    return D <= 128 || idle ? 2 : 4;
+}
+
 template <typename T>
 hipError_t conv(const void *x, const ConvArgs &a, const void *init, const Seqs &sq, int32_t width, void *out, void *fin,
                 hipStream_t s)
 {
     auto f = [&](auto w, auto v) { return run_conv<T, w(), v()>(x, a, init, sq, out, fin, s); };
-    if (a.D <= 64) return with_width<1>(width, f);
-    const bool idle = a.D > 256 && 4 * a.D <= 3 * 256 * up(a.D, 256);
-    return a.D <= 128 || idle ? with_width<2>(width, f) : with_width<4>(width, f);
+    const int lane = conv_lane(a.D);
+    return lane == 1 ? with_width<1>(width, f) : lane == 2 ? with_width<2>(width, f) : with_width<4>(width, f);
 }
+
+// Channels a thread of the token call: 16 bytes, where rows are made of them.
+template <typename T> constexpr int step_lane(int64_t D) { return D % (16 / sizeof(T)) == 0 ? 16 / sizeof(T) : 1; }
 
 template <typename T>
 hipError_t conv_step(const void *x, const ConvArgs &a, void *state, int32_t N, int32_t width, void *out, hipStream_t s)
 {
-    constexpr int V = 16 / sizeof(T);
     auto f = [&](auto w, auto v) { return run_conv_step<T, w(), v()>(x, a, state, N, out, s); };
-    return a.D % V == 0 ? with_width<V>(width, f) : with_width<1>(width, f);
+    return step_lane<T>(a.D) > 1 ? with_width<16 / sizeof(T)>(width, f) : with_width<1>(width, f);
 }
 
 template <typename T>
@@ -586,6 +598,23 @@ hipError_t conv_backward(const void *x, const ConvArgs &a, const void *init, con
 }  // namespace kda
 
 using namespace kda;
+
+bool kda_conv_fits(int32_t N, int32_t T, int32_t D, const void *init, const void *fin)
+{
+    return kda_grid_ok(conv_walks(T, D, conv_lane(D)) + empty_groups(N, init, fin), 256);
+}
+
+bool kda_conv_step_fits(bool bf16, int32_t N, int32_t D)
+{
+    const int64_t cols = up(D, 256 * (bf16 ? step_lane<bf16_t>(D) : step_lane<float>(D)));
+    return kda_grid_ok(step_many(N, cols) ? cols * up(N, 4) : cols * N, 256);
+}
+
+bool kda_conv_backward_fits(int32_t N, int32_t T, int32_t D, int32_t width, const void *dfinal, const void *dinit)
+{
+    return kda_grid_ok(bwd_walks(N, T, D) * bwd_cols(D) + empty_groups(N, dfinal, dinit), 256) &&
+           kda_grid_ok(up((width + 1) * (int64_t)D, COLSUM_COLS), COLSUM_THREADS);
+}
 
 hipError_t kda_launch_conv(bool bf16, const void *x, const float *w, const float *bias, const void *init,
                            const int32_t *cu, int32_t N, int32_t T, int32_t D, int32_t width, bool silu, void *out,

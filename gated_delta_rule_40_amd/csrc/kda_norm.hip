@@ -363,16 +363,26 @@ inline RowShape row_shape(int32_t pieces, int C, int lanes)
     return {tpr, tpr < 256 ? 256 : tpr};
 }
 
+// threads and workgroups of the norm at C pieces a thread
+template <typename T> RowShape norm_shape(int32_t D, int C)
+{
+    constexpr int VW = 16 / sizeof(T);
+    return row_shape((D + VW - 1) / VW, C, MXB / VW);
+}
+inline int64_t norm_groups(int32_t rows, const RowShape &sh)
+{
+    const int64_t per = sh.threads / sh.tpr;
+    return (rows + per - 1) / per;
+}
+
 template <typename T, int C, bool ONCE, bool TAIL, bool RES, bool MX>
 hipError_t run_rmsnorm(const void *x, const void *res, const float *w, int32_t rows, int32_t D, float eps, void *sum,
                        void *out, uint8_t *mx, uint8_t *scales, hipStream_t s)
 {
     constexpr int VW = 16 / sizeof(T);
-    const RowShape sh = row_shape((D + VW - 1) / VW, C, MXB / VW);
-    const int64_t per = sh.threads / sh.tpr, blocks = (rows + per - 1) / per;
-    if (!kda_grid_ok(blocks, sh.threads)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)blocks), dim3(sh.threads), 0,
-                       s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, 1.0 / D, eps, (T *)sum, (T *)out, mx,
+    const RowShape sh = norm_shape<T>(D, C);
+    hipLaunchKernelGGL((kda_rmsnorm_kernel<T, VW, C, ONCE, TAIL, RES, MX>), dim3((unsigned)norm_groups(rows, sh)),
+                       dim3(sh.threads), 0, s, (const T *)x, (const T *)res, w, rows, D, sh.tpr, 1.0 / D, eps, (T *)sum, (T *)out, mx,
                        scales);
     return hipGetLastError();
 }
@@ -393,7 +403,7 @@ hipError_t rmsnorm_as(const void *x, const void *res, const float *w, int32_t ro
 // one piece a thread, so that a row's latency is short (64 x 4,096: 3.3 us, 4.5
 // with four; 512 x 7,168: 7.1, 6.9); and for short rows, so that a row has
 // threads enough (200,000 x 128: 35 us, 56 with four; 100,000 x 512: 68, 71).
-template <typename T, int MOST, typename F> hipError_t with_shape(int32_t rows, int32_t D, F f)
+template <typename T, int MOST, typename F> auto with_shape(int32_t rows, int32_t D, F f)
 {
     constexpr int VW = 16 / sizeof(T);
     const int32_t pieces = (D + VW - 1) / VW;
@@ -404,6 +414,14 @@ template <typename T, int MOST, typename F> hipError_t with_shape(int32_t rows, 
     if (rows <= 512 && pieces <= 1024) return tail(one, std::false_type());
     if (pieces <= 64) return tail(one, std::true_type());
     return tail(std::integral_constant<int, MOST>(), std::true_type());
+}
+
+template <typename T> bool rmsnorm_fits(int32_t rows, int32_t D)
+{
+    return with_shape<T, 4>(rows, D, [&](auto c, auto, auto) {
+        const RowShape sh = norm_shape<T>(D, c());
+        return kda_grid_ok(norm_groups(rows, sh), sh.threads);
+    });
 }
 
 template <typename T>
@@ -455,6 +473,11 @@ hipError_t rmsnorm_backward(const void *x, const float *w, const void *dout, con
 }  // namespace kda
 
 using namespace kda;
+
+bool kda_rmsnorm_fits(bool bf16, int32_t rows, int32_t D)
+{
+    return bf16 ? rmsnorm_fits<bf16_t>(rows, D) : rmsnorm_fits<float>(rows, D);
+}
 
 hipError_t kda_launch_rmsnorm(bool bf16, const void *x, const void *residual, const float *w, int32_t rows, int32_t D,
                               float eps, void *sum, void *out, uint8_t *mx, uint8_t *scales, hipStream_t s)

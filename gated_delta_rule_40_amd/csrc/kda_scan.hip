@@ -585,12 +585,6 @@ inline Chain chain_at(uint64_t *p, int32_t T, int32_t D)
     return {reinterpret_cast<uint32_t *>(p), p + l.tile, p + l.block, tiles_of(T), (int64_t)D, 0};
 }
 
-// whether the widest grid there can be for these sizes (of columns of 64) is one
-inline bool grid_ok(const Seqs &sq, int32_t D)
-{
-    return kda_grid_ok((int64_t)tiles_of(sq.T) * (((int64_t)D + 63) / 64) + sq.N / EMPTY_SEQS + 1, NTH);
-}
-
 inline hipError_t fill_chain(uint64_t *p, size_t words, hipStream_t s)
 {
     if (words == 0) return hipSuccess;
@@ -665,6 +659,12 @@ hipError_t scan_backward(const void *x, const float *g, const float *init, const
 
 using namespace kda;
 
+// (by the widest grid there can be for these sizes, of columns of 64)
+bool kda_scan_fits(int32_t N, int32_t T, int32_t D)
+{
+    return kda_grid_ok((int64_t)tiles_of(T) * (((int64_t)D + 63) / 64) + N / EMPTY_SEQS + 1, NTH);
+}
+
 size_t kda_scan_ws_bytes(int32_t T, int32_t D) { return chain_layout(T, D).words * sizeof(uint64_t); }
 
 hipError_t kda_launch_scan(bool bf16, const void *x, const float *g, const float *init, const int32_t *cu, int32_t N,
@@ -672,7 +672,6 @@ hipError_t kda_launch_scan(bool bf16, const void *x, const float *g, const float
 {
     const Seqs sq{cu, N, T};
     const Chain ch = chain_at((uint64_t *)ws, T, D);
-    if (!grid_ok(sq, D)) return hipErrorInvalidConfiguration;
     if (hipError_t e = fill_chain((uint64_t *)ws, chain_layout(T, D).words, s)) return e;
     return bf16 ? scan<bf16_t>(x, g, init, sq, D, out, fin, chk, ch, s)
                 : scan<float>(x, g, init, sq, D, out, fin, chk, ch, s);
@@ -709,7 +708,6 @@ hipError_t kda_launch_scan_backward(bool bf16, const void *x, const float *g, co
     const size_t words = chain_layout(T, D).words;
     uint64_t *w = (uint64_t *)ws;
     const bool states = words > 0 && !checkpoints;
-    if (!grid_ok(sq, D)) return hipErrorInvalidConfiguration;
     if (hipError_t e = fill_chain(w, states ? 2 * words : words, s)) return e;
     if (states) {
         float *chk = reinterpret_cast<float *>(w + 2 * words);

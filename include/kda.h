@@ -370,9 +370,9 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  *     of gates, weights, biases and fp32 states in fp32.
  *   - No result depends on the order in which workgroups run: every sum has a
  *     fixed order, so calls on the same inputs give the same bits.
- *   - An output shares no memory with another argument unless that is said
- *     here; token arrays and states that overlap otherwise are refused
- *     (KDA_ERR_INVALID_ARG).
+ *   - An output shares no memory with another argument (the workspace among
+ *     them, as far as it is needed) unless it is said here that it may equal
+ *     one; other overlaps are refused (KDA_ERR_INVALID_ARG).
  *   - Sizes whose launch would have 2^32 threads or more are
  *     KDA_ERR_UNSUPPORTED.  Only arrays of hundreds of GB, or of hundreds of
  *     millions of rows of few channels, have them.

@@ -225,3 +225,77 @@ def test_offsets_beyond_32_bits():
     K.kda_rmsnorm_backward(x, b, x, grads=dict(dx=out, dweight=torch.empty(D, device="cuda")))
     K.kda_rmsnorm_backward(small, b, small, grads=dict(dx=ref, dweight=torch.empty(D, device="cuda")))
     assert near(out[-L:], ref, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("D", [40, 257])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)
+def test_arrays_side_by_side(D, dt):
+    # all arrays of a call cut from one buffer without gaps: taken, and the same bits as from arrays of their own
+    T, N, W, f32 = 300, 3, 4, torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    pool, at = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda"), [0]
+    cu = torch.tensor([0, 100, 130, T], dtype=torch.int32, device="cuda")
+
+    def cut(shape, dtype, like=None):
+        e = torch.empty(0, dtype=dtype).element_size()
+        start = (at[0] + e - 1) // e * e
+        n = int(np.prod(shape))
+        at[0] = start + n * e
+        t = pool[start:at[0]].view(dtype).view(shape)
+        if like is not None:
+            t.copy_(like)
+        return t
+
+    r = lambda *s, dtype=f32: torch.randn(*s, device="cuda", generator=gen).to(dtype)   # noqa: E731
+    x, dout, res, dres = (r(T, D, dtype=dt) for _ in range(4))
+    g, st, w, b, nw = -r(T, D).abs(), r(N, D), r(D, W), r(D), r(D)
+    cst = r(N, W - 1, D, dtype=dt)
+
+    def ws(size):   # (the scan's are 8-byte aligned)
+        return (-(-size // 8),), torch.int64
+
+    calls = [   # call(inputs, outputs), inputs, the outputs' shapes and types
+        (lambda i, o: K.kda_scan_prefill(i[0], i[1], i[2], i[3], o[0], o[1], checkpoints=o[2], workspace=o[3]),
+         [x, g, st, cu], [((T, D), dt), ((N, D), f32), ((3, D), f32), ws(K.kda_scan_workspace_size(N, T, D, dt))]),
+        (lambda i, o: K.kda_scan_backward(i[0], i[1], i[2], i[3], i[4], i[5], workspace=o[3],
+                                          grads=dict(dx=o[0], dg=o[1], dinit=o[2])),
+         [x, g, st, cu, dout, st], [((T, D), dt), ((T, D), f32), ((N, D), f32),
+                                    ws(K.kda_scan_backward_workspace_size(N, T, D, dt))]),
+        (lambda i, o: K.kda_conv_prefill(i[0], i[1], i[2], i[3], i[4], o[0], o[1]),
+         [x, w, b, cst, cu], [((T, D), dt), ((N, W - 1, D), dt)]),
+        (lambda i, o: K.kda_conv_backward(i[0], i[1], i[2], i[3], i[4], i[5], i[6], workspace=o[4],
+                                          grads=dict(dx=o[0], dweight=o[1], dbias=o[2], dinit=o[3])),
+         [x, w, b, cst, cu, dout, cst], [((T, D), dt), ((D, W), f32), ((D,), f32), ((N, W - 1, D), dt),
+                                         ws(K.kda_conv_backward_workspace_size(N, T, D, W, dt))]),
+        (lambda i, o: K.kda_rmsnorm(i[0], i[1], o[0], residual=i[2], residual_out=o[1], out_mx=o[2], scales=o[3]),
+         [x, nw, res], [((T, D), dt), ((T, D), dt), ((T, D), torch.uint8), ((T, -(-D // 32)), torch.uint8)]),
+        (lambda i, o: K.kda_rmsnorm_backward(i[0], i[1], i[2], i[3], workspace=o[2], grads=dict(dx=o[0], dweight=o[1])),
+         [x, nw, dout, dres], [((T, D), dt), ((D,), f32), ws(K.kda_rmsnorm_backward_workspace_size(T, D, dt))]),
+    ]
+    for fn, ins, outs in calls:
+        own = [torch.zeros(s, dtype=t, device="cuda") for s, t in outs]
+        fn(ins, own)
+        at[0] = 0
+        side_in = [cut(t.shape, t.dtype, t) for t in ins]
+        side = [cut(s, t) for s, t in outs]
+        fn(side_in, side)
+        assert all(torch.equal(a, c) for a, c in zip(own, side) if a.dtype is not torch.int64)
+        assert all(torch.equal(a, c) for a, c in zip(ins, side_in))
+
+
+def test_overlaps_raise():
+    x, g = torch.randn(64, 64, device="cuda"), -torch.rand(64, 64, device="cuda")
+    cu, before = torch.tensor([0, 64], dtype=torch.int32, device="cuda"), x.clone()
+    x3, g3, o3 = torch.cat((x, x, x)), torch.cat((g, g, g)), torch.empty(192, 64, device="cuda")
+    bad = [lambda: K.kda_rmsnorm(x, None, out_mx=x.view(torch.uint8)[:16].view(64, 64),
+                                 scales=torch.empty(64, 2, dtype=torch.uint8, device="cuda")),
+           lambda: K.kda_scan_prefill(x, g, None, cu, g, None),
+           lambda: K.kda_scan_prefill(x, g, None, cu, torch.empty_like(x), x[:1]),
+           lambda: K.kda_scan_decode_step(x, g, x, torch.empty_like(x)),
+           lambda: K.kda_scan_backward(x, g, None, cu, x, grads=dict(dx=torch.empty_like(x), dg=x)),
+           lambda: K.kda_scan_prefill(x3, g3, None, cu, o3, None, workspace=o3)]
+    for fn in bad:
+        with pytest.raises(K.KdaError) as e:
+            fn()
+        assert e.value.status == K.KDA_ERR_INVALID_ARG
+    assert torch.equal(x, before)

@@ -158,3 +158,59 @@ def test_binding_workspace_sizes_reject_unknown_types():
                      (K.kda_conv_backward_workspace_size, (1, 16, 8, 4)), (K.kda_rmsnorm_backward_workspace_size, (4, 8))):
         with pytest.raises(TypeError):
             fn(*args, torch.float16)
+
+
+# ------------------------------------------------------------------ overlaps, every output against every other argument
+# Sizes in bytes for 300 tokens of 40 channels in 3 sequences (decode: 3 tokens), bf16, width 4; norm: 300 rows of 40.
+def _arrays(lib):
+    tok, f32, st, row, cu = 300 * 40 * 2, 300 * 40 * 4, 3 * 40 * 4, 40 * 4, 4 * 4
+    conv, chk, w = 3 * 3 * 40 * 2, 3 * 40 * 4, 40 * 4 * 4
+    return {   # name: (arguments as in CALLS, their sizes, outputs: inputs each may equal)
+        "kda_scan_prefill": (dict(N=3, D=40), dict(x=tok, g=f32, init=st, cu=cu, out=tok, fin=st, chk=chk,
+                                                   ws=lib.kda_scan_workspace_size(3, 300, 40, B)),
+                             dict(out="x", fin="init", chk="", ws="")),
+        "kda_scan_decode_step": (dict(N=3, D=40), dict(x=240, g=480, state=480, out=240), dict(out="x", state="")),
+        "kda_scan_backward": (dict(N=3, D=40), dict(x=tok, g=f32, init=st, cu=cu, dout=tok, dfin=st, chk=chk, dx=tok,
+                                                    dg=f32, dinit=st,
+                                                    ws=lib.kda_scan_backward_workspace_size(3, 300, 40, B, 1)),
+                              dict(dx="x dout", dg="g", dinit="", ws="")),
+        "kda_conv_prefill": (dict(N=3, D=40), dict(x=tok, w=w, b=row, init=conv, cu=cu, out=tok, fin=conv),
+                             dict(out="", fin="init")),
+        "kda_conv_decode_step": (dict(N=3, D=40), dict(x=240, w=w, b=row, state=conv, out=240), dict(out="x", state="")),
+        "kda_conv_backward": (dict(N=3, D=40), dict(x=tok, w=w, b=row, init=conv, cu=cu, dout=tok, dfin=conv, dx=tok, dw=w,
+                                                    db=row, dinit=conv,
+                                                    ws=lib.kda_conv_backward_workspace_size(3, 300, 40, 4, B)),
+                              dict(dx="", dw="", db="", dinit="", ws="")),
+        "kda_rmsnorm": (dict(rows=300, D=40), dict(x=tok, res=tok, w=row, sum=tok, out=tok, mx=300 * 40, sc=300 * 2),
+                        dict(sum="x res", out="x res", mx="", sc="")),
+        "kda_rmsnorm_backward": (dict(rows=300, D=40), dict(x=tok, w=row, dout=tok, dres=tok, dx=tok, dw=row,
+                                                            ws=lib.kda_rmsnorm_backward_workspace_size(300, 40, B)),
+                                 dict(dx="x dout dres", dw="", ws="")),
+    }
+
+
+def _places(lib):
+    """Every output moved onto every other argument: (call, its arguments, whether the output may lie there)."""
+    for name, (sizes, arrays, outs) in _arrays(lib).items():
+        at = {a: (i + 1) << 24 for i, a in enumerate(arrays)}
+        assert all(0 < n < 1 << 24 for n in arrays.values())
+        for o, may in outs.items():
+            for a in set(arrays) - {o}:
+                # on its first byte, on its last bytes, and so that it ends on its first (offsets of 8 bytes)
+                for p in {at[a], at[a] + (arrays[a] - 1) // 8 * 8, at[a] - (arrays[o] - 1) // 8 * 8}:
+                    kw = {k: ctypes.c_void_p(v) for k, v in {**at, o: p}.items()}
+                    yield name, {**sizes, **kw}, p == at[a] and a in may.split()
+                for p in (at[a] + (arrays[a] + 7) // 8 * 8, at[a] - (arrays[o] + 7) // 8 * 8):     # beside it
+                    yield name, {**sizes, **{k: ctypes.c_void_p(v) for k, v in {**at, o: p}.items()}}, True
+
+
+def test_overlaps_are_refused(lib):
+    refused = taken = 0
+    for name, kw, may in _places(lib):
+        if not may:
+            assert call(lib, name, **kw) == INVALID, (name, kw)
+            refused += 1
+        elif not torch.cuda.is_available():   # these addresses would reach a kernel: only where there is none
+            assert call(lib, name, **kw) == K.KDA_ERR_LAUNCH, (name, kw)
+            taken += 1
+    assert refused > 500 and (taken > 300 or torch.cuda.is_available())
