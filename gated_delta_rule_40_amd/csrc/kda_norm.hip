@@ -233,9 +233,11 @@ __global__ void kda_rmsnorm_kernel(const T *x, const T *res, const float *w, int
             uint32_t near = (top & 0x7fffffu) - (0x600000u - 4);
 #pragma unroll
             for (int j = 0; j < VW; ++j) near = min(near, (__float_as_uint(y[j]) & 0xfffffu) - (0x80000u - 4));
+            // (the pieces in doubt alone: a row's bytes do not go by the rows beside it)
             if (__any(near <= 8)) {
+                if (near <= 8)
 #pragma unroll
-                for (int j = 0; j < VW; ++j) y[j] = rstd.odd(r[k][j], w ? g[j] : 1.f);
+                    for (int j = 0; j < VW; ++j) y[j] = rstd.odd(r[k][j], w ? g[j] : 1.f);
                 top = block_top();
             }
             const int sc = mx_scale(top);

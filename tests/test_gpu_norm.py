@@ -356,3 +356,34 @@ def test_mx_of_values_below_fp32_beside_ties(D, dtype, same_row):
     v = y / np.repeat(2.0 ** e, 32, 1)
     step = 2.0 ** (np.maximum(np.frexp(v)[1] - 1, -6) - 3)
     assert np.array_equal(host(mx.float()), np.rint(v / step) * step)
+
+
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_mx_of_a_row_alone_and_among_others(D, dtype):
+    """Values below 2^-6 of their scale, beside the ties that e4m3 has there: they may be rounded from fp32's y, and a
+    row gets the same bytes whatever lies beside it, with ties of its own or without."""
+    gen = np.random.default_rng(D)
+    rows, x = [], torch.tensor(gen.standard_normal((6, D))).to(DT[dtype])
+    x[x == 0] = 1.0
+    x[1, D // 2:] = x[0, D // 2:]
+    wide = np.abs(host(x))
+    rms = np.sqrt((wide * wide).sum(1) / D + np.float64(np.float32(EPS)))
+    goal = (2 * gen.integers(0, 8, D) + 1) * 2.0 ** -10              # ties below 2^-6
+    goal[::32] = 300.0                                               # the largest of a block: scale 1
+    w = (goal * rms[0] / wide[0]).astype(np.float32)
+    w[1] = 1.0625 * 8 * rms[1] / wide[1, 1]                          # a tie for row 1, and one for row 5
+    w[3] = 1.0625 * 4 * rms[5] / wide[5, 3]
+    wd = torch.tensor(w).cuda()
+
+    def call(t):
+        mx = torch.empty(len(t), D, dtype=torch.uint8, device="cuda")
+        sc = torch.empty(len(t), D // 32, dtype=torch.uint8, device="cuda")
+        K.kda_rmsnorm(t.cuda().contiguous(), wd, out_mx=mx, scales=sc, eps=EPS)
+        return mx, sc
+
+    rows = [call(x[i:i + 1]) for i in range(6)]
+    for order in ([0, 1, 2, 3, 4, 5], [5, 0, 4, 0, 0, 3], [2, 0, 3], [0, 1], [1, 0], [4, 5, 0, 0]):
+        mx, sc = call(x[order])
+        for i, n in enumerate(order):
+            assert torch.equal(mx[i:i + 1], rows[n][0]) and torch.equal(sc[i:i + 1], rows[n][1]), (order, i)
