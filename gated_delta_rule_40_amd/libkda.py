@@ -439,8 +439,9 @@ def _empty(shape, dtype, dev, stream) -> torch.Tensor:
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
-                                           device=dev)
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        # (ExternalStream(0) would be a new stream, not the null stream)
+        stream = torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 

@@ -299,3 +299,32 @@ def test_overlaps_raise():
             fn()
         assert e.value.status == K.KDA_ERR_INVALID_ARG
     assert torch.equal(x, before)
+
+
+def test_new_tensors_belong_to_the_call_s_stream():
+    """Gradients that a call allocates lie in the memory of the stream it runs on, however that is given: as a stream,
+    as its number (0: the null stream), or not at all."""
+    x, g = torch.randn(600, 512, device="cuda"), -torch.rand(600, 512, device="cuda")
+    w, cu = torch.randn(512, 4, device="cuda"), torch.tensor([0, 600], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def owner(t):
+        p = t.data_ptr()
+        return [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= p < s["address"] + s["total_size"]][0]
+
+    class Other:   # another library's stream object
+        cuda_stream = side.cuda_stream
+
+    want = K.kda_scan_backward(x, g, None, cu, x)
+    for stream, raw in ((None, 0), (0, 0), (torch.cuda.default_stream(), 0), (side, side.cuda_stream),
+                        (side.cuda_stream, side.cuda_stream), (Other(), side.cuda_stream)):
+        for call in (lambda: K.kda_scan_backward(x, g, None, cu, x, stream=stream),
+                     lambda: K.kda_conv_backward(x, w, None, None, cu, x, stream=stream),
+                     lambda: K.kda_rmsnorm_backward(x, w[:, 0].contiguous(), x, stream=stream)):
+            torch.cuda.synchronize()
+            got = call()
+            torch.cuda.synchronize()
+            assert all(owner(t) == raw for t in got.values() if t is not None), stream
+            if "dg" in got:
+                assert all(torch.equal(got[k], want[k]) for k in want)
