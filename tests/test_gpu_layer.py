@@ -328,3 +328,43 @@ def test_new_tensors_belong_to_the_call_s_stream():
             assert all(owner(t) == raw for t in got.values() if t is not None), stream
             if "dg" in got:
                 assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("D", [64, 130])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)
+def test_any_alignment_gives_the_same_bits(D, dt):
+    # every token array and state one element off a 16-byte boundary, against the same values on one
+    T, N, W = 190, 2, 4
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    r = lambda *s, dtype=torch.float32: torch.randn(*s, device="cuda", generator=gen).to(dtype)   # noqa: E731
+
+    def off(t):
+        base = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        v = base[1:].view(t.shape)
+        assert v.data_ptr() % 16
+        return v.copy_(t)
+
+    cu = torch.tensor([0, 150, T], dtype=torch.int32, device="cuda")
+    x, dout, res, g = r(T, D, dtype=dt), r(T, D, dtype=dt), r(T, D, dtype=dt), -r(T, D).abs()
+    st, cst, w, b = r(N, D), r(N, W - 1, D, dtype=dt), r(D, W), r(D)
+    e = torch.zeros_like
+    u8 = torch.zeros(T, D, dtype=torch.uint8, device="cuda")
+
+    def all_calls(v):   # v: how a tensor is laid out
+        out, fin, o2, cf, o3, total, m8 = v(e(x)), v(e(st)), v(e(x)), v(e(cst)), v(e(x)), v(e(x)), v(u8)
+        sc = torch.zeros(T, -(-D // 32), dtype=torch.uint8, device="cuda")
+        K.kda_scan_prefill(v(x), v(g), v(st), cu, out, fin)
+        gs = K.kda_scan_backward(v(x), v(g), v(st), cu, v(dout), v(st),
+                                 grads=dict(dx=v(e(x)), dg=v(e(g)), dinit=v(e(st))))
+        K.kda_conv_prefill(v(x), v(w), v(b), v(cst), cu, o2, cf)
+        gc = K.kda_conv_backward(v(x), v(w), v(b), v(cst), cu, v(dout), v(cst),
+                                 grads=dict(dx=v(e(x)), dweight=v(e(w)), dbias=v(e(b)), dinit=v(e(cst))))
+        K.kda_rmsnorm(v(x), v(b), o3, residual=v(res), residual_out=total, out_mx=m8, scales=sc)
+        gn = K.kda_rmsnorm_backward(v(x), v(b), v(dout), v(res), grads=dict(dx=v(e(x)), dweight=v(e(b))))
+        s1, s2, d1, d2 = v(st), v(cst), v(x[:N].clone()), v(x[:N].clone())
+        K.kda_scan_decode_step(d1, v(g[:N]), s1, d1)
+        K.kda_conv_decode_step(d2, v(w), v(b), s2, d2)
+        return [out, fin, *gs.values(), o2, cf, *gc.values(), o3, total, m8, sc, *gn.values(), s1, s2, d1, d2]
+
+    for a, c in zip(all_calls(lambda t: t.clone()), all_calls(off)):
+        assert torch.equal(a, c)
