@@ -506,8 +506,10 @@ hipError_t run_conv(const void *x, const ConvArgs &a, const void *init, const Se
     return hipGetLastError();
 }
 
-// four sequences to a reading of the weights where there are many (512 x 4,096:
-// 8.6 us, 13.3 with one; 64 x 12,288: 5.9, 7.2; 8 x 12,288: 5.1, 4.1)
+// Four sequences to a reading of the weights where there are many, by the
+// workgroups of one each (replays, bf16; 1,024: 512 x 4,096 10.7 us, 15.0 with one
+// sequence; 384: 192 x 4,096 6.9, 8.2 and 64 x 12,288 7.1, 8.3; 288: 48 x 12,288
+// 6.8, 8.0; 256: 128 x 4,096 6.7, 6.3; 48: 8 x 12,288 6.3, 5.5).
 inline bool step_many(int32_t N, int64_t cols) { return N * cols >= 384; }
 
 template <typename T, int W, int V>
@@ -557,7 +559,8 @@ template <int V, typename F> hipError_t with_width(int32_t width, F f)
 
 // Channels a lane: four (65,536 x 4,096 in bf16: 196 us, 203 with two, 206 with
 // eight; 16,384 x 4,096: 44, 47, 54), or fewer where many lanes would be idle
-// (200,000 x 320: 51 us, 45 with two; 200,000 x 64: 26, 16 with one).
+// (200,000 x 320: 51 us, 45 with two; x 300: bf16 55, 59, fp32 134, 119; 200,000 x
+// 64: 26, 16 with one).
 inline int conv_lane(int64_t D)
 {
     if (D <= 64) return 1;

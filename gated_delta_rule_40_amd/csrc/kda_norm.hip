@@ -12,9 +12,9 @@
 // only; the last one of a row may be a part of one (TAIL).
 //
 // Measured on one MI355X (a large copy reaches 4.9-5.4 TB/s there), bf16:
-// 16,384 x 7,168 with the residual and the 8-bit output 141-144 us (5.7-5.8 TB/s
+// 16,384 x 7,168 with the residual and the 8-bit output 144-147 us (5.6-5.7 TB/s
 // of 7.03 bytes an element), 65,536 x 2,048 with the residual 176-179 us (6.0
-// TB/s of 8 bytes), its gradients 196 us (5.5 TB/s of 8 bytes), 64 x 4,096 3.6 us.
+// TB/s of 8 bytes), its gradients 190 us (5.7 TB/s of 8 bytes), 64 x 4,096 3.8 us.
 #include "kda_colsum.hpp"
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
@@ -28,8 +28,9 @@ constexpr int MAX_PARTIALS = 1024;   // partial sums of a weight's gradient
 
 // ---------------------------------------------------------------- pieces
 // VW consecutive elements, moved as one access: as read, and as fp32.  ONCE:
-// past the caches, for rows too many to be found there again (16,384 x 7,168
-// with the 8-bit output 152 -> 135 us); a few rows stay in them for the reader.
+// past the caches, for rows too many to be found there again (65,536 x 2,048:
+// 179 us, 189 through them; 16,384 x 7,168 with the 8-bit output: 147, 152); a
+// few rows stay in them for the reader.
 template <typename T, int VW, bool ONCE> struct Piece {
     typedef T raw __attribute__((ext_vector_type(VW)));
     typedef raw mem __attribute__((aligned(sizeof(T))));
@@ -98,8 +99,9 @@ template <int VW, bool TAIL> struct Pieces {
     }
 };
 
-// 4 or 8 bytes at any alignment (through the caches, which make whole lines of
-// them: past them 16,384 x 7,168 takes 141 us instead of 134)
+// 4 or 8 bytes at any alignment, through the caches: the product that follows
+// reads them (past them 16,384 x 7,168 takes 144 us instead of 147, 100,000 x 512
+// 64 instead of 63)
 __device__ __forceinline__ void store_words(uint8_t *p, const uint32_t (&q)[1])
 {
     typedef uint32_t mem __attribute__((aligned(1)));

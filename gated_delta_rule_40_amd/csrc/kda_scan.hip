@@ -12,13 +12,14 @@
 // is read once and every output written once, which is all the traffic there
 // has to be (8 bytes an element with bf16 x), and HBM's rate is the bound.
 //
-// The state that enters a tile is joined from the runs of the tiles before it
-// in its block of 16, 32 or 64 tiles (for V = 4, 2, 1), all read side by side,
-// and the state that enters the block, which is passed from block to block.
-// Which runs are joined, and in which order, depends on the tile alone, not on
-// what is ready first, so that results are the same bits on every call.  A published run is
-// one 64-bit word a channel, written and polled with relaxed device-scope
-// atomics: the word is its own flag (all ones: not there yet), so no fence is
+// The state that enters a tile is found in one pass by looking back (the method
+// of D. Merrill and M. Garland, 2016, in another form): it is joined from the runs
+// of the tiles before it in its block of 16, 32 or 64 tiles (for V = 4, 2, 1), all
+// read side by side, and the state that enters the block, which is passed from
+// block to block.  Which runs are joined, and in which order, depends on the tile
+// alone, not on what is ready first, so that results are the same bits on every
+// call.  A published run is one 64-bit word a channel, written and polled with
+// relaxed device-scope atomics: the word is its own flag (all ones: not there yet), so no fence is
 // needed between data and flag.  Tiles of a channel block are handed out in
 // order by a counter, so a tile waits only for workgroups that are already
 // running, and these wait for earlier ones in turn: every wait ends.
@@ -28,9 +29,11 @@
 // with the state entering each tile taken from the forward pass's checkpoints.
 //
 // Measured on one MI355X (a large copy reaches 4.9-5.4 TB/s there): 2^20 tokens
-// x 1,024 channels in bf16 1.57 ms (5.5 TB/s of the 8 bytes an element, counters
-// show 3 % more read and 10 % more written, the published words), forward and
-// backward of 65,536 x 4,096 1.07 ms (5.5 TB/s of 22 bytes an element).  Short
+// x 1,024 channels in bf16 1.57 ms (5.5 TB/s of the 8 bytes an element; counters
+// show 3 % more read and 10 % more written: 71 MB of published words, and 138 MB
+// that are most likely the 6 registers a lane which V = 4 keeps in scratch, as
+// the gradients at V = 2 do with 7 or 8), forward and backward of 65,536 x 4,096
+// 1.07 ms (5.5 TB/s of 22 bytes an element).  Short
 // batches are bound by the chain of waits: 4,096 x 1,024 takes 13 us in the
 // kernel, of which the counter's answer is 2, the reads 2, the gates and runs 2,
 // passing the state on 3 and the writes 2.
@@ -622,9 +625,10 @@ hipError_t scan(const void *x, const float *g, const float *init, const Seqs &sq
                 float *chk, const Chain &ch, hipStream_t s)
 {
     // Four channels a lane for bf16 where that leaves two workgroups for every
-    // CU and few lanes idle (2^20 x 1,024: 1.70 ms, 1.94 with two; 4,096 x 1,024
-    // with its 128 workgroups: 23.7 us, 19.4 with two; fp32 tokens of four would
-    // not fit the registers).
+    // CU and few lanes idle (2^20 x 1,024: 1.57 ms, 1.68 with two; 65,536 x 4,096:
+    // 389 us both; 4,096 x 1,024 with its 128 workgroups: 22 us, 16 with two).  In
+    // between, two can be better: 32,768 x 1,024 takes 77 us, 66 with two.  fp32
+    // tokens of four would not fit the registers.
     const int64_t wide = ((int64_t)D + 255) / 256;
     if (sizeof(T) == 2 && ch.ntiles * wide >= 512 && 4 * (int64_t)D >= 3 * 256 * wide)
         return run_scan<T, sizeof(T) == 2 ? 4 : 2>(x, g, init, sq, D, out, fin, chk, ch, s);

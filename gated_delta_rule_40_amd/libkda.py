@@ -377,6 +377,11 @@ def kda_backward(q, k, v, g, beta, initial_state, cu_seqlens, dout, dfinal=None,
 # checks of a tensor are one expression each (a host tensor's device number is
 # -1), the reasons are worked out only when it fails, and pointers and the
 # stream go to the library as plain ints.
+#
+# A call given a `stream` runs there, and tensors that it makes (gradients,
+# a workspace) come from that stream's memory: who uses them on another stream
+# waits for this one and records the use (Tensor.record_stream), or supplies
+# tensors of their own.
 _MOST = 2 ** 31 - 1                                # int32 sizes in the C ABI
 _DTYPE_CODE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 _F32 = torch.float32
@@ -538,7 +543,8 @@ def kda_scan_backward(x, g, initial_state, cu_seqlens, dout, dfinal=None, checkp
     dfinal [N, ...channels] fp32 or None.  ``checkpoints`` are those
     kda_scan_prefill wrote for the same inputs; without them the states are
     computed again.  Returns a dict of dx (x's type), dg (fp32) and dinit (fp32;
-    None unless want_dinit); ``grads`` may supply the tensors."""
+    None unless want_dinit); ``grads`` may supply the tensors, which otherwise
+    belong to ``stream`` (record_stream them for use on another)."""
     px, dev, code, shape, T, D = _rows("x", x)
     pcu, N = _cu(cu_seqlens, dev)
     dt, state = x.dtype, (N, *shape[1:])
@@ -599,7 +605,8 @@ def kda_conv_backward(x, weight, bias, initial_state, cu_seqlens, dout, dfinal=N
     """Gradients of kda_conv_prefill given dout [T, ...channels] and dfinal
     [N, width - 1, ...channels] (x's type) or None.  Returns a dict of dx and
     dinit (x's type; dinit None unless want_dinit), dweight and dbias (fp32;
-    dbias None without a bias); ``grads`` may supply the tensors."""
+    dbias None without a bias); ``grads`` may supply the tensors, which otherwise
+    belong to ``stream`` (record_stream them for use on another)."""
     px, dev, code, shape, T, D = _rows("x", x)
     pcu, N = _cu(cu_seqlens, dev)
     pw, W = _conv_weight(weight, dev, shape)
@@ -665,7 +672,8 @@ def kda_rmsnorm_backward(x, weight, dout, dresidual=None, eps: float = 1e-6, gra
     """Gradients of kda_rmsnorm's y given the normed rows x (its residual_out,
     where it added one) and dout; dresidual, a gradient of x from elsewhere, is
     added.  Returns a dict of dx (x's type) and dweight (fp32; None without a
-    weight); ``grads`` may supply the tensors."""
+    weight); ``grads`` may supply the tensors, which otherwise belong to
+    ``stream`` (record_stream them for use on another)."""
     px, dev, code, shape, rows, D = _norm_rows("x", x)
     dt = x.dtype
     lib = _lib or load()

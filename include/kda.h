@@ -363,8 +363,7 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  * allocation, asynchronous on `stream`), with these differences:
  *   - `channels` is any positive count (a [T, H, d] tensor is [T, channels]
  *     with channels = H * d).  Pointers need the alignment of their element
- *     type only; rows of 16-byte multiples at 16-byte aligned pointers are
- *     read and written in wider pieces.
+ *     type only, and results do not go by it.
  *   - Token arrays may be NULL when there are no tokens (total_tokens = 0).
  *   - Gradients of activations and of convolution states are in `dtype`, those
  *     of gates, weights, biases and fp32 states in fp32.
@@ -389,9 +388,11 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  *
  *   x             [total_tokens, channels]        dtype
  *   g             [total_tokens, channels]        fp32, log-decay; -infinity
- *                 drops the state.  Growth (g > 0) is taken as long as g sums
- *                 to less than 88 over any 1,024 tokens of a channel: products
- *                 of exp(g) over so many are formed.
+ *                 drops the state.  Products of exp(g) over up to 1,024 tokens
+ *                 of a channel are formed in fp32: what decays to less than
+ *                 10^-38 of itself over so many counts as gone (also where
+ *                 growth follows), and growth (g > 0) is taken as long as g
+ *                 sums to less than 88 over them.
  *   initial_state [num_seqs, channels]            fp32, or NULL for zeros
  *   cu_seqlens    [num_seqs + 1]                  int32, DEVICE (as kda_prefill)
  *   out           [total_tokens, channels]        dtype; rows owned by a
@@ -563,6 +564,7 @@ kda_status kda_rmsnorm(const void *x, const void *residual, const float *weight,
  *   dweight       [channels]                      fp32, or NULL (not written)
  *   workspace     at least kda_rmsnorm_backward_workspace_size(...) bytes,
  *                 4-byte aligned; NULL allowed when dweight is NULL
+ * The sums of a row are formed in fp32, those of its squares too: |x| up to 10^17.
  */
 size_t kda_rmsnorm_backward_workspace_size(int32_t rows, int32_t channels, kda_dtype dtype);
 
