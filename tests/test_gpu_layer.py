@@ -368,3 +368,47 @@ def test_any_alignment_gives_the_same_bits(D, dt):
 
     for a, c in zip(all_calls(lambda t: t.clone()), all_calls(off)):
         assert torch.equal(a, c)
+
+
+def test_token_calls_and_new_tensors_in_a_graph():
+    # a decoding step captured (states move with every replay), and training calls that make their own tensors there
+    N, D, W = 5, 200, 4
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=gen)   # noqa: E731
+    x, res, g, nw, cw, cb = r(N, D), r(N, D), -r(N, D).abs(), r(D), r(D, W), r(D)
+    y, total, u, h = (torch.empty(N, D, device="cuda") for _ in range(4))
+    conv0, state0 = r(N, W - 1, D), r(N, D)
+    conv, state = conv0.clone(), state0.clone()
+    T = 700
+    cu = torch.tensor([0, 300, 300, T], dtype=torch.int32, device="cuda")
+    px, pg, dout, pout = r(T, D), -r(T, D).abs(), r(T, D), torch.empty(T, D, device="cuda")
+
+    def step():
+        K.kda_rmsnorm(x, nw, y, residual=res, residual_out=total)
+        K.kda_conv_decode_step(y, cw, cb, conv, u)
+        K.kda_scan_decode_step(u, g, state, h)
+        K.kda_scan_prefill(px, pg, None, cu, pout, None)
+        return [K.kda_scan_backward(px, pg, None, cu, dout), K.kda_conv_backward(px, cw, cb, None, cu, dout),
+                K.kda_rmsnorm_backward(px, nw, dout)]
+
+    results = lambda grads: [t.clone() for t in (y, total, u, h, conv, state, pout,   # noqa: E731
+                                                 *(v for d in grads for v in d.values() if v is not None))]
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        made = step()
+    conv.copy_(conv0), state.copy_(state0)
+    replayed, eager, px0 = [], [], px.clone()
+    for i in range(4):
+        x.copy_(res * (i + 1))
+        px.copy_(px0 * (2 - i))
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed.append(results(made))
+    conv.copy_(conv0), state.copy_(state0)
+    for i in range(4):
+        x.copy_(res * (i + 1))
+        px.copy_(px0 * (2 - i))
+        eager.append(results(step()))
+    assert all(torch.equal(p, q) for a, b in zip(replayed, eager) for p, q in zip(a, b))
