@@ -745,7 +745,7 @@ const char *kda_status_string(kda_status status)
 {
     switch (status) {
     case KDA_OK: return "KDA_OK: success";
-    case KDA_ERR_INVALID_ARG: return "KDA_ERR_INVALID_ARG: invalid argument (null, negative, misaligned or bad dtype)";
+    case KDA_ERR_INVALID_ARG: return "KDA_ERR_INVALID_ARG: invalid argument (null, negative, misaligned, overlapping or bad dtype)";
     case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: valid but unsupported configuration (v1: dk = dv = 128)";
     case KDA_ERR_LAUNCH: return "KDA_ERR_LAUNCH: HIP kernel launch failed";
     case KDA_ERR_SCRATCH:
