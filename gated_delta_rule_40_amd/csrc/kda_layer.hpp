@@ -1,5 +1,6 @@
 // kda_layer.hpp -- launchers of the layer operators' kernels, as the host API
-// calls them (kda_scan.hip, kda_conv.hip, kda_norm.hip).  Arguments have been
+// calls them (kda_scan.hip, kda_conv.hip, kda_norm.hip, kda_qknorm.hip,
+// kda_cache.hip, kda_cached_decode.hip, kda_verify.hip).  Arguments have been
 // checked; every launcher returns the HIP status of its launches.
 #pragma once
 
@@ -58,3 +59,42 @@ size_t kda_rmsnorm_bwd_ws_bytes(int32_t rows, int32_t D);
 hipError_t kda_launch_rmsnorm_backward(bool bf16, const void *x, const float *w, const void *dout, const void *dres,
                                        int32_t rows, int32_t D, float eps, void *dx, float *dw, void *ws,
                                        hipStream_t s);
+
+// What kda_qknorm and its gradients share (include/kda.h); without a rotation rot is 0.
+struct KdaQkNorm {
+    const void *q, *k;
+    int64_t q_stride, k_stride;
+    const float *q_weight, *k_weight;
+    const int32_t *positions;
+    const float *inv_freq;
+    const int32_t *pair_axis;
+    int32_t tokens, q_heads, k_heads, dim, rot, axes;
+    bool interleaved;
+    int32_t norm;
+    float eps, q_scale;
+};
+bool kda_qknorm_fits(bool bf16, const KdaQkNorm &a);
+hipError_t kda_launch_qknorm(bool bf16, const KdaQkNorm &a, void *q_out, void *k_out, hipStream_t s);
+size_t kda_qknorm_bwd_ws_bytes(int32_t d);
+hipError_t kda_launch_qknorm_backward(bool bf16, bool grad_bf16, const KdaQkNorm &a, const void *dq_out, const void *dk_out,
+                                      int64_t dq_stride, int64_t dk_stride, void *dq, void *dk, float *dq_weight,
+                                      float *dk_weight, void *ws, hipStream_t s);
+
+bool kda_cache_fits(bool bf16, int32_t entries, int32_t elems);
+hipError_t kda_launch_cache_store(bool bf16, const void *src, const int32_t *slots, int32_t entries, int32_t elems,
+                                  int format, int64_t entry_bytes, int32_t num_slots, uint8_t *cache, uint8_t *scales,
+                                  hipStream_t s);
+hipError_t kda_launch_cache_load(bool bf16, const uint8_t *cache, const uint8_t *scales, const int32_t *slots,
+                                 int32_t entries, int32_t elems, int format, int64_t entry_bytes, int32_t num_slots,
+                                 void *dst, hipStream_t s);
+bool kda_cached_tokens_fits(int32_t N, int32_t H);
+hipError_t kda_launch_cached_tokens(bool bf16, const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                    const int32_t *cu, const int32_t *num_tokens, uint8_t *cache, uint8_t *scales,
+                                    const int32_t *slots, bool write, int32_t num_slots, int32_t N, int32_t T_tot,
+                                    int32_t H, int format, void *out, hipStream_t s);
+
+bool kda_verify_fits(int32_t N, int32_t vocab);
+size_t kda_verify_ws_bytes(int32_t N, int32_t vocab);
+hipError_t kda_launch_verify(bool bf16, const void *target, const void *draft, const int32_t *tokens, const int32_t *cu,
+                             const float *accept_rand, const float *sample_rand, int32_t N, int32_t T_tot, int32_t vocab,
+                             int32_t *num_tokens, int32_t *next_token, void *ws, hipStream_t s);

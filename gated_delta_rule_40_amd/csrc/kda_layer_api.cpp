@@ -1,5 +1,5 @@
 // kda_layer_api.cpp -- host side of the layer operators of the libkda C ABI
-// (kda_scan_*, kda_conv_*, kda_rmsnorm*; declared in include/kda.h).
+// (kda_scan_*, kda_conv_*, kda_rmsnorm*, kda_qknorm*; declared in include/kda.h).
 //
 // Validates every argument before touching HIP and launches on the caller's
 // stream.  Nothing is allocated and no stream is synchronised.
@@ -7,7 +7,6 @@
 
 #include <cmath>
 #include <cstdint>
-#include <initializer_list>
 
 #include "kda.h"
 #include "kda_host.hpp"
@@ -17,67 +16,9 @@ using namespace kda_host;
 
 namespace {
 
-bool dtype_ok(kda_dtype dtype) { return dtype == KDA_F32 || dtype == KDA_BF16; }
-size_t elem_size(kda_dtype dtype) { return dtype == KDA_BF16 ? 2 : 4; }
-
-// A token array: present (unless it has no elements) and aligned to its type.
-bool array_ok(const void *p, int64_t elems, size_t size) { return (p || elems == 0) && aligned(p, size); }
-
-// Arrays in bytes.  Bit i of an output's `may`: it may take the place of input i.
-struct In {
-    const void *p;
-    size_t n;
-};
-struct Out {
-    const void *p;
-    size_t n;
-    unsigned may;
-};
-
-template <typename A, typename B> bool meet(const A &a, const B &b)
-{
-    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && a.n && b.n && (p < q ? q - p < a.n : p - q < b.n);
-}
-
-// Whether no output shares memory with another one, or with an input that it is not, whole, in the place of.
-bool keep_apart(std::initializer_list<Out> outs, std::initializer_list<In> ins)
-{
-    for (const Out *o = outs.begin(); o != outs.end(); ++o) {
-        for (const Out *other = outs.begin(); other != o; ++other)
-            if (meet(*o, *other)) return false;
-        for (const In *i = ins.begin(); i != ins.end(); ++i)
-            if (meet(*o, *i) && !(o->may >> (i - ins.begin()) & 1 && o->p == i->p)) return false;
-    }
-    return true;
-}
-
-kda_status from_hip(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_LAUNCH; }
-
-hipStream_t hip_stream(kda_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
-
-// What the packed calls share: sizes, type, cu_seqlens.  The kernels look a
-// tile beyond a token, and a wave beyond a sequence, in int32.
-bool packed_ok(const int32_t *cu, int32_t N, int32_t T, int32_t D, kda_dtype dtype)
-{
-    return dtype_ok(dtype) && N >= 0 && N <= INT32_MAX - 65536 && T >= 0 && T <= INT32_MAX - 65536 && D > 0 && cu &&
-           aligned(cu, 4);
-}
-
-bool workspace_ok(const void *ws, size_t bytes, size_t need, size_t align)
-{
-    return need == 0 || (ws && aligned(ws, align) && bytes >= need);
-}
-
-size_t cu_bytes(int32_t N) { return ((size_t)N + 1) * sizeof(int32_t); }
 size_t checkpoint_bytes(int32_t T, int32_t D)
 {
     return ((size_t)T + KDA_SCAN_TILE - 1) / KDA_SCAN_TILE * D * sizeof(float);
-}
-
-kda_status check_cu(const int32_t *cu, int32_t N, int32_t T, kda_stream_t stream)
-{
-    return validate_enabled() ? validate_cu(cu, N, T, hip_stream(stream)) : KDA_OK;
 }
 
 }  // namespace
@@ -298,6 +239,128 @@ kda_status kda_rmsnorm_backward(const void *x, const float *weight, const void *
         return KDA_ERR_INVALID_ARG;
     return from_hip(kda_launch_rmsnorm_backward(dtype == KDA_BF16, x, weight, dout, dresidual, rows, channels, eps,
                                                 dx, dweight, workspace, hip_stream(stream)));
+}
+
+// ---------------------------------------------------------------- norm and rotation of queries and keys
+namespace {
+
+constexpr int64_t kMaxStride = INT64_C(1) << 29;   // elements between tokens: spans stay below 2^62 bytes
+
+// What forward and backward check alike.
+kda_status check_qknorm(const KdaQkNorm &a, kda_dtype dtype, bool in_use)
+{
+    if (!dtype_ok(dtype) || a.tokens < 0 || a.q_heads < 0 || a.k_heads < 0 || a.dim <= 0 || a.rot < 0 || a.rot > a.dim ||
+        a.rot % 2 || a.norm < KDA_NORM_NONE || a.norm > KDA_NORM_RMS || !std::isfinite(a.eps) || a.eps < 0.f ||
+        !std::isfinite(a.q_scale))
+        return KDA_ERR_INVALID_ARG;
+    const size_t e = elem_size(dtype);
+    const int64_t qc = (int64_t)a.q_heads * a.dim, kc = (int64_t)a.k_heads * a.dim;
+    if (qc > INT32_MAX - 65536 || kc > INT32_MAX - 65536) return KDA_ERR_INVALID_ARG;
+    if (!array_ok(a.q, a.tokens * qc, e) || !array_ok(a.k, a.tokens * kc, e) || (a.tokens > 0 && (a.q_stride < qc || a.k_stride < kc)) ||
+        !aligned(a.q_weight, 4) || !aligned(a.k_weight, 4))
+        return KDA_ERR_INVALID_ARG;
+    if (a.q_stride > kMaxStride || a.k_stride > kMaxStride) return KDA_ERR_INVALID_ARG;
+    if (a.rot && in_use &&
+        (a.axes <= 0 || !a.positions || !aligned(a.positions, 4) || !a.inv_freq || !aligned(a.inv_freq, 4) || !aligned(a.pair_axis, 4)))
+        return KDA_ERR_INVALID_ARG;
+    return a.dim > KDA_QKNORM_MAX_DIM ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
+// the arrays that are read: q, k, weights, positions, frequencies, axes
+constexpr int kQkInputs = 7;
+void qknorm_inputs(const KdaQkNorm &a, size_t e, Rows (&in)[kQkInputs])
+{
+    const int64_t n = a.tokens, qw = (int64_t)a.q_heads * a.dim * e, kw = (int64_t)a.k_heads * a.dim * e;
+    in[0] = {a.q, n, qw, (int64_t)(a.q_stride * e)};
+    in[1] = {a.k, n, kw, (int64_t)(a.k_stride * e)};
+    in[2] = dense(a.q_weight, (size_t)a.dim * 4), in[3] = dense(a.k_weight, (size_t)a.dim * 4);
+    const size_t pairs = a.rot / 2;
+    in[4] = dense(a.rot ? a.positions : nullptr, (size_t)a.axes * n * 4);
+    in[5] = dense(a.rot ? a.inv_freq : nullptr, pairs * 4), in[6] = dense(a.rot ? a.pair_axis : nullptr, pairs * 4);
+}
+
+// Whether `o` shares memory with one of `in`, other than lying whole in the place of number `may`.
+bool meets_any(const Rows &o, const Rows *in, int n, int may)
+{
+    for (int i = 0; i < n; ++i) {
+        const bool same = i == may && o.p == in[i].p && (o.rows <= 1 || o.pitch == in[i].pitch);
+        if (!same && rows_meet(o, in[i])) return true;
+    }
+    return false;
+}
+
+}  // namespace
+
+kda_status kda_qknorm(const void *q, const void *k, int64_t q_stride, int64_t k_stride, const float *q_weight,
+                      const float *k_weight, const int32_t *positions, const float *inv_freq,
+                      const int32_t *pair_axis, int32_t num_tokens, int32_t num_q_heads, int32_t num_k_heads,
+                      int32_t head_dim, int32_t rot_dim, int32_t num_axes, int32_t interleaved, kda_norm norm,
+                      float eps, float q_scale, kda_dtype dtype, void *q_out, void *k_out, kda_stream_t stream)
+{
+    const KdaQkNorm a{q, k, q_stride, k_stride, q_weight, k_weight, positions, inv_freq, pair_axis, num_tokens, num_q_heads,
+                      num_k_heads, head_dim, rot_dim, num_axes, interleaved != 0, norm, eps, q_scale};
+    const bool in_use = num_tokens > 0 && (num_q_heads > 0 || num_k_heads > 0);
+    if (kda_status st = check_qknorm(a, dtype, in_use)) return st;
+    const size_t e = elem_size(dtype);
+    const int64_t qc = (int64_t)num_q_heads * head_dim, kc = (int64_t)num_k_heads * head_dim;
+    if (!array_ok(q_out, num_tokens * qc, e) || !array_ok(k_out, num_tokens * kc, e)) return KDA_ERR_INVALID_ARG;
+    if (!in_use) return KDA_OK;
+    Rows in[kQkInputs];
+    qknorm_inputs(a, e, in);
+    const Rows qo{q_out, num_tokens, (int64_t)(qc * e), (int64_t)(qc * e)}, ko{k_out, num_tokens, (int64_t)(kc * e), (int64_t)(kc * e)};
+    if (rows_meet(qo, ko) || meets_any(qo, in, kQkInputs, 0) || meets_any(ko, in, kQkInputs, 1)) return KDA_ERR_INVALID_ARG;
+    if (!kda_qknorm_fits(dtype == KDA_BF16, a)) return KDA_ERR_UNSUPPORTED;
+    return from_hip(kda_launch_qknorm(dtype == KDA_BF16, a, q_out, k_out, hip_stream(stream)));
+}
+
+size_t kda_qknorm_backward_workspace_size(int32_t num_tokens, int32_t num_q_heads, int32_t num_k_heads,
+                                          int32_t head_dim, kda_dtype dtype)
+{
+    if (num_tokens < 0 || num_q_heads < 0 || num_k_heads < 0 || head_dim <= 0 || head_dim > KDA_QKNORM_MAX_DIM || !dtype_ok(dtype))
+        return 0;
+    return kda_qknorm_bwd_ws_bytes(head_dim);
+}
+
+kda_status kda_qknorm_backward(const void *q, const void *k, int64_t q_stride, int64_t k_stride,
+                               const float *q_weight, const float *k_weight, const int32_t *positions,
+                               const float *inv_freq, const int32_t *pair_axis, int32_t num_tokens,
+                               int32_t num_q_heads, int32_t num_k_heads, int32_t head_dim, int32_t rot_dim,
+                               int32_t num_axes, int32_t interleaved, kda_norm norm, float eps, float q_scale,
+                               kda_dtype dtype, kda_dtype grad_dtype, const void *dq_out, const void *dk_out,
+                               int64_t dq_stride, int64_t dk_stride, void *dq, void *dk, float *dq_weight,
+                               float *dk_weight, void *workspace, size_t workspace_bytes, kda_stream_t stream)
+{
+    const KdaQkNorm a{q, k, q_stride, k_stride, q_weight, k_weight, positions, inv_freq, pair_axis, num_tokens, num_q_heads,
+                      num_k_heads, head_dim, rot_dim, num_axes, interleaved != 0, norm, eps, q_scale};
+    const bool in_use = num_tokens > 0 && (num_q_heads > 0 || num_k_heads > 0);
+    if (kda_status st = check_qknorm(a, dtype, in_use)) return st;
+    if (!dtype_ok(grad_dtype) || (grad_dtype == KDA_BF16 && dtype != KDA_BF16)) return KDA_ERR_INVALID_ARG;
+    const size_t e = elem_size(dtype), ge = elem_size(grad_dtype);
+    const int64_t n = num_tokens, qc = (int64_t)num_q_heads * head_dim, kc = (int64_t)num_k_heads * head_dim;
+    if (!array_ok(dq_out, n * qc, ge) || !array_ok(dk_out, n * kc, ge) || !array_ok(dq, n * qc, e) || !array_ok(dk, n * kc, e) ||
+        (n > 0 && (dq_stride < qc || dk_stride < kc)) || dq_stride > kMaxStride || dk_stride > kMaxStride ||
+        !aligned(dq_weight, 4) || !aligned(dk_weight, 4) || (dq_weight && !q_weight) || (dk_weight && !k_weight))
+        return KDA_ERR_INVALID_ARG;
+    const size_t need = dq_weight || dk_weight ? kda_qknorm_bwd_ws_bytes(head_dim) : 0;
+    if (!workspace_ok(workspace, workspace_bytes, need, 4)) return KDA_ERR_INVALID_ARG;
+    if (!in_use && !need) return KDA_OK;
+    Rows in[kQkInputs + 2];
+    {
+        Rows first[kQkInputs];
+        qknorm_inputs(a, e, first);
+        std::copy(first, first + kQkInputs, in);
+        in[kQkInputs] = dense(dq_out, n * qc * ge), in[kQkInputs + 1] = dense(dk_out, n * kc * ge);
+    }
+    const Rows outs[] = {{dq, n, (int64_t)(qc * e), (int64_t)(dq_stride * e)}, {dk, n, (int64_t)(kc * e), (int64_t)(dk_stride * e)},
+                         dense(dq_weight, (size_t)head_dim * 4), dense(dk_weight, (size_t)head_dim * 4), dense(workspace, need)};
+    for (int i = 0; i < 5; ++i) {
+        if (meets_any(outs[i], in, kQkInputs + 2, i < 2 ? i : -1)) return KDA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (rows_meet(outs[i], outs[j])) return KDA_ERR_INVALID_ARG;
+    }
+    // without tokens the weights' gradients are still written (zeros)
+    return from_hip(kda_launch_qknorm_backward(dtype == KDA_BF16, grad_dtype == KDA_BF16, a, dq_out, dk_out, dq_stride, dk_stride,
+                                               dq, dk, dq_weight, dk_weight, workspace, hip_stream(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,399 @@
+// kda_qknorm.hip -- the norm of every head's query and key with the rotation by
+// position in the same pass, and its gradients.
+//
+//     n = x inv,  inv = 1 / sqrt(sum(x^2) m + eps)     (m = 1, or 1 / head_dim)
+//     y = scale w n,  and pairs (a, b) of y turn by the token's angle
+//     backward: dy turned back, dn = scale w dy, dx = inv (dn - n m sum(dn n)),
+//     dw = sum over tokens and heads of scale dy n
+//
+// A head is held by a few lanes, each with "slots" of two pieces of VW values: the
+// first and second members of VW rotated pairs, or two pieces of the part that is
+// not rotated.  So a pair never leaves its lane, every value is read once and
+// written once, and HBM's rate is the bound.  A workgroup takes some tokens of q
+// or of k; the cosines and sines of its tokens are formed once for all heads,
+// angles in fp64 and reduced there, and lie in LDS.
+#include "kda_colsum.hpp"
+#include "kda_device.hpp"
+#include "kda_layer.hpp"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace kda {
+
+constexpr int QK_THREADS = 256;
+constexpr int QK_ITEMS = 2;            // heads a lane's group takes at once
+constexpr int QK_MAX_PARTIALS = 1024;  // workgroups of the backward that sum a weight's gradient, of q and of k each
+
+enum { ROT_NONE = 0, ROT_HALVES = 1, ROT_NEIGHBOURS = 2 };
+
+// One of q and k: its arrays, and the workgroups that take it.
+struct Heads {
+    const void *x;        // [T][heads][d], tokens `stride` apart
+    void *y;              // forward: out, dense; backward: dx, tokens `y_stride` apart
+    const void *dy;       // backward: the gradient of out, dense
+    const float *weight;  // [d] or null
+    float *partial;       // backward: [workgroups][d], or null
+    int64_t stride, y_stride;
+    int32_t heads;
+    float scale;
+    int32_t tile, groups;   // tokens of a tile; workgroups
+};
+
+struct QkShape {
+    Heads of[2];
+    const int32_t *positions, *pair_axis;
+    const float *inv_freq;
+    int32_t T, d, rot, axes;
+    int32_t slots, rot_slots, lanes;   // slots of a head, those rotated, lanes of a head (a power of two)
+    float mean, eps;                   // m; with norm == 0 no division
+    int32_t norm;
+};
+
+// Where a slot's two pieces begin, and how many values they have (VW but at the end
+// of an odd part, where VW = 1 and the second piece is missing).
+template <int VW, int ROT> struct Slot {
+    int32_t c0, c1, n1;
+    __device__ __forceinline__ Slot(const QkShape &sh, int32_t s) {
+        if (ROT == ROT_NEIGHBOURS && s < sh.rot_slots) {
+            c0 = 2 * VW * s, c1 = c0 + VW, n1 = VW;
+        } else if (ROT == ROT_HALVES && s < sh.rot_slots) {
+            c0 = VW * s, c1 = c0 + sh.rot / 2, n1 = VW;
+        } else {
+            const int32_t rest = (sh.d - sh.rot + 1) / 2;
+            c0 = sh.rot + VW * (s - sh.rot_slots), c1 = c0 + rest;
+            n1 = c1 < sh.d ? VW : 0;
+        }
+    }
+};
+
+template <typename T, int VW> struct QkPiece {
+    typedef T raw __attribute__((ext_vector_type(VW)));
+    typedef raw mem __attribute__((aligned(sizeof(T))));
+    static __device__ __forceinline__ raw load(const T *p) { return *reinterpret_cast<const mem *>(p); }
+    static __device__ __forceinline__ void store(T *p, const float *v) {
+        raw r;
+#pragma unroll
+        for (int j = 0; j < VW; ++j) r[j] = from_f<T>(v[j]);
+        *reinterpret_cast<mem *>(p) = r;
+    }
+};
+
+// cos and sin of tokens [t0, t0 + count) into table[token][pair]
+__device__ __forceinline__ void turn_table(const QkShape &sh, int64_t t0, int32_t count, float2 *table)
+{
+    const int32_t pairs = sh.rot / 2;
+    for (int32_t i = threadIdx.x; i < count * pairs; i += blockDim.x) {
+        const int32_t t = i / pairs, j = i % pairs;
+        const int32_t axis = sh.pair_axis ? min(max(sh.pair_axis[j], 0), sh.axes - 1) : 0;
+        const double angle = (double)sh.positions[(int64_t)axis * sh.T + t0 + t] * (double)sh.inv_freq[j];
+        // less whole turns, 2 pi in two pieces
+        const double turns = __builtin_rint(angle * 0.15915494309189535);
+        double r = __builtin_fma(-turns, 6.283185307179586, angle);
+        r = __builtin_fma(-turns, 2.4492935982947064e-16, r);
+        float sn, cs;
+        sincosf((float)r, &sn, &cs);
+        table[i] = float2{cs, sn};
+    }
+}
+
+// (a, b) of pair i among a slot's 2 VW values
+template <int VW, int ROT> __device__ __forceinline__ float &first_of(float *v, int i) { return ROT == ROT_NEIGHBOURS ? v[2 * i] : v[i]; }
+template <int VW, int ROT> __device__ __forceinline__ float &second_of(float *v, int i) { return ROT == ROT_NEIGHBOURS ? v[2 * i + 1] : v[VW + i]; }
+
+// the sums over a head's lanes
+template <int M> __device__ __forceinline__ void head_sums(float (&s)[M], int32_t lanes)
+{
+    for (int off = lanes >> 1; off > 0; off >>= 1)
+#pragma unroll
+        for (int m = 0; m < M; ++m) s[m] += __shfl_xor(s[m], off);
+}
+
+// The forward and the gradients walk the same items: (token, head) number
+// `item` of a workgroup's tile of tokens.  C slots a lane.
+template <typename T, typename G, int VW, int C, int ROT, bool BACK>
+__global__ __launch_bounds__(QK_THREADS) void kda_qknorm_kernel(QkShape sh)
+{
+    typedef QkPiece<T, VW> P;
+    typedef QkPiece<G, VW> PG;
+    extern __shared__ float2 table[];
+    const bool second = (int32_t)blockIdx.x >= sh.of[0].groups;
+    const Heads hd = second ? sh.of[1] : sh.of[0];
+    const int32_t group = (int32_t)blockIdx.x - (second ? sh.of[0].groups : 0);
+    const int32_t lane = threadIdx.x & (sh.lanes - 1), slot0 = lane, per = QK_THREADS / sh.lanes, g0 = threadIdx.x / sh.lanes;
+    const T *const xs = (const T *)hd.x;
+    const G *const dys = (const G *)hd.dy;
+    T *const ys = (T *)hd.y;
+    const int32_t pairs = sh.rot / 2;
+    float dw[C][2 * VW] = {}, w[C][2 * VW];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int32_t s = slot0 + c * sh.lanes;
+        const Slot<VW, ROT> sl(sh, s);
+#pragma unroll
+        for (int j = 0; j < 2 * VW; ++j)
+            w[c][j] = hd.weight && s < sh.slots && (j < VW || sl.n1) ? hd.weight[(j < VW ? sl.c0 : sl.c1 - VW) + j] : 1.f;
+    }
+
+    for (int64_t t0 = (int64_t)group * hd.tile; t0 < sh.T; t0 += (int64_t)hd.groups * hd.tile) {
+        const int32_t count = (int32_t)min((int64_t)hd.tile, sh.T - t0), items = count * hd.heads;
+        if (ROT) {
+            __syncthreads();
+            turn_table(sh, t0, count, table);
+            __syncthreads();
+        }
+        for (int32_t i0 = g0; i0 - g0 < items; i0 += per * QK_ITEMS) {
+            typename P::raw x[QK_ITEMS][C][2];
+            typename PG::raw dy[QK_ITEMS][C][2];
+            int32_t token[QK_ITEMS];
+            int64_t at[QK_ITEMS];
+            bool live[QK_ITEMS];
+#pragma unroll
+            for (int u = 0; u < QK_ITEMS; ++u) {
+                const int32_t item = i0 + u * per;
+                live[u] = item < items;
+                token[u] = live[u] ? item / hd.heads : 0;
+                const int32_t head = live[u] ? item % hd.heads : 0;
+                at[u] = ((t0 + token[u]) * hd.heads + head) * sh.d;
+                const T *row = xs + (t0 + token[u]) * hd.stride + (int64_t)head * sh.d;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    x[u][c][0] = x[u][c][1] = typename P::raw{};
+                    if (BACK) dy[u][c][0] = dy[u][c][1] = typename PG::raw{};
+                    const int32_t s = slot0 + c * sh.lanes;
+                    if (s >= sh.slots) continue;
+                    const Slot<VW, ROT> sl(sh, s);
+                    x[u][c][0] = P::load(row + sl.c0);
+                    if (sl.n1) x[u][c][1] = P::load(row + sl.c1);
+                    if (BACK) {
+                        dy[u][c][0] = PG::load(dys + at[u] + sl.c0);
+                        if (sl.n1) dy[u][c][1] = PG::load(dys + at[u] + sl.c1);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < QK_ITEMS; ++u) {
+                float v[C][2 * VW], e[C][2 * VW];
+                float sum[BACK ? 2 : 1] = {};
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int32_t s = slot0 + c * sh.lanes;
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) v[c][j] = to_f(x[u][c][0][j]), v[c][VW + j] = to_f(x[u][c][1][j]);
+                    if (BACK) {
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) {
+                            e[c][j] = to_f(dy[u][c][0][j]) * hd.scale;
+                            e[c][VW + j] = to_f(dy[u][c][1][j]) * hd.scale;
+                        }
+                        if (ROT && s < sh.rot_slots) {
+                            const float2 *turn = table + token[u] * pairs + s * VW;
+#pragma unroll
+                            for (int j = 0; j < VW; ++j) {
+                                float &a = first_of<VW, ROT>(e[c], j), &b = second_of<VW, ROT>(e[c], j);
+                                const float2 t = turn[j];
+                                const float a1 = a * t.x + b * t.y;
+                                b = b * t.x - a * t.y;
+                                a = a1;
+                            }
+                        }
+                    }
+                    // (e: the gradient of w n)
+#pragma unroll
+                    for (int j = 0; j < 2 * VW; ++j) {
+                        sum[0] += v[c][j] * v[c][j];
+                        if (BACK) sum[BACK ? 1 : 0] += e[c][j] * w[c][j] * v[c][j];
+                    }
+                }
+                head_sums(sum, sh.lanes);
+                const float inv = sh.norm ? 1.f / sqrtf(sum[0] * sh.mean + sh.eps) : 1.f;
+                const float along = BACK && sh.norm ? sum[BACK ? 1 : 0] * inv * sh.mean * inv : 0.f;   // of x, not of n
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const int32_t s = slot0 + c * sh.lanes;
+                    if (s >= sh.slots || !live[u]) continue;
+                    const Slot<VW, ROT> sl(sh, s);
+                    if (!BACK) {
+#pragma unroll
+                        for (int j = 0; j < 2 * VW; ++j) v[c][j] *= inv * hd.scale, v[c][j] *= w[c][j];
+                        if (ROT && s < sh.rot_slots) {
+                            const float2 *turn = table + token[u] * pairs + s * VW;
+#pragma unroll
+                            for (int j = 0; j < VW; ++j) {
+                                float &a = first_of<VW, ROT>(v[c], j), &b = second_of<VW, ROT>(v[c], j);
+                                const float2 t = turn[j];
+                                const float a1 = a * t.x - b * t.y;
+                                b = b * t.x + a * t.y;
+                                a = a1;
+                            }
+                        }
+                        P::store(ys + at[u] + sl.c0, v[c]);
+                        if (sl.n1) P::store(ys + at[u] + sl.c1, v[c] + VW);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 2 * VW; ++j) {
+                            dw[c][j] += e[c][j] * (v[c][j] * inv);
+                            v[c][j] = inv * (e[c][j] * w[c][j] - along * v[c][j]);
+                        }
+                        // (a row of dx: the same token and head, at its own stride)
+                        T *row = ys + (t0 + token[u]) * hd.y_stride + (at[u] - (t0 + token[u]) * hd.heads * sh.d);
+                        P::store(row + sl.c0, v[c]);
+                        if (sl.n1) P::store(row + sl.c1, v[c] + VW);
+                    }
+                }
+            }
+        }
+    }
+    if (!BACK || !hd.partial) return;
+    // the groups' sums of a slot's values, added in order by the first
+    float *fold = reinterpret_cast<float *>(table);
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 2 * VW; ++j) fold[(c * 2 * VW + j) * QK_THREADS + threadIdx.x] = dw[c][j];
+    __syncthreads();
+    if (g0 > 0) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int32_t s = slot0 + c * sh.lanes;
+        if (s >= sh.slots) continue;
+        const Slot<VW, ROT> sl(sh, s);
+#pragma unroll
+        for (int j = 0; j < 2 * VW; ++j) {
+            if (j >= VW && !sl.n1) continue;
+            float sum = 0.f;
+            for (int32_t i = 0; i < per; ++i) sum += fold[(c * 2 * VW + j) * QK_THREADS + i * sh.lanes + lane];
+            hd.partial[(int64_t)group * sh.d + (j < VW ? sl.c0 : sl.c1 - VW) + j] = sum;
+        }
+    }
+}
+
+// dq_weight and dk_weight: the sums over the workgroups' parts
+__global__ __launch_bounds__(COLSUM_THREADS) void kda_qknorm_weights_kernel(const float *part0, int32_t n0, float *dst0,
+                                                                            const float *part1, int32_t n1, float *dst1,
+                                                                            int32_t d)
+{
+    const bool second = blockIdx.y == 1;
+    const float *part = second ? part1 : part0;
+    float *dst = second ? dst1 : dst0;
+    if (!dst) return;
+    const int64_t c = (int64_t)blockIdx.x * COLSUM_COLS + threadIdx.x % COLSUM_COLS;
+    const float s = column_sum(part, second ? n1 : n0, d, c);
+    if (threadIdx.x < COLSUM_COLS && c < d) dst[c] = s;
+}
+
+// ---------------------------------------------------------------- host
+template <int VW, int C> void lay_out(QkShape &sh, int64_t most_groups)
+{
+    sh.rot_slots = sh.rot / 2 / VW;
+    sh.slots = sh.rot_slots + ((sh.d - sh.rot + 1) / 2 + VW - 1) / VW;
+    sh.lanes = 1;
+    while (sh.lanes * C < sh.slots) sh.lanes *= 2;
+    const int32_t at_once = QK_THREADS / sh.lanes * QK_ITEMS;
+    for (Heads &h : sh.of) {
+        h.tile = h.heads ? (at_once + h.heads - 1) / h.heads : 1;
+        const int64_t tiles = ((int64_t)sh.T + h.tile - 1) / h.tile;
+        h.groups = h.heads ? (int32_t)(tiles < most_groups ? tiles : most_groups) : 0;
+    }
+}
+
+template <typename T, typename G, int VW, int C, int ROT, bool BACK> hipError_t run_qknorm(QkShape sh, hipStream_t s)
+{
+    const int32_t groups = sh.of[0].groups + sh.of[1].groups;
+    if (groups == 0) return hipSuccess;
+    size_t lds = 0;
+    if (ROT)
+        for (const Heads &h : sh.of) lds = std::max(lds, sizeof(float2) * h.tile * (size_t)(sh.rot / 2));
+    if (BACK && (sh.of[0].partial || sh.of[1].partial)) lds = std::max(lds, sizeof(float) * QK_THREADS * C * 2 * VW);
+    hipLaunchKernelGGL((kda_qknorm_kernel<T, G, VW, C, ROT, BACK>), dim3((unsigned)groups), dim3(QK_THREADS), lds, s, sh);
+    return hipGetLastError();
+}
+
+// Calls f with the width of a piece and the slots of a lane: the widest piece, of
+// 16 bytes at most, that divides the halves of the rotated part and of the rest.
+template <typename T, typename Fn> auto with_width(const QkShape &sh, Fn f)
+{
+    const auto fits = [&](int w) { return sh.rot % (2 * w) == 0 && (sh.d - sh.rot) % (2 * w) == 0; };
+    if constexpr (sizeof(T) == 2)
+        if (fits(8)) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+    if (fits(4)) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+    if (fits(2)) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
+}
+
+template <typename T, typename G, bool BACK> hipError_t qknorm(QkShape sh, int mode, hipStream_t s)
+{
+    return with_width<T>(sh, [&](auto w, auto c) {
+        lay_out<w(), c()>(sh, BACK ? QK_MAX_PARTIALS : INT32_MAX);
+        return mode == ROT_NONE     ? run_qknorm<T, G, w(), c(), ROT_NONE, BACK>(sh, s)
+               : mode == ROT_HALVES ? run_qknorm<T, G, w(), c(), ROT_HALVES, BACK>(sh, s)
+                                    : run_qknorm<T, G, w(), c(), ROT_NEIGHBOURS, BACK>(sh, s);
+    });
+}
+
+}  // namespace kda
+
+using namespace kda;
+
+static int qk_mode(int32_t rot, bool interleaved) { return rot == 0 ? ROT_NONE : interleaved ? ROT_NEIGHBOURS : ROT_HALVES; }
+
+static QkShape qk_shape(const KdaQkNorm &a)
+{
+    QkShape sh{};
+    sh.of[0] = {a.q, nullptr, nullptr, a.q_weight, nullptr, a.q_stride, 0, a.q_heads, a.q_scale, 0, 0};
+    sh.of[1] = {a.k, nullptr, nullptr, a.k_weight, nullptr, a.k_stride, 0, a.k_heads, 1.f, 0, 0};
+    sh.positions = a.positions, sh.pair_axis = a.pair_axis, sh.inv_freq = a.inv_freq;
+    sh.T = a.tokens, sh.d = a.dim, sh.rot = a.rot, sh.axes = a.axes;
+    sh.mean = a.norm == 2 ? 1.f / a.dim : 1.f, sh.eps = a.eps, sh.norm = a.norm;
+    return sh;
+}
+
+hipError_t kda_launch_qknorm(bool bf16, const KdaQkNorm &a, void *q_out, void *k_out, hipStream_t s)
+{
+    QkShape sh = qk_shape(a);
+    sh.of[0].y = q_out, sh.of[1].y = k_out;
+    const int mode = qk_mode(a.rot, a.interleaved);
+    return bf16 ? qknorm<bf16_t, bf16_t, false>(sh, mode, s) : qknorm<float, float, false>(sh, mode, s);
+}
+
+size_t kda_qknorm_bwd_ws_bytes(int32_t d) { return sizeof(float) * 2 * QK_MAX_PARTIALS * (size_t)d; }
+
+hipError_t kda_launch_qknorm_backward(bool bf16, bool grad_bf16, const KdaQkNorm &a, const void *dq_out, const void *dk_out,
+                                      int64_t dq_stride, int64_t dk_stride, void *dq, void *dk, float *dq_weight,
+                                      float *dk_weight, void *ws, hipStream_t s)
+{
+    QkShape sh = qk_shape(a);
+    float *const part0 = (float *)ws, *const part1 = part0 + (size_t)QK_MAX_PARTIALS * a.dim;
+    sh.of[0].y = dq, sh.of[0].y_stride = dq_stride, sh.of[0].dy = dq_out, sh.of[0].partial = dq_weight ? part0 : nullptr;
+    sh.of[1].y = dk, sh.of[1].y_stride = dk_stride, sh.of[1].dy = dk_out, sh.of[1].partial = dk_weight ? part1 : nullptr;
+    const int mode = qk_mode(a.rot, a.interleaved);
+    hipError_t e = hipSuccess;
+    int32_t groups[2] = {0, 0};
+    const auto run = [&](auto t, auto g) {
+        typedef decltype(t) T;
+        typedef decltype(g) G;
+        with_width<T>(sh, [&](auto w, auto c) {
+            lay_out<w(), c()>(sh, QK_MAX_PARTIALS);
+            return 0;
+        });
+        groups[0] = sh.of[0].groups, groups[1] = sh.of[1].groups;
+        return qknorm<T, G, true>(sh, mode, s);
+    };
+    e = !bf16 ? run(float(), float()) : grad_bf16 ? run(bf16_t(), bf16_t()) : run(bf16_t(), float());
+    if (e != hipSuccess || (!dq_weight && !dk_weight)) return e;
+    hipLaunchKernelGGL(kda_qknorm_weights_kernel, dim3((unsigned)((a.dim + COLSUM_COLS - 1) / COLSUM_COLS), 2),
+                       dim3(COLSUM_THREADS), 0, s, (const float *)part0, groups[0], dq_weight, (const float *)part1, groups[1],
+                       dk_weight, a.dim);
+    return hipGetLastError();
+}
+
+bool kda_qknorm_fits(bool bf16, const KdaQkNorm &a)
+{
+    QkShape sh = qk_shape(a);
+    const auto groups = [&](auto w, auto c) {
+        lay_out<w(), c()>(sh, INT32_MAX);
+        return (int64_t)sh.of[0].groups + sh.of[1].groups;
+    };
+    return kda_grid_ok(bf16 ? with_width<bf16_t>(sh, groups) : with_width<float>(sh, groups), QK_THREADS);
+}

@@ -25,6 +25,16 @@ The operators around the recurrence in a layer:
     kda_conv_backward(x, weight, bias, initial_state, cu_seqlens, dout, dfinal=None, silu=True, ...) -> gradients
     kda_rmsnorm(x, weight, out=None, residual=None, residual_out=None, out_mx=None, scales=None, eps=1e-6)
     kda_rmsnorm_backward(x, weight, dout, dresidual=None, eps=1e-6, ...) -> gradients
+
+What stands before the recurrence, and around its states when they are cached
+and tokens are drafted:
+
+    kda_qknorm(q, k, q_out, k_out, q_weight=None, k_weight=None, norm="l2", eps=1e-6, q_scale=1.0, positions=None, ...)
+    kda_qknorm_backward(q, k, dq_out, dk_out, ...) -> gradients
+    kda_cache_store(src, slots, cache, scales, format="fp8")
+    kda_cache_load(cache, scales, slots, dst, format="fp8")
+    kda_decode_tokens_cached(q, k, v, g, beta, cu_seqlens, cache, scales, slots, format="fp8", out=None, ..., write=True)
+    kda_verify_drafts(target_probs, draft_probs, tokens, cu_seqlens, accept_rand, sample_rand, num_tokens, next_token)
 """
 from __future__ import annotations
 
@@ -42,13 +52,19 @@ KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_LAUNCH, KDA_ERR_SCRATC
 KDA_STATIC_SCRATCH_BYTES = 256 * 1024 * 1024      # include/kda.h
 KDA_F32, KDA_BF16 = 0, 1
 KDA_SCAN_TILE, KDA_MX_BLOCK = 128, 32              # include/kda.h
+KDA_QKNORM_MAX_DIM = 512
+KDA_NORMS = {"none": 0, "l2": 1, "rms": 2}         # kda_norm
+KDA_CACHE_FORMATS = {"fp8": 0, "int8": 1, "fp4": 2}  # kda_cache_format
 
 EXPORTS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_snapshots", "kda_prefill_cp",
            "kda_prefill_cp_workspace_size", "kda_prefill_cp_noalloc", "kda_decode_step", "kda_decode_tokens", "kda_backward",
            "kda_backward_workspace_size", "kda_scan_prefill", "kda_scan_workspace_size", "kda_scan_decode_step",
            "kda_scan_backward", "kda_scan_backward_workspace_size", "kda_conv_prefill", "kda_conv_decode_step",
            "kda_conv_backward", "kda_conv_backward_workspace_size", "kda_rmsnorm", "kda_rmsnorm_backward",
-           "kda_rmsnorm_backward_workspace_size", "kda_status_string", "kda_version")
+           "kda_rmsnorm_backward_workspace_size", "kda_qknorm", "kda_qknorm_backward",
+           "kda_qknorm_backward_workspace_size", "kda_cache_entry_bytes", "kda_cache_store", "kda_cache_load",
+           "kda_decode_tokens_cached", "kda_verify_drafts", "kda_verify_drafts_workspace_size", "kda_status_string",
+           "kda_version")
 
 _lib = None
 
@@ -95,7 +111,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kda_backward.restype = ctypes.c_int
     lib.kda_backward_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.c_int]
     lib.kda_backward_workspace_size.restype = ctypes.c_size_t
-    size = ctypes.c_size_t
+    size, i64, f32, enum = ctypes.c_size_t, ctypes.c_int64, ctypes.c_float, ctypes.c_int
     for name, restype, args in (
             ("kda_scan_prefill", ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, ctypes.c_int, vp, vp, vp, vp, size, vp]),
             ("kda_scan_workspace_size", size, [i32, i32, i32, ctypes.c_int]),
@@ -111,7 +127,20 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
             ("kda_rmsnorm", ctypes.c_int, [vp, vp, vp, i32, i32, ctypes.c_float, ctypes.c_int, vp, vp, vp, vp, vp]),
             ("kda_rmsnorm_backward", ctypes.c_int, [vp, vp, vp, vp, i32, i32, ctypes.c_float, ctypes.c_int, vp, vp, vp,
                                                     size, vp]),
-            ("kda_rmsnorm_backward_workspace_size", size, [i32, i32, ctypes.c_int])):
+            ("kda_rmsnorm_backward_workspace_size", size, [i32, i32, ctypes.c_int]),
+            ("kda_qknorm", ctypes.c_int, [vp, vp, i64, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, enum, f32,
+                                          f32, enum, vp, vp, vp]),
+            ("kda_qknorm_backward", ctypes.c_int, [vp, vp, i64, i64, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                                   enum, f32, f32, enum, enum, vp, vp, i64, i64, vp, vp, vp, vp, vp, size,
+                                                   vp]),
+            ("kda_qknorm_backward_workspace_size", size, [i32, i32, i32, i32, enum]),
+            ("kda_cache_entry_bytes", size, [i32, enum]),
+            ("kda_cache_store", ctypes.c_int, [vp, vp, i32, i32, enum, enum, i32, vp, vp, vp]),
+            ("kda_cache_load", ctypes.c_int, [vp, vp, vp, i32, i32, enum, enum, i32, vp, vp]),
+            ("kda_decode_tokens_cached", ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                                        i32, enum, enum, vp, vp]),
+            ("kda_verify_drafts", ctypes.c_int, [vp, vp, vp, vp, vp, vp, i32, i32, i32, enum, vp, vp, vp, size, vp]),
+            ("kda_verify_drafts_workspace_size", size, [i32, i32, enum])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = restype, args
     lib.kda_status_string.argtypes = [ctypes.c_int]
@@ -688,3 +717,215 @@ def kda_rmsnorm_backward(x, weight, dout, dresidual=None, eps: float = 1e-6, gra
         ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_rmsnorm_backward_workspace_size", rows, D, code)
     _call(lib.kda_rmsnorm_backward, dev, stream, *args, pws, nbytes)
     return grads
+
+
+# ---------------------------------------------------------------- norm and rotation of queries and keys
+_I32 = torch.int32
+
+
+def _heads(name, x, dev=None, dtype=None):
+    """A device tensor [T, heads, d] of a supported type whose tokens are dense rows, at any distance from each other: its
+    address, device, type code, sizes and the distance in elements."""
+    _require(isinstance(x, torch.Tensor) and x.is_cuda, "%s must be a device tensor" % name)
+    code = _DTYPE_CODE.get(x.dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, x.dtype))
+    _require(x.dim() == 3 and x.shape[2] > 0, "%s must be [T, heads, d]" % name)
+    T, H, d = x.shape
+    st = x.stride()
+    _require((st[2] == 1 or d == 1) and (st[1] == d or H <= 1) and (st[0] >= H * d or T <= 1),
+             "%s must have dense tokens, strides (any, d, 1)" % name)
+    if dev is not None:
+        _require(x.get_device() == dev and x.dtype is dtype, "%s must be %s on cuda:%d" % (name, dtype, dev))
+    _require(T <= _MOST and H * d <= _MOST, "%s has too many tokens or channels" % name)
+    return x.data_ptr(), x.get_device(), code, T, H, d, (st[0] if T > 1 else H * d)
+
+
+def _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis, interleaved):
+    """The arguments that kda_qknorm and its gradients share, up to the type: (device, code, T, Hq, Hk, d, arguments)."""
+    pq, dev, code, T, Hq, d, sq = _heads("q", q)
+    pk, Hk, sk = None, 0, 0
+    if k is not None:
+        pk, _, _, Tk, Hk, dk, sk = _heads("k", k, dev, q.dtype)
+        _require(Tk == T and dk == d, "k must have q's tokens and head size, got %s" % list(k.shape))
+    kind = KDA_NORMS.get(norm)
+    _require(kind is not None, "norm must be one of %s, got %r" % (", ".join(KDA_NORMS), norm))
+    ppos = pfreq = paxis = None
+    rot, axes = 0, 1
+    if inv_freq is not None or positions is not None:
+        _require(isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1 and isinstance(positions, torch.Tensor) and
+                 positions.dim() in (1, 2), "a rotation needs inv_freq [rot_dim / 2] and positions [T] or [axes, T]")
+        rot = 2 * inv_freq.shape[0]
+        _require(rot <= d, "inv_freq must have at most d / 2 entries")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        pfreq = _addr("inv_freq", inv_freq, dev, _F32, (rot // 2,))
+        ppos = _addr("positions", positions, dev, _I32, (T,) if positions.dim() == 1 else (axes, T))
+        paxis = _addr_if("pair_axis", pair_axis, dev, _I32, (rot // 2,))
+    else:
+        _require(pair_axis is None, "pair_axis goes with positions and inv_freq")
+    return dev, code, T, Hq, Hk, d, (pq, pk, sq, sk, _addr_if("q_weight", q_weight, dev, _F32, (d,)),
+                                     _addr_if("k_weight", k_weight, dev, _F32, (d,)), ppos, pfreq, paxis, T, Hq, Hk, d, rot,
+                                     axes, int(interleaved), kind, eps, q_scale, code)
+
+
+def kda_qknorm(q, k, q_out, k_out, q_weight=None, k_weight=None, norm: str = "l2", eps: float = 1e-6, q_scale: float = 1.0,
+               positions=None, inv_freq=None, pair_axis=None, interleaved: bool = False, stream=None) -> None:
+    """The norm of every head's query and key, with a rotation by position in
+    the same pass.  q: [T, Hq, d], k: [T, Hk, d] or None, of one type; their
+    tokens may be apart (columns of one projection's rows).  q_out, k_out: the
+    same shapes, contiguous.  norm: "l2", "rms" or "none"; q_weight, k_weight:
+    [d] fp32 or None; q_scale multiplies the queries.  A rotation turns the
+    first 2 * len(inv_freq) values of a head: positions [T] or [axes, T] int32,
+    inv_freq fp32 radians a position, pair_axis [len(inv_freq)] int32 the axis
+    of every pair (None: axis 0); pairs are halves apart, or neighbours if
+    interleaved."""
+    dev, _, T, Hq, Hk, d, form = _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis,
+                                          interleaved)
+    _call((_lib or load()).kda_qknorm, dev, stream, *form, _addr("q_out", q_out, dev, q.dtype, (T, Hq, d)),
+          None if k is None else _addr("k_out", k_out, dev, q.dtype, (T, Hk, d)))
+
+
+def kda_qknorm_backward_workspace_size(num_tokens: int, num_q_heads: int, num_k_heads: int, head_dim: int,
+                                       dtype=torch.bfloat16) -> int:
+    """Bytes of workspace kda_qknorm_backward needs for the weights' gradients."""
+    return int(load().kda_qknorm_backward_workspace_size(num_tokens, num_q_heads, num_k_heads, head_dim, _code(dtype)))
+
+
+def kda_qknorm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, norm: str = "l2", eps: float = 1e-6,
+                        q_scale: float = 1.0, positions=None, inv_freq=None, pair_axis=None, interleaved: bool = False,
+                        grads=None, workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of kda_qknorm given those of its outputs, dq_out [T, Hq, d] and
+    dk_out [T, Hk, d], contiguous, of q's type or fp32 (kda_backward's).
+    Returns a dict of dq and dk (q's type; dk None without k), dq_weight and
+    dk_weight (fp32; None without that weight); ``grads`` may supply the
+    tensors (dq and dk with tokens apart, such as columns of one array),
+    which otherwise belong to ``stream`` (record_stream them for use on
+    another)."""
+    dev, code, T, Hq, Hk, d, form = _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis,
+                                             interleaved)
+    dt = q.dtype
+    lib = _lib or load()
+    grads = _grads(grads, dev, {"dq": (dt, (T, Hq, d)), "dk": None if k is None else (dt, (T, Hk, d)),
+                                "dq_weight": None if q_weight is None else (_F32, (d,)),
+                                "dk_weight": None if k_weight is None else (_F32, (d,))}, stream)
+    _require(isinstance(dq_out, torch.Tensor), "dq_out must be a tensor")
+    gt = dq_out.dtype if dq_out.dtype is _F32 else dt
+    pdq, _, _, Tq, H, dd, sdq = _heads("grads['dq']", grads.get("dq"), dev, dt)
+    _require((Tq, H, dd) == (T, Hq, d), "grads['dq'] must have q's shape")
+    pdk, sdk = None, 0
+    if k is not None:
+        pdk, _, _, Tk, H, dd, sdk = _heads("grads['dk']", grads.get("dk"), dev, dt)
+        _require((Tk, H, dd) == (T, Hk, d), "grads['dk'] must have k's shape")
+    pqw = _addr_if("grads['dq_weight']", grads.get("dq_weight"), dev, _F32, (d,))
+    pkw = _addr_if("grads['dk_weight']", grads.get("dk_weight"), dev, _F32, (d,))
+    args = (*form, _DTYPE_CODE[gt], _addr("dq_out", dq_out, dev, gt, (T, Hq, d)),
+            None if k is None else _addr("dk_out", dk_out, dev, gt, (T, Hk, d)), sdq, sdk, pdq, pdk, pqw, pkw)
+    ws = pws = None
+    nbytes = 0
+    if pqw is not None or pkw is not None:
+        ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_qknorm_backward_workspace_size", T, Hq, Hk, d, code)
+    _call(lib.kda_qknorm_backward, dev, stream, *args, pws, nbytes)
+    return grads
+
+
+# ---------------------------------------------------------------- cached states and drafted tokens
+_BYTES = (torch.uint8, torch.int8, torch.float8_e4m3fn)   # types that codes may come in
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _format(name) -> int:
+    code = KDA_CACHE_FORMATS.get(name)
+    _require(code is not None, "format must be one of %s, got %r" % (", ".join(KDA_CACHE_FORMATS), name))
+    return code
+
+
+def _slots_of(name, t, dev, types, per_slot):
+    """The address of an array of slots with per_slot bytes each, and their number."""
+    _require(isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in types and t.is_contiguous(),
+             "%s must be a contiguous tensor of bytes on cuda:%d" % (name, dev))
+    shape = t.shape
+    _require(len(shape) >= 2 and shape[1:].numel() == per_slot and shape[0] <= _MOST,
+             "%s must be [slots, ...] with %d bytes a slot, got %s" % (name, per_slot, list(shape)))
+    return t.data_ptr(), shape[0]
+
+
+def _cache(cache, scales, dev, elems, fmt):
+    """Addresses of a cache's codes and scales for entries of `elems` values, and its slots."""
+    pc, S = _slots_of("cache", cache, dev, _BYTES, (elems + 1) // 2 if fmt == 2 else elems)
+    ps, n = _slots_of("scales", scales, dev, _SCALES, -(-elems // KDA_MX_BLOCK))
+    _require(n == S, "cache and scales must have the same slots")
+    return pc, ps, S
+
+
+def kda_cache_entry_bytes(entry_elems: int, format: str = "fp8") -> int:
+    """Bytes of the codes of an entry of entry_elems values."""
+    return int(load().kda_cache_entry_bytes(entry_elems, _format(format)))
+
+
+def kda_cache_store(src, slots, cache, scales, format: str = "fp8", stream=None) -> None:
+    """Write rows src [n, ...] (bf16 or fp32) into slots [n] (int32 on the
+    device; a negative one is not stored) of a cache: cache [slots, ...] uint8
+    (or the format's own type), kda_cache_entry_bytes(...) a slot; scales
+    [slots, ...] uint8 or float8_e8m0fnu, one for every 32 values.  format:
+    "fp8", "int8" or "fp4"."""
+    px, dev, code, _, n, elems = _rows("src", src)
+    fmt = _format(format)
+    pc, ps, S = _cache(cache, scales, dev, elems, fmt)
+    _call((_lib or load()).kda_cache_store, dev, stream, px, _addr("slots", slots, dev, _I32, (n,)), n, elems, code, fmt, S,
+          pc, ps)
+
+
+def kda_cache_load(cache, scales, slots, dst, format: str = "fp8", stream=None) -> None:
+    """Read slots [n] of a cache (as kda_cache_store has it) into rows dst
+    [n, ...], bf16 or fp32; rows of negative slots become zeros."""
+    px, dev, code, _, n, elems = _rows("dst", dst)
+    fmt = _format(format)
+    pc, ps, S = _cache(cache, scales, dev, elems, fmt)
+    _call((_lib or load()).kda_cache_load, dev, stream, pc, ps, _addr("slots", slots, dev, _I32, (n,)), n, elems, code, fmt, S,
+          px)
+
+
+def kda_decode_tokens_cached(q, k, v, g, beta, cu_seqlens, cache, scales, slots, format: str = "fp8", out=None,
+                             num_tokens=None, write: bool = True, stream=None) -> None:
+    """kda_decode_tokens on states that stay in a cache: cache [slots, H, dk, dv]
+    (dv / 2 bytes for "fp4") and scales [slots, H, dk, dv / 32], slots [N] int32
+    the place of every sequence's state (negative: begins from zeros and is not
+    kept).  write=False verifies a draft and leaves the cache as it is;
+    write=True replaces the states by those after the processed tokens."""
+    pq, dev, code, shape, T, _ = _rows("q", q)
+    _require(len(shape) == 3, "q must be [T, H, dk]")
+    H, dk = shape[1:]
+    pcu, N = _cu(cu_seqlens, dev)
+    _require(isinstance(v, torch.Tensor) and v.dim() == 3, "v must be [T, H, dv]")
+    dv, fmt, dt = v.shape[2], _format(format), q.dtype
+    pc, ps, S = _cache(cache, scales, dev, H * dk * dv, fmt)
+    _call((_lib or load()).kda_decode_tokens_cached, dev, stream, pq, _addr("k", k, dev, dt, shape),
+          _addr("v", v, dev, dt, (T, H, dv)), _addr("g", g, dev, _F32, shape), _addr("beta", beta, dev, _F32, (T, H)), pcu,
+          _addr_if("num_tokens", num_tokens, dev, _I32, (N,)), pc, ps, _addr("slots", slots, dev, _I32, (N,)), int(write), S,
+          N, T, H, dk, dv, code, fmt, _addr_if("out", out, dev, dt, (T, H, dv)))
+
+
+def kda_verify_drafts_workspace_size(num_seqs: int, vocab: int, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace kda_verify_drafts needs."""
+    return int(load().kda_verify_drafts_workspace_size(num_seqs, vocab, _code(dtype)))
+
+
+def kda_verify_drafts(target_probs, draft_probs, tokens, cu_seqlens, accept_rand, sample_rand, num_tokens, next_token,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Which drafted tokens the target accepts, and the token after them, from
+    given random numbers.  target_probs: [T, vocab], row i the distribution
+    after token row i; draft_probs: [T, vocab], row i what token row i was
+    drawn from, or None (picked without one); tokens: [T] int32, a sequence's
+    last token and its drafts; accept_rand: [T] and sample_rand: [N] fp32 in
+    [0, 1).  Written: num_tokens [N] int32, 1 + the drafts accepted (what
+    kda_decode_tokens and kda_decode_tokens_cached take to commit them), and
+    next_token [N] int32."""
+    pt, dev, code, shape, T, V = _rows("target_probs", target_probs)
+    _require(len(shape) == 2, "target_probs must be [T, vocab]")
+    pcu, N = _cu(cu_seqlens, dev)
+    lib = _lib or load()
+    args = (pt, _addr_if("draft_probs", draft_probs, dev, target_probs.dtype, shape), _addr("tokens", tokens, dev, _I32, (T,)),
+            pcu, _addr("accept_rand", accept_rand, dev, _F32, (T,)), _addr("sample_rand", sample_rand, dev, _F32, (N,)), N, T, V,
+            code, _addr("num_tokens", num_tokens, dev, _I32, (N,)), _addr("next_token", next_token, dev, _I32, (N,)))
+    ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_verify_drafts_workspace_size", N, V, code)
+    _call(lib.kda_verify_drafts, dev, stream, *args, pws, nbytes)

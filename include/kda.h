@@ -573,6 +573,214 @@ kda_status kda_rmsnorm_backward(const void *x, const float *weight, const void *
                                 float *dweight, void *workspace, size_t workspace_bytes,
                                 kda_stream_t stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * What stands before the recurrence and around its states when they are cached
+ * and tokens are drafted: the norm and rotation of queries and keys, states held
+ * in 8 or 4 bits, decoding on states that stay there, and the verification of
+ * drafted tokens.  Conventions as for the layer operators (element alignment,
+ * fixed order of every sum, refused overlaps, launches of fewer than 2^32
+ * threads).
+ */
+
+/*
+ * kda_qknorm -- the norm of every head's query and key, with a rotation by
+ * position in the same pass.  kda_prefill and kda_decode_* take q and k as they
+ * come out of it (unit keys, scaled queries).  For a head x of head_dim values:
+ *
+ *     n   = x / sqrt(sum(x^2) + eps)     (KDA_NORM_L2)
+ *           x / sqrt(mean(x^2) + eps)    (KDA_NORM_RMS)
+ *           x                            (KDA_NORM_NONE)
+ *     y   = scale * weight * n           (scale: q_scale for queries, 1 for keys)
+ *     out = y, with its first rot_dim values turned in pairs (a, b):
+ *           a cos - b sin,  b cos + a sin,  of the pair's angle at the token:
+ *           positions[pair_axis[j]][token] * inv_freq[j]  for pair j
+ *
+ *   q             [num_tokens, num_q_heads, head_dim] dtype, tokens q_stride
+ *                 elements apart (num_q_heads * head_dim to 2^29): q and k may be
+ *                 columns of one projection's rows.  Without tokens or heads it
+ *                 may be NULL.
+ *   k             [num_tokens, num_k_heads, head_dim] dtype, likewise; any number
+ *                 of heads, zero too
+ *   q_weight, k_weight [head_dim]                fp32, or NULL for ones
+ *   positions     [num_axes, num_tokens]         int32, DEVICE; any values
+ *   inv_freq      [rot_dim / 2]                  fp32, DEVICE: radians a position.
+ *                 An angle is formed in fp64, so that far positions keep it.
+ *   pair_axis     [rot_dim / 2]                  int32, DEVICE: the axis that
+ *                 turns a pair (time, height, width, in any order; entries
+ *                 outside [0, num_axes) are clamped), or NULL: all by axis 0
+ *                 These three are not read where rot_dim = 0.
+ *   head_dim      1 to KDA_QKNORM_MAX_DIM (KDA_ERR_UNSUPPORTED above)
+ *   rot_dim       even, 0 to head_dim
+ *   interleaved   pairs are (2j, 2j + 1) if not 0, else (j, rot_dim / 2 + j)
+ *   eps           finite, >= 0.  A head of zeros with eps = 0 is NaN.
+ *   q_scale       finite
+ *   q_out         [num_tokens, num_q_heads, head_dim] dtype, dense; may equal q
+ *                 where that is dense
+ *   k_out         [num_tokens, num_k_heads, head_dim] dtype, dense; likewise
+ * Sums of squares are formed in fp32: a head's sum(x^2) has to stay in its range.
+ */
+#define KDA_QKNORM_MAX_DIM 512
+
+typedef enum { KDA_NORM_NONE = 0, KDA_NORM_L2 = 1, KDA_NORM_RMS = 2 } kda_norm;
+
+kda_status kda_qknorm(const void *q, const void *k, int64_t q_stride, int64_t k_stride, const float *q_weight,
+                      const float *k_weight, const int32_t *positions, const float *inv_freq,
+                      const int32_t *pair_axis, int32_t num_tokens, int32_t num_q_heads, int32_t num_k_heads,
+                      int32_t head_dim, int32_t rot_dim, int32_t num_axes, int32_t interleaved, kda_norm norm,
+                      float eps, float q_scale, kda_dtype dtype, void *q_out, void *k_out, kda_stream_t stream);
+
+/*
+ * kda_qknorm_backward -- gradients of kda_qknorm:
+ *   q, k ... dtype: as there
+ *   dq_out, dk_out  gradients of q_out and k_out, dense, in grad_dtype: `dtype`,
+ *                 or KDA_F32 whatever that is (kda_backward's gradients)
+ *   dq, dk        as q and k, dtype, tokens dq_stride and dk_stride elements
+ *                 apart; the elements between the rows stay as they were.  dq may
+ *                 equal q at q's stride, dk may equal k at k's, and both may be
+ *                 columns of the same rows.
+ *   dq_weight, dk_weight [head_dim]              fp32, or NULL (not written): sums
+ *                 over all tokens and heads; only with that weight
+ *   workspace     at least kda_qknorm_backward_workspace_size(...) bytes, 4-byte
+ *                 aligned (partial sums of the weights' gradients); NULL allowed
+ *                 where neither is written
+ */
+size_t kda_qknorm_backward_workspace_size(int32_t num_tokens, int32_t num_q_heads, int32_t num_k_heads,
+                                          int32_t head_dim, kda_dtype dtype);
+
+kda_status kda_qknorm_backward(const void *q, const void *k, int64_t q_stride, int64_t k_stride,
+                               const float *q_weight, const float *k_weight, const int32_t *positions,
+                               const float *inv_freq, const int32_t *pair_axis, int32_t num_tokens,
+                               int32_t num_q_heads, int32_t num_k_heads, int32_t head_dim, int32_t rot_dim,
+                               int32_t num_axes, int32_t interleaved, kda_norm norm, float eps, float q_scale,
+                               kda_dtype dtype, kda_dtype grad_dtype, const void *dq_out, const void *dk_out,
+                               int64_t dq_stride, int64_t dk_stride, void *dq, void *dk, float *dq_weight,
+                               float *dk_weight, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * A cache of states in 8 or 4 bits.  It has num_slots slots; a slot holds an entry
+ * of entry_elems values (a sequence's recurrent states, [num_heads, dk, dv]; its
+ * convolution's inputs, [width - 1, channels]; any other array) in blocks of
+ * KDA_MX_BLOCK consecutive values that share a scale:
+ *
+ *     value = number(code) * 2^(scale - 127)
+ *
+ *   KDA_CACHE_FP8   code: one byte, OCP e4m3; largest number 448
+ *   KDA_CACHE_INT8  code: one byte, two's complement, number = code / 64 (OCP
+ *                   MXINT8); largest number 127/64, -128 is not written
+ *   KDA_CACHE_FP4   code: four bits, OCP e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
+ *                   sign), the first of two in the low half; largest number 6
+ *   cache           [num_slots, kda_cache_entry_bytes(entry_elems, format)]
+ *   scales          [num_slots, ceil(entry_elems / KDA_MX_BLOCK)] one byte each
+ *                   (OCP e8m0): the smallest power of two with max|x| / scale at
+ *                   most the largest number (at least 2^-127 and at most 2^127; 1
+ *                   for a block of zeros; 255, which is NaN, for a block that holds
+ *                   an infinity or a NaN, its codes zeros)
+ * A code is the nearest number, ties to the even code: scaling by a power of two
+ * is exact, so there is one rounding.  (KDA_CACHE_INT8: magnitudes above 127/64
+ * 2^127 become that.)
+ */
+typedef enum { KDA_CACHE_FP8 = 0, KDA_CACHE_INT8 = 1, KDA_CACHE_FP4 = 2 } kda_cache_format;
+
+/* Bytes of one entry's codes; 0 for negative sizes and unknown formats. */
+size_t kda_cache_entry_bytes(int32_t entry_elems, kda_cache_format format);
+
+/*
+ * kda_cache_store -- write entries into the cache:
+ *   src           [num_entries, entry_elems]     dtype
+ *   slots         [num_entries]                  int32, DEVICE: entry i goes to
+ *                 slot slots[i]; one outside [0, num_slots) is not stored (-1 in
+ *                 the place of a snapshot that is not kept, or of a padded row).
+ *                 No slot is named twice: what such a slot holds afterwards is
+ *                 unspecified (nothing else is touched).  With KDA_VALIDATE=1 in
+ *                 the environment the call looks, synchronising `stream`, and
+ *                 returns KDA_ERR_INVALID_ARG.
+ * Other slots stay as they were.
+ */
+kda_status kda_cache_store(const void *src, const int32_t *slots, int32_t num_entries, int32_t entry_elems,
+                           kda_dtype dtype, kda_cache_format format, int32_t num_slots, uint8_t *cache,
+                           uint8_t *scales, kda_stream_t stream);
+
+/*
+ * kda_cache_load -- read entries back:
+ *   dst           [num_entries, entry_elems]     dtype: row i receives the values of
+ *                 slot slots[i], zeros where that is outside [0, num_slots) (a
+ *                 sequence without a cached state).  Slots may be named repeatedly.
+ */
+kda_status kda_cache_load(const uint8_t *cache, const uint8_t *scales, const int32_t *slots, int32_t num_entries,
+                          int32_t entry_elems, kda_dtype dtype, kda_cache_format format, int32_t num_slots,
+                          void *dst, kda_stream_t stream);
+
+/*
+ * kda_decode_tokens_cached -- kda_decode_tokens on states that stay in a cache:
+ * each is read from its slot in 8 or 4 bits, moved on in fp32 by its sequence's
+ * tokens, and, if `write` is not 0, rounded once and written back.
+ *   q, k, v, g, beta, cu_seqlens, num_tokens, out: as kda_decode_tokens
+ *   cache         [num_slots, num_heads, dk, dv] codes of `format`
+ *   scales        [num_slots, num_heads, dk, dv / KDA_MX_BLOCK] one byte each
+ *   slots         [num_seqs]                     int32, DEVICE: the slot of every
+ *                 sequence's state.  A sequence whose slot is outside
+ *                 [0, num_slots) begins from zeros, and its state is not kept.
+ *                 Where the call writes, no slot is named twice (as in
+ *                 kda_cache_store; both sequences' outputs are unspecified then,
+ *                 too); where it does not, sequences may share one.
+ *   write         0: the cache is only read (a draft is verified); else the states
+ *                 after the processed tokens replace those of the slots.  A
+ *                 sequence without processed tokens keeps its slot's bytes.
+ *   out           may be NULL where the call writes
+ */
+kda_status kda_decode_tokens_cached(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                    const int32_t *cu_seqlens, const int32_t *num_tokens, uint8_t *cache,
+                                    uint8_t *scales, const int32_t *slots, int32_t write, int32_t num_slots,
+                                    int32_t num_seqs, int32_t total_tokens, int32_t num_heads, int32_t dk,
+                                    int32_t dv, kda_dtype dtype, kda_cache_format format, void *out,
+                                    kda_stream_t stream);
+
+/*
+ * kda_verify_drafts -- which drafted tokens the target accepts, and the token after
+ * them, from given random numbers.  A sequence's tokens [cu[n], cu[n+1]) are the
+ * last one it has already and its drafts; the target has run over all of them.
+ * For its drafts in order, token row i is accepted if
+ *
+ *     accept_rand[i] * draft_probs[i][x] < target_probs[i - 1][x],   x = tokens[i],
+ *
+ * up to the first that is not.  The next token is drawn from the weights w:
+ * max(target_probs[i - 1] - draft_probs[i], 0) if token row i was rejected, else
+ * the target's last row.  It is the first x with w[x] > 0 and
+ *
+ *     w[0] + ... + w[x] > sample_rand[n] * (w[0] + ... + w[vocab - 1])
+ *
+ * (the last x with w[x] > 0 if none is; where rejected weights are all zero, the
+ * target's row itself).  So the next token is distributed as the target's own.
+ * Sums and products are formed in fp64; probabilities need not sum to one, those
+ * below zero and NaN count as zero.
+ *
+ *   target_probs  [total_tokens, vocab]          dtype: row i, after token row i
+ *   draft_probs   [total_tokens, vocab]          dtype: row i, the distribution that
+ *                 token row i was drawn from (the row of a sequence's first token
+ *                 is not read), or NULL: tokens picked without one, for which
+ *                 draft_probs[i][tokens[i]] stands for 1 and the others for 0
+ *   tokens        [total_tokens]                 int32; a draft outside [0, vocab)
+ *                 is rejected (with draft_probs[i] as its distribution)
+ *   cu_seqlens    [num_seqs + 1]                 int32, DEVICE (as kda_prefill)
+ *   accept_rand   [total_tokens]                 fp32 in [0, 1)
+ *   sample_rand   [num_seqs]                     fp32 in [0, 1)
+ *   num_tokens    [num_seqs]                     int32: 1 + the drafts accepted, 0
+ *                 of an empty sequence: what kda_decode_tokens and
+ *                 kda_decode_tokens_cached take to commit them
+ *   next_token    [num_seqs]                     int32; -1 of an empty sequence, or
+ *                 where every weight is zero
+ *   workspace     at least kda_verify_drafts_workspace_size(...) bytes, 8-byte
+ *                 aligned, contents ignored on entry
+ */
+size_t kda_verify_drafts_workspace_size(int32_t num_seqs, int32_t vocab, kda_dtype dtype);
+
+kda_status kda_verify_drafts(const void *target_probs, const void *draft_probs, const int32_t *tokens,
+                             const int32_t *cu_seqlens, const float *accept_rand, const float *sample_rand,
+                             int32_t num_seqs, int32_t total_tokens, int32_t vocab, kda_dtype dtype,
+                             int32_t *num_tokens, int32_t *next_token, void *workspace, size_t workspace_bytes,
+                             kda_stream_t stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *kda_status_string(kda_status status);
 

@@ -1,0 +1,387 @@
+"""The cache of states in 8 and 4 bits: kda_cache_store and kda_cache_load bit for
+bit against the definition, and kda_decode_tokens_cached against the recurrence
+in fp64 from the values that the codes stand for (tests/cache_ref.py)."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as C
+from layer_ref import close
+from gated_delta_rule_40_amd import libkda as K
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+FORMATS = ["fp8", "int8", "fp4"]
+D = 128
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    K.load()
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def new_cache(slots, elems, fmt, fill=0xA5):
+    per = (elems + 1) // 2 if fmt == "fp4" else elems
+    return (torch.full((slots, per), fill, dtype=torch.uint8, device="cuda"),
+            torch.full((slots, -(-elems // 32)), fill, dtype=torch.uint8, device="cuda"))
+
+
+def check_store_load(src, fmt, slots, num_slots):
+    """src [n, elems] on the device, slots a list."""
+    n, elems = src.shape
+    cache, scales = new_cache(num_slots, elems, fmt)
+    K.kda_cache_store(src, torch.tensor(slots, dtype=torch.int32, device="cuda"), cache, scales, fmt)
+    code, sc = C.quantise(host(src), fmt)
+    packed = C.pack(code, fmt)
+    want_c, want_s = np.full(tuple(cache.shape), 0xA5, np.uint8), np.full(tuple(scales.shape), 0xA5, np.uint8)
+    for i, s in enumerate(slots):
+        if 0 <= s < num_slots:
+            want_c[s], want_s[s] = packed[i], sc[i]
+    got_c, got_s = cache.cpu().numpy(), scales.cpu().numpy()
+    assert np.array_equal(got_s, want_s), np.argwhere(got_s != want_s)[:5]
+    if fmt == "int8":
+        assert np.array_equal(got_c, want_c), np.argwhere(got_c != want_c)[:5]
+    else:                                                  # (a negative value that rounds to zero is -0)
+        bad = np.argwhere(got_c != want_c)
+        assert not len(bad), [(b, got_c[tuple(b)], want_c[tuple(b)]) for b in bad[:5]]
+    back = [s for s in slots] + [slots[0], -1, num_slots]
+    for dt in (torch.float32, torch.bfloat16):
+        dst = torch.full((len(back), elems), 9.0, dtype=dt, device="cuda")
+        K.kda_cache_load(cache, scales, torch.tensor(back, dtype=torch.int32, device="cuda"), dst, fmt)
+        for i, s in enumerate(back):
+            want = np.zeros(elems)
+            if 0 <= s < num_slots:
+                want = C.dequantise(want_c[s:s + 1], want_s[s:s + 1], fmt, elems)[0]
+            with np.errstate(over="ignore"):
+                want = torch.tensor(want.astype(np.float32)).to(dt).double().numpy()
+            assert np.array_equal(host(dst[i]), want, equal_nan=True), (i, s, dt)
+
+
+SHAPES = [(1, 1), (3, 5), (2, 31), (4, 32), (3, 33), (9, 100), (5, 1024), (2, 4097), (70, 64), (300, 3), (3, 8200), (2, D * D)]
+
+
+@pytest.mark.parametrize("n,elems", SHAPES, ids=str)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_store_and_load(n, elems, fmt, dtype):
+    gen = torch.Generator().manual_seed(n + elems)
+    x = torch.randn(n, elems, generator=gen) * torch.exp(6 * torch.randn(n, 1, generator=gen))
+    slots = torch.randperm(n + 3, generator=gen)[:n].tolist()
+    if n > 2:
+        slots[1], slots[2] = -1, n + 3
+    check_store_load(x.to(DT[dtype]).cuda(), fmt, slots, n + 3)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_every_tie_and_end_of_a_scale(fmt):
+    """Values on, next to and between all numbers of the format, at scales from the smallest to the largest."""
+    steps = C.NUMBERS[fmt]
+    mids = (steps[1:] + steps[:-1]) / 2
+    v = np.concatenate((steps, mids)).astype(np.float32)
+    v = np.concatenate((v, np.nextafter(v, np.float32(1e9)), np.nextafter(v, np.float32(-1e9))))
+    v = np.concatenate((v, -v))
+    v = v[np.abs(v) <= steps[-1]]
+    v = np.pad(v, (0, -len(v) % 31)).reshape(-1, 31)
+    blocks = np.concatenate((np.full((len(v), 1), steps[-1], np.float32), v.astype(np.float32)), 1).reshape(1, -1)
+    scaled = np.concatenate([blocks * np.float32(2.0) ** np.float32(e) for e in (0, -3, 7, 60, -90, -117)])
+    check_store_load(torch.tensor(scaled).cuda(), fmt, list(range(len(scaled))), len(scaled))
+    # a block's largest on, below and above the ends of its scale
+    top = np.float32(steps[-1]) * np.float32(2.0) ** np.arange(-120, 100, 7, dtype=np.float32)
+    ends = np.stack((top, np.nextafter(top, np.float32(0)), np.nextafter(top, np.float32(np.inf)), top * np.float32(0.5)))
+    x = np.zeros((ends.size, 64), np.float32)
+    x[:, 3], x[:, 35], x[:, 40] = ends.ravel(), -ends.ravel() / 3, ends.ravel()
+    check_store_load(torch.tensor(x).cuda(), fmt, list(range(len(x))), len(x))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_zeros_infinities_nan_and_the_smallest(fmt, dtype):
+    x = torch.randn(1, 12 * 32)
+    b = x.view(12, 32)
+    b[0], b[1, 4], b[2, 31], b[3, 0] = 0.0, float("inf"), -float("inf"), float("nan")
+    b[4] *= 1e-38
+    b[5] = 0.0
+    b[5, 7] = 1e-45 if dtype == "fp32" else 1e-40
+    b[6] = 3.3e38
+    b[7] = -3.3e38
+    b[8] = 2.0 ** -127
+    b[9] = 2.0 ** -126 * 0.99
+    b[10, 3] = 3.4e38
+    b[11] = -0.0
+    check_store_load(x.to(DT[dtype]).cuda(), fmt, [0], 1)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_off_boundaries(fmt):
+    x = torch.randn(5, 333).cuda()
+    slots = torch.tensor([4, 0, 3, 1, 2], dtype=torch.int32, device="cuda")
+    cache, scales = new_cache(5, 333, fmt)
+    K.kda_cache_store(x, slots, cache, scales, fmt)
+    for sh in (1, 2, 3):
+        y = torch.empty(5 * 333 + 3, device="cuda")[sh:sh + 5 * 333].view(5, 333).copy_(x)
+        c2 = torch.empty(cache.numel() + 3, dtype=torch.uint8, device="cuda")[sh:sh + cache.numel()].view(cache.shape)
+        s2 = torch.empty(scales.numel() + 3, dtype=torch.uint8, device="cuda")[sh:sh + scales.numel()].view(scales.shape)
+        K.kda_cache_store(y, slots, c2, s2, fmt)
+        assert torch.equal(c2, cache) and torch.equal(s2, scales)
+        z = torch.empty(5 * 333 + 3, dtype=torch.bfloat16, device="cuda")[sh:sh + 5 * 333].view(5, 333)
+        w = torch.empty(5, 333, dtype=torch.bfloat16, device="cuda")
+        K.kda_cache_load(c2, s2, slots, z, fmt)
+        K.kda_cache_load(cache, scales, slots, w, fmt)
+        assert torch.equal(z, w)
+
+
+def test_types_that_codes_come_in():
+    x = torch.randn(2, 64).cuda()
+    slots = torch.arange(2, dtype=torch.int32, device="cuda")
+    cache, scales = new_cache(2, 64, "fp8")
+    K.kda_cache_store(x, slots, cache.view(torch.float8_e4m3fn), scales.view(torch.float8_e8m0fnu), "fp8")
+    value = cache.view(torch.float8_e4m3fn).float() * scales.view(torch.float8_e8m0fnu).float().repeat_interleave(32, 1)
+    back = torch.empty_like(x)
+    K.kda_cache_load(cache, scales, slots, back, "fp8")
+    assert torch.equal(back, value)
+
+
+# ------------------------------------------------------------------ decoding on it
+def make(lens, H, fmt, dtype="bf16", seed=0, extra=3, pad=0):
+    gen = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=gen)                       # noqa: E731
+    N, T = len(lens), sum(lens) + pad
+    k = rnd(T, H, D)
+    p = dict(q=rnd(T, H, D) * D ** -0.5, k=k / k.norm(dim=-1, keepdim=True), v=rnd(T, H, D))
+    p = {n: t.to(DT[dtype]).cuda() for n, t in p.items()}
+    p["g"] = (-5 / 16 * torch.rand(T, H, D, generator=gen)).cuda()
+    p["beta"] = torch.sigmoid(rnd(T, H)).cuda()
+    p["cu"] = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32).cuda()
+    S = N + extra
+    state = 0.1 * rnd(S, H * D * D)
+    cache, scales = new_cache(S, H * D * D, fmt)
+    K.kda_cache_store(state.cuda(), torch.arange(S, dtype=torch.int32, device="cuda"), cache, scales, fmt)
+    p["cache"], p["scales"] = cache.view(S, H, D, -1), scales.view(S, H, D, 4)
+    p["slots"] = torch.randperm(S, generator=gen)[:N].to(torch.int32).cuda()
+    return p
+
+
+def decode(p, fmt, write, counts=None, out=True):
+    o = torch.full(p["v"].shape, 7.0, dtype=p["v"].dtype, device="cuda") if out else None
+    cache, scales = p["cache"].clone(), p["scales"].clone()
+    K.kda_decode_tokens_cached(p["q"], p["k"], p["v"], p["g"], p["beta"], p["cu"], cache, scales, p["slots"], fmt, out=o,
+                               num_tokens=None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda(), write=write)
+    return o, cache, scales
+
+
+def check_codes(value, scale, S, E, fmt, what):
+    """Values [128, 128] and scale bytes [128, 4] written for a state within E of S: the scale's rule, half a step, or the
+    end of the format."""
+    blocks, bound = np.abs(S).reshape(D, 4, 32).max(-1), 1.01 * E.reshape(D, 4, 32).max(-1)
+    rules = [C.scale_bytes(np.maximum(blocks + x, 0), fmt) for x in (-bound, 0, bound)]
+    assert np.all((scale >= rules[0]) & (scale <= rules[2])), what
+    s = np.repeat(2.0 ** (scale.astype(float) - 127), 32, 1)
+    steps = C.NUMBERS[fmt]
+    number = np.abs(value / s)
+    i = np.searchsorted(steps, number)
+    assert np.array_equal(steps[i], number), what
+    gap = np.maximum(steps[np.minimum(i + 1, len(steps) - 1)] - number, number - steps[np.maximum(i - 1, 0)])
+    assert np.all(np.abs(value - S) <= gap / 2 * s + 1.01 * E + 1e-37), what
+
+
+def check_decode(p, fmt, write, counts=None, out=True):
+    o, cache, scales = decode(p, fmt, write, counts, out)
+    N, H, dt = len(p["slots"]), p["q"].shape[1], {v: k for k, v in DT.items()}[p["q"].dtype]
+    cu, slots = p["cu"].tolist(), p["slots"].tolist()
+    h = {n: host(p[n]) for n in ("q", "k", "v", "g", "beta")}
+    before, bsc = p["cache"].cpu().numpy(), p["scales"].cpu().numpy()
+    after, asc = cache.cpu().numpy(), scales.cpu().numpy()
+    rows, touched = np.zeros(p["q"].shape[0], bool), np.zeros(len(before), bool)
+    for n in range(N):
+        length = cu[n + 1] - cu[n] if counts is None else max(0, min(counts[n], cu[n + 1] - cu[n]))
+        at, kept = slice(cu[n], cu[n] + length), 0 <= slots[n] < len(before)
+        rows[at] = True
+        for hd in range(H):
+            S = np.zeros((D, D))
+            if kept:
+                S = C.dequantise(before[slots[n], hd], bsc[slots[n], hd], fmt, D)
+            ro, S, eo, E = C.decode(h["q"][at, hd], h["k"][at, hd], h["v"][at, hd], h["g"][at, hd], h["beta"][at, hd], S)
+            if out:
+                close(host(o[at, hd]), ro, eo, dt, "out %d %d" % (n, hd))
+            if write and kept and length:
+                touched[slots[n]] = True
+                value = C.dequantise(after[slots[n], hd], asc[slots[n], hd], fmt, D)
+                check_codes(value, asc[slots[n], hd], S, E, fmt, (n, hd))
+    if out:
+        assert torch.all(o[torch.tensor(~rows).cuda()] == 7.0)             # rows of no processed token
+    assert np.array_equal(before[~touched], after[~touched]) and np.array_equal(bsc[~touched], asc[~touched])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,H", [([1], 1), ([1, 1, 1], 5), ([5, 0, 2, 1, 9], 3)], ids=str)
+def test_decode_on_the_cache(fmt, dtype, lens, H):
+    p = make(lens, H, fmt, dtype, pad=2)
+    check_decode(p, fmt, write=False)
+    check_decode(p, fmt, write=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_accepted_prefixes_are_committed(fmt):
+    p = make([4, 5, 3, 2, 0, 3], 2, fmt, "bf16")
+    p["slots"][3], p["slots"][4] = -1, 999
+    check_decode(p, fmt, write=True, counts=[2, 9, 0, 1, 5, -3], out=False)
+    check_decode(p, fmt, write=True, counts=[2, 9, 0, 1, 5, -3])
+    check_decode(p, fmt, write=False, counts=[1, 5, 3, 2, 0, 2])
+
+
+def test_readers_may_share_a_slot():
+    p = make([2, 3, 2], 2, "int8")
+    p["slots"][:] = 1
+    check_decode(p, "int8", write=False)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_several_tokens_are_the_same_tokens_one_by_one(fmt):
+    """Outputs of the first token do not go by what follows; a state is rounded once a call."""
+    p = make([3, 3], 2, fmt, "fp32")
+    o, _, _ = decode(p, fmt, write=False)
+    o1, _, _ = decode(p, fmt, write=False, counts=[1, 1])
+    first = [0, 3]
+    assert torch.equal(o[first], o1[first])
+    again, c, s = decode(p, fmt, write=True)
+    assert torch.equal(again, o)
+    o2, c2, s2 = decode(p, fmt, write=True)
+    assert torch.equal(o2, o) and torch.equal(c, c2) and torch.equal(s, s2)   # the same bits again
+
+
+def test_decay_to_nothing_and_blocks_without_a_number():
+    p = make([2, 2], 1, "fp8", "fp32")
+    p["g"][0:2] = -200.0
+    check_decode(p, "fp8", write=True)
+    p["scales"][p["slots"][1], 0, 5, 2] = 255                                # a block that held an infinity
+    o, cache, scales = decode(p, "fp8", write=True)
+    bad = torch.isnan(o[2:, 0]).cpu()
+    assert bad[:, 64:96].all() and not bad[:, :64].any() and not bad[:, 96:].any() and not torch.isnan(o[:2]).any()
+    sc = scales[p["slots"][1], 0].cpu()
+    assert torch.all(sc[:, 2] == 255) and not torch.any(sc[:, [0, 1, 3]] == 255)
+
+
+def test_against_kda_decode_tokens():
+    """From the same values, the uncached call's outputs: both within their bounds of the recurrence."""
+    p = make([4, 1, 3], 4, "int8", "fp32")
+    state = torch.empty(3, 4, D, D, device="cuda")
+    K.kda_cache_load(p["cache"], p["scales"], p["slots"], state, "int8")
+    o, _, _ = decode(p, "int8", write=False)
+    o2 = torch.empty_like(o)
+    K.kda_decode_tokens(p["q"], p["k"], p["v"], p["g"], p["beta"], p["cu"], state, None, o2)
+    h = {n: host(p[n]) for n in ("q", "k", "v", "g", "beta")}
+    for n, (a, b) in enumerate(((0, 4), (4, 5), (5, 8))):
+        for hd in range(4):
+            ro, _, eo, _ = C.decode(*(h[x][a:b, hd] for x in ("q", "k", "v", "g", "beta")), host(state[n, hd]))
+            close(host(o[a:b, hd]), host(o2[a:b, hd]), 2 * eo, "fp32", "cached against uncached")
+
+
+def test_bad_cu_seqlens_stay_in_bounds():
+    p = make([2, 2, 2], 2, "fp8")
+    p["cu"] = torch.tensor([-5, 4, 1, 99], dtype=torch.int32, device="cuda")
+    decode(p, "fp8", write=True)
+    torch.cuda.synchronize()
+
+
+def test_offsets_beyond_32_bits():
+    """Slots whose entries begin beyond 2^31 bytes."""
+    H, S = 96, 1500
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 3 GB")
+    cache = torch.empty(S, H, D, D, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(S, H, D, 4, dtype=torch.uint8, device="cuda")
+    small = make([1, 2], H, "fp8", extra=0)
+    slots = torch.tensor([S - 1, S - 2], dtype=torch.int32, device="cuda")
+    for i in range(2):
+        cache[slots[i]], scales[slots[i]] = small["cache"][small["slots"][i]], small["scales"][small["slots"][i]]
+    want_o, want_c, want_s = decode(small, "fp8", write=True)
+    o = torch.full_like(want_o, 7.0)
+    K.kda_decode_tokens_cached(small["q"], small["k"], small["v"], small["g"], small["beta"], small["cu"], cache, scales, slots,
+                               "fp8", out=o)
+    assert torch.equal(o, want_o)
+    for i in range(2):
+        assert torch.equal(cache[slots[i]], want_c[small["slots"][i]]) and torch.equal(scales[slots[i]], want_s[small["slots"][i]])
+    state = torch.empty(2, H, D, D, device="cuda")
+    K.kda_cache_load(cache, scales, slots, state, "fp8")
+    K.kda_cache_store(state, slots, cache, scales, "fp8")
+    for i in range(2):                                       # values that came from codes give values, if not codes, again
+        value = torch.empty(1, H, D, D, device="cuda")
+        K.kda_cache_load(cache, scales, slots[i:i + 1], value, "fp8")
+        assert torch.equal(value[0], state[i])
+
+
+def test_binding_refusals():
+    p = make([1, 1], 2, "fp8")
+    args = [p[n] for n in ("q", "k", "v", "g", "beta", "cu", "cache", "scales", "slots")]
+    out = torch.empty_like(p["v"])
+    for i, bad in ((1, p["k"].float()), (2, p["v"][:, :1]), (3, p["g"].bfloat16()), (4, p["beta"][:1]), (5, p["cu"].long()),
+                   (6, p["cache"][..., :64]), (6, p["cache"].float()), (7, p["scales"][:2]), (7, p["scales"][..., :3]),
+                   (8, p["slots"].long()), (8, p["slots"][:1])):
+        a = list(args)
+        a[i] = bad
+        with pytest.raises(ValueError):
+            K.kda_decode_tokens_cached(*a, "fp8", out=out)
+    with pytest.raises(ValueError):
+        K.kda_decode_tokens_cached(*args, "fp4", out=out)          # codes of another format's size
+    with pytest.raises(ValueError):
+        K.kda_decode_tokens_cached(*args, "bf16", out=out)
+    with pytest.raises(K.KdaError):
+        K.kda_decode_tokens_cached(*args, "fp8", write=False)      # nothing to give
+    x, slots = torch.zeros(2, 64, device="cuda"), p["slots"]
+    cache, scales = new_cache(3, 64, "fp8")
+    for bad in ((x, slots[:1], cache, scales), (x, slots, cache[:, :32], scales), (x, slots, cache, scales[:2]),
+                (x[:, ::2], slots, cache, scales), (x, slots, cache, scales.int())):
+        with pytest.raises(ValueError):
+            K.kda_cache_store(*bad)
+        with pytest.raises(ValueError):
+            K.kda_cache_load(bad[2], bad[3], bad[1], bad[0])
+
+
+VALIDATED = """
+import torch, sys
+sys.path.insert(0, %r)
+from gated_delta_rule_40_amd import libkda as K
+x = torch.randn(3, 64, device="cuda")
+cache, scales = torch.zeros(4, 64, dtype=torch.uint8, device="cuda"), torch.zeros(4, 2, dtype=torch.uint8, device="cuda")
+i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+K.kda_cache_store(x, i(3, -1, -1), cache, scales)
+K.kda_cache_store(x, i(3, 9, 9), cache, scales)
+try:
+    K.kda_cache_store(x, i(3, 0, 3), cache, scales)
+    raise SystemExit("a slot named twice was stored")
+except K.KdaError as e:
+    assert e.status == K.KDA_ERR_INVALID_ARG
+q = torch.randn(2, 1, 128, device="cuda")
+g, beta = -torch.rand(2, 1, 128, device="cuda"), torch.rand(2, 1, device="cuda")
+cache = torch.zeros(4, 1, 128, 128, dtype=torch.uint8, device="cuda")
+scales = torch.full((4, 1, 128, 4), 127, dtype=torch.uint8, device="cuda")
+K.kda_decode_tokens_cached(q, q, q, g, beta, i(0, 1, 2), cache, scales, i(1, 1), out=torch.empty_like(q), write=False)
+for cu, slots in ((i(0, 1, 2), i(1, 1)), (i(0, 2, 1), i(1, 2))):
+    try:
+        K.kda_decode_tokens_cached(q, q, q, g, beta, cu, cache, scales, slots)
+        raise SystemExit("taken")
+    except K.KdaError as e:
+        assert e.status == K.KDA_ERR_INVALID_ARG
+K.kda_decode_tokens_cached(q, q, q, g, beta, i(0, 1, 2), cache, scales, i(1, 2))
+torch.cuda.synchronize()
+print("validated")
+"""
+
+
+def test_slots_named_twice_are_refused_under_validation():
+    env = dict(os.environ, KDA_VALIDATE="1")
+    r = subprocess.run([sys.executable, "-c", VALIDATED % ROOT], env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "validated" in r.stdout, r.stdout + r.stderr

@@ -1,0 +1,181 @@
+"""kda_verify_drafts against the definition in fp64 (tests/cache_ref.py): the same
+counts and tokens."""
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as C
+from gated_delta_rule_40_amd import libkda as K
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    K.load()
+
+
+def run(target, draft, tokens, cu, accept, sample, **kw):
+    N = len(cu) - 1
+    dev = lambda t, dt: torch.as_tensor(t, dtype=dt).cuda()              # noqa: E731
+    num, nxt = (torch.full((N,), 77, dtype=torch.int32, device="cuda") for _ in range(2))
+    K.kda_verify_drafts(target, draft, dev(tokens, torch.int32), dev(cu, torch.int32), dev(accept, torch.float32),
+                        dev(sample, torch.float32), num, nxt, **kw)
+    return num.tolist(), nxt.tolist()
+
+
+def check(target, draft, tokens, cu, accept, sample):
+    got = run(target, draft, tokens, cu, accept, sample)
+    h = lambda t: None if t is None else t.detach().double().cpu().numpy()   # noqa: E731
+    f32 = lambda t: np.asarray(t, np.float32).astype(np.float64)            # noqa: E731
+    want = C.verify(h(target), h(draft), np.asarray(tokens), list(cu), f32(accept), f32(sample))
+    assert got[0] == want[0], (got[0], want[0])
+    assert got[1] == want[1], (got[1], want[1])
+    return got
+
+
+def make(lens, V, dtype="fp32", seed=0, pad=0, closeness=0.5):
+    gen = torch.Generator().manual_seed(seed)
+    T = sum(lens) + pad
+    logits = 2 * torch.randn(T, V, generator=gen)
+    near = logits + closeness * torch.randn(T, V, generator=gen)
+    drafted = torch.softmax(near, 1)
+    tokens = torch.multinomial(drafted, 1, generator=gen)[:, 0].roll(1).to(torch.int32)
+    return (torch.softmax(logits, 1).to(DT[dtype]).cuda(), drafted.roll(1, 0).to(DT[dtype]).cuda(), tokens.numpy(),
+            np.cumsum([0] + lens), torch.rand(T, generator=gen).numpy(), torch.rand(len(lens), generator=gen).numpy())
+
+
+@pytest.mark.parametrize("V", [1, 2, 63, 64, 257, 1000, 1024, 1025, 5003, 32000, 65537])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("greedy", [False, True])
+def test_vocabularies(V, dtype, greedy):
+    a = list(make([1, 5, 0, 2, 9, 1], V, dtype, seed=V, pad=3))
+    if greedy:
+        a[1] = None
+    check(*a)
+
+
+@pytest.mark.parametrize("lens", [[1], [0], [300], [0, 0, 66, 0], [3] * 200, [130, 65, 64, 1, 129]], ids=lambda v: str(v[:6]))
+@pytest.mark.parametrize("closeness", [0.0, 0.3, 3.0])
+def test_lengths(lens, closeness):
+    """Drafts of one to hundreds of tokens, all, some or hardly any of them accepted."""
+    check(*make(lens, 300, seed=len(lens), closeness=closeness, pad=1))
+
+
+def test_all_accepted_and_all_rejected():
+    t, d, tok, cu, acc, smp = make([70, 5, 2], 128)
+    assert check(t, d, tok, cu, np.zeros(77), smp)[0] == [70, 5, 2]
+    assert check(t * 0 + 1e-9, d, tok, cu, np.full(77, 0.999), smp)[0] == [1, 1, 1]
+
+
+def test_ties_are_decided_exactly():
+    """Probabilities that fp32 sums exactly, thresholds on the borders."""
+    V = 4096
+    t = torch.full((V, V), 1 / V).cuda()
+    num, nxt = check(t, t, np.zeros(V), np.arange(V + 1), np.zeros(V), np.arange(V) / V)
+    assert nxt == list(range(V))
+    below = np.nextafter((np.arange(V) / V).astype(np.float32), np.float32(-1))
+    assert check(t, t, np.zeros(V), np.arange(V + 1), np.zeros(V), below)[1] == [max(i - 1, 0) for i in range(V)]
+    two = torch.zeros(2, 8).cuda()
+    two[0], two[1] = 0.25, 0.5
+    # u q < p: 0.5 * 0.5 is not below 0.25
+    assert check(two, two, [0, 3], [0, 2], [0, 0.5], [0.3])[0] == [1]
+    assert check(two, two, [0, 3], [0, 2], [0, np.nextafter(np.float32(0.5), np.float32(0))], [0.3])[0] == [2]
+
+
+def test_weights_that_vanish():
+    V = 2500
+    t, d, tok, cu, acc, smp = make([2, 3, 1], V)
+    one = np.full(6, 0.9999)
+    check(t, t.roll(1, 0).contiguous(), tok, cu, one, smp)              # nothing is left of p - q
+    z = torch.zeros_like(t)
+    assert check(z, d, tok, cu, acc, smp) == ([1, 1, 1], [-1, -1, -1])
+    assert check(z, None, tok, cu, acc, smp) == ([1, 1, 1], [-1, -1, -1])
+    # a single weight, anywhere
+    for x in (0, 1023, 1024, V - 1):
+        s = torch.zeros_like(t)
+        s[:, x] = 1e-30
+        for u in (0.0, 0.5, 0.99999994, 1.0, 2.0, -1.0, float("nan")):
+            assert check(s, None, tok * 0 + (x + 1) % V, cu, acc, [u] * 3)[1] == [x] * 3
+    # the rejected token had all of the target's weight: its row, whole
+    s = torch.zeros_like(t)
+    s[:, 7] = 0.5
+    assert check(s, None, [0, 7, 0, 7, 7, 0], cu, [0.6] * 6, [0.3] * 3) == ([1, 1, 1], [7, 7, 7])
+
+
+def test_values_that_are_no_probabilities():
+    t, d, tok, cu, acc, smp = make([3, 2, 4, 1], 700)
+    t[0, ::3], t[2, 5:90], d[1, 4::7], t[5, 9] = -1.0, float("nan"), float("nan"), 0.0
+    d[2] = -3.0
+    check(t, d, tok, cu, acc, smp)
+    tok[1], tok[4], tok[6] = -1, 700, 2 ** 31 - 1                        # no tokens: rejected
+    check(t, d, tok, cu, acc, smp)
+    check(t, None, tok, cu, acc, smp)
+    t[8, 3] = float("inf")                                               # in bounds, and a token
+    assert 0 <= run(t, d, tok, cu, acc, smp)[1][2] < 700
+
+
+def test_the_first_row_of_a_draft_is_not_read():
+    t, d, tok, cu, acc, smp = make([3, 4], 200)
+    want = check(t, d, tok, cu, acc, smp)
+    d[[0, 3]] = float("nan")
+    tok[[0, 3]] = -9
+    acc[[0, 3]] = np.nan
+    assert run(t, d, tok, cu, acc, smp) == want
+
+
+def test_bad_cu_seqlens_stay_in_bounds():
+    t, d, tok, _, acc, smp = make([3, 4, 2], 200)
+    run(t, d, tok, [-4, 5, 2, 100], acc, smp)
+    torch.cuda.synchronize()
+
+
+def test_off_boundaries_and_given_workspaces():
+    t, d, tok, cu, acc, smp = make([3, 4, 2], 1001, "bf16")
+    want = check(t, d, tok, cu, acc, smp)
+    off = lambda x: torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape).copy_(x)   # noqa: E731
+    need = K.kda_verify_drafts_workspace_size(3, 1001)
+    ws = torch.full((need + 8,), 255, dtype=torch.uint8, device="cuda")
+    assert run(off(t), off(d), tok, cu, acc, smp, workspace=ws) == want
+    assert torch.all(ws[need:] == 255)
+    if need:
+        with pytest.raises(K.KdaError):
+            run(t, d, tok, cu, acc, smp, workspace=ws[:need - 1])
+
+
+def test_offsets_beyond_32_bits():
+    V = 200000
+    T = 12000                                                            # 2.4 billion probabilities
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 10 GB")
+    t = torch.zeros(T, V, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    t[-6:] = torch.rand(6, V, device="cuda", generator=gen).bfloat16()
+    d = torch.zeros(T, V, dtype=torch.bfloat16, device="cuda")
+    d[-6:] = torch.rand(6, V, device="cuda", generator=gen).bfloat16()
+    cu = np.array([0, 0, T - 5, T])
+    tok, acc, smp = np.zeros(T, np.int32), np.full(T, 0.5, np.float32), np.array([.1, .2, .7], np.float32)
+    tok[-5:] = [5, 199999, 7, 8, 9]
+    got = run(t, d, tok, cu, acc, smp)
+    want = C.verify(t[-6:].double().cpu().numpy(), d[-6:].double().cpu().numpy(), tok[-6:], [0, 1, 6], acc[-6:], smp[1:])
+    assert got[0][2] == want[0][1] and got[1][2] == want[1][1] and got[0][0] == 0
+
+
+def test_binding_refusals():
+    t, d, tok, cu, acc, smp = make([3, 4], 200)
+    dev = [torch.as_tensor(x).cuda() for x in (tok, cu.astype(np.int32), acc, smp)]
+    num, nxt = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    good = [t, d, *dev, num, nxt]
+    K.kda_verify_drafts(*good)
+    for i, bad in ((0, t[:, ::2]), (1, d.bfloat16()), (1, d[:3]), (2, dev[0].long()), (3, dev[1].long()), (4, dev[2].double()),
+                   (5, dev[3][:1]), (6, num[:1]), (7, nxt.cpu()), (0, t.view(7, 20, 10))):
+        a = list(good)
+        a[i] = bad
+        with pytest.raises(ValueError):
+            K.kda_verify_drafts(*a)
+    with pytest.raises(K.KdaError):
+        K.kda_verify_drafts(t, d, *dev, num, num)
