@@ -2,19 +2,29 @@
 // them, from given random numbers.
 //
 // The row of the vocabulary that the next token comes from is known once the
-// accepted drafts are counted, which takes two values a draft.  So every wave counts
-// them for itself, and of all rows only that one is read: its weights
-// w = max(p - q, 0) are summed in parts side by side (kernel 1), and the part where
-// the running sum passes sample_rand * total is searched (kernel 2; it is in the
-// caches still).  Sums are formed in fp64 in a fixed order.
+// accepted drafts are counted, which takes two values a draft.  So every workgroup
+// counts them for itself, and of all rows only that one is read: its weights
+// w = max(p - q, 0) are summed in parts of 1,024, a wave each (kernel 1), and the part
+// where the running sum passes sample_rand * total is searched (kernel 2).  Sums are
+// formed in fp64 in a fixed order, where a difference of two probabilities is exact.
+//
+// HBM bounds large calls, latency small ones: the counting takes two dependent reads,
+// each kernel about three.  One MI355X, fp32, four drafts, both kernels of a replayed
+// graph: 256 sequences of 131,072 49.6 us, 256 x 32,000 20.8 us, one of 32,000 11.2 us.
+// Read past the caches, rows take 10-20 % less (256 x 131,072: 59.6 us through them).
+// One launch with a workgroup of 1,024 threads a sequence and the sums in LDS took
+// 15.5 us for one sequence of 32,000, 28.9 for one of 131,072 (13.4 with two launches)
+// and 60.9 for 256: a CU alone does not read a row fast enough.
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
 #include "kda_seq.hpp"
 
+#include <type_traits>
+
 namespace kda {
 
-constexpr int VF_THREADS = 256;
-constexpr int VF_PART_MIN = 1024, VF_PART_MAX = 16384;   // weights of a part
+constexpr int VF_THREADS = 256, VF_WAVES = VF_THREADS / 64;
+constexpr int VF_PART = 1024;   // weights that one wave sums, and that are searched at once
 
 // A sequence's verdict, the same in every lane.
 struct Verdict {
@@ -29,10 +39,7 @@ template <typename T> struct Verify {
     Seqs sq;
 
     // probabilities below zero and NaN count as zero
-    static __device__ __forceinline__ double prob(T x) {
-        const float f = to_f(x);
-        return f > 0.f ? (double)f : 0.0;
-    }
+    static __device__ __forceinline__ double prob(T x) { return (double)fmaxf(to_f(x), 0.f); }
     // called by a whole wave
     __device__ __forceinline__ Verdict judge(int32_t n) const {
         const int32_t first = sq.at(n), rows = max(sq.at(n + 1) - first, 0), lane = threadIdx.x & 63;
@@ -59,152 +66,252 @@ template <typename T> struct Verify {
     struct Row {
         const T *p, *q;     // q: the draft's row, or null
         int32_t without;    // the token that is left out (drafts picked without a distribution), or -1
-        __device__ __forceinline__ double at(int32_t x) const {
-            const double a = prob(p[x]);
-            if (q) {
-                const double d = a - prob(q[x]);
-                return d > 0. ? d : 0.;
+        int32_t vocab;
+
+        // VW consecutive weights from x0 on, zeros beyond the row; q's part is read with p's
+        template <int VW> __device__ __forceinline__ void read(int32_t x0, T (&a)[VW], T (&b)[VW]) const {
+            typedef T raw __attribute__((ext_vector_type(VW)));
+            typedef raw mem __attribute__((aligned(sizeof(T))));
+            raw u{}, v{};
+            if (x0 + VW <= vocab) {
+                u = __builtin_nontemporal_load(reinterpret_cast<const mem *>(p + x0));
+                if (q) v = __builtin_nontemporal_load(reinterpret_cast<const mem *>(q + x0));
+            } else {
+#pragma unroll
+                for (int j = 0; j < VW; ++j)
+                    if (x0 + j < vocab) {
+                        u[j] = p[x0 + j];
+                        if (q) v[j] = q[x0 + j];
+                    }
             }
-            return x == without ? 0. : a;
+#pragma unroll
+            for (int j = 0; j < VW; ++j) a[j] = u[j], b[j] = v[j];
+        }
+        __device__ __forceinline__ double weight(int32_t x, T a, T b) const {
+            const double w = fmax(prob(a) - prob(b), 0.);   // (infinity less infinity: zero)
+            return x == without ? 0. : w;
         }
     };
     __device__ __forceinline__ Row row(const Verdict &v) const {
         const int64_t at = (int64_t)v.first + v.accepted;
         const bool rejected = v.accepted + 1 < v.rows;
         return {target + at * vocab, rejected && draft ? draft + (at + 1) * vocab : nullptr,
-                rejected && !draft ? tokens[at + 1] : -1};
+                rejected && !draft ? tokens[at + 1] : -1, (int32_t)vocab};
     }
 };
 
-// the sum over a workgroup, in every thread
-__device__ __forceinline__ double group_sum(double s, double *red)
+// The sums up to each lane of a wave: within rows of 16 lanes, then over the rows.
+template <int CTRL, int ROWS> __device__ __forceinline__ double add_from(double x)
 {
-    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
-    __syncthreads();
-    double t = 0.;
-    for (int i = 0; i < VF_THREADS / 64; ++i) t += red[i];
-    return t;
+    union { double d; int i[2]; } u{x}, y;
+    y.i[0] = __builtin_amdgcn_update_dpp(0, u.i[0], CTRL, ROWS, 0xf, true);
+    y.i[1] = __builtin_amdgcn_update_dpp(0, u.i[1], CTRL, ROWS, 0xf, true);
+    return x + y.d;   // (lanes without a source add zero)
+}
+__device__ __forceinline__ double wave_scan(double s)
+{
+    s = add_from<0x111, 0xf>(s);   // row_shr:1
+    s = add_from<0x112, 0xf>(s);
+    s = add_from<0x114, 0xf>(s);
+    s = add_from<0x118, 0xf>(s);
+    s = add_from<0x142, 0xa>(s);   // row_bcast:15 into rows 1 and 3
+    return add_from<0x143, 0xc>(s);   // row_bcast:31 into rows 2 and 3
 }
 
-template <typename T>
-__global__ __launch_bounds__(VF_THREADS) void kda_verify_sums_kernel(Verify<T> in, int32_t parts, int32_t part, double *sums)
+// The sums of parts `part` to part + K - 1 of a row, by one wave, in its last lane.
+template <typename T, int K> __device__ __forceinline__ void part_sums(const typename Verify<T>::Row &w, int32_t part, double (&sum)[K])
 {
-    __shared__ double red[VF_THREADS / 64];
-    const int32_t n = blockIdx.x / parts, i = blockIdx.x % parts;
-    const Verdict v = in.judge(n);
-    if (v.rows == 0) return;
-    const auto w = in.row(v);
-    const int32_t end = (int32_t)min(((int64_t)i + 1) * part, in.vocab);
-    double s = 0.;
-    for (int32_t x = i * part + threadIdx.x; x < end; x += VF_THREADS) s += w.at(x);
-    s = group_sum(s, red);
-    if (threadIdx.x == 0) sums[blockIdx.x] = s;
-}
-
-// The first x of [begin, end) with base + w[begin] + ... + w[x] > mark and w[x] > 0,
-// or the last with w[x] > 0, or -1.
-template <typename Row>
-__device__ __forceinline__ int32_t search(const Row &w, int32_t begin, int32_t end, double base, double mark, double *red,
-                                          int32_t *pick)
-{
-    const int32_t per = (end - begin + VF_THREADS - 1) / VF_THREADS;
-    const int32_t mine = min(begin + (int32_t)threadIdx.x * per, end), stop = min(mine + per, end);
-    double s = 0.;
-    for (int32_t x = mine; x < stop; ++x) s += w.at(x);
-    // sums of the threads before this one
-    double before = s;
-    for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(before, off);
-        if ((int)(threadIdx.x & 63) >= off) before += y;
-    }
-    __syncthreads();   // (a sum may have been read from `red` just now)
-    if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6] = before;
-    if (threadIdx.x == 0) pick[0] = INT32_MAX, pick[1] = -1;
-    __syncthreads();
-    before -= s;
-    for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) before += red[i];
-    double sum = base + before;
-    int32_t found = INT32_MAX, last = -1;
-    for (int32_t x = mine; x < stop; ++x) {
-        const double y = w.at(x);
-        sum += y;
-        if (y > 0.) {
-            last = x;
-            if (found == INT32_MAX && sum > mark) found = x;
+    constexpr int VW = 16 / sizeof(T), PIECES = VF_PART / 64 / VW;
+    const int32_t x0 = part * VF_PART + (threadIdx.x & 63) * VW;
+    T a[K * PIECES][VW], b[K * PIECES][VW];
+#pragma unroll
+    for (int c = 0; c < K * PIECES; ++c) w.template read<VW>(x0 + c * 64 * VW, a[c], b[c]);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        sum[k] = 0.;
+#pragma unroll
+        for (int c = k * PIECES; c < (k + 1) * PIECES; ++c) {
+            double s = 0.;
+#pragma unroll
+            for (int j = 0; j < VW; ++j) s += w.weight(x0 + c * 64 * VW + j, a[c][j], b[c][j]);
+            sum[k] += s;
         }
+        sum[k] = wave_scan(sum[k]);
     }
-    if (found != INT32_MAX) atomicMin(&pick[0], found);
-    if (last >= 0) atomicMax(&pick[1], last);
-    __syncthreads();
-    return pick[0] != INT32_MAX ? pick[0] : pick[1];
 }
 
+// What a workgroup finds: every thread has the weights of some places, `run` their
+// sum, in the order of the threads.
+struct Search {
+    double waves[VF_WAVES];
+    double base;           // the sum before the part that is searched
+    int32_t first, last;   // the first place that passes the mark; the last that has a weight
+
+    // The sum before this thread's places, and of all (called by the whole workgroup).
+    __device__ __forceinline__ double before(double run, double &total) {
+        const double s = wave_scan(run);
+        __syncthreads();   // (the search before is over)
+        if ((threadIdx.x & 63) == 63) waves[threadIdx.x >> 6] = s;
+        if (threadIdx.x == 0) first = INT32_MAX, last = -1;
+        __syncthreads();
+        double up = s - run;
+        total = 0.;
+#pragma unroll
+        for (int i = 0; i < VF_WAVES; ++i) {
+            if (i == (int)(threadIdx.x >> 6)) up += total;
+            total += waves[i];
+        }
+        return up;
+    }
+    __device__ __forceinline__ void found(int32_t mine_first, int32_t mine_last) {
+        if (mine_first != INT32_MAX) atomicMin(&first, mine_first);
+        if (mine_last >= 0) atomicMax(&last, mine_last);
+        __syncthreads();
+    }
+    __device__ __forceinline__ int32_t place() const { return first != INT32_MAX ? first : last; }
+
+    // The next token, given the sums of the row's parts.  The first place x with
+    // w[x] > 0 whose running sum is above the mark lies in the first part with a
+    // weight whose running sum is (running sums of weights never fall); if there is
+    // none, the last place with a weight in the last such part.
+    // A thread has parts [p0, p1), whose sum is `run`.
+    template <typename T>
+    __device__ __forceinline__ int32_t pick(typename Verify<T>::Row w, const double *sums, int32_t parts, int32_t p0, int32_t p1,
+                                            double run, double sample) {
+        constexpr int VW = VF_PART / VF_THREADS;
+        double total, sum = before(run, total);
+        const bool whole = total == 0. && (w.q || w.without >= 0);   // nothing is left: the target's own row
+        if (whole) {
+            w.q = nullptr, w.without = -1;
+            run = 0.;
+            for (int32_t x0 = threadIdx.x * VW; x0 < w.vocab; x0 += VF_PART) {
+                T a[VW], b[VW];
+                w.template read<VW>(x0, a, b);
+#pragma unroll
+                for (int j = 0; j < VW; ++j) run += w.weight(x0 + j, a[j], b[j]);
+            }
+            before(run, total);
+        }
+        const double mark = sample * total;
+        int32_t part = 0, end = parts;
+        double from = 0.;
+        if (!whole) {
+            int32_t mine_first = INT32_MAX, mine_last = -1;
+            double first_base = 0., last_base = 0.;
+            for (int32_t i = p0; i < p1; ++i) {
+                const double s = sums[i];
+                if (s > 0.) {
+                    mine_last = i, last_base = sum;
+                    if (mine_first == INT32_MAX && sum + s > mark) mine_first = i, first_base = sum;
+                }
+                sum += s;
+            }
+            found(mine_first, mine_last);
+            part = max(place(), 0);
+            if (part >= p0 && part < p1) base = part == mine_first ? first_base : last_base;
+            end = part + 1;
+            __syncthreads();
+            from = base;
+        }
+        // the part; of a whole row the parts in turn, to the first that has it
+        int32_t next = -1;
+        for (; part < end; ++part) {
+            const int32_t x0 = part * VF_PART + threadIdx.x * VW;
+            T a[VW], b[VW];
+            double y[VW];
+            w.template read<VW>(x0, a, b);
+            run = 0.;
+#pragma unroll
+            for (int j = 0; j < VW; ++j) y[j] = w.weight(x0 + j, a[j], b[j]), run += y[j];
+            double all;
+            sum = from + before(run, all);
+            int32_t mine_first = INT32_MAX, mine_last = -1;
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+                sum += y[j];
+                if (y[j] > 0.) {
+                    mine_last = x0 + j;
+                    if (mine_first == INT32_MAX && sum > mark) mine_first = x0 + j;
+                }
+            }
+            found(mine_first, mine_last);
+            if (place() >= 0) next = place();
+            if (first != INT32_MAX) break;
+            from += all;
+        }
+        return next;
+    }
+};
+
+// Kernel 1: a row's parts over many workgroups.  A wave takes K of them, all reads
+// before the first use.
+template <typename T, int K>
+__global__ __launch_bounds__(VF_THREADS) void kda_verify_sums_kernel(Verify<T> in, int32_t groups, int32_t parts, double *sums,
+                                                                     int32_t *counts)
+{
+    const int32_t n = blockIdx.x / groups, group = blockIdx.x % groups;
+    const int32_t part = (group * VF_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * K;
+    const Verdict v = in.judge(n);
+    if (group == 0 && threadIdx.x == 0) counts[n] = v.accepted;
+    if (v.rows == 0 || part >= parts) return;
+    double s[K];
+    part_sums<T, K>(in.row(v), part, s);
+    if ((threadIdx.x & 63) == 63)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (part + k < parts) sums[(int64_t)n * parts + part + k] = s[k];
+}
+
+// Kernel 2: a workgroup a sequence.
 template <typename T>
 __global__ __launch_bounds__(VF_THREADS) void kda_verify_pick_kernel(Verify<T> in, const float *sample_rand, int32_t parts,
-                                                                     int32_t part, const double *sums, int32_t *num_tokens,
-                                                                     int32_t *next_token)
+                                                                     const double *sums, const int32_t *counts,
+                                                                     int32_t *num_tokens, int32_t *next_token)
 {
-    __shared__ double red[VF_THREADS / 64];
-    __shared__ int32_t pick[2];
+    __shared__ Search find;
     const int32_t n = blockIdx.x;
-    const Verdict v = in.judge(n);
+    const Verdict v{in.sq.at(n), max(in.sq.at(n + 1) - in.sq.at(n), 0), counts[n]};
+    const double sample = sample_rand[n];
+    sums += (int64_t)n * parts;
+    const int32_t per = (parts + VF_THREADS - 1) / VF_THREADS;
+    const int32_t p0 = min((int32_t)threadIdx.x * per, parts), p1 = min(p0 + per, parts);
+    double run = 0.;
+    for (int32_t i = p0; i < p1; ++i) run += sums[i];
+    asm volatile("" ::: "memory");   // (keeps these reads ahead of what waits for the counts)
     if (v.rows == 0) {
         if (threadIdx.x == 0) num_tokens[n] = 0, next_token[n] = -1;
         return;
     }
-    auto w = in.row(v);
-    sums += (int64_t)n * parts;
-    double total = 0.;
-    for (int32_t i = 0; i < parts; ++i) total += sums[i];
-    int32_t begin = 0, end = (int32_t)in.vocab;
-    double base = 0.;
-    if (total == 0. && (w.q || w.without >= 0)) {   // nothing is left: the target's own row, whole
-        w.q = nullptr, w.without = -1;
-        double s = 0.;
-        for (int32_t x = threadIdx.x; x < in.vocab; x += VF_THREADS) s += w.at(x);
-        total = group_sum(s, red);
-    } else {
-        // the part in which the running sum passes the mark, or the last that has a weight
-        int32_t at = 0;
-        double sum = 0.;
-        for (int32_t i = 0; i < parts; ++i) {
-            if (!(sums[i] > 0.)) continue;
-            at = i, base = sum;
-            sum += sums[i];
-            if (sum > (double)sample_rand[n] * total) break;
-        }
-        begin = at * part;
-        end = (int32_t)min((int64_t)begin + part, in.vocab);
-    }
-    const int32_t x = search(w, begin, end, base, (double)sample_rand[n] * total, red, pick);
-    if (threadIdx.x == 0) num_tokens[n] = 1 + v.accepted, next_token[n] = x;
+    const int32_t next = find.template pick<T>(in.row(v), sums, parts, p0, p1, run, sample);
+    if (threadIdx.x == 0) num_tokens[n] = 1 + v.accepted, next_token[n] = next;
 }
 
-// weights of a part: about 2,048 workgroups in all
-inline int32_t part_size(int32_t N, int32_t vocab)
+inline int32_t part_count(int32_t vocab) { return (int32_t)(((int64_t)vocab + VF_PART - 1) / VF_PART); }
+// Parts of a wave: two from 16,384 parts on (us of both kernels, one and two: 256 rows of
+// 131,072 53.2 and 49.6, 256 x 200,000 72.9 and 65.7; 64 x 131,072 22.9 and 23.0,
+// 1 x 32,000 11.2 and 12.1).
+inline int parts_each(int32_t N, int32_t vocab)
 {
-    int64_t part = (int64_t)vocab * N / 2048;
-    part = part < VF_PART_MIN ? VF_PART_MIN : part > VF_PART_MAX ? VF_PART_MAX : part;
-    return (int32_t)((part + VF_THREADS - 1) / VF_THREADS * VF_THREADS);
+    return N * (int64_t)part_count(vocab) < 16384 ? 1 : 2;
 }
-inline int32_t part_count(int32_t N, int32_t vocab)
+// workgroups of a sequence
+inline int64_t sum_groups(int32_t N, int32_t vocab)
 {
-    const int32_t part = part_size(N, vocab);
-    return (int32_t)(((int64_t)vocab + part - 1) / part);
+    const int64_t per = VF_WAVES * (int64_t)parts_each(N, vocab);
+    return (part_count(vocab) + per - 1) / per;
 }
 
 }  // namespace kda
 
 using namespace kda;
 
-size_t kda_verify_ws_bytes(int32_t N, int32_t vocab) { return (size_t)N * part_count(N, vocab) * sizeof(double); }
-
-bool kda_verify_fits(int32_t N, int32_t vocab)
+// the parts' sums, and the drafts accepted
+size_t kda_verify_ws_bytes(int32_t N, int32_t vocab)
 {
-    return (int64_t)N * part_count(N, vocab) <= INT32_MAX && kda_grid_ok((int64_t)N * part_count(N, vocab), VF_THREADS);
+    return (size_t)N * part_count(vocab) * sizeof(double) + (size_t)N * sizeof(int32_t);
 }
+
+bool kda_verify_fits(int32_t N, int32_t vocab) { return kda_grid_ok(N * sum_groups(N, vocab), VF_THREADS); }
 
 template <typename T>
 static hipError_t verify(const void *target, const void *draft, const int32_t *tokens, const int32_t *cu,
@@ -212,11 +319,17 @@ static hipError_t verify(const void *target, const void *draft, const int32_t *t
                          int32_t *num_tokens, int32_t *next_token, void *ws, hipStream_t s)
 {
     const Verify<T> in{(const T *)target, (const T *)draft, tokens, accept_rand, vocab, {cu, N, T_tot}};
-    const int32_t part = part_size(N, vocab), parts = part_count(N, vocab);
-    hipLaunchKernelGGL(kda_verify_sums_kernel<T>, dim3((unsigned)(N * parts)), dim3(VF_THREADS), 0, s, in, parts, part,
-                       (double *)ws);
-    hipLaunchKernelGGL(kda_verify_pick_kernel<T>, dim3((unsigned)N), dim3(VF_THREADS), 0, s, in, sample_rand, parts, part,
-                       (const double *)ws, num_tokens, next_token);
+    const int32_t parts = part_count(vocab), groups = (int32_t)sum_groups(N, vocab);
+    double *const sums = (double *)ws;
+    int32_t *const counts = (int32_t *)(sums + (size_t)N * parts);
+    const auto sum = [&](auto k) {
+        hipLaunchKernelGGL((kda_verify_sums_kernel<T, k()>), dim3((unsigned)(N * (int64_t)groups)), dim3(VF_THREADS), 0, s, in,
+                           groups, parts, sums, counts);
+    };
+    if (parts_each(N, vocab) == 1) sum(std::integral_constant<int, 1>());
+    else sum(std::integral_constant<int, 2>());
+    hipLaunchKernelGGL(kda_verify_pick_kernel<T>, dim3((unsigned)N), dim3(VF_THREADS), 0, s, in, sample_rand, parts, sums,
+                       counts, num_tokens, next_token);
     return hipGetLastError();
 }
 

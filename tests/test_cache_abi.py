@@ -53,7 +53,7 @@ ARRAYS = {
     "kda_decode_tokens_cached": (dict(q=2 * TOK, k=2 * TOK, v=2 * TOK, g=4 * TOK, beta=70 * 16, cu=16, num=12,
                                       cache=7 * 4 * 128 * 128, scales=7 * 4 * 128 * 4, slots=12, out=2 * TOK),
                                  dict(cache="", scales="", out="")),
-    "kda_verify_drafts": (dict(target=140000, draft=140000, tokens=280, cu=16, accept=280, sample=12, num=12, next=12, ws=24),
+    "kda_verify_drafts": (dict(target=140000, draft=140000, tokens=280, cu=16, accept=280, sample=12, num=12, next=12, ws=36),
                           dict(num="", next="", ws="")),
 }
 
