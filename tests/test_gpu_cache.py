@@ -124,22 +124,42 @@ def test_zeros_infinities_nan_and_the_smallest(fmt, dtype):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_off_boundaries(fmt):
-    x = torch.randn(5, 333).cuda()
+@pytest.mark.parametrize("elems", [333, 2048])
+def test_off_boundaries(fmt, elems):
+    x = torch.randn(5, elems).cuda()
     slots = torch.tensor([4, 0, 3, 1, 2], dtype=torch.int32, device="cuda")
-    cache, scales = new_cache(5, 333, fmt)
+    cache, scales = new_cache(5, elems, fmt)
     K.kda_cache_store(x, slots, cache, scales, fmt)
     for sh in (1, 2, 3):
-        y = torch.empty(5 * 333 + 3, device="cuda")[sh:sh + 5 * 333].view(5, 333).copy_(x)
+        y = torch.empty(5 * elems + 3, device="cuda")[sh:sh + 5 * elems].view(5, elems).copy_(x)
         c2 = torch.empty(cache.numel() + 3, dtype=torch.uint8, device="cuda")[sh:sh + cache.numel()].view(cache.shape)
         s2 = torch.empty(scales.numel() + 3, dtype=torch.uint8, device="cuda")[sh:sh + scales.numel()].view(scales.shape)
         K.kda_cache_store(y, slots, c2, s2, fmt)
         assert torch.equal(c2, cache) and torch.equal(s2, scales)
-        z = torch.empty(5 * 333 + 3, dtype=torch.bfloat16, device="cuda")[sh:sh + 5 * 333].view(5, 333)
-        w = torch.empty(5, 333, dtype=torch.bfloat16, device="cuda")
+        z = torch.empty(5 * elems + 3, dtype=torch.bfloat16, device="cuda")[sh:sh + 5 * elems].view(5, elems)
+        w = torch.empty(5, elems, dtype=torch.bfloat16, device="cuda")
         K.kda_cache_load(c2, s2, slots, z, fmt)
         K.kda_cache_load(cache, scales, slots, w, fmt)
         assert torch.equal(z, w)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_large_calls_are_the_small_ones(fmt, dtype):
+    """More than the caches hold, against its entries one by one, whole chunks and others."""
+    for elems in (1 << 21, (1 << 21) + 7):
+        n = 20
+        x = torch.randn(n, elems, device="cuda").to(DT[dtype])
+        slots = torch.randperm(n).to(torch.int32).cuda()
+        cache, scales = new_cache(n, elems, fmt)
+        K.kda_cache_store(x, slots, cache, scales, fmt)
+        c2, s2 = new_cache(n, elems, fmt)
+        y, z = torch.empty_like(x), torch.empty_like(x)
+        K.kda_cache_load(cache, scales, slots, y, fmt)
+        for i in range(n):
+            K.kda_cache_store(x[i:i + 1], slots[i:i + 1], c2, s2, fmt)
+            K.kda_cache_load(cache, scales, slots[i:i + 1], z[i:i + 1], fmt)
+        assert torch.equal(cache, c2) and torch.equal(scales, s2) and torch.equal(y, z)
 
 
 def test_types_that_codes_come_in():
