@@ -723,49 +723,68 @@ def kda_rmsnorm_backward(x, weight, dout, dresidual=None, eps: float = 1e-6, gra
 _I32 = torch.int32
 
 
-def _heads(name, x, dev=None, dtype=None):
-    """A device tensor [T, heads, d] of a supported type whose tokens are dense rows, at any distance from each other: its
-    address, device, type code, sizes and the distance in elements."""
+def _bad_heads(name, x) -> None:
     _require(isinstance(x, torch.Tensor) and x.is_cuda, "%s must be a device tensor" % name)
-    code = _DTYPE_CODE.get(x.dtype)
-    if code is None:
+    if x.dtype not in _DTYPE_CODE:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, x.dtype))
     _require(x.dim() == 3 and x.shape[2] > 0, "%s must be [T, heads, d]" % name)
-    T, H, d = x.shape
-    st = x.stride()
-    _require((st[2] == 1 or d == 1) and (st[1] == d or H <= 1) and (st[0] >= H * d or T <= 1),
-             "%s must have dense tokens, strides (any, d, 1)" % name)
-    if dev is not None:
-        _require(x.get_device() == dev and x.dtype is dtype, "%s must be %s on cuda:%d" % (name, dtype, dev))
-    _require(T <= _MOST and H * d <= _MOST, "%s has too many tokens or channels" % name)
-    return x.data_ptr(), x.get_device(), code, T, H, d, (st[0] if T > 1 else H * d)
+    _require(x.shape[0] <= _MOST and x.shape[1:].numel() <= _MOST, "%s has too many tokens or channels" % name)
+    raise ValueError("%s must have dense tokens, strides (any, d, 1), got %s" % (name, x.stride()))
+
+
+def _heads(name, x):
+    """A device tensor [T, heads, d] of a supported type whose tokens are dense rows, at any distance from each other: its
+    address, shape and the distance in elements."""
+    try:
+        T, H, d = shape = x.shape
+        t, h, e = x.stride()
+        row = H * d
+        if x.is_cuda and x.dtype in _DTYPE_CODE and 0 < d and T <= _MOST and row <= _MOST:
+            if e == 1 and h == d and t >= row:
+                return x.data_ptr(), shape, t
+            # dimensions of one or none have any stride
+            if (e == 1 or d == 1) and (h == d or H <= 1) and (t >= row or T <= 1):
+                return x.data_ptr(), shape, t if T > 1 else row
+    except (AttributeError, ValueError):   # no tensor, or not of three dimensions
+        pass
+    _bad_heads(name, x)
 
 
 def _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis, interleaved):
-    """The arguments that kda_qknorm and its gradients share, up to the type: (device, code, T, Hq, Hk, d, arguments)."""
-    pq, dev, code, T, Hq, d, sq = _heads("q", q)
-    pk, Hk, sk = None, 0, 0
+    """The arguments that kda_qknorm and its gradients share, up to the type: (device, q's shape, k's shape, arguments)."""
+    pq, qs, sq = _heads("q", q)
+    T, Hq, d = qs
+    dev, dt = q.get_device(), q.dtype
+    pk, ks, Hk, sk = None, None, 0, 0
     if k is not None:
-        pk, _, _, Tk, Hk, dk, sk = _heads("k", k, dev, q.dtype)
-        _require(Tk == T and dk == d, "k must have q's tokens and head size, got %s" % list(k.shape))
+        pk, ks, sk = _heads("k", k)
+        Hk = ks[1]
+        _require(k.dtype is dt and k.get_device() == dev, "k must be %s on cuda:%d" % (dt, dev))
+        _require(ks[0] == T and ks[2] == d, "k must have q's tokens and head size")
     kind = KDA_NORMS.get(norm)
-    _require(kind is not None, "norm must be one of %s, got %r" % (", ".join(KDA_NORMS), norm))
+    if kind is None:
+        raise ValueError("norm must be one of %s, got %r" % (", ".join(KDA_NORMS), norm))
+    if q_weight is not None:
+        q_weight = _addr("q_weight", q_weight, dev, _F32, (d,))
+    if k_weight is not None:
+        k_weight = _addr("k_weight", k_weight, dev, _F32, (d,))
     ppos = pfreq = paxis = None
     rot, axes = 0, 1
     if inv_freq is not None or positions is not None:
         _require(isinstance(inv_freq, torch.Tensor) and inv_freq.dim() == 1 and isinstance(positions, torch.Tensor) and
                  positions.dim() in (1, 2), "a rotation needs inv_freq [rot_dim / 2] and positions [T] or [axes, T]")
-        rot = 2 * inv_freq.shape[0]
+        pairs = inv_freq.shape[0]
+        rot = 2 * pairs
         _require(rot <= d, "inv_freq must have at most d / 2 entries")
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        pfreq = _addr("inv_freq", inv_freq, dev, _F32, (rot // 2,))
-        ppos = _addr("positions", positions, dev, _I32, (T,) if positions.dim() == 1 else (axes, T))
-        paxis = _addr_if("pair_axis", pair_axis, dev, _I32, (rot // 2,))
-    else:
-        _require(pair_axis is None, "pair_axis goes with positions and inv_freq")
-    return dev, code, T, Hq, Hk, d, (pq, pk, sq, sk, _addr_if("q_weight", q_weight, dev, _F32, (d,)),
-                                     _addr_if("k_weight", k_weight, dev, _F32, (d,)), ppos, pfreq, paxis, T, Hq, Hk, d, rot,
-                                     axes, int(interleaved), kind, eps, q_scale, code)
+        one = positions.dim() == 1
+        axes = 1 if one else positions.shape[0]
+        pfreq = _addr("inv_freq", inv_freq, dev, _F32, (pairs,))
+        ppos = _addr("positions", positions, dev, _I32, (T,) if one else (axes, T))
+        paxis = _addr_if("pair_axis", pair_axis, dev, _I32, (pairs,))
+    elif pair_axis is not None:
+        raise ValueError("pair_axis goes with positions and inv_freq")
+    return dev, qs, ks, (pq, pk, sq, sk, q_weight, k_weight, ppos, pfreq, paxis, T, Hq, Hk, d, rot, axes, 1 if interleaved else 0,
+                         kind, eps, q_scale, _DTYPE_CODE[dt])
 
 
 def kda_qknorm(q, k, q_out, k_out, q_weight=None, k_weight=None, norm: str = "l2", eps: float = 1e-6, q_scale: float = 1.0,
@@ -779,10 +798,10 @@ def kda_qknorm(q, k, q_out, k_out, q_weight=None, k_weight=None, norm: str = "l2
     inv_freq fp32 radians a position, pair_axis [len(inv_freq)] int32 the axis
     of every pair (None: axis 0); pairs are halves apart, or neighbours if
     interleaved."""
-    dev, _, T, Hq, Hk, d, form = _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis,
-                                          interleaved)
-    _call((_lib or load()).kda_qknorm, dev, stream, *form, _addr("q_out", q_out, dev, q.dtype, (T, Hq, d)),
-          None if k is None else _addr("k_out", k_out, dev, q.dtype, (T, Hk, d)))
+    dev, qs, ks, form = _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis, interleaved)
+    dt = q.dtype
+    _call((_lib or load()).kda_qknorm, dev, stream, *form, _addr("q_out", q_out, dev, dt, qs),
+          None if k is None else _addr("k_out", k_out, dev, dt, ks))
 
 
 def kda_qknorm_backward_workspace_size(num_tokens: int, num_q_heads: int, num_k_heads: int, head_dim: int,
@@ -801,59 +820,70 @@ def kda_qknorm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, norm
     tensors (dq and dk with tokens apart, such as columns of one array),
     which otherwise belong to ``stream`` (record_stream them for use on
     another)."""
-    dev, code, T, Hq, Hk, d, form = _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis,
-                                             interleaved)
-    dt = q.dtype
+    dev, qs, ks, form = _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis, interleaved)
+    dt, d = q.dtype, qs[2]
     lib = _lib or load()
-    grads = _grads(grads, dev, {"dq": (dt, (T, Hq, d)), "dk": None if k is None else (dt, (T, Hk, d)),
+    grads = _grads(grads, dev, {"dq": (dt, qs), "dk": None if k is None else (dt, ks),
                                 "dq_weight": None if q_weight is None else (_F32, (d,)),
                                 "dk_weight": None if k_weight is None else (_F32, (d,))}, stream)
     _require(isinstance(dq_out, torch.Tensor), "dq_out must be a tensor")
     gt = dq_out.dtype if dq_out.dtype is _F32 else dt
-    pdq, _, _, Tq, H, dd, sdq = _heads("grads['dq']", grads.get("dq"), dev, dt)
-    _require((Tq, H, dd) == (T, Hq, d), "grads['dq'] must have q's shape")
-    pdk, sdk = None, 0
-    if k is not None:
-        pdk, _, _, Tk, H, dd, sdk = _heads("grads['dk']", grads.get("dk"), dev, dt)
-        _require((Tk, H, dd) == (T, Hk, d), "grads['dk'] must have k's shape")
+    out = []
+    for name, x, shape in (("dq", q, qs), ("dk", k, ks)):
+        if x is None:
+            out.append((None, 0))
+            continue
+        g = grads.get(name)
+        address, got, stride = _heads("grads['%s']" % name, g)
+        _require(got == shape and g.dtype is dt and g.get_device() == dev,
+                 "grads['%s'] must be %s %s on cuda:%d" % (name, dt, list(shape), dev))
+        out.append((address, stride))
+    (pdq, sdq), (pdk, sdk) = out
     pqw = _addr_if("grads['dq_weight']", grads.get("dq_weight"), dev, _F32, (d,))
     pkw = _addr_if("grads['dk_weight']", grads.get("dk_weight"), dev, _F32, (d,))
-    args = (*form, _DTYPE_CODE[gt], _addr("dq_out", dq_out, dev, gt, (T, Hq, d)),
-            None if k is None else _addr("dk_out", dk_out, dev, gt, (T, Hk, d)), sdq, sdk, pdq, pdk, pqw, pkw)
+    args = (*form, _DTYPE_CODE[gt], _addr("dq_out", dq_out, dev, gt, qs),
+            None if k is None else _addr("dk_out", dk_out, dev, gt, ks), sdq, sdk, pdq, pdk, pqw, pkw)
     ws = pws = None
     nbytes = 0
     if pqw is not None or pkw is not None:
-        ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_qknorm_backward_workspace_size", T, Hq, Hk, d, code)
+        ws, pws, nbytes = _workspace(workspace, dev, stream, "kda_qknorm_backward_workspace_size", qs[0], qs[1],
+                                     0 if k is None else ks[1], d, _DTYPE_CODE[dt])
     _call(lib.kda_qknorm_backward, dev, stream, *args, pws, nbytes)
     return grads
 
 
 # ---------------------------------------------------------------- cached states and drafted tokens
-_BYTES = (torch.uint8, torch.int8, torch.float8_e4m3fn)   # types that codes may come in
-_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+_BYTES = {torch.uint8, torch.int8, torch.float8_e4m3fn}   # types that codes may come in
+_SCALES = {torch.uint8, torch.float8_e8m0fnu}
 
 
 def _format(name) -> int:
     code = KDA_CACHE_FORMATS.get(name)
-    _require(code is not None, "format must be one of %s, got %r" % (", ".join(KDA_CACHE_FORMATS), name))
+    if code is None:
+        raise ValueError("format must be one of %s, got %r" % (", ".join(KDA_CACHE_FORMATS), name))
     return code
 
 
 def _slots_of(name, t, dev, types, per_slot):
     """The address of an array of slots with per_slot bytes each, and their number."""
+    try:
+        if t.dtype in types and t.get_device() == dev and t.is_contiguous():
+            S = t.shape[0]
+            if t.numel() == S * per_slot and S <= _MOST:
+                return t.data_ptr(), S
+    except (AttributeError, IndexError):   # no tensor, or one of no dimensions
+        pass
     _require(isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in types and t.is_contiguous(),
              "%s must be a contiguous tensor of bytes on cuda:%d" % (name, dev))
-    shape = t.shape
-    _require(len(shape) >= 2 and shape[1:].numel() == per_slot and shape[0] <= _MOST,
-             "%s must be [slots, ...] with %d bytes a slot, got %s" % (name, per_slot, list(shape)))
-    return t.data_ptr(), shape[0]
+    raise ValueError("%s must be [slots, ...] with %d bytes a slot, got %s" % (name, per_slot, list(t.shape)))
 
 
 def _cache(cache, scales, dev, elems, fmt):
     """Addresses of a cache's codes and scales for entries of `elems` values, and its slots."""
     pc, S = _slots_of("cache", cache, dev, _BYTES, (elems + 1) // 2 if fmt == 2 else elems)
-    ps, n = _slots_of("scales", scales, dev, _SCALES, -(-elems // KDA_MX_BLOCK))
-    _require(n == S, "cache and scales must have the same slots")
+    ps, n = _slots_of("scales", scales, dev, _SCALES, (elems + KDA_MX_BLOCK - 1) // KDA_MX_BLOCK)
+    if n != S:
+        raise ValueError("cache and scales must have the same slots")
     return pc, ps, S
 
 
