@@ -68,8 +68,7 @@ __device__ __forceinline__ float sum_half_wave(float x)
     x += dpp<DPP_XOR2>(x);
     x += dpp<DPP_HALF_MIRROR>(x);
     x += dpp<DPP_MIRROR>(x);
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    return add_xor16(x);
 }
 
 // What a lane reads of a token: key, query and gate of one of its wave's rows (lanes

@@ -73,7 +73,7 @@ struct KdaQkNorm {
     int32_t norm;
     float eps, q_scale;
 };
-bool kda_qknorm_fits(bool bf16, const KdaQkNorm &a);
+bool kda_qknorm_fits(bool bf16, const KdaQkNorm &a, bool back);
 hipError_t kda_launch_qknorm(bool bf16, const KdaQkNorm &a, void *q_out, void *k_out, hipStream_t s);
 size_t kda_qknorm_bwd_ws_bytes(int32_t d);
 hipError_t kda_launch_qknorm_backward(bool bf16, bool grad_bf16, const KdaQkNorm &a, const void *dq_out, const void *dk_out,

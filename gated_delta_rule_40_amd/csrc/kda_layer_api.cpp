@@ -309,7 +309,7 @@ kda_status kda_qknorm(const void *q, const void *k, int64_t q_stride, int64_t k_
     qknorm_inputs(a, e, in);
     const Rows qo{q_out, num_tokens, (int64_t)(qc * e), (int64_t)(qc * e)}, ko{k_out, num_tokens, (int64_t)(kc * e), (int64_t)(kc * e)};
     if (rows_meet(qo, ko) || meets_any(qo, in, kQkInputs, 0) || meets_any(ko, in, kQkInputs, 1)) return KDA_ERR_INVALID_ARG;
-    if (!kda_qknorm_fits(dtype == KDA_BF16, a)) return KDA_ERR_UNSUPPORTED;
+    if (!kda_qknorm_fits(dtype == KDA_BF16, a, false)) return KDA_ERR_UNSUPPORTED;
     return from_hip(kda_launch_qknorm(dtype == KDA_BF16, a, q_out, k_out, hip_stream(stream)));
 }
 
@@ -358,6 +358,7 @@ kda_status kda_qknorm_backward(const void *q, const void *k, int64_t q_stride, i
         for (int j = 0; j < i; ++j)
             if (rows_meet(outs[i], outs[j])) return KDA_ERR_INVALID_ARG;
     }
+    if (!kda_qknorm_fits(dtype == KDA_BF16, a, true)) return KDA_ERR_UNSUPPORTED;
     // without tokens the weights' gradients are still written (zeros)
     return from_hip(kda_launch_qknorm_backward(dtype == KDA_BF16, grad_dtype == KDA_BF16, a, dq_out, dk_out, dq_stride, dk_stride,
                                                dq, dk, dq_weight, dk_weight, workspace, hip_stream(stream)));

@@ -7,25 +7,11 @@
 // conversions round to nearest, ties to even: a code is rounded once.
 #pragma once
 
-#include <hip/hip_runtime.h>
-#include <stdint.h>
+#include "kda_lanes.hpp"
 
 namespace kda {
 
 constexpr int MXB = 32;   // values of a block
-
-// A lane's value from another lane, without the LDS unit.
-template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t x)
-{
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
-}
-template <int CTRL> __device__ __forceinline__ float dpp(float x) { return __uint_as_float(dpp<CTRL>(__float_as_uint(x))); }
-constexpr int DPP_XOR1 = 0xb1;          // quad_perm [1,0,3,2]
-constexpr int DPP_XOR2 = 0x4e;          // quad_perm [2,3,0,1]
-constexpr int DPP_HALF_MIRROR = 0x141;  // i -> 7 - i in groups of eight
-constexpr int DPP_REVERSE4 = 0x1b;      // quad_perm [3,2,1,0]
-constexpr int DPP_MIRROR = 0x140;       // i -> 15 - i in rows of 16
-constexpr int DPP_ROR8 = 0x128;         // i -> i ^ 8 in rows of 16
 
 // decode: the raw numbers of a word's codes.  encode: the codes of a word's values
 // in a block with this scale byte (0 to 254).  The scaled conversions take a scale

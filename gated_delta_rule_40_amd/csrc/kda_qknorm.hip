@@ -11,9 +11,16 @@
 // not rotated.  So a pair never leaves its lane, every value is read once and
 // written once, and HBM's rate is the bound.  A workgroup takes some tokens of q
 // or of k; the cosines and sines of its tokens are formed once for all heads,
-// angles in fp64 and reduced there, and lie in LDS.
+// angles in fp64 and reduced there, and lie in LDS, while the heads are read.
+//
+// One MI355X, bf16, replays of a graph: 65,536 tokens of 32 and 32 heads of 128, no
+// rotation, 354 us (6.1 TB/s), its gradients 501 us (6.4), from fp32 ones 674 (6.4);
+// 32,768 tokens of 32 and 8 heads with weights, three axes, 126 us (5.3) and 194 (5.2):
+// there the wait for the table shows.  64 tokens of 32 and 32 heads 3.5 us, a launch's
+// own time.
 #include "kda_colsum.hpp"
 #include "kda_device.hpp"
+#include "kda_lanes.hpp"
 #include "kda_layer.hpp"
 
 #include <algorithm>
@@ -22,10 +29,14 @@
 namespace kda {
 
 constexpr int QK_THREADS = 256;
-constexpr int QK_ITEMS = 2;            // heads a lane's group takes at once
 constexpr int QK_MAX_PARTIALS = 1024;  // workgroups of the backward that sum a weight's gradient, of q and of k each
 
 enum { ROT_NONE = 0, ROT_HALVES = 1, ROT_NEIGHBOURS = 2 };
+
+// Heads that a lane's group reads at once: more where a table of turns has to be waited
+// for (32,768 tokens of 32 and 8 heads, four: 129 us, two: 139), but not in the gradients,
+// whose registers they would take (196, 210 with three).
+constexpr int qk_items(int rot, bool back) { return rot && !back ? 4 : 2; }
 
 // One of q and k: its arrays, and the workgroups that take it.
 struct Heads {
@@ -38,6 +49,7 @@ struct Heads {
     int32_t heads;
     float scale;
     int32_t tile, groups;   // tokens of a tile; workgroups
+    uint32_t per_head;      // 2^32 / heads, rounded up
 };
 
 struct QkShape {
@@ -46,6 +58,7 @@ struct QkShape {
     const float *inv_freq;
     int32_t T, d, rot, axes;
     int32_t slots, rot_slots, lanes;   // slots of a head, those rotated, lanes of a head (a power of two)
+    uint32_t per_pair;                 // 2^32 / (rot / 2), rounded up (not used for one pair)
     float mean, eps;                   // m; with norm == 0 no division
     int32_t norm;
 };
@@ -67,33 +80,51 @@ template <int VW, int ROT> struct Slot {
     }
 };
 
+// VW consecutive values, past the caches (65,536 tokens of 32 and 32 heads: 354 us, 396
+// through them; 512 tokens 5.3 us either way; a branch between the two costs 4 %).
 template <typename T, int VW> struct QkPiece {
     typedef T raw __attribute__((ext_vector_type(VW)));
     typedef raw mem __attribute__((aligned(sizeof(T))));
-    static __device__ __forceinline__ raw load(const T *p) { return *reinterpret_cast<const mem *>(p); }
+    static __device__ __forceinline__ raw load(const T *p) { return __builtin_nontemporal_load(reinterpret_cast<const mem *>(p)); }
     static __device__ __forceinline__ void store(T *p, const float *v) {
         raw r;
 #pragma unroll
         for (int j = 0; j < VW; ++j) r[j] = from_f<T>(v[j]);
-        *reinterpret_cast<mem *>(p) = r;
+        __builtin_nontemporal_store(r, reinterpret_cast<mem *>(p));
     }
 };
+
+// cos and sin of an angle: less whole quarters of a turn in fp64 (pi / 2 in two
+// pieces), then the Taylor series of both on [-pi / 4, pi / 4], whose next terms are
+// below 2^-28 there.
+__device__ __forceinline__ float2 cos_sin(double angle)
+{
+    const double quarters = __builtin_rint(angle * 0.63661977236758134);
+    double rest = __builtin_fma(-quarters, 1.5707963267948966, angle);
+    rest = __builtin_fma(-quarters, 6.123233995736766e-17, rest);
+    const float r = (float)rest, z = r * r;
+    float sn = __builtin_fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+    sn = __builtin_fmaf(z, sn, 1.f / 120.f);
+    sn = __builtin_fmaf(z, sn, -1.f / 6.f);
+    sn = __builtin_fmaf(r * z, sn, r);
+    float cs = __builtin_fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+    cs = __builtin_fmaf(z, cs, -1.f / 720.f);
+    cs = __builtin_fmaf(z, cs, 1.f / 24.f);
+    cs = __builtin_fmaf(z, cs, -0.5f);
+    cs = __builtin_fmaf(z, cs, 1.f);
+    const int q = (int)(int64_t)quarters;   // (its last two bits; an angle that is no number gives NaN above)
+    const float a = q & 1 ? sn : cs, b = q & 1 ? cs : sn;
+    return float2{(q + 1) & 2 ? -a : a, q & 2 ? -b : b};
+}
 
 // cos and sin of tokens [t0, t0 + count) into table[token][pair]
 __device__ __forceinline__ void turn_table(const QkShape &sh, int64_t t0, int32_t count, float2 *table)
 {
     const int32_t pairs = sh.rot / 2;
-    for (int32_t i = threadIdx.x; i < count * pairs; i += blockDim.x) {
-        const int32_t t = i / pairs, j = i % pairs;
+    for (int32_t i = threadIdx.x; i < count * pairs; i += QK_THREADS) {
+        const int32_t t = pairs == 1 ? i : (int32_t)__umulhi((uint32_t)i, sh.per_pair), j = i - t * pairs;   // i / pairs
         const int32_t axis = sh.pair_axis ? min(max(sh.pair_axis[j], 0), sh.axes - 1) : 0;
-        const double angle = (double)sh.positions[(int64_t)axis * sh.T + t0 + t] * (double)sh.inv_freq[j];
-        // less whole turns, 2 pi in two pieces
-        const double turns = __builtin_rint(angle * 0.15915494309189535);
-        double r = __builtin_fma(-turns, 6.283185307179586, angle);
-        r = __builtin_fma(-turns, 2.4492935982947064e-16, r);
-        float sn, cs;
-        sincosf((float)r, &sn, &cs);
-        table[i] = float2{cs, sn};
+        table[i] = cos_sin((double)sh.positions[(int64_t)axis * sh.T + t0 + t] * (double)sh.inv_freq[j]);
     }
 }
 
@@ -104,9 +135,15 @@ template <int VW, int ROT> __device__ __forceinline__ float &second_of(float *v,
 // the sums over a head's lanes
 template <int M> __device__ __forceinline__ void head_sums(float (&s)[M], int32_t lanes)
 {
-    for (int off = lanes >> 1; off > 0; off >>= 1)
 #pragma unroll
-        for (int m = 0; m < M; ++m) s[m] += __shfl_xor(s[m], off);
+    for (int m = 0; m < M; ++m) {
+        if (lanes >= 2) s[m] += dpp<DPP_XOR1>(s[m]);
+        if (lanes >= 4) s[m] += dpp<DPP_XOR2>(s[m]);
+        if (lanes >= 8) s[m] += dpp<DPP_HALF_MIRROR>(s[m]);
+        if (lanes >= 16) s[m] += dpp<DPP_MIRROR>(s[m]);
+        if (lanes >= 32) s[m] = add_xor16(s[m]);
+        if (lanes >= 64) s[m] = add_xor32(s[m]);
+    }
 }
 
 // The forward and the gradients walk the same items: (token, head) number
@@ -116,6 +153,7 @@ __global__ __launch_bounds__(QK_THREADS) void kda_qknorm_kernel(QkShape sh)
 {
     typedef QkPiece<T, VW> P;
     typedef QkPiece<G, VW> PG;
+    constexpr int ITEMS = qk_items(ROT, BACK);
     extern __shared__ float2 table[];
     const bool second = (int32_t)blockIdx.x >= sh.of[0].groups;
     const Heads hd = second ? sh.of[1] : sh.of[0];
@@ -135,59 +173,68 @@ __global__ __launch_bounds__(QK_THREADS) void kda_qknorm_kernel(QkShape sh)
             w[c][j] = hd.weight && s < sh.slots && (j < VW || sl.n1) ? hd.weight[(j < VW ? sl.c0 : sl.c1 - VW) + j] : 1.f;
     }
 
+    struct Batch {
+        typename P::raw x[ITEMS][C][2];
+        typename PG::raw dy[ITEMS][C][2];
+        int32_t token[ITEMS];
+        int64_t at[ITEMS];
+        bool live[ITEMS];
+    };
     for (int64_t t0 = (int64_t)group * hd.tile; t0 < sh.T; t0 += (int64_t)hd.groups * hd.tile) {
         const int32_t count = (int32_t)min((int64_t)hd.tile, sh.T - t0), items = count * hd.heads;
-        if (ROT) {
-            __syncthreads();
-            turn_table(sh, t0, count, table);
-            __syncthreads();
-        }
-        for (int32_t i0 = g0; i0 - g0 < items; i0 += per * QK_ITEMS) {
-            typename P::raw x[QK_ITEMS][C][2];
-            typename PG::raw dy[QK_ITEMS][C][2];
-            int32_t token[QK_ITEMS];
-            int64_t at[QK_ITEMS];
-            bool live[QK_ITEMS];
+        // reads the heads of items i0, i0 + per, ...
+        const auto fetch = [&](int32_t i0) {
+            Batch in;
 #pragma unroll
-            for (int u = 0; u < QK_ITEMS; ++u) {
+            for (int u = 0; u < ITEMS; ++u) {
                 const int32_t item = i0 + u * per;
-                live[u] = item < items;
-                token[u] = live[u] ? item / hd.heads : 0;
-                const int32_t head = live[u] ? item % hd.heads : 0;
-                at[u] = ((t0 + token[u]) * hd.heads + head) * sh.d;
-                const T *row = xs + (t0 + token[u]) * hd.stride + (int64_t)head * sh.d;
+                in.live[u] = item < items;
+                // item / heads (items are below 2^12 where a tile has several tokens)
+                in.token[u] = !in.live[u] || hd.tile == 1 ? 0 : hd.heads == 1 ? item : (int32_t)__umulhi((uint32_t)item, hd.per_head);
+                const int32_t head = in.live[u] ? item - in.token[u] * hd.heads : 0;
+                in.at[u] = ((t0 + in.token[u]) * hd.heads + head) * sh.d;
+                const T *row = xs + (t0 + in.token[u]) * hd.stride + (int64_t)head * sh.d;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    x[u][c][0] = x[u][c][1] = typename P::raw{};
-                    if (BACK) dy[u][c][0] = dy[u][c][1] = typename PG::raw{};
+                    in.x[u][c][0] = in.x[u][c][1] = typename P::raw{};
+                    if (BACK) in.dy[u][c][0] = in.dy[u][c][1] = typename PG::raw{};
                     const int32_t s = slot0 + c * sh.lanes;
                     if (s >= sh.slots) continue;
                     const Slot<VW, ROT> sl(sh, s);
-                    x[u][c][0] = P::load(row + sl.c0);
-                    if (sl.n1) x[u][c][1] = P::load(row + sl.c1);
+                    in.x[u][c][0] = P::load(row + sl.c0);
+                    if (sl.n1) in.x[u][c][1] = P::load(row + sl.c1);
                     if (BACK) {
-                        dy[u][c][0] = PG::load(dys + at[u] + sl.c0);
-                        if (sl.n1) dy[u][c][1] = PG::load(dys + at[u] + sl.c1);
+                        in.dy[u][c][0] = PG::load(dys + in.at[u] + sl.c0);
+                        if (sl.n1) in.dy[u][c][1] = PG::load(dys + in.at[u] + sl.c1);
                     }
                 }
             }
+            return in;
+        };
+        Batch in = fetch(g0);
+        if (ROT) {   // the table while they arrive
+            turn_table(sh, t0, count, table);
+            __syncthreads();
+        }
+        for (int32_t i0 = g0; i0 - g0 < items; i0 += per * ITEMS) {
+            if (i0 != g0) in = fetch(i0);
 #pragma unroll
-            for (int u = 0; u < QK_ITEMS; ++u) {
+            for (int u = 0; u < ITEMS; ++u) {
                 float v[C][2 * VW], e[C][2 * VW];
                 float sum[BACK ? 2 : 1] = {};
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int32_t s = slot0 + c * sh.lanes;
 #pragma unroll
-                    for (int j = 0; j < VW; ++j) v[c][j] = to_f(x[u][c][0][j]), v[c][VW + j] = to_f(x[u][c][1][j]);
+                    for (int j = 0; j < VW; ++j) v[c][j] = to_f(in.x[u][c][0][j]), v[c][VW + j] = to_f(in.x[u][c][1][j]);
                     if (BACK) {
 #pragma unroll
                         for (int j = 0; j < VW; ++j) {
-                            e[c][j] = to_f(dy[u][c][0][j]) * hd.scale;
-                            e[c][VW + j] = to_f(dy[u][c][1][j]) * hd.scale;
+                            e[c][j] = to_f(in.dy[u][c][0][j]) * hd.scale;
+                            e[c][VW + j] = to_f(in.dy[u][c][1][j]) * hd.scale;
                         }
                         if (ROT && s < sh.rot_slots) {
-                            const float2 *turn = table + token[u] * pairs + s * VW;
+                            const float2 *turn = table + in.token[u] * pairs + s * VW;
 #pragma unroll
                             for (int j = 0; j < VW; ++j) {
                                 float &a = first_of<VW, ROT>(e[c], j), &b = second_of<VW, ROT>(e[c], j);
@@ -211,13 +258,13 @@ __global__ __launch_bounds__(QK_THREADS) void kda_qknorm_kernel(QkShape sh)
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int32_t s = slot0 + c * sh.lanes;
-                    if (s >= sh.slots || !live[u]) continue;
+                    if (s >= sh.slots || !in.live[u]) continue;
                     const Slot<VW, ROT> sl(sh, s);
                     if (!BACK) {
 #pragma unroll
                         for (int j = 0; j < 2 * VW; ++j) v[c][j] *= inv * hd.scale, v[c][j] *= w[c][j];
                         if (ROT && s < sh.rot_slots) {
-                            const float2 *turn = table + token[u] * pairs + s * VW;
+                            const float2 *turn = table + in.token[u] * pairs + s * VW;
 #pragma unroll
                             for (int j = 0; j < VW; ++j) {
                                 float &a = first_of<VW, ROT>(v[c], j), &b = second_of<VW, ROT>(v[c], j);
@@ -227,8 +274,8 @@ __global__ __launch_bounds__(QK_THREADS) void kda_qknorm_kernel(QkShape sh)
                                 a = a1;
                             }
                         }
-                        P::store(ys + at[u] + sl.c0, v[c]);
-                        if (sl.n1) P::store(ys + at[u] + sl.c1, v[c] + VW);
+                        P::store(ys + in.at[u] + sl.c0, v[c]);
+                        if (sl.n1) P::store(ys + in.at[u] + sl.c1, v[c] + VW);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 2 * VW; ++j) {
@@ -236,13 +283,14 @@ __global__ __launch_bounds__(QK_THREADS) void kda_qknorm_kernel(QkShape sh)
                             v[c][j] = inv * (e[c][j] * w[c][j] - along * v[c][j]);
                         }
                         // (a row of dx: the same token and head, at its own stride)
-                        T *row = ys + (t0 + token[u]) * hd.y_stride + (at[u] - (t0 + token[u]) * hd.heads * sh.d);
+                        T *row = ys + (t0 + in.token[u]) * hd.y_stride + (in.at[u] - (t0 + in.token[u]) * hd.heads * sh.d);
                         P::store(row + sl.c0, v[c]);
                         if (sl.n1) P::store(row + sl.c1, v[c] + VW);
                     }
                 }
             }
         }
+        if (ROT) __syncthreads();   // the table is done with
     }
     if (!BACK || !hd.partial) return;
     // the groups' sums of a slot's values, added in order by the first
@@ -284,17 +332,24 @@ __global__ __launch_bounds__(COLSUM_THREADS) void kda_qknorm_weights_kernel(cons
 }
 
 // ---------------------------------------------------------------- host
-template <int VW, int C> void lay_out(QkShape &sh, int64_t most_groups)
+// The slots and lanes of a head, and the tiles: as many tokens as a workgroup takes
+// heads at once, `items` a lane's group.
+template <int VW, int C> void lay_out(QkShape &sh, int items)
 {
     sh.rot_slots = sh.rot / 2 / VW;
     sh.slots = sh.rot_slots + ((sh.d - sh.rot + 1) / 2 + VW - 1) / VW;
+    sh.per_pair = sh.rot > 2 ? (uint32_t)((((uint64_t)1 << 32) + sh.rot / 2 - 1) / (sh.rot / 2)) : 0;
     sh.lanes = 1;
     while (sh.lanes * C < sh.slots) sh.lanes *= 2;
-    const int32_t at_once = QK_THREADS / sh.lanes * QK_ITEMS;
+    const int32_t at_once = QK_THREADS / sh.lanes * items;
     for (Heads &h : sh.of) {
         h.tile = h.heads ? (at_once + h.heads - 1) / h.heads : 1;
-        const int64_t tiles = ((int64_t)sh.T + h.tile - 1) / h.tile;
-        h.groups = h.heads ? (int32_t)(tiles < most_groups ? tiles : most_groups) : 0;
+        // (a table of 32 KB at most: five workgroups a CU)
+        if (sh.rot) h.tile = std::min(h.tile, std::max(1, 4096 / (sh.rot / 2)));
+        h.per_head = h.heads > 1 ? (uint32_t)((((uint64_t)1 << 32) + h.heads - 1) / h.heads) : 0;
+        h.groups = h.heads ? (int32_t)(((int64_t)sh.T + h.tile - 1) / h.tile) : 0;
+        // sums of a weight's gradient: few workgroups, which take several tiles
+        if (h.partial) h.groups = std::min(h.groups, QK_MAX_PARTIALS);
     }
 }
 
@@ -325,7 +380,7 @@ template <typename T, typename Fn> auto with_width(const QkShape &sh, Fn f)
 template <typename T, typename G, bool BACK> hipError_t qknorm(QkShape sh, int mode, hipStream_t s)
 {
     return with_width<T>(sh, [&](auto w, auto c) {
-        lay_out<w(), c()>(sh, BACK ? QK_MAX_PARTIALS : INT32_MAX);
+        lay_out<w(), c()>(sh, qk_items(mode, BACK));
         return mode == ROT_NONE     ? run_qknorm<T, G, w(), c(), ROT_NONE, BACK>(sh, s)
                : mode == ROT_HALVES ? run_qknorm<T, G, w(), c(), ROT_HALVES, BACK>(sh, s)
                                     : run_qknorm<T, G, w(), c(), ROT_NEIGHBOURS, BACK>(sh, s);
@@ -341,8 +396,8 @@ static int qk_mode(int32_t rot, bool interleaved) { return rot == 0 ? ROT_NONE :
 static QkShape qk_shape(const KdaQkNorm &a)
 {
     QkShape sh{};
-    sh.of[0] = {a.q, nullptr, nullptr, a.q_weight, nullptr, a.q_stride, 0, a.q_heads, a.q_scale, 0, 0};
-    sh.of[1] = {a.k, nullptr, nullptr, a.k_weight, nullptr, a.k_stride, 0, a.k_heads, 1.f, 0, 0};
+    sh.of[0] = {a.q, nullptr, nullptr, a.q_weight, nullptr, a.q_stride, 0, a.q_heads, a.q_scale, 0, 0, 0};
+    sh.of[1] = {a.k, nullptr, nullptr, a.k_weight, nullptr, a.k_stride, 0, a.k_heads, 1.f, 0, 0, 0};
     sh.positions = a.positions, sh.pair_axis = a.pair_axis, sh.inv_freq = a.inv_freq;
     sh.T = a.tokens, sh.d = a.dim, sh.rot = a.rot, sh.axes = a.axes;
     sh.mean = a.norm == 2 ? 1.f / a.dim : 1.f, sh.eps = a.eps, sh.norm = a.norm;
@@ -374,7 +429,7 @@ hipError_t kda_launch_qknorm_backward(bool bf16, bool grad_bf16, const KdaQkNorm
         typedef decltype(t) T;
         typedef decltype(g) G;
         with_width<T>(sh, [&](auto w, auto c) {
-            lay_out<w(), c()>(sh, QK_MAX_PARTIALS);
+            lay_out<w(), c()>(sh, qk_items(mode, true));
             return 0;
         });
         groups[0] = sh.of[0].groups, groups[1] = sh.of[1].groups;
@@ -388,11 +443,11 @@ hipError_t kda_launch_qknorm_backward(bool bf16, bool grad_bf16, const KdaQkNorm
     return hipGetLastError();
 }
 
-bool kda_qknorm_fits(bool bf16, const KdaQkNorm &a)
+bool kda_qknorm_fits(bool bf16, const KdaQkNorm &a, bool back)
 {
     QkShape sh = qk_shape(a);
     const auto groups = [&](auto w, auto c) {
-        lay_out<w(), c()>(sh, INT32_MAX);
+        lay_out<w(), c()>(sh, qk_items(qk_mode(a.rot, a.interleaved), back));
         return (int64_t)sh.of[0].groups + sh.of[1].groups;
     };
     return kda_grid_ok(bf16 ? with_width<bf16_t>(sh, groups) : with_width<float>(sh, groups), QK_THREADS);
