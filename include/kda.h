@@ -605,7 +605,8 @@ kda_status kda_rmsnorm_backward(const void *x, const float *weight, const void *
  *   q_weight, k_weight [head_dim]                fp32, or NULL for ones
  *   positions     [num_axes, num_tokens]         int32, DEVICE; any values
  *   inv_freq      [rot_dim / 2]                  fp32, DEVICE: radians a position.
- *                 An angle is formed in fp64, so that far positions keep it.
+ *                 An angle is formed in fp64, within 2^-53 of itself, so that far
+ *                 positions keep it (angles of 2^50 and more are unspecified).
  *   pair_axis     [rot_dim / 2]                  int32, DEVICE: the axis that
  *                 turns a pair (time, height, width, in any order; entries
  *                 outside [0, num_axes) are clamped), or NULL: all by axis 0
