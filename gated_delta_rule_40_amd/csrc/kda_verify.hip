@@ -10,11 +10,10 @@
 //
 // HBM bounds large calls, latency small ones: the counting takes two dependent reads,
 // each kernel about three.  One MI355X, fp32, four drafts, both kernels of a replayed
-// graph: 256 sequences of 131,072 49.6 us, 256 x 32,000 20.8 us, one of 32,000 11.2 us.
-// Read past the caches, rows take 10-20 % less (256 x 131,072: 59.6 us through them).
-// One launch with a workgroup of 1,024 threads a sequence and the sums in LDS took
-// 15.5 us for one sequence of 32,000, 28.9 for one of 131,072 (13.4 with two launches)
-// and 60.9 for 256: a CU alone does not read a row fast enough.
+// graph: 256 sequences of 131,072 42 us (kernel 1 37, 5.8 TB/s), 256 x 32,000 16 us, one
+// of 32,000 6.3 us.  Read through the caches, rows take 10-20 % longer.  One launch with
+// a workgroup of 1,024 threads a sequence and the sums in LDS was slower for all but
+// vocabularies of 8,000: a CU alone does not read a row fast enough.
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
 #include "kda_seq.hpp"
@@ -144,15 +143,14 @@ template <typename T, int K> __device__ __forceinline__ void part_sums(const typ
 // sum, in the order of the threads.
 struct Search {
     double waves[VF_WAVES];
-    double base;           // the sum before the part that is searched
-    int32_t first, last;   // the first place that passes the mark; the last that has a weight
+    double base;                                // the sum before the part that is searched
+    int32_t firsts[VF_WAVES], lasts[VF_WAVES];
 
     // The sum before this thread's places, and of all (called by the whole workgroup).
     __device__ __forceinline__ double before(double run, double &total) {
         const double s = wave_scan(run);
         __syncthreads();   // (the search before is over)
         if ((threadIdx.x & 63) == 63) waves[threadIdx.x >> 6] = s;
-        if (threadIdx.x == 0) first = INT32_MAX, last = -1;
         __syncthreads();
         double up = s - run;
         total = 0.;
@@ -163,12 +161,20 @@ struct Search {
         }
         return up;
     }
-    __device__ __forceinline__ void found(int32_t mine_first, int32_t mine_last) {
-        if (mine_first != INT32_MAX) atomicMin(&first, mine_first);
-        if (mine_last >= 0) atomicMax(&last, mine_last);
+    // From every thread's first place that passes the mark (INT32_MAX: none) and last
+    // that has a weight (-1), those of all: places go up with the threads, so they are
+    // the lowest lane's and the highest lane's.  (Atomics on two words of LDS, 256
+    // threads each, took 2 to 4 us.)
+    __device__ __forceinline__ void found(int32_t &first, int32_t &last) {
+        const uint64_t passed = __ballot(first != INT32_MAX), some = __ballot(last >= 0);
+        const int32_t f = __shfl(first, passed ? __builtin_ctzll(passed) : 0);
+        const int32_t l = __shfl(last, some ? 63 - __builtin_clzll(some) : 0);
+        if ((threadIdx.x & 63) == 0) firsts[threadIdx.x >> 6] = f, lasts[threadIdx.x >> 6] = l;
         __syncthreads();
+        first = INT32_MAX, last = -1;
+#pragma unroll
+        for (int i = 0; i < VF_WAVES; ++i) first = min(first, firsts[i]), last = max(last, lasts[i]);
     }
-    __device__ __forceinline__ int32_t place() const { return first != INT32_MAX ? first : last; }
 
     // The next token, given the sums of the row's parts.  The first place x with
     // w[x] > 0 whose running sum is above the mark lies in the first part with a
@@ -206,8 +212,9 @@ struct Search {
                 }
                 sum += s;
             }
-            found(mine_first, mine_last);
-            part = max(place(), 0);
+            int32_t first = mine_first, last = mine_last;
+            found(first, last);
+            part = max(first != INT32_MAX ? first : last, 0);
             if (part >= p0 && part < p1) base = part == mine_first ? first_base : last_base;
             end = part + 1;
             __syncthreads();
@@ -225,17 +232,17 @@ struct Search {
             for (int j = 0; j < VW; ++j) y[j] = w.weight(x0 + j, a[j], b[j]), run += y[j];
             double all;
             sum = from + before(run, all);
-            int32_t mine_first = INT32_MAX, mine_last = -1;
+            int32_t first = INT32_MAX, last = -1;
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
                 sum += y[j];
                 if (y[j] > 0.) {
-                    mine_last = x0 + j;
-                    if (mine_first == INT32_MAX && sum > mark) mine_first = x0 + j;
+                    last = x0 + j;
+                    if (first == INT32_MAX && sum > mark) first = x0 + j;
                 }
             }
-            found(mine_first, mine_last);
-            if (place() >= 0) next = place();
+            found(first, last);
+            next = first != INT32_MAX ? first : max(next, last);
             if (first != INT32_MAX) break;
             from += all;
         }
@@ -288,8 +295,8 @@ __global__ __launch_bounds__(VF_THREADS) void kda_verify_pick_kernel(Verify<T> i
 
 inline int32_t part_count(int32_t vocab) { return (int32_t)(((int64_t)vocab + VF_PART - 1) / VF_PART); }
 // Parts of a wave: two from 16,384 parts on (us of both kernels, one and two: 256 rows of
-// 131,072 53.2 and 49.6, 256 x 200,000 72.9 and 65.7; 64 x 131,072 22.9 and 23.0,
-// 1 x 32,000 11.2 and 12.1).
+// 131,072 46.3 and 42.4, 400 of 65,537 39.4 and 37.2, 128 of 131,072 26.7 and 25.7; 64 of
+// 131,072 15.8 and 16.4, one of 32,000 6.1 and 7.0).
 inline int parts_each(int32_t N, int32_t vocab)
 {
     return N * (int64_t)part_count(vocab) < 16384 ? 1 : 2;
