@@ -823,11 +823,19 @@ def kda_qknorm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, norm
     dev, qs, ks, form = _qk_form(q, k, q_weight, k_weight, norm, eps, q_scale, positions, inv_freq, pair_axis, interleaved)
     dt, d = q.dtype, qs[2]
     lib = _lib or load()
-    grads = _grads(grads, dev, {"dq": (dt, qs), "dk": None if k is None else (dt, ks),
-                                "dq_weight": None if q_weight is None else (_F32, (d,)),
-                                "dk_weight": None if k_weight is None else (_F32, (d,))}, stream)
     _require(isinstance(dq_out, torch.Tensor), "dq_out must be a tensor")
     gt = dq_out.dtype if dq_out.dtype is _F32 else dt
+    pdqo = _addr("dq_out", dq_out, dev, gt, qs)
+    pdko = None if k is None else _addr("dk_out", dk_out, dev, gt, ks)
+    if grads is None and stream is None:
+        like = torch.empty_like       # (of a contiguous tensor: half the time of torch.empty)
+        grads = {"dq": like(dq_out, dtype=dt), "dk": None if k is None else like(dk_out, dtype=dt),
+                 "dq_weight": None if q_weight is None else like(q_weight),
+                 "dk_weight": None if k_weight is None else like(k_weight)}
+    else:
+        grads = _grads(grads, dev, {"dq": (dt, qs), "dk": None if k is None else (dt, ks),
+                                    "dq_weight": None if q_weight is None else (_F32, (d,)),
+                                    "dk_weight": None if k_weight is None else (_F32, (d,))}, stream)
     out = []
     for name, x, shape in (("dq", q, qs), ("dk", k, ks)):
         if x is None:
@@ -841,8 +849,7 @@ def kda_qknorm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, norm
     (pdq, sdq), (pdk, sdk) = out
     pqw = _addr_if("grads['dq_weight']", grads.get("dq_weight"), dev, _F32, (d,))
     pkw = _addr_if("grads['dk_weight']", grads.get("dk_weight"), dev, _F32, (d,))
-    args = (*form, _DTYPE_CODE[gt], _addr("dq_out", dq_out, dev, gt, qs),
-            None if k is None else _addr("dk_out", dk_out, dev, gt, ks), sdq, sdk, pdq, pdk, pqw, pkw)
+    args = (*form, _DTYPE_CODE[gt], pdqo, pdko, sdq, sdk, pdq, pdk, pqw, pkw)
     ws = pws = None
     nbytes = 0
     if pqw is not None or pkw is not None:
