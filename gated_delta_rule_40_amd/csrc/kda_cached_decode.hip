@@ -110,8 +110,9 @@ __global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_tokens_kernel(
     const int my_row = lane % CD_WROWS;
     const auto read = [&](int32_t t) {
         const int64_t row = ((int64_t)(t0 + t) * H + h) * CD, at = row + wave * CD_WROWS + my_row;
-        Token<T> x;
-        x.k = k[at], x.q = q[at], x.g = g[at];
+        Token<T> x{};
+        x.k = k[at], x.g = g[at];
+        if (OUT) x.q = q[at];
         x.v = *reinterpret_cast<const two_mem *>(v + row + 2 * lane);
         x.beta = beta[(int64_t)(t0 + t) * H + h];
         return x;

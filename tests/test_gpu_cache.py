@@ -280,6 +280,8 @@ def test_several_tokens_are_the_same_tokens_one_by_one(fmt):
     assert torch.equal(again, o)
     o2, c2, s2 = decode(p, fmt, write=True)
     assert torch.equal(o2, o) and torch.equal(c, c2) and torch.equal(s, s2)   # the same bits again
+    _, c2, s2 = decode(p, fmt, write=True, out=False)
+    assert torch.equal(c, c2) and torch.equal(s, s2)                          # and without outputs
 
 
 def test_decay_to_nothing_and_blocks_without_a_number():
