@@ -303,7 +303,8 @@ __global__ __launch_bounds__(QK_THREADS, 3) void kda_qknorm_kernel(QkShape sh)
 #pragma unroll
                         for (int j = 0; j < 2 * VW; ++j) {
                             dw[c][j] += e[c][j] * (v[c][j] * inv);
-                            v[c][j] = inv * (e[c][j] * w[c][j] - along * v[c][j]);
+                            // (a selection: without a norm an infinite x has no part in its gradient)
+                            v[c][j] = inv * (e[c][j] * w[c][j] - (sh.norm ? along * v[c][j] : 0.f));
                         }
                         // (the same token and head, at dx's own stride)
                         row = ys + (t0 + in.token[u]) * hd.y_stride + (in.at[u] - (t0 + in.token[u]) * hd.heads * sh.d);

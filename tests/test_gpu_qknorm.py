@@ -171,6 +171,18 @@ def test_heads_of_zeros_infinities_and_nan_stay_their_own():
     assert torch.all(torch.isfinite(g[~touched])) and torch.all(torch.isfinite(g[0, 1]))
 
 
+def test_without_a_norm_an_infinite_value_has_no_part_in_its_gradient():
+    p = make(5, 3, 2, 77, 20)
+    for x in (p["q"], p["k"]):
+        x[1, 0, 3], x[2, 1, 76], x[4, 1, 0] = float("inf"), float("nan"), float("-inf")
+    form = dict(norm="none", q_scale=0.5, **p["turn"])
+    g = K.kda_qknorm_backward(p["q"], p["k"], p["dq"], p["dk"], **form)
+    clean = [torch.nan_to_num(x, 0., 0., 0.) for x in (p["q"], p["k"])]
+    want = K.kda_qknorm_backward(*clean, p["dq"], p["dk"], **form)
+    for name in ("dq", "dk"):
+        assert bool(torch.isfinite(g[name]).all()) and torch.equal(g[name], want[name])
+
+
 def test_offsets_beyond_32_bits():
     """Tokens whose rows begin beyond 2^31 elements, in an array of which few rows are touched."""
     T, stride = 40, 1 << 26
