@@ -16,7 +16,7 @@
 //
 // One MI355X, bf16, replays of a graph: 65,536 tokens of 32 and 32 heads of 128, no
 // rotation, 348 us (6.2 TB/s), its gradients 501 us (6.4), from fp32 ones 674 (6.4);
-// 32,768 tokens of 32 and 8 heads with weights, three axes, 123 us (5.5) and 194 (5.2):
+// 32,768 tokens of 32 and 8 heads with weights, three axes, 122 us (5.5) and 185 (5.5):
 // there the wait for the table shows.  60,000 tokens of 8 and 8 heads of 77, fp32, 130 us
 // (4.6).  64 tokens of 32 and 32 heads 3.6 us, a launch's own time.
 #include "kda_colsum.hpp"
@@ -30,13 +30,16 @@
 namespace kda {
 
 constexpr int QK_THREADS = 256;
-constexpr int QK_MAX_PARTIALS = 1024;  // workgroups of the backward that sum a weight's gradient, of q and of k each
+// Workgroups of the backward that sum a weight's gradient, of q and of k each (32,768 tokens
+// of 32 and 8 heads, 384, 512, 768, 1,024: 213, 185, 186, 184 us; 16,384 of 16 and 2 heads of
+// 256: 108, 92, 94, 101).
+constexpr int QK_MAX_PARTIALS = 512;
 
 enum { ROT_NONE = 0, ROT_HALVES = 1, ROT_NEIGHBOURS = 2 };
 
 // Heads that a lane's group reads at once: more where a table of turns has to be waited
 // for (32,768 tokens of 32 and 8 heads, four: 126 us, two: 139), but not in the gradients,
-// whose registers they would take (194, 210 with three).
+// whose registers they would take (with 1,024 sums a weight 194, 210 with three).
 constexpr int qk_items(int rot, bool back) { return rot && !back ? 4 : 2; }
 
 // One of q and k: its arrays, and the workgroups that take it.
@@ -317,24 +320,26 @@ __global__ __launch_bounds__(QK_THREADS, 3) void kda_qknorm_kernel(QkShape sh)
         if (ROT) __syncthreads();   // the table is done with
     }
     if (!BACK || !hd.partial) return;
-    // the groups' sums of a slot's values, added in order by the first
+    // the sums of a slot's values over the groups, in order: a value a thread (32,768 tokens of
+    // 32 and 8 heads 185 us, 8 tokens 8.2; by the first group alone 190 and 14.5)
     float *fold = reinterpret_cast<float *>(table);
+    const int32_t pitch = QK_THREADS + sh.lanes;   // (values of a wave on different banks)
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int j = 0; j < 2 * VW; ++j) fold[(c * 2 * VW + j) * QK_THREADS + threadIdx.x] = dw[c][j];
+        for (int j = 0; j < 2 * VW; ++j) fold[(c * 2 * VW + j) * pitch + threadIdx.x] = dw[c][j];
     __syncthreads();
-    if (g0 > 0) return;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-#pragma unroll
-        for (int j = 0; j < 2 * VW; ++j) {
-            if (j < VW ? j < sl[c].f0 : j - VW < sl[c].f1) continue;
-            float sum = 0.f;
-            for (int32_t i = 0; i < per; ++i) sum += fold[(c * 2 * VW + j) * QK_THREADS + i * sh.lanes + lane];
-            hd.partial[(int64_t)group * sh.d + (j < VW ? sl[c].c0 : sl[c].c1 - VW) + j] = sum;
-        }
+    for (int32_t i = threadIdx.x; i < sh.lanes * C * 2 * VW; i += QK_THREADS) {
+        const int32_t l = i & (sh.lanes - 1), value = i / sh.lanes, j = value % (2 * VW), s = l + value / (2 * VW) * sh.lanes;
+        if (s >= sh.slots) continue;
+        const Slot of = slot_of<VW, ROT>(sh, s);
+        if (j < VW ? j < of.f0 : j - VW < of.f1) continue;
+        const float *part = fold + value * pitch + l;
+        float sum = 0.f;
+#pragma unroll 4
+        for (int32_t g = 0; g < per; ++g) sum += part[g * sh.lanes];
+        hd.partial[(int64_t)group * sh.d + (j < VW ? of.c0 : of.c1 - VW) + j] = sum;
     }
 }
 
@@ -376,7 +381,10 @@ template <int VW, int C> void lay_out(QkShape &sh, int mode, int items)
     while (sh.lanes * C < sh.slots) sh.lanes *= 2;
     const int32_t at_once = QK_THREADS / sh.lanes * items;
     for (Heads &h : sh.of) {
-        h.tile = h.heads ? (at_once + h.heads - 1) / h.heads : 1;
+        const auto tokens_of = [&](int32_t n) { return h.heads ? (n + h.heads - 1) / h.heads : 1; };
+        // a round of heads at least; more while 256 workgroups are left (64 tokens of 32 and 8
+        // heads with three axes, 2 and 8 tokens of k: 5.5 and 7.5 us)
+        h.tile = std::max(tokens_of(QK_THREADS / sh.lanes), std::min(tokens_of(at_once), sh.T / 256));
         // (a table of 32 KB at most: five workgroups a CU)
         if (sh.rot) h.tile = std::min(h.tile, std::max(1, 4096 / (sh.rot / 2)));
         h.per_head = h.heads > 1 ? (uint32_t)((((uint64_t)1 << 32) + h.heads - 1) / h.heads) : 0;
@@ -393,7 +401,7 @@ template <typename T, typename G, int VW, int C, int ROT, bool BACK> hipError_t 
     size_t lds = 0;
     if (ROT)
         for (const Heads &h : sh.of) lds = std::max(lds, sizeof(float2) * h.tile * (size_t)(sh.rot / 2));
-    if (BACK && (sh.of[0].partial || sh.of[1].partial)) lds = std::max(lds, sizeof(float) * QK_THREADS * C * 2 * VW);
+    if (BACK && (sh.of[0].partial || sh.of[1].partial)) lds = std::max(lds, sizeof(float) * (QK_THREADS + sh.lanes) * C * 2 * VW);
     hipLaunchKernelGGL((kda_qknorm_kernel<T, G, VW, C, ROT, BACK>), dim3((unsigned)groups), dim3(QK_THREADS), lds, s, sh);
     return hipGetLastError();
 }
