@@ -10,15 +10,16 @@
 // first and second members of VW rotated pairs, or two pieces of the part that is
 // not rotated.  So a pair never leaves its lane, every value is read once and
 // written once, and HBM's rate is the bound.  Where VW does not divide a part its
-// last piece is moved back over the one before: what both hold counts once.  A workgroup takes some tokens of q
-// or of k; the cosines and sines of its tokens are formed once for all heads,
-// angles in fp64 and reduced there, and lie in LDS, while the heads are read.
+// last piece is moved back over the one before: what both hold counts once.  A
+// workgroup takes some tokens of q or of k; the cosines and sines of its tokens are
+// formed once for all heads, angles in fp64 and reduced there, and lie in LDS, while
+// the heads are read.
 //
 // One MI355X, bf16, replays of a graph: 65,536 tokens of 32 and 32 heads of 128, no
 // rotation, 348 us (6.2 TB/s), its gradients 501 us (6.4), from fp32 ones 674 (6.4);
 // 32,768 tokens of 32 and 8 heads with weights, three axes, 122 us (5.5) and 185 (5.5):
 // there the wait for the table shows.  60,000 tokens of 8 and 8 heads of 77, fp32, 130 us
-// (4.6).  64 tokens of 32 and 32 heads 3.6 us, a launch's own time.
+// (4.6).  64 tokens of 32 and 32 heads 3.4 us, a launch's own time.
 #include "kda_colsum.hpp"
 #include "kda_device.hpp"
 #include "kda_lanes.hpp"

@@ -46,7 +46,7 @@ ARRAYS = {
     "kda_qknorm": (dict(q=HEADS, k=KHEADS, qw=256, kw=256, pos=2400, freq=64, axis=64, q_out=HEADS, k_out=KHEADS),
                    dict(q_out="q", k_out="k")),
     "kda_qknorm_backward": (dict(q=HEADS, k=KHEADS, qw=256, kw=256, pos=2400, freq=64, axis=64, dq_out=2 * HEADS,
-                                 dk_out=2 * KHEADS, dq=HEADS, dk=KHEADS, dqw=256, dkw=256, ws=2 * 1024 * 64 * 4),
+                                 dk_out=2 * KHEADS, dq=HEADS, dk=KHEADS, dqw=256, dkw=256, ws=2 * 512 * 64 * 4),
                             dict(dq="q", dk="k", dqw="", dkw="", ws="")),
     "kda_cache_store": (dict(src=1000, slots=20, cache=700, scales=28), dict(cache="", scales="")),
     "kda_cache_load": (dict(cache=700, scales=28, slots=20, dst=1000), dict(dst="")),
