@@ -13,14 +13,19 @@
 // which takes one barrier a token: every wave adds them up for itself.
 //
 // HBM bounds one token (33 KB of codes and scales a state, past the caches), vector
-// instructions several (about 380 a wave and token for 64 values a lane: the decay, two
-// products, the update, and the halving).  One MI355X, bf16, replays of a graph: 512
-// sequences of 32 heads, one token committed, fp8 104-106 us (5.5 TB/s), int8 106, fp4 88;
-// five tokens verified 213, committed without outputs 131; 8 x 8 heads 4.5.
+// instructions several (token by token about 390 a wave and token for 64 values a lane:
+// the decay, two products, the update, and the halving).  So calls with more tokens than
+// sequences take them in chunks, from one state, if they have outputs: 512 sequences of 32
+// heads, fp8, two, five and eight tokens verified 87, 168 and 290 us, token by token 105, 214
+// and 325; five of 64 x 16 in int8 16.4 and 18.7.  Without outputs b and the queries fall away
+// and chunks gain nothing (five committed 131 us, token by token 124).
+// One MI355X, bf16, replays of a graph: 512 sequences of 32 heads, one token committed, fp8
+// 103-106 us (5.5 TB/s), int8 106, fp4 88; 8 x 8 heads 4.4.
 // Waves that each had 32 columns of all rows needed no barrier, but their reads of 32
 // bytes a row bound them to 129 us; 8 columns by 8 rows a lane 119 (198 for five tokens
-// verified); decays kept apart from the state, as factors of its rows, gained 4 % for
-// five tokens and lost 1-4 % for one.
+// verified token by token); decays kept apart from the state, as factors of its rows, gained
+// 4 % for five tokens and lost 1-4 % for one; products by matrix instructions of 16 blocks
+// of 4 x 4 halved the vector instructions and took 270 us for 214.
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
 #include "kda_mx.hpp"
@@ -79,6 +84,46 @@ template <typename T> struct Token {
     two v;
     float g, beta;
 };
+
+// A lane's part of a state, rounded and written to its codes and scales.
+template <typename F> __device__ __forceinline__ void write_state(float (&s)[CD_ROWS][CD_COLS], uint8_t *codes, uint8_t *scales, int side)
+{
+    constexpr int WORDS = CD_COLS * F::BITS / 32, ROW_BYTES = CD * F::BITS / 8;
+    typedef uint32_t words __attribute__((ext_vector_type(WORDS)));
+    typedef words words_mem __attribute__((aligned(1)));
+    typedef uint32_t word_mem __attribute__((aligned(1)));
+    uint32_t top[CD_ROWS], most = 0;
+#pragma unroll
+    for (int i = 0; i < CD_ROWS; ++i) {
+        float largest = 0.f;
+#pragma unroll
+        for (int j = 0; j < CD_COLS; ++j) largest = mx_top(largest, s[i][j]);
+        top[i] = __float_as_uint(largest) & 0x7fffffffu;   // (as bits a NaN is above all others)
+        top[i] = max(top[i], dpp<DPP_XOR1>(top[i]));
+        most = max(most, top[i]);
+    }
+    if (__any(most >= 0x7f800000u)) {   // a block without a number, hardly ever: its codes are zeros
+#pragma unroll
+        for (int i = 0; i < CD_ROWS; ++i)
+#pragma unroll
+            for (int j = 0; j < CD_COLS; ++j) s[i][j] = top[i] >= 0x7f800000u ? 0.f : s[i][j];
+    }
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < CD_ROWS; ++i) {
+        const int new_sc = mx_scale_of<F>(top[i]), finite = min(new_sc, 254);
+        words y;
+#pragma unroll
+        for (int j = 0; j < WORDS; ++j) y[j] = F::encode(&s[i][j * 32 / F::BITS], finite);
+        __builtin_nontemporal_store(y, reinterpret_cast<words_mem *>(codes + i * CD_APART * ROW_BYTES));
+        // the row's four bytes, in all of its lanes; lane number i of a row keeps those of row i
+        uint32_t bytes = (uint32_t)new_sc << (8 * (side / 2));
+        bytes |= dpp<DPP_XOR2>(bytes);
+        bytes |= dpp<DPP_HALF_MIRROR>(bytes);
+        if (side == i) mine = bytes;
+    }
+    if (side < CD_ROWS) *reinterpret_cast<word_mem *>(scales + CD_APART * side * CD_BLOCKS) = mine;
+}
 
 // OUT: with outputs (else a and the states alone).
 template <typename T, typename F, bool OUT>
@@ -204,38 +249,203 @@ __global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_tokens_kernel(
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    if (!write || !kept) return;
-    uint32_t top[CD_ROWS], most = 0;
+    if (write && kept) write_state<F>(s, codes, scales + (entry + r0) * CD_BLOCKS, side);
+}
+
+// ---------------------------------------------------------------- several tokens
+// Up to CH tokens from one state: with c_t the decays up to token t, k_s^(t) the key of
+// token s decayed up to t,
+//     a_t = S^T (c_t k_t) + sum over s < t of (k_s^(t).k_t) f_s,   f_t = beta_t (v_t - a_t)
+//     o_t = S^T (c_t q_t) + sum over s <= t of (k_s^(t).q_t) f_s
+//     S'  = Diag(c) S + sum over s of k_s^(last) f_s^T
+// so the state is multiplied by all keys and queries as it is, without a barrier between
+// tokens, and moved on once (where it is only read, never).  No decay is divided by.
+// Six tokens spill registers (five tokens 171 us for 168), eight more (178); four leave one over.
+constexpr int CH = 5;
+
+template <typename T, typename F>
+__global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_chunk_kernel(
+    const T *q, const T *k, const T *v, const float *g, const float *beta, const int32_t *cu, const int32_t *num_tokens,
+    uint8_t *cache, uint8_t *scales, const int32_t *slots, int32_t write, int32_t num_slots, int32_t H,
+    uint32_t per_head, int32_t shift, int32_t T_tot, T *out)
+{
+    constexpr int WORDS = CD_COLS * F::BITS / 32;   // of a lane's codes in a row
+    constexpr int ROW_BYTES = CD * F::BITS / 8;
+    typedef uint32_t words __attribute__((ext_vector_type(WORDS)));
+    typedef words words_mem __attribute__((aligned(1)));
+    typedef uint32_t word_mem __attribute__((aligned(1)));
+    typedef typename Token<T>::two two;
+    typedef two two_mem __attribute__((aligned(sizeof(T))));
+    // of a wave's rows: c_t k_t and c_t q_t, then k_s^(last); c (and at first the scale bytes)
+    __shared__ float rows[CD_WAVES][CH][2][CD_WROWS], ends[CD_WAVES][CD_WROWS];
+    __shared__ float grams[CD_WAVES][2][CH][CH];        // a wave's part of k_s^(t).k_t and k_s^(t).q_t
+    __shared__ __attribute__((aligned(16))) float sums[CH][CD_WAVES][2][CD];   // of the waves: S^T (c_t k_t), S^T (c_t q_t)
+    __shared__ __attribute__((aligned(16))) float offs[CH][CD];                // f_t
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int side = lane % CD_LANES, r0 = lane / CD_LANES;
+    const uint32_t u = blockIdx.x;
+    const int32_t n = (int32_t)((uint64_t)u * per_head >> shift), h = (int32_t)u - n * H;   // u / H, u % H
+    const int32_t t0 = min(max(cu[n], 0), T_tot);
+    int32_t len = min(max(cu[n + 1], t0), T_tot) - t0;
+    if (num_tokens) len = min(len, max(num_tokens[n], 0));
+    const int32_t slot = slots[n];
+    if (len == 0) return;
+
+    const int my_row = lane % CD_WROWS, query = lane / CD_WROWS;   // (keys by the lower half of a wave, queries by the upper)
+    const bool kept = slot >= 0 && slot < num_slots;
+    const int64_t entry = (((int64_t)slot * H + h) * CD) + wave * CD_WROWS;   // rows before this wave's
+    uint8_t *const codes = cache + (entry + r0) * ROW_BYTES + side * (CD_COLS * F::BITS / 8);
+    words w[CD_ROWS];
+    uint32_t sc = 0x7f7f7f7f;
 #pragma unroll
-    for (int i = 0; i < CD_ROWS; ++i) {
-        float largest = 0.f;
-#pragma unroll
-        for (int j = 0; j < CD_COLS; ++j) largest = mx_top(largest, s[i][j]);
-        top[i] = __float_as_uint(largest) & 0x7fffffffu;   // (as bits a NaN is above all others)
-        top[i] = max(top[i], dpp<DPP_XOR1>(top[i]));
-        most = max(most, top[i]);
-    }
-    if (__any(most >= 0x7f800000u)) {   // a block without a number, hardly ever: its codes are zeros
+    for (int i = 0; i < CD_ROWS; ++i) w[i] = words{};
+    if (kept) {
+        sc = *reinterpret_cast<const word_mem *>(scales + (entry + my_row) * CD_BLOCKS);
 #pragma unroll
         for (int i = 0; i < CD_ROWS; ++i)
-#pragma unroll
-            for (int j = 0; j < CD_COLS; ++j) s[i][j] = top[i] >= 0x7f800000u ? 0.f : s[i][j];
+            w[i] = __builtin_nontemporal_load(reinterpret_cast<const words_mem *>(codes + i * CD_APART * ROW_BYTES));
     }
-    uint32_t mine = 0;
+    T kx[CH], qx[CH];
+    float gx[CH], bt[CH];
+    two vx[CH];
+    const int64_t step = (int64_t)H * CD;   // from token to token
+    const auto read = [&](int32_t from) {
+        const int64_t row0 = ((int64_t)(t0 + from) * H + h) * CD;
 #pragma unroll
-    for (int i = 0; i < CD_ROWS; ++i) {
-        const int new_sc = mx_scale_of<F>(top[i]), finite = min(new_sc, 254);
-        words y;
+        for (int t = 0; t < CH; ++t) {
+            kx[t] = qx[t] = T(0.f), gx[t] = bt[t] = 0.f, vx[t] = two{};
+            if (t < len - from) {
+                const int64_t row = row0 + t * step, at = row + wave * CD_WROWS;
+                kx[t] = (k + at)[my_row], qx[t] = (q + at)[my_row], gx[t] = (g + at)[my_row];
+                vx[t] = *reinterpret_cast<const two_mem *>((v + row) + 2 * lane);
+                bt[t] = beta[(int64_t)(t0 + from + t) * H + h];
+            }
+        }
+    };
+    read(0);
+    float s[CD_ROWS][CD_COLS], factor[CD_ROWS];
+    // the factors from raw numbers, which go with the keys and queries of the first tokens
+    ends[wave][my_row] = __uint_as_float(sc);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int j = 0; j < WORDS; ++j) y[j] = F::encode(&s[i][j * 32 / F::BITS], finite);
-        __builtin_nontemporal_store(y, reinterpret_cast<words_mem *>(codes + i * CD_APART * ROW_BYTES));
-        // the row's four bytes, in all of its lanes; lane number i of a row keeps those of row i
-        uint32_t bytes = (uint32_t)new_sc << (8 * (side / 2));
-        bytes |= dpp<DPP_XOR2>(bytes);
-        bytes |= dpp<DPP_HALF_MIRROR>(bytes);
-        if (side == i) mine = bytes;
+    for (int i = 0; i < CD_ROWS; ++i)
+        factor[i] = mx_down<F>(__float_as_uint(ends[wave][r0 + CD_APART * i]) >> (8 * (side / 2)) & 255);
+#pragma unroll
+    for (int i = 0; i < CD_ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < CD_COLS; j += 32 / F::BITS) F::decode(w[i][j * F::BITS / 32], &s[i][j]);
+#pragma unroll 1
+    for (int32_t from = 0;;) {
+        const int32_t count = min(len - from, CH);
+        const int64_t row0 = ((int64_t)(t0 + from) * H + h) * CD;
+        float key[CH], c = 1.f;   // k_s^(t) of this lane's row
+#pragma unroll
+        for (int t = 0; t < CH; ++t) {
+            if (t >= count) break;
+            const float decay = expf(gx[t]), mine = query ? to_f(qx[t]) : to_f(kx[t]);
+            c *= decay;
+            rows[wave][t][query][my_row] = mine * c;
+            float dots = 0.f;
+#pragma unroll
+            for (int p = 0; p <= t; ++p) {
+                key[p] = p == t ? to_f(kx[t]) : key[p] * decay;
+                const float dot = sum_half_wave(key[p] * mine);
+                dots = my_row == p ? dot : dots;
+            }
+            if (my_row < CH) grams[wave][query][t][my_row] = dots;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+        for (int32_t t = 0; t < count; ++t) {
+            float x[2 * CD_COLS];
+#pragma unroll
+            for (int i = 0; i < CD_ROWS; ++i) {
+                const float kr = rows[wave][t][0][r0 + CD_APART * i] * factor[i];
+                const float qr = rows[wave][t][1][r0 + CD_APART * i] * factor[i];
+#pragma unroll
+                for (int j = 0; j < CD_COLS; ++j) {
+                    x[j] = i == 0 ? s[i][j] * kr : x[j] + s[i][j] * kr;
+                    x[CD_COLS + j] = i == 0 ? s[i][j] * qr : x[CD_COLS + j] + s[i][j] * qr;
+                }
+            }
+            // over the lanes of a column, as for one token
+            halve32<16>(x);
+            halve16<8>(x);
+            halve<4>(x, lane & 8, [](float y) { return dpp<DPP_ROR8>(y); });
+            const int bits = (lane >> 5 & 1) * 4 | (lane >> 4 & 1) * 2 | (lane >> 3 & 1);
+            *reinterpret_cast<f32x4 *>(&sums[t][wave][bits >> 2][side * CD_COLS + (bits & 3) * 4]) = f32x4{x[0], x[1], x[2], x[3]};
+        }
+        const bool moves = write || from + CH < len;
+        if (moves) {   // k_s^(last) and c in the place of what the products have read
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int t = 0; t < CH; ++t)
+                if (t < count) rows[wave][t][0][my_row] = key[t];
+            ends[wave][my_row] = c;
+        }
+        __syncthreads();
+        // every wave forms all f_t of two columns a lane; token t's are written by wave t % 4
+        const int gram = min(lane, CH * CH - 1);
+        float gk = 0.f, gq = 0.f;   // lane CH t + s: k_s^(t).k_t and .q_t
+#pragma unroll
+        for (int i = 0; i < CD_WAVES; ++i) gk += (&grams[i][0][0][0])[gram], gq += (&grams[i][1][0][0])[gram];
+        f32x2 f[CH];
+#pragma unroll
+        for (int t = 0; t < CH; ++t) {
+            if (t >= count) break;
+            f32x2 a{};
+#pragma unroll
+            for (int i = 0; i < CD_WAVES; ++i) a += *reinterpret_cast<const f32x2 *>(&sums[t][i][0][2 * lane]);
+            const auto lane_of = [](float x, int l) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), l)); };
+#pragma unroll
+            for (int p = 0; p < t; ++p) {
+                const float m = lane_of(gk, CH * t + p);
+                a[0] += m * f[p][0], a[1] += m * f[p][1];
+            }
+            f[t] = f32x2{bt[t] * (to_f(vx[t][0]) - a[0]), bt[t] * (to_f(vx[t][1]) - a[1])};
+            if (wave == t % CD_WAVES) {
+                if (moves) *reinterpret_cast<f32x2 *>(&offs[t][2 * lane]) = f[t];
+                f32x2 b{};
+#pragma unroll
+                for (int i = 0; i < CD_WAVES; ++i) b += *reinterpret_cast<const f32x2 *>(&sums[t][i][1][2 * lane]);
+#pragma unroll
+                for (int p = 0; p <= t; ++p) {
+                    const float m = lane_of(gq, CH * t + p);
+                    b[0] += m * f[p][0], b[1] += m * f[p][1];
+                }
+                two o;
+                o[0] = from_f<T>(b[0]), o[1] = from_f<T>(b[1]);
+                *reinterpret_cast<two_mem *>(out + row0 + t * step + 2 * lane) = o;
+            }
+        }
+        if (!moves) return;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < CD_ROWS; ++i) {
+            const float decay = ends[wave][r0 + CD_APART * i] * factor[i];
+            factor[i] = 1.f;
+#pragma unroll
+            for (int j = 0; j < CD_COLS; ++j) s[i][j] *= decay;
+        }
+#pragma unroll 1
+        for (int32_t t = 0; t < count; ++t) {
+            float kk[CD_ROWS];
+#pragma unroll
+            for (int i = 0; i < CD_ROWS; ++i) kk[i] = rows[wave][t][0][r0 + CD_APART * i];
+#pragma unroll
+            for (int j = 0; j < CD_COLS; ++j) {
+                const float off = offs[t][side * CD_COLS + j];
+#pragma unroll
+                for (int i = 0; i < CD_ROWS; ++i) s[i][j] += kk[i] * off;
+            }
+        }
+        from += CH;
+        if (from >= len) break;
+        read(from);
+        __syncthreads();   // (what the next tokens write has been read)
     }
-    if (side < CD_ROWS) *reinterpret_cast<word_mem *>(scales + (entry + r0 + CD_APART * side) * CD_BLOCKS) = mine;
+    if (write && kept) write_state<F>(s, codes, scales + (entry + r0) * CD_BLOCKS, side);
 }
 
 }  // namespace kda
@@ -253,7 +463,9 @@ static hipError_t cached_tokens(const void *q, const void *k, const void *v, con
         int32_t shift = 24;
         while ((1 << (shift - 24)) < H && shift < 54) ++shift;
         const uint32_t per_head = (uint32_t)((((uint64_t)1 << shift) + H - 1) / H);
-        const auto kernel = out ? kda_cached_tokens_kernel<T, decltype(f), true> : kda_cached_tokens_kernel<T, decltype(f), false>;
+        typedef decltype(f) F;
+        const auto kernel = !out ? kda_cached_tokens_kernel<T, F, false>
+                            : T_tot > N ? kda_cached_chunk_kernel<T, F> : kda_cached_tokens_kernel<T, F, true>;
         hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)N * H)), dim3(CD_THREADS), 0, s, (const T *)q, (const T *)k,
                            (const T *)v, g, beta, cu, num_tokens, cache, scales, slots, (int32_t)write, num_slots, H,
                            per_head, shift, T_tot, (T *)out);

@@ -262,6 +262,32 @@ def test_accepted_prefixes_are_committed(fmt):
     check_decode(p, fmt, write=False, counts=[1, 5, 3, 2, 0, 2])
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_longer_drafts(fmt, dtype):
+    """Sequences over several chunks of tokens, whole ones, one token more and one less; some of their tokens processed."""
+    p = make([11, 4, 5, 6, 0, 16, 1, 10], 2, fmt, dtype)
+    check_decode(p, fmt, write=False)
+    check_decode(p, fmt, write=True)
+    check_decode(p, fmt, write=True, out=False)
+    p["slots"][0], p["slots"][5] = -1, 999
+    check_decode(p, fmt, write=True, counts=[7, 4, 0, 5, 2, 10, 1, 6])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_draft_s_outputs_do_not_go_by_what_follows(fmt):
+    p = make([13, 13], 2, fmt, "bf16")
+    whole, _, _ = decode(p, fmt, write=False)
+    part, _, _ = decode(p, fmt, write=True, counts=[7, 1])
+    assert torch.equal(part[:7], whole[:7]) and torch.equal(part[13:14], whole[13:14])
+    # nor by numbers that are none in later tokens
+    for name in ("q", "k", "v"):
+        p[name][9] = float("nan")
+    after, _, _ = decode(p, fmt, write=False)
+    assert torch.equal(after[:9], whole[:9]) and torch.equal(after[13:], whole[13:])
+    assert torch.isnan(after[9:13]).all()
+
+
 def test_readers_may_share_a_slot():
     p = make([2, 3, 2], 2, "int8")
     p["slots"][:] = 1
