@@ -11,9 +11,8 @@
 // HBM bounds large calls, latency small ones: the counting takes two dependent reads,
 // each kernel about three.  One MI355X, fp32, four drafts, both kernels of a replayed
 // graph: 256 sequences of 131,072 42 us (kernel 1 37, 5.8 TB/s), 256 x 32,000 16 us, one
-// of 32,000 6.3 us.  Read through the caches, rows take 10-20 % longer.  One launch with
-// a workgroup of 1,024 threads a sequence and the sums in LDS was slower for all but
-// vocabularies of 8,000: a CU alone does not read a row fast enough.
+// of 32,000 6.3 us.  Read through the caches, rows take 10-20 % longer.  Small rows of few
+// sequences are done in one launch.
 #include "kda_device.hpp"
 #include "kda_layer.hpp"
 #include "kda_seq.hpp"
@@ -141,10 +140,11 @@ template <typename T, int K> __device__ __forceinline__ void part_sums(const typ
 
 // What a workgroup finds: every thread has the weights of some places, `run` their
 // sum, in the order of the threads.
-struct Search {
-    double waves[VF_WAVES];
+template <int THREADS> struct Search {
+    static constexpr int WAVES = THREADS / 64;
+    double waves[WAVES];
     double base;                                // the sum before the part that is searched
-    int32_t firsts[VF_WAVES], lasts[VF_WAVES];
+    int32_t firsts[WAVES], lasts[WAVES];
 
     // The sum before this thread's places, and of all (called by the whole workgroup).
     __device__ __forceinline__ double before(double run, double &total) {
@@ -155,7 +155,7 @@ struct Search {
         double up = s - run;
         total = 0.;
 #pragma unroll
-        for (int i = 0; i < VF_WAVES; ++i) {
+        for (int i = 0; i < WAVES; ++i) {
             if (i == (int)(threadIdx.x >> 6)) up += total;
             total += waves[i];
         }
@@ -173,7 +173,7 @@ struct Search {
         __syncthreads();
         first = INT32_MAX, last = -1;
 #pragma unroll
-        for (int i = 0; i < VF_WAVES; ++i) first = min(first, firsts[i]), last = max(last, lasts[i]);
+        for (int i = 0; i < WAVES; ++i) first = min(first, firsts[i]), last = max(last, lasts[i]);
     }
 
     // The next token, given the sums of the row's parts.  The first place x with
@@ -184,7 +184,7 @@ struct Search {
     template <typename T>
     __device__ __forceinline__ int32_t pick(typename Verify<T>::Row w, const double *sums, int32_t parts, int32_t p0, int32_t p1,
                                             double run, double sample) {
-        constexpr int VW = VF_PART / VF_THREADS;
+        constexpr int VW = VF_PART / THREADS;
         double total, sum = before(run, total);
         const bool whole = total == 0. && (w.q || w.without >= 0);   // nothing is left: the target's own row
         if (whole) {
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(VF_THREADS) void kda_verify_pick_kernel(Verify<T> i
                                                                      const double *sums, const int32_t *counts,
                                                                      int32_t *num_tokens, int32_t *next_token)
 {
-    __shared__ Search find;
+    __shared__ Search<VF_THREADS> find;
     const int32_t n = blockIdx.x;
     const Verdict v{in.sq.at(n), max(in.sq.at(n + 1) - in.sq.at(n), 0), counts[n]};
     const double sample = sample_rand[n];
@@ -293,7 +293,39 @@ __global__ __launch_bounds__(VF_THREADS) void kda_verify_pick_kernel(Verify<T> i
     if (threadIdx.x == 0) num_tokens[n] = 1 + v.accepted, next_token[n] = next;
 }
 
+// Both in one launch: a workgroup of 16 waves a sequence, a part a wave, sums in LDS.
+constexpr int VF_ONE_THREADS = 1024, VF_ONE_PARTS = 16;
+template <typename T>
+__global__ __launch_bounds__(VF_ONE_THREADS) void kda_verify_one_kernel(Verify<T> in, const float *sample_rand, int32_t parts,
+                                                                        int32_t *num_tokens, int32_t *next_token)
+{
+    __shared__ Search<VF_ONE_THREADS> find;
+    __shared__ double sums[VF_ONE_PARTS];
+    const int32_t n = blockIdx.x, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const double sample = sample_rand[n];
+    const Verdict v = in.judge(n);
+    if (v.rows == 0) {
+        if (threadIdx.x == 0) num_tokens[n] = 0, next_token[n] = -1;
+        return;
+    }
+    const auto row = in.row(v);
+    if (wave < parts) {   // (at most as many as waves)
+        double s[1];
+        part_sums<T, 1>(row, wave, s);
+        if ((threadIdx.x & 63) == 63) sums[wave] = s[0];
+    }
+    __syncthreads();
+    const int32_t p0 = min((int32_t)threadIdx.x, parts), p1 = min(p0 + 1, parts);
+    const int32_t next = find.template pick<T>(row, sums, parts, p0, p1, p0 < p1 ? sums[p0] : 0., sample);
+    if (threadIdx.x == 0) num_tokens[n] = 1 + v.accepted, next_token[n] = next;
+}
+
 inline int32_t part_count(int32_t vocab) { return (int32_t)(((int64_t)vocab + VF_PART - 1) / VF_PART); }
+// One launch for rows of up to 16 parts and as many sequences as CUs: a call's time is the
+// host's, 8.2 us for 10.9 (fp32, one, 16 or 61 of 8,000); replayed one of 8,000 takes 6.5 us for
+// 6.3, 256 8.8 for 8.8, one of 16,000 7.8 for 6.2, 256 10.7 for 11.5.  Above, one CU reads a row too
+// slowly (one of 32,000 9.7 for 6.3), or two workgroups share one (512 of 8,000 16.5 for 12.0).
+inline bool one_launch(int32_t N, int32_t parts) { return parts <= VF_ONE_PARTS && N <= 256; }
 // Parts of a wave: two from 16,384 parts on (us of both kernels, one and two: 256 rows of
 // 131,072 46.3 and 42.4, 400 of 65,537 39.4 and 37.2, 128 of 131,072 26.7 and 25.7; 64 of
 // 131,072 15.8 and 16.4, one of 32,000 6.1 and 7.0).
@@ -329,6 +361,11 @@ static hipError_t verify(const void *target, const void *draft, const int32_t *t
     const int32_t parts = part_count(vocab), groups = (int32_t)sum_groups(N, vocab);
     double *const sums = (double *)ws;
     int32_t *const counts = (int32_t *)(sums + (size_t)N * parts);
+    if (one_launch(N, parts)) {
+        hipLaunchKernelGGL(kda_verify_one_kernel<T>, dim3((unsigned)N), dim3(VF_ONE_THREADS), 0, s, in, sample_rand, parts,
+                           num_tokens, next_token);
+        return hipGetLastError();
+    }
     const auto sum = [&](auto k) {
         hipLaunchKernelGGL((kda_verify_sums_kernel<T, k()>), dim3((unsigned)(N * (int64_t)groups)), dim3(VF_THREADS), 0, s, in,
                            groups, parts, sums, counts);

@@ -66,6 +66,20 @@ def test_lengths(lens, closeness):
     check(*make(lens, 300, seed=len(lens), closeness=closeness, pad=1))
 
 
+@pytest.mark.parametrize("V", [300, 16384, 16385])
+@pytest.mark.parametrize("N", [256, 257])
+def test_where_one_launch_ends(V, N):
+    """The most sequences and the longest rows that one launch takes, and one more of each: the same sequences alone."""
+    lens = [1 + n % 3 if n % 5 else 0 for n in range(N)]
+    a = make(lens, V, "bf16", seed=V + N)
+    num, nxt = check(*a)
+    t, d, tok, cu, acc, smp = a
+    for n in (1, N - 1):
+        at = slice(int(cu[n]), int(cu[n + 1]))
+        one = run(t[at], d[at], tok[at], [0, lens[n]], acc[at], smp[n:n + 1])
+        assert one == ([num[n]], [nxt[n]])
+
+
 def test_all_accepted_and_all_rejected():
     t, d, tok, cu, acc, smp = make([70, 5, 2], 128)
     assert check(t, d, tok, cu, np.zeros(77), smp)[0] == [70, 5, 2]
