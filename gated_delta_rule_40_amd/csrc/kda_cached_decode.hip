@@ -14,13 +14,15 @@
 //
 // HBM bounds one token (33 KB of codes and scales a state, past the caches), vector
 // instructions several (token by token about 390 a wave and token for 64 values a lane:
-// the decay, two products, the update, and the halving).  So calls with more tokens than
-// sequences take them in chunks, from one state, if they have outputs: 512 sequences of 32
-// heads, fp8, two, five and eight tokens verified 87, 168 and 290 us, token by token 105, 214
-// and 325; five of 64 x 16 in int8 16.4 and 18.7.  Without outputs b and the queries fall away
+// the decay, two products, the update, and the halving).  So a sequence of several token
+// rows takes them in chunks, from one state, if there are outputs: 512 sequences of 32
+// heads, fp8, two, five and eight tokens verified 88, 172 and 293 us, token by token 105, 214
+// and 325; five of 64 x 16 in int8 16.8 and 18.7.  Without outputs b and the queries fall away
 // and chunks gain nothing (five committed 131 us, token by token 124).
+// The form goes by a sequence's own rows (cu_seqlens), not by how many of them are processed
+// and not by the batch: its results have the same bits whatever stands beside it.
 // One MI355X, bf16, replays of a graph: 512 sequences of 32 heads, one token committed, fp8
-// 103-106 us (5.5 TB/s), int8 106, fp4 88; 8 x 8 heads 4.4.
+// 101 us (5.7 TB/s), int8 107, fp4 75; beside a sequence of five 105; 8 x 8 heads 3.9.
 // Waves that each had 32 columns of all rows needed no barrier, but their reads of 32
 // bytes a row bound them to 129 us; 8 columns by 8 rows a lane 119 (198 for five tokens
 // verified token by token); decays kept apart from the state, as factors of its rows, gained
@@ -125,12 +127,18 @@ template <typename F> __device__ __forceinline__ void write_state(float (&s)[CD_
     if (side < CD_ROWS) *reinterpret_cast<word_mem *>(scales + CD_APART * side * CD_BLOCKS) = mine;
 }
 
-// OUT: with outputs (else a and the states alone).
+// ---------------------------------------------------------------- token by token
+struct TokensShared {
+    f32x4 rows[CD_WAVES][CD_WROWS];                      // key, query, decay (and at first the scale bytes)
+    float sums[2][CD_WAVES][2][CD], dots[2][CD_WAVES];   // of the waves: a and b; q.k
+    float offs[CD_WAVES][CD];                            // a wave's own copy of beta u
+};
+
+// `len` tokens from row t0 on of head h.  OUT: with outputs (else a and the states alone).
 template <typename T, typename F, bool OUT>
-__global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_tokens_kernel(
-    const T *q, const T *k, const T *v, const float *g, const float *beta, const int32_t *cu, const int32_t *num_tokens,
-    uint8_t *cache, uint8_t *scales, const int32_t *slots, int32_t write, int32_t num_slots, int32_t H,
-    uint32_t per_head, int32_t shift, int32_t T_tot, T *out)
+__device__ __forceinline__ void by_tokens(const T *q, const T *k, const T *v, const float *g, const float *beta, uint8_t *cache,
+                                          uint8_t *scales, int32_t slot, int32_t write, int32_t num_slots, int32_t H, int32_t h,
+                                          int32_t t0, int32_t len, T *out, TokensShared &sh)
 {
     constexpr int WORDS = CD_COLS * F::BITS / 32;   // of a lane's codes in a row
     constexpr int ROW_BYTES = CD * F::BITS / 8;
@@ -138,19 +146,15 @@ __global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_tokens_kernel(
     typedef words words_mem __attribute__((aligned(1)));
     typedef uint32_t word_mem __attribute__((aligned(1)));
     typedef typename Token<T>::two two_mem __attribute__((aligned(sizeof(T))));
-    __shared__ f32x4 rows[CD_WAVES][CD_WROWS];                  // key, query, decay (and at first the scale bytes)
-    __shared__ float sums[2][CD_WAVES][2][CD], dots[2][CD_WAVES];   // of the waves: a and b; q.k
-    __shared__ float offs[CD_WAVES][CD];                        // a wave's own copy of beta u
+    auto &rows = sh.rows;
+    auto &sums = sh.sums;
+    auto &dots = sh.dots;
+    auto &offs = sh.offs;
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int thread = threadIdx.x;
+    asm("" : "+v"(thread));   // (places that the chunks below share with this would be held over the branch, and spilled)
+    const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6);
     const int side = lane % CD_LANES, r0 = lane / CD_LANES;
-    const uint32_t u = blockIdx.x;
-    const int32_t n = (int32_t)((uint64_t)u * per_head >> shift), h = (int32_t)u - n * H;   // u / H, u % H
-    const int32_t t0 = min(max(cu[n], 0), T_tot);
-    int32_t len = min(max(cu[n + 1], t0), T_tot) - t0;
-    if (num_tokens) len = min(len, max(num_tokens[n], 0));
-    const int32_t slot = slots[n];
-    if (len == 0) return;
 
     const int my_row = lane % CD_WROWS;
     const auto read = [&](int32_t t) {
@@ -252,6 +256,23 @@ __global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_tokens_kernel(
     if (write && kept) write_state<F>(s, codes, scales + (entry + r0) * CD_BLOCKS, side);
 }
 
+// without outputs
+template <typename T, typename F>
+__global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_commit_kernel(
+    const T *q, const T *k, const T *v, const float *g, const float *beta, const int32_t *cu, const int32_t *num_tokens,
+    uint8_t *cache, uint8_t *scales, const int32_t *slots, int32_t write, int32_t num_slots, int32_t H,
+    uint32_t per_head, int32_t shift, int32_t T_tot, T *out)
+{
+    const uint32_t u = blockIdx.x;
+    const int32_t n = (int32_t)((uint64_t)u * per_head >> shift), h = (int32_t)u - n * H;   // u / H, u % H
+    const int32_t t0 = min(max(cu[n], 0), T_tot);
+    int32_t len = min(max(cu[n + 1], t0), T_tot) - t0;
+    if (num_tokens) len = min(len, max(num_tokens[n], 0));
+    if (len == 0) return;
+    __shared__ TokensShared sh;
+    by_tokens<T, F, false>(q, k, v, g, beta, cache, scales, slots[n], write, num_slots, H, h, t0, len, out, sh);
+}
+
 // ---------------------------------------------------------------- several tokens
 // Up to CH tokens from one state: with c_t the decays up to token t, k_s^(t) the key of
 // token s decayed up to t,
@@ -259,12 +280,15 @@ __global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_tokens_kernel(
 //     o_t = S^T (c_t q_t) + sum over s <= t of (k_s^(t).q_t) f_s
 //     S'  = Diag(c) S + sum over s of k_s^(last) f_s^T
 // so the state is multiplied by all keys and queries as it is, without a barrier between
-// tokens, and moved on once (where it is only read, never).  No decay is divided by.
+// tokens, and moved on once (where it is only read, never).  No decay is divided by; one
+// of several tokens that falls below 2^-126 keeps steps of 2^-149.
 // Six tokens spill registers (five tokens 171 us for 168), eight more (178); four leave one over.
 constexpr int CH = 5;
 
-template <typename T, typename F>
-__global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_chunk_kernel(
+// With outputs: a sequence of one row as it is, of several by chunks.  WAVES: workgroups of a CU
+// that registers are left for, and no matter to the results.
+template <typename T, typename F, int WAVES>
+__global__ __launch_bounds__(CD_THREADS, WAVES) void kda_cached_outputs_kernel(
     const T *q, const T *k, const T *v, const float *g, const float *beta, const int32_t *cu, const int32_t *num_tokens,
     uint8_t *cache, uint8_t *scales, const int32_t *slots, int32_t write, int32_t num_slots, int32_t H,
     uint32_t per_head, int32_t shift, int32_t T_tot, T *out)
@@ -279,8 +303,12 @@ __global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_chunk_kernel(
     // of a wave's rows: c_t k_t and c_t q_t, then k_s^(last); c (and at first the scale bytes)
     __shared__ float rows[CD_WAVES][CH][2][CD_WROWS], ends[CD_WAVES][CD_WROWS];
     __shared__ float grams[CD_WAVES][2][CH][CH];        // a wave's part of k_s^(t).k_t and k_s^(t).q_t
-    __shared__ __attribute__((aligned(16))) float sums[CH][CD_WAVES][2][CD];   // of the waves: S^T (c_t k_t), S^T (c_t q_t)
-    __shared__ __attribute__((aligned(16))) float offs[CH][CD];                // f_t
+    __shared__ __attribute__((aligned(16))) union {
+        float sums[CH][CD_WAVES][2][CD];                // of the waves: S^T (c_t k_t), S^T (c_t q_t)
+        TokensShared single;
+    } sh;
+    __shared__ __attribute__((aligned(16))) float offs[CH][CD];   // f_t
+    auto &sums = sh.sums;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int side = lane % CD_LANES, r0 = lane / CD_LANES;
@@ -288,9 +316,14 @@ __global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_chunk_kernel(
     const int32_t n = (int32_t)((uint64_t)u * per_head >> shift), h = (int32_t)u - n * H;   // u / H, u % H
     const int32_t t0 = min(max(cu[n], 0), T_tot);
     int32_t len = min(max(cu[n + 1], t0), T_tot) - t0;
+    const bool single = len == 1;
     if (num_tokens) len = min(len, max(num_tokens[n], 0));
     const int32_t slot = slots[n];
     if (len == 0) return;
+    if (single) {
+        by_tokens<T, F, true>(q, k, v, g, beta, cache, scales, slot, write, num_slots, H, h, t0, 1, out, sh.single);
+        return;
+    }
 
     const int my_row = lane % CD_WROWS, query = lane / CD_WROWS;   // (keys by the lower half of a wave, queries by the upper)
     const bool kept = slot >= 0 && slot < num_slots;
@@ -464,8 +497,11 @@ static hipError_t cached_tokens(const void *q, const void *k, const void *v, con
         while ((1 << (shift - 24)) < H && shift < 54) ++shift;
         const uint32_t per_head = (uint32_t)((((uint64_t)1 << shift) + H - 1) / H);
         typedef decltype(f) F;
-        const auto kernel = !out ? kda_cached_tokens_kernel<T, F, false>
-                            : T_tot > N ? kda_cached_chunk_kernel<T, F> : kda_cached_tokens_kernel<T, F, true>;
+        // Where no sequence need have several rows, registers for four workgroups a CU: 512 x 32, one
+        // token committed, fp8 101 us (three: 105), int8 107 (116), fp4 75 (87).  The chunks spill
+        // then: 64 drafts of eight tokens among 448 empty sequences take 77 us (three: 53).
+        const auto kernel = !out ? kda_cached_commit_kernel<T, F>
+                            : T_tot > N ? kda_cached_outputs_kernel<T, F, 3> : kda_cached_outputs_kernel<T, F, 4>;
         hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)N * H)), dim3(CD_THREADS), 0, s, (const T *)q, (const T *)k,
                            (const T *)v, g, beta, cu, num_tokens, cache, scales, slots, (int32_t)write, num_slots, H,
                            per_head, shift, T_tot, (T *)out);

@@ -729,6 +729,12 @@ kda_status kda_cache_load(const uint8_t *cache, const uint8_t *scales, const int
  *                 after the processed tokens replace those of the slots.  A
  *                 sequence without processed tokens keeps its slot's bytes.
  *   out           may be NULL where the call writes
+ * What a sequence gives depends on its own token rows alone, to the bit: not on the
+ * sequences beside it, nor on rows behind the last, and a token's output not on the
+ * tokens after it.  A sequence of one row, one of several, and a call without `out`
+ * sum in orders of their own (and not in kda_decode_step's): the same tokens in
+ * another of these forms agree within fp32's rounding, and codes where that does
+ * not reach over a tie.
  */
 kda_status kda_decode_tokens_cached(const void *q, const void *k, const void *v, const float *g, const float *beta,
                                     const int32_t *cu_seqlens, const int32_t *num_tokens, uint8_t *cache,

@@ -1,0 +1,79 @@
+"""kda_decode_tokens_cached: what a sequence gives goes by its own token rows, to the
+bit, whatever batch it stands in."""
+import pytest
+import torch
+
+from gated_delta_rule_40_amd import libkda as K
+from test_gpu_cache import D, DT, FORMATS, check_decode, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    K.load()
+
+
+def batch_of(p, order, pad=0):
+    """The sequences `order` of p (None: an empty one, whose slot nothing is in) as a batch of their own, over the same cache."""
+    cu, at, lens = p["cu"].tolist(), [], []
+    for n in order:
+        rows = [] if n is None else list(range(cu[n], cu[n + 1]))
+        at += rows
+        lens.append(len(rows))
+    pick = torch.tensor(at + [at[0]] * pad).cuda()             # (rows behind the last, of some token)
+    s = {name: p[name][pick].contiguous() for name in ("q", "k", "v", "g", "beta")}
+    s["cu"] = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32).cuda()
+    s["slots"] = torch.stack([p["slots"][0] * 0 - 1 if n is None else p["slots"][n] for n in order])
+    return s, at
+
+
+@pytest.mark.parametrize("write", [False, True])
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_bits_are_those_of_the_sequence_alone(dtype, fmt, write):
+    """One-row sequences and drafts: alone, side by side, among empty ones, in front of rows that are no sequence's."""
+    lens = [1, 4, 1, 1, 9, 1, 2, 1]
+    p = make(lens, 3, fmt, dtype, seed=11)
+    want = {}
+
+    def run(order, pad):
+        s, at = batch_of(p, order, pad)
+        cache, scales = p["cache"].clone(), p["scales"].clone()
+        out = torch.full(s["v"].shape, 7.0, dtype=DT[dtype], device="cuda")
+        K.kda_decode_tokens_cached(*(s[x] for x in ("q", "k", "v", "g", "beta", "cu")), cache, scales, s["slots"], fmt, out=out,
+                                   write=write)
+        assert torch.all(out[len(at):] == 7.0)
+        for i, n in enumerate(order):
+            if n is None:
+                continue
+            slot = int(p["slots"][n])
+            got = (out[int(s["cu"][i]):int(s["cu"][i + 1])], cache[slot], scales[slot])
+            for a, b in zip(got, want.setdefault(n, got)):
+                assert torch.equal(a, b), (order, pad, n)
+
+    for n in range(len(lens)):
+        run([n], 0)
+    singles = [n for n, length in enumerate(lens) if length == 1]
+    drafts = [n for n, length in enumerate(lens) if length > 1]
+    for order in (list(range(len(lens))), singles, drafts, drafts + [None] * 20, [None] + singles + [None], [4, 0] + [None] * 12):
+        for pad in (0, 1, 40):
+            run(order, pad)
+    check_decode(dict(p, **batch_of(p, list(range(len(lens))))[0]), fmt, write)
+    check_decode(dict(p, **batch_of(p, drafts + [None] * 20)[0]), fmt, write)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_sequence_goes_by_its_rows_and_not_by_those_processed(fmt):
+    """The first token of a draft has one output, however many tokens are processed."""
+    p = make([5, 5, 1], 2, fmt, "fp32")
+    outs = []
+    for counts in (None, [1, 1, 1], [2, 5, 1], [5, 1, 9]):
+        out = torch.full_like(p["v"], 7.0)
+        K.kda_decode_tokens_cached(*(p[x] for x in ("q", "k", "v", "g", "beta", "cu")), p["cache"], p["scales"], p["slots"], fmt,
+                                   out=out, write=False,
+                                   num_tokens=None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda())
+        outs.append(out[[0, 5, 10]])
+    assert all(torch.equal(o, outs[0]) for o in outs)
