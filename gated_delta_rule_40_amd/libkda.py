@@ -860,7 +860,8 @@ def kda_qknorm_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, norm
 
 
 # ---------------------------------------------------------------- cached states and drafted tokens
-_BYTES = {torch.uint8, torch.int8, torch.float8_e4m3fn}   # types that codes may come in
+# types that a format's codes may come in (two 4-bit codes to an element)
+_CODES = ({torch.uint8, torch.float8_e4m3fn}, {torch.uint8, torch.int8}, {torch.uint8, torch.float4_e2m1fn_x2})
 _SCALES = {torch.uint8, torch.float8_e8m0fnu}
 
 
@@ -881,13 +882,13 @@ def _slots_of(name, t, dev, types, per_slot):
     except (AttributeError, IndexError):   # no tensor, or one of no dimensions
         pass
     _require(isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in types and t.is_contiguous(),
-             "%s must be a contiguous tensor of bytes on cuda:%d" % (name, dev))
+             "%s must be a contiguous tensor of bytes on cuda:%d, %s" % (name, dev, " or ".join(sorted(map(str, types)))))
     raise ValueError("%s must be [slots, ...] with %d bytes a slot, got %s" % (name, per_slot, list(t.shape)))
 
 
 def _cache(cache, scales, dev, elems, fmt):
     """Addresses of a cache's codes and scales for entries of `elems` values, and its slots."""
-    pc, S = _slots_of("cache", cache, dev, _BYTES, (elems + 1) // 2 if fmt == 2 else elems)
+    pc, S = _slots_of("cache", cache, dev, _CODES[fmt], (elems + 1) // 2 if fmt == 2 else elems)
     ps, n = _slots_of("scales", scales, dev, _SCALES, (elems + KDA_MX_BLOCK - 1) // KDA_MX_BLOCK)
     if n != S:
         raise ValueError("cache and scales must have the same slots")
@@ -904,7 +905,7 @@ def kda_cache_store(src, slots, cache, scales, format: str = "fp8", stream=None)
     device; a negative one is not stored) of a cache: cache [slots, ...] uint8
     (or the format's own type), kda_cache_entry_bytes(...) a slot; scales
     [slots, ...] uint8 or float8_e8m0fnu, one for every 32 values.  format:
-    "fp8", "int8" or "fp4"."""
+    "fp8" (float8_e4m3fn), "int8" (int8) or "fp4" (float4_e2m1fn_x2)."""
     px, dev, code, _, n, elems = _rows("src", src)
     fmt = _format(format)
     pc, ps, S = _cache(cache, scales, dev, elems, fmt)

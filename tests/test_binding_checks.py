@@ -60,3 +60,17 @@ def test_workspace_size_rejects_unknown_dtype():
         K.kda_prefill_cp_workspace_size(1, 16, 1, 128, 128, torch.float16)
     with pytest.raises(TypeError):
         K.kda_backward_workspace_size(1, 16, 1, 128, 128, torch.float16)
+
+
+def test_codes_come_as_bytes_or_in_the_format_s_own_type():
+    own = {"fp8": torch.float8_e4m3fn, "int8": torch.int8, "fp4": torch.float4_e2m1fn_x2}
+    for name, fmt in K.KDA_CACHE_FORMATS.items():
+        per = 32 if name == "fp4" else 64
+        scales = torch.zeros(3, 2, dtype=torch.uint8)
+        for dtype in (torch.uint8, *own.values()):
+            cache = torch.zeros(3, per, dtype=torch.uint8).view(dtype)
+            if dtype in (torch.uint8, own[name]):
+                assert K._cache(cache, scales, -1, 64, fmt) == (cache.data_ptr(), scales.data_ptr(), 3)
+            else:
+                with pytest.raises(ValueError, match="cache must be"):
+                    K._cache(cache, scales, -1, 64, fmt)

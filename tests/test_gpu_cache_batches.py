@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from gated_delta_rule_40_amd import libkda as K
-from test_gpu_cache import D, DT, FORMATS, check_decode, make
+from test_gpu_cache import DT, FORMATS, check_decode, make
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,25 @@ def test_a_sequence_goes_by_its_rows_and_not_by_those_processed(fmt):
                                    num_tokens=None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda())
         outs.append(out[[0, 5, 10]])
     assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_every_format_s_own_type_holds_the_same_codes():
+    x = torch.randn(3, 77, device="cuda")
+    slots = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda")
+    for fmt, own in (("fp8", torch.float8_e4m3fn), ("int8", torch.int8), ("fp4", torch.float4_e2m1fn_x2)):
+        per = K.kda_cache_entry_bytes(77, fmt)
+        cache, scales = torch.zeros(3, per, dtype=torch.uint8, device="cuda"), torch.zeros(3, 3, dtype=torch.uint8, device="cuda")
+        again, again_scales = torch.zeros_like(cache).view(own), torch.zeros_like(scales).view(torch.float8_e8m0fnu)
+        K.kda_cache_store(x, slots, cache, scales, fmt)
+        K.kda_cache_store(x, slots, again, again_scales, fmt)
+        assert torch.equal(cache, again.view(torch.uint8)) and torch.equal(scales, again_scales.view(torch.uint8))
+        a, b = torch.empty_like(x), torch.empty_like(x)
+        K.kda_cache_load(cache, scales, slots, a, fmt)
+        K.kda_cache_load(again, again_scales, slots, b, fmt)
+        assert torch.equal(a, b)
+        p = make([2, 1], 2, fmt)
+        o, o2 = torch.empty_like(p["v"]), torch.empty_like(p["v"])
+        for out, cache, scales in ((o, p["cache"].clone(), p["scales"].clone()),
+                                   (o2, p["cache"].clone().view(own), p["scales"].clone().view(torch.float8_e8m0fnu))):
+            K.kda_decode_tokens_cached(*(p[n] for n in ("q", "k", "v", "g", "beta", "cu")), cache, scales, p["slots"], fmt, out=out)
+        assert torch.equal(o, o2)
