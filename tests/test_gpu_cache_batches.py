@@ -1,5 +1,6 @@
 """kda_decode_tokens_cached: what a sequence gives goes by its own token rows, to the
-bit, whatever batch it stands in."""
+bit, whatever batch it stands in; and cached calls whose cu_seqlens or slots break
+their rules, or whose codes come in a type of their own."""
 import pytest
 import torch
 
@@ -99,3 +100,69 @@ def test_every_format_s_own_type_holds_the_same_codes():
                                    (o2, p["cache"].clone().view(own), p["scales"].clone().view(torch.float8_e8m0fnu))):
             K.kda_decode_tokens_cached(*(p[n] for n in ("q", "k", "v", "g", "beta", "cu")), cache, scales, p["slots"], fmt, out=out)
         assert torch.equal(o, o2)
+
+
+# ------------------------------------------------------------------ cu_seqlens and slots against the rules
+GUARD = 4096
+
+
+def guarded(t):
+    """A copy of t inside a larger array, and a function that tells whether what lies around it is as it was."""
+    n = t.numel() * t.element_size()
+    rows = torch.full((n + 2 * GUARD,), 0x5C, dtype=torch.uint8, device="cuda")
+    inner = rows[GUARD:GUARD + n].view(t.dtype).view(t.shape).copy_(t)
+    return inner, lambda: bool((rows[:GUARD] == 0x5C).all()) and bool((rows[GUARD + n:] == 0x5C).all())
+
+
+# entries, and what they come to for six token rows: an entry is held to [0, 6], and a sequence ends no earlier than it begins
+BAD_CU = [([-5, 2, 99, 7], [(0, 2), (2, 6), (6, 6)]), ([4, 1, 3, -9], [(4, 4), (1, 3), (3, 3)]),
+          ([2 ** 31 - 1, -2 ** 31, 5, 2 ** 31 - 1], [(6, 6), (0, 5), (5, 6)]), ([-1, -1, -1, -1], [(0, 0)] * 3)]
+
+
+@pytest.mark.parametrize("cu,means", BAD_CU, ids=str)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("out", [True, False])
+def test_bad_cu_seqlens_are_held_to_the_token_rows(cu, means, fmt, out):
+    p = make([2, 2, 2], 2, fmt, extra=4)
+    p["slots"] = torch.tensor([5, 2, 3], dtype=torch.int32, device="cuda")
+    want = {}
+    for n, (a, b) in enumerate(means):                        # the rows that they come to, as calls of their own
+        s = {x: p[x][a:b].contiguous() for x in ("q", "k", "v", "g", "beta")}
+        o, cache, scales = torch.empty_like(s["v"]), p["cache"].clone(), p["scales"].clone()
+        if b > a:
+            K.kda_decode_tokens_cached(*s.values(), torch.tensor([0, b - a], dtype=torch.int32, device="cuda"), cache, scales,
+                                       p["slots"][n:n + 1].clone(), fmt, out=o if out else None)
+        want[n] = o, cache[p["slots"][n]], scales[p["slots"][n]]
+    arrays, intact = {}, []
+    for name, t in (("out", torch.full_like(p["v"], 7.0)), ("cache", p["cache"]), ("scales", p["scales"])):
+        arrays[name], ok = guarded(t)
+        intact.append(ok)
+    K.kda_decode_tokens_cached(*(p[x] for x in ("q", "k", "v", "g", "beta")), torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                               arrays["cache"], arrays["scales"], p["slots"], fmt, out=arrays["out"] if out else None)
+    assert all(ok() for ok in intact)
+    rows = torch.zeros(6, dtype=torch.bool)
+    for n, (a, b) in enumerate(means):
+        o, cache, scales = want[n]
+        rows[a:b] = True
+        assert not out or torch.equal(arrays["out"][a:b], o)
+        slot = int(p["slots"][n])
+        assert torch.equal(arrays["cache"][slot], cache) and torch.equal(arrays["scales"][slot], scales)
+    others = [s for s in range(7) if s not in (5, 2, 3)]
+    assert torch.equal(arrays["cache"][others], p["cache"][others]) and torch.equal(arrays["scales"][others], p["scales"][others])
+    assert torch.all(arrays["out"][~rows.cuda() if out else slice(None)] == 7.0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("elems", [77, 2048])
+def test_slots_out_of_range_are_not_written(fmt, elems):
+    x = torch.randn(5, elems, device="cuda")
+    per = K.kda_cache_entry_bytes(elems, fmt)
+    cache, c_ok = guarded(torch.full((3, per), 9, dtype=torch.uint8, device="cuda"))
+    scales, s_ok = guarded(torch.full((3, -(-elems // 32)), 9, dtype=torch.uint8, device="cuda"))
+    dst, d_ok = guarded(torch.full((5, elems), 7.0, device="cuda"))
+    slots = torch.tensor([-1, 3, 1, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
+    K.kda_cache_store(x, slots, cache, scales, fmt)
+    K.kda_cache_load(cache, scales, slots, dst, fmt)
+    assert c_ok() and s_ok() and d_ok()
+    assert torch.all(cache[[0, 2]] == 9) and torch.all(scales[[0, 2]] == 9)
+    assert not dst[[0, 1, 3, 4]].any() and dst[2].any()

@@ -1,9 +1,11 @@
-"""kda_verify_drafts where a wave sums two parts of a row, and on either side of that,
-against the definition in fp64 (tests/cache_ref.py)."""
+"""kda_verify_drafts where a wave sums two parts of a row, on either side of that, and
+where cu_seqlens breaks its rules, against the definition in fp64
+(tests/cache_ref.py)."""
 import pytest
 import torch
 
 from gated_delta_rule_40_amd import libkda as K
+from test_gpu_cache_batches import guarded
 from test_gpu_verify import check, make, run
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +50,26 @@ def test_the_first_and_last_weights_of_rows_by_twos(dtype):
     t[:, 1:V - 1] = 0
     sample = [0.5 if n % 2 else 0.49999997 for n in range(N)]
     assert check(t, None, [0] * N, range(N + 1), zeros, sample)[1] == [V - 1 if n % 2 else 0 for n in range(N)]
+
+
+# entries, and what they come to for nine token rows: an entry is held to [0, 9], and a sequence ends no earlier than it begins
+@pytest.mark.parametrize("V", [200, 20000])                   # one launch and two
+@pytest.mark.parametrize("cu,means", [([-4, 3, 100, 5], [(0, 3), (3, 9), (9, 9)]), ([7, 2, 2 ** 31 - 1, -2 ** 31],
+                                      [(7, 7), (2, 9), (9, 9)]), ([-1, -2, -3, -4], [(0, 0)] * 3)], ids=str)
+def test_bad_cu_seqlens_are_held_to_the_token_rows(cu, means, V):
+    t, d, tok, _, acc, smp = make([3, 4, 2], V)
+    dev = lambda x, dt: torch.as_tensor(x, dtype=dt).cuda()   # noqa: E731
+    need = K.kda_verify_drafts_workspace_size(3, V)
+    arrays, intact = {}, []
+    for name, x in (("num", torch.zeros(3, dtype=torch.int32)), ("next", torch.zeros(3, dtype=torch.int32)),
+                    ("ws", torch.zeros(need, dtype=torch.uint8))):
+        arrays[name], ok = guarded(x)
+        intact.append(ok)
+    K.kda_verify_drafts(t, d, dev(tok, torch.int32), dev(cu, torch.int32), dev(acc, torch.float32), dev(smp, torch.float32),
+                        arrays["num"], arrays["next"], workspace=arrays["ws"])
+    assert all(ok() for ok in intact)
+    for n, (a, b) in enumerate(means):
+        want = ([0], [-1])
+        if b > a:
+            want = check(t[a:b], d[a:b], tok[a:b], [0, b - a], acc[a:b], smp[n:n + 1])
+        assert ([int(arrays["num"][n])], [int(arrays["next"][n])]) == want
