@@ -286,13 +286,16 @@ __global__ __launch_bounds__(CD_THREADS, 3) void kda_cached_commit_kernel(
 constexpr int CH = 5;
 
 // With outputs: a sequence of one row as it is, of several by chunks.  WAVES: workgroups of a CU
-// that registers are left for, and no matter to the results.
+// that registers are left for (four: a key's and a query's product one after the other, as both
+// would spill more; 64 drafts of eight among 448 empty sequences 54 us for 77).  The results
+// are the same bits.
 template <typename T, typename F, int WAVES>
 __global__ __launch_bounds__(CD_THREADS, WAVES) void kda_cached_outputs_kernel(
     const T *q, const T *k, const T *v, const float *g, const float *beta, const int32_t *cu, const int32_t *num_tokens,
     uint8_t *cache, uint8_t *scales, const int32_t *slots, int32_t write, int32_t num_slots, int32_t H,
     uint32_t per_head, int32_t shift, int32_t T_tot, T *out)
 {
+    constexpr int AT_ONCE = WAVES == 3 ? 2 : 1;     // products of the state
     constexpr int WORDS = CD_COLS * F::BITS / 32;   // of a lane's codes in a row
     constexpr int ROW_BYTES = CD * F::BITS / 8;
     typedef uint32_t words __attribute__((ext_vector_type(WORDS)));
@@ -340,19 +343,19 @@ __global__ __launch_bounds__(CD_THREADS, WAVES) void kda_cached_outputs_kernel(
             w[i] = __builtin_nontemporal_load(reinterpret_cast<const words_mem *>(codes + i * CD_APART * ROW_BYTES));
     }
     T kx[CH], qx[CH];
-    float gx[CH], bt[CH];
+    float gx[CH], bx = 0.f;   // (beta of token t by lane t)
     two vx[CH];
     const int64_t step = (int64_t)H * CD;   // from token to token
     const auto read = [&](int32_t from) {
         const int64_t row0 = ((int64_t)(t0 + from) * H + h) * CD;
+        if (lane < min(len - from, CH)) bx = beta[(int64_t)(t0 + from + lane) * H + h];
 #pragma unroll
         for (int t = 0; t < CH; ++t) {
-            kx[t] = qx[t] = T(0.f), gx[t] = bt[t] = 0.f, vx[t] = two{};
+            kx[t] = qx[t] = T(0.f), gx[t] = 0.f, vx[t] = two{};
             if (t < len - from) {
                 const int64_t row = row0 + t * step, at = row + wave * CD_WROWS;
                 kx[t] = (k + at)[my_row], qx[t] = (q + at)[my_row], gx[t] = (g + at)[my_row];
                 vx[t] = *reinterpret_cast<const two_mem *>((v + row) + 2 * lane);
-                bt[t] = beta[(int64_t)(t0 + from + t) * H + h];
             }
         }
     };
@@ -391,23 +394,33 @@ __global__ __launch_bounds__(CD_THREADS, WAVES) void kda_cached_outputs_kernel(
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll 1
         for (int32_t t = 0; t < count; ++t) {
-            float x[2 * CD_COLS];
+#pragma unroll 1
+            for (int which = 0; which < 2; which += AT_ONCE) {   // key and query
+                float x[AT_ONCE * CD_COLS];
 #pragma unroll
-            for (int i = 0; i < CD_ROWS; ++i) {
-                const float kr = rows[wave][t][0][r0 + CD_APART * i] * factor[i];
-                const float qr = rows[wave][t][1][r0 + CD_APART * i] * factor[i];
+                for (int i = 0; i < CD_ROWS; ++i)
 #pragma unroll
-                for (int j = 0; j < CD_COLS; ++j) {
-                    x[j] = i == 0 ? s[i][j] * kr : x[j] + s[i][j] * kr;
-                    x[CD_COLS + j] = i == 0 ? s[i][j] * qr : x[CD_COLS + j] + s[i][j] * qr;
-                }
+                    for (int p = 0; p < AT_ONCE; ++p) {
+                        const float r = rows[wave][t][which + p][r0 + CD_APART * i] * factor[i];
+#pragma unroll
+                        for (int j = 0; j < CD_COLS; ++j) {
+                            float &to = x[p * CD_COLS + j];
+                            to = i == 0 ? s[i][j] * r : to + s[i][j] * r;
+                        }
+                    }
+                // over the lanes of a column, as for one token
+                constexpr int LEFT = 2 * AT_ONCE;   // sums that a lane is left with
+                halve32<4 * LEFT>(x);
+                halve16<2 * LEFT>(x);
+                halve<LEFT>(x, lane & 8, [](float y) { return dpp<DPP_ROR8>(y); });
+                const int bits = (lane >> 5 & 1) * 4 | (lane >> 4 & 1) * 2 | (lane >> 3 & 1);
+                typedef float left __attribute__((ext_vector_type(LEFT)));
+                left y;
+#pragma unroll
+                for (int j = 0; j < LEFT; ++j) y[j] = x[j];
+                *reinterpret_cast<left *>(AT_ONCE == 2 ? &sums[t][wave][bits >> 2][side * CD_COLS + (bits & 3) * 4]
+                                                       : &sums[t][wave][which][side * CD_COLS + bits * 2]) = y;
             }
-            // over the lanes of a column, as for one token
-            halve32<16>(x);
-            halve16<8>(x);
-            halve<4>(x, lane & 8, [](float y) { return dpp<DPP_ROR8>(y); });
-            const int bits = (lane >> 5 & 1) * 4 | (lane >> 4 & 1) * 2 | (lane >> 3 & 1);
-            *reinterpret_cast<f32x4 *>(&sums[t][wave][bits >> 2][side * CD_COLS + (bits & 3) * 4]) = f32x4{x[0], x[1], x[2], x[3]};
         }
         const bool moves = write || from + CH < len;
         if (moves) {   // k_s^(last) and c in the place of what the products have read
@@ -436,7 +449,8 @@ __global__ __launch_bounds__(CD_THREADS, WAVES) void kda_cached_outputs_kernel(
                 const float m = lane_of(gk, CH * t + p);
                 a[0] += m * f[p][0], a[1] += m * f[p][1];
             }
-            f[t] = f32x2{bt[t] * (to_f(vx[t][0]) - a[0]), bt[t] * (to_f(vx[t][1]) - a[1])};
+            const float bt = lane_of(bx, t);
+            f[t] = f32x2{bt * (to_f(vx[t][0]) - a[0]), bt * (to_f(vx[t][1]) - a[1])};
             if (wave == t % CD_WAVES) {
                 if (moves) *reinterpret_cast<f32x2 *>(&offs[t][2 * lane]) = f[t];
                 f32x2 b{};
@@ -498,10 +512,12 @@ static hipError_t cached_tokens(const void *q, const void *k, const void *v, con
         const uint32_t per_head = (uint32_t)((((uint64_t)1 << shift) + H - 1) / H);
         typedef decltype(f) F;
         // Where no sequence need have several rows, registers for four workgroups a CU: 512 x 32, one
-        // token committed, fp8 101 us (three: 105), int8 107 (116), fp4 75 (87).  The chunks spill
-        // then: 64 drafts of eight tokens among 448 empty sequences take 77 us (three: 53).
+        // token committed, fp8 101 us (three: 103), int8 106 (116), fp4 75 (86).  The chunks spill a
+        // little then: eight drafts of five, 32 heads, among 56 empty sequences 16 us (three: 12).  So
+        // not where three of every CU take all sequences with a row.
+        const bool three = T_tot > N || (int64_t)T_tot * H <= 3 * 256;
         const auto kernel = !out ? kda_cached_commit_kernel<T, F>
-                            : T_tot > N ? kda_cached_outputs_kernel<T, F, 3> : kda_cached_outputs_kernel<T, F, 4>;
+                            : three ? kda_cached_outputs_kernel<T, F, 3> : kda_cached_outputs_kernel<T, F, 4>;
         hipLaunchKernelGGL(kernel, dim3((unsigned)((int64_t)N * H)), dim3(CD_THREADS), 0, s, (const T *)q, (const T *)k,
                            (const T *)v, g, beta, cu, num_tokens, cache, scales, slots, (int32_t)write, num_slots, H,
                            per_head, shift, T_tot, (T *)out);

@@ -67,6 +67,32 @@ def test_the_bits_are_those_of_the_sequence_alone(dtype, fmt, write):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_bits_do_not_go_by_the_registers(dtype, fmt):
+    """No more rows than sequences, and more than 768 of all heads: the kernel for four workgroups a CU.  One row less, or one
+    sequence less: the one for three."""
+    lens, H = [1, 7, 1, 1, 5, 1, 2, 1, 1, 3, 1, 1], 32                  # 25 rows, 800 with their heads
+    p = make(lens, H, fmt, dtype, seed=5)
+    whole = list(range(len(lens)))
+    results = []
+    for order, pad in ((whole + [None] * 13, 0), (whole + [None] * 12, 0), (whole, 30), (whole + [None] * 30, 2)):
+        s, at = batch_of(p, order, pad)
+        cache, scales = p["cache"].clone(), p["scales"].clone()
+        out = torch.empty_like(s["v"])
+        K.kda_decode_tokens_cached(*(s[x] for x in ("q", "k", "v", "g", "beta", "cu")), cache, scales, s["slots"], fmt, out=out)
+        results.append((out[:25], cache, scales))
+    few, _ = batch_of(p, whole[:11] + [None] * 13)                       # 24 rows: 768
+    cache, scales = p["cache"].clone(), p["scales"].clone()
+    out = torch.empty_like(few["v"])
+    K.kda_decode_tokens_cached(*(few[x] for x in ("q", "k", "v", "g", "beta", "cu")), cache, scales, few["slots"], fmt, out=out)
+    slots = p["slots"][:11].long()
+    for o, c, sc in results:
+        assert torch.equal(o, results[0][0]) and torch.equal(c, results[0][1]) and torch.equal(sc, results[0][2])
+        assert torch.equal(o[:24], out) and torch.equal(c[slots], cache[slots]) and torch.equal(sc[slots], scales[slots])
+    check_decode(dict(p, **batch_of(p, whole + [None] * 13)[0]), fmt, True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_a_sequence_goes_by_its_rows_and_not_by_those_processed(fmt):
     """The first token of a draft has one output, however many tokens are processed."""
     p = make([5, 5, 1], 2, fmt, "fp32")
