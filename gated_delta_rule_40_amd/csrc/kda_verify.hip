@@ -5,8 +5,18 @@
 // accepted drafts are counted, which takes two values a draft.  So every workgroup
 // counts them for itself, and of all rows only that one is read: its weights
 // w = max(p - q, 0) are summed in parts of 1,024, a wave each (kernel 1), and the part
-// where the running sum passes sample_rand * total is searched (kernel 2).  Sums are
-// formed in fp64 in a fixed order, where a difference of two probabilities is exact.
+// where the running sum passes sample_rand * total is searched (kernel 2).
+//
+// Sums are formed in fp64 in a fixed order.  A difference has its sign exactly and is
+// rounded once (fp32 probabilities may lie more than 53 binary places apart).  No
+// partial sum is above the total, so every rounding is off by at most u = 2^-53 of it.
+// With P = ceil(vocab / 2^18) parts a thread, the total passes at most 36 + P roundings
+// (1 of the difference, 8 in a lane, 6 over lanes, P, 6 over lanes, 15 over waves), the
+// mark one more, and the running sum at a place 69 + 2 P (36 + 2 P + 1 up to its part, 32
+// within).  So a token is the one that real numbers give unless the mark lies within
+// (106 + 3 P) u of the total from a running sum: 2^-46 up to 2^18 tokens, 2^-39 at 2^30.
+// (Where nothing is left and the target's row is summed by one workgroup, each thread
+// adds 1,024 P weights and 256 P parts: (110 + 1,300 P) u, 2^-42 and 2^-30.)
 //
 // HBM bounds large calls, latency small ones: the counting takes two dependent reads,
 // each kernel about three.  One MI355X, fp32, four drafts, both kernels of a replayed

@@ -759,8 +759,10 @@ kda_status kda_decode_tokens_cached(const void *q, const void *k, const void *v,
  *
  * (the last x with w[x] > 0 if none is; where rejected weights are all zero, the
  * target's row itself).  So the next token is distributed as the target's own.
- * Sums and products are formed in fp64; probabilities need not sum to one, those
- * below zero and NaN count as zero.
+ * Differences, sums and products are formed in fp64, so that the next token is the
+ * one of real numbers unless sample_rand * total lies within 2^-42 of the total
+ * (2^-30 for the largest vocabularies) from a running sum.  Probabilities need not
+ * sum to one, those below zero and NaN count as zero.
  *
  *   target_probs  [total_tokens, vocab]          dtype: row i, after token row i
  *   draft_probs   [total_tokens, vocab]          dtype: row i, the distribution that

@@ -73,3 +73,30 @@ def test_bad_cu_seqlens_are_held_to_the_token_rows(cu, means, V):
         if b > a:
             want = check(t[a:b], d[a:b], tok[a:b], [0, b - a], acc[a:b], smp[n:n + 1])
         assert ([int(arrays["num"][n])], [int(arrays["next"][n])]) == want
+
+
+@pytest.mark.parametrize("V", [4000, 40000])                  # one launch and two
+def test_differences_are_rounded_once(V):
+    """fp32 probabilities more than 53 binary places apart: the sign of what is left is exact, and so is a tiny remainder alone."""
+    t, d = torch.zeros(2, V, device="cuda"), torch.zeros(2, V, device="cuda")
+    t[0, 5], d[1, 5] = 0.5, 2.0 ** -70                        # rounds to 0.5
+    t[0, V - 1], d[1, V - 1] = 2.0 ** -70, 2.0 ** -71         # left over: 2^-71
+    t[0, 9], d[1, 9] = 2.0 ** -71, 2.0 ** -70                 # nothing left
+    for sample, want in ((0.0, 5), (0.9999, 5)):
+        assert check(t, d, [0, 9], [0, 2], [0, 0.9], [sample]) == ([1], [want])
+    d[1, 5] = 0.5                                             # the remainder alone
+    for sample in (0.0, 0.5, 0.99999994):
+        assert check(t, d, [0, 9], [0, 2], [0, 0.9], [sample]) == ([1], [V - 1])
+
+
+def test_draws_beside_a_boundary():
+    """Running sums that fp64 holds exactly in any order, and marks one step of fp32 beside them, in rows of one part to 65."""
+    for V in (1024, 16384, 17000, 66000):
+        n = 16
+        t = torch.zeros(n, V, device="cuda")
+        at = torch.linspace(0, V - 1, 8).long()
+        t[:, at.cuda()] = 0.125
+        marks = torch.arange(n) % 8 / 8.0
+        sample = torch.where(torch.arange(n) < 8, marks, torch.nextafter(marks, torch.tensor(-1.0)).clamp(min=0)).tolist()
+        want = [int(at[i]) for i in range(8)] + [int(at[max(i - 1, 0)]) for i in range(8)]
+        assert check(t, None, [0] * n, range(n + 1), [0.0] * n, sample)[1] == want
