@@ -57,3 +57,18 @@ def test_a_tile_s_turns_are_its_own():
         into.append((qo, ko, g["dq"], g["dk"]))
     for a, b in zip(whole[0], map(torch.cat, zip(*parts))):
         assert torch.equal(a, b)
+
+
+# the last piece of a part lies over the one before, in the same wave
+@pytest.mark.parametrize("d,rot,dtype", [(77, 0, "fp32"), (77, 20, "bf16"), (100, 50, "bf16"), (129, 2, "fp32"), (511, 0, "fp32"),
+                                         (13, 6, "bf16")])
+def test_in_place_where_pieces_overlap(d, rot, dtype):
+    p = make(41, 9, 6, d, rot, dtype=dtype, grad="fp32")
+    qo, ko, g = check(p)
+    form = dict(q_weight=p["qw"], k_weight=p["kw"], eps=1e-5, q_scale=0.25, **p["turn"])
+    q, k = p["q"].clone(), p["k"].clone()
+    K.kda_qknorm(q, k, q, k, **form)
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+    q, k = p["q"].clone(), p["k"].clone()
+    K.kda_qknorm_backward(q, k, p["dq"], p["dk"], grads=dict(g, dq=q, dk=k), **form)
+    assert torch.equal(q, g["dq"]) and torch.equal(k, g["dk"])
