@@ -16,13 +16,13 @@
 // instructions several (token by token about 390 a wave and token for 64 values a lane:
 // the decay, two products, the update, and the halving).  So a sequence of several token
 // rows takes them in chunks, from one state, if there are outputs: 512 sequences of 32
-// heads, fp8, two, five and eight tokens verified 88, 172 and 293 us, token by token 105, 214
-// and 325; five of 64 x 16 in int8 16.8 and 18.7.  Without outputs b and the queries fall away
+// heads, fp8, two, five and eight tokens verified 88, 170 and 292 us, token by token 105, 214
+// and 325; five of 64 x 16 in int8 16.6 and 18.7.  Without outputs b and the queries fall away
 // and chunks gain nothing (five committed 131 us, token by token 124).
 // The form goes by a sequence's own rows (cu_seqlens), not by how many of them are processed
 // and not by the batch: its results have the same bits whatever stands beside it.
 // One MI355X, bf16, replays of a graph: 512 sequences of 32 heads, one token committed, fp8
-// 101 us (5.7 TB/s), int8 107, fp4 75; beside a sequence of five 105; 8 x 8 heads 3.9.
+// 101 us (5.7 TB/s), int8 106, fp4 75; beside a sequence of five 103; 8 x 8 heads 3.8.
 // Waves that each had 32 columns of all rows needed no barrier, but their reads of 32
 // bytes a row bound them to 129 us; 8 columns by 8 rows a lane 119 (198 for five tokens
 // verified token by token); decays kept apart from the state, as factors of its rows, gained
